@@ -74,9 +74,12 @@ typedef enum {
     QG_ETIMEOUT = -7,    /* a kernel gave up waiting (see qg_device_status)  */
     QG_EEXPERT = -8,     /* qgemv_moe: a slot's expert id was out of range   */
                          /* or its weights misaligned (qg_device_status)     */
-    QG_EBOUNDS = -9      /* bounds-checking build only: a kernel formed an   */
+    QG_EBOUNDS = -9,     /* bounds-checking build only: a kernel formed an   */
                          /* index outside its arrays and skipped the access  */
                          /* (qg_device_status; never raised by libqgemv.so)  */
+    QG_EPAGE = -10       /* paged cache: a block table, length or slot in    */
+                         /* device memory names no place of the cache; the   */
+                         /* access was skipped (qg_device_status)            */
 } qg_status;
 
 /* Static name of a status code ("QG_EGS: ..."). Never NULL. */
@@ -455,6 +458,127 @@ int qgemm_mq4v1(float *Y, const uint16_t *X, const uint8_t *blocks,
                 int M, int I, int O, void *ws, size_t ws_bytes, qg_stream_t stream);
 int qgemm_mq4c(float *Y, const uint16_t *X, const uint8_t *blocks,
                int M, int I, int O, void *ws, size_t ws_bytes, qg_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* The attention block between the QKV and output projections of a decode   */
+/* step: rotary positions and the cache write, attention of the new tokens  */
+/* over a paged key-value cache, and eviction from it.  The pages have no   */
+/* counterpart: their engines' attention is outside the quantized path.     */
+/*                                                                          */
+/* The cache (host struct, read during the call only):                      */
+/*   k, v    DEVICE pools of n_pages pages of page_size slots: element d of */
+/*           head h of slot t of page p is element                          */
+/*           p * page_stride + h * head_stride + t * token_stride + d of    */
+/*           either pool (strides in elements, the same for k and v; pages  */
+/*           may be [head][slot][dim] or [slot][head][dim], k and v may lie */
+/*           in one allocation).  With [head][slot][dim] a page's slots of  */
+/*           one head are one contiguous run of HBM, which reads fastest.   */
+/*   type    QG_BF16, QG_F16, or QG_E4M3 (OCP E4M3-FN codes; the element is */
+/*           code * k_scale[h] or v_scale[h])                               */
+/*   k_scale, v_scale  DEVICE f32 [n_heads], QG_E4M3 only                   */
+/*   weight  DEVICE f32 [n_pages][n_heads][page_size], or NULL: attention   */
+/*           weight every slot has drawn (qattn_paged), for qg_kv_evict     */
+/*   head_dim  1 .. 256, whole 16-byte lines (a multiple of 8; of 16 for    */
+/*           QG_E4M3).  k, v and all strides are whole 16-byte lines too.   */
+/* A sequence b owns slots 0 .. lens[b] - 1; slot t is slot t % page_size   */
+/* of page table[b * table_stride + t / page_size] (DEVICE int32; entries   */
+/* past the last slot are not read).  Sequences may share pages that are    */
+/* only read.  Tables, lengths, slots and positions live in device memory   */
+/* and are read after the previous kernel on the stream has finished, so    */
+/* a captured graph replays with new ones.  They are out of the host's      */
+/* reach: an entry that names no place of the cache is not accessed, and    */
+/* the device error word says QG_EPAGE (qg_device_status); what the call    */
+/* makes of the skipped slot is said at each entry point.                   */
+/* ------------------------------------------------------------------------ */
+enum { QG_F32 = 0, QG_BF16 = 1, QG_F16 = 2, QG_E4M3 = 3 };   /* element types */
+
+typedef struct {
+    void *k, *v;
+    const float *k_scale, *v_scale;
+    float *weight;
+    size_t page_stride, head_stride, token_stride;
+    int type;
+    int n_pages, page_size, n_heads, head_dim;
+} qg_kv_cache;
+
+/* Rotary positions and the cache write.
+ *   qkv    DEVICE [T] rows of qkv_stride elements (QG_F32 as the GEMVs and
+ *          GEMMs here write them, QG_BF16 or QG_F16): n_q_heads q heads, then
+ *          n_heads k heads, then n_heads v heads, head_dim each
+ *   pos    DEVICE int32 [T][n_axes] positions; pair j of a q or k head turns
+ *          by pos[t][axis[j]] * inv_freq[j] (axis: HOST bytes [rotary_dim/2]
+ *          below n_axes, NULL = all 0; inv_freq: DEVICE f32 [rotary_dim/2]):
+ *          (x, y) -> (x cos - y sin, y cos + x sin).  Several axes (time,
+ *          height, width) share the pairs out among them by `axis`.
+ *   style  QG_ROPE_HALF: pair j is elements j and j + rotary_dim/2;
+ *          QG_ROPE_INTERLEAVED: 2j and 2j + 1.  Elements from rotary_dim
+ *          (even, 0 .. head_dim) on pass through.
+ *   q      DEVICE [T][n_q_heads][head_dim], QG_BF16 or QG_F16
+ *   seq, slot  DEVICE int32 [T]: token t's k and v go to slot slot[t] of
+ *          sequence seq[t] (of n_seq), the slot's weight becomes 0; a
+ *          negative slot writes q only (padding).  No two tokens may name
+ *          one slot.  A slot or page that is not there: QG_EPAGE, k and v
+ *          not written.
+ * Angles are formed and reduced in 64 bits, the rotation in 32; one rounding
+ * (nearest even) to the type stored.  QG_E4M3 stores x / scale, held to the
+ * largest finite code; NaN stays NaN.  T = 0 launches nothing.  Alignment:
+ * elements; qkv rows and q on four-element boundaries and rotary_dim % 8 == 0
+ * take the fastest path. */
+enum { QG_ROPE_HALF = 0, QG_ROPE_INTERLEAVED = 1 };
+
+int qg_rope_append(const qg_kv_cache *cache, const int *table, int table_stride, int n_seq, const int *seq,
+                   const int *slot, int T, void *q, int q_type, const void *qkv, int qkv_type, size_t qkv_stride,
+                   int n_q_heads, const int *pos, int n_axes, const unsigned char *axis, const float *inv_freq,
+                   int rotary_dim, int style, qg_stream_t stream);
+
+/* Attention of S (1 .. 8) new tokens a sequence over its cached slots, theirs
+ * among them (append first): row (b, s, h) of q sees slots
+ * t < lens[b] - S + 1 + s, and
+ *   z_t = scale * q . k_t,   lse = log sum_t exp(z_t),
+ *   o = sum_t exp(z_t - lse) * v_t.
+ * A row that sees nothing gives o = 0, lse = -inf.
+ *   q      DEVICE rows (b * S + s) of q_stride elements, n_q_heads heads of
+ *          head_dim; q head h reads cache head h / (n_q_heads / n_heads).
+ *          The cache's type, QG_BF16 or QG_F16 over a QG_E4M3 cache.
+ *   lens   DEVICE int32 [n_seq], each in [0, max_len]; max_len at most
+ *          table_stride * page_size (it bounds the workspace)
+ *   o      DEVICE [n_seq * S][n_q_heads][head_dim], QG_F32, QG_BF16 or QG_F16
+ *   lse    DEVICE f32 [n_seq * S][n_q_heads], or NULL
+ *   accumulate  non-zero: weight[slot] += sum over the S * n_q_heads/n_heads
+ *          rows that read it of exp(z_t - lse) (cache->weight needed; slots
+ *          of a page that sequences share must not be accumulated to by two
+ *          of them in one call)
+ *   ws     qattn_workspace_bytes() bytes, 256-byte aligned; contents on entry
+ *          do not matter
+ * A masked slot never touches its row, whatever it holds (NaN, infinity).
+ * A visible slot whose page is not in the pool makes its rows NaN and raises
+ * QG_EPAGE; a length outside [0, max_len] is held to it and raises QG_EPAGE.
+ * Sums and softmax statistics are f32, in an order that depends on the
+ * lengths alone, so repeated calls give identical results.  n_seq = 0
+ * launches nothing. */
+size_t qattn_workspace_bytes(const qg_kv_cache *cache, int n_seq, int max_len, int S, int n_q_heads, int accumulate);
+
+int qattn_paged(const qg_kv_cache *cache, const int *table, int table_stride, const int *lens, int n_seq,
+                int max_len, void *o, int o_type, float *lse, const void *q, int q_type, size_t q_stride, int S,
+                int n_q_heads, float scale, int accumulate, void *ws, size_t ws_bytes, qg_stream_t stream);
+
+/* Eviction: each sequence and head keeps N = min(lens[b], budget) slots -- the
+ * first `sinks`, the last `recent` (sinks + recent <= budget), and of the
+ * slots between them those of largest weight (equal weights: the lower slot;
+ * NaN ranks above every number) -- and copies them in slot order (k, v and
+ * weight) to slots 0 .. N - 1 of the pages that dst_table names.  Heads of a
+ * sequence may keep different slots.
+ *   kept      DEVICE int32 [n_seq][n_heads][budget]: the slots kept,
+ *             ascending, then -1
+ *   new_lens  DEVICE int32 [n_seq]: N (not the array lens)
+ * Destination pages must not be among the source pages of the call; the
+ * source pages keep their contents (a shared prompt stays whole for the other
+ * sequences) and are the caller's to free.  A slot whose page, either side, is
+ * not in the pool is not copied (its weight ranks as the lowest) and raises
+ * QG_EPAGE; lengths as in qattn_paged.  n_seq = 0 launches nothing. */
+int qg_kv_evict(const qg_kv_cache *cache, const int *table, int table_stride, const int *dst_table, int dst_stride,
+                const int *lens, int n_seq, int max_len, int budget, int sinks, int recent, int *kept,
+                int *new_lens, qg_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Weight preparation on the device (not on the decode path)                */

@@ -23,10 +23,13 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
-QG_OK, QG_EINVAL, QG_EGS, QG_ESHAPE, QG_EALIGN, QG_EWORKSPACE, QG_ECUDA, QG_ETIMEOUT, QG_EEXPERT, QG_EBOUNDS = (
-    0, -1, -2, -3, -4, -5, -6, -7, -8, -9)
+QG_OK, QG_EINVAL, QG_EGS, QG_ESHAPE, QG_EALIGN, QG_EWORKSPACE, QG_ECUDA, QG_ETIMEOUT, QG_EEXPERT, QG_EBOUNDS, QG_EPAGE = (
+    0, -1, -2, -3, -4, -5, -6, -7, -8, -9, -10)
 QG_FMT_I4G, QG_FMT_FP8B128, QG_FMT_FP8UE8M0, QG_FMT_MQ4V1, QG_FMT_MQ4V2, QG_FMT_MQ4C, QG_FMT_Q2_0 = (
     4, 7, 71, 13, 44, 45, 20)
+
+QG_F32, QG_BF16, QG_F16, QG_E4M3 = 0, 1, 2, 3
+QG_ROPE_HALF, QG_ROPE_INTERLEAVED = 0, 1
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -59,6 +62,10 @@ _SIGNATURES = {
     "qgemv_moe": ([_I, _P, _P, _Z, _P, _I, _P, _I, _I, _I, _I, _I, _P], _I),
     "qgemm_moe": ([_I, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _P, _Z, _P], _I),
     "qg_moe_gemm_workspace_bytes": ([_I, _P, _I, _I, _I, _I], _Z),
+    "qg_rope_append": ([_P, _P, _I, _I, _P, _P, _I, _P, _I, _P, _I, _Z, _I, _P, _I, _P, _P, _I, _I, _P], _I),
+    "qattn_workspace_bytes": ([_P, _I, _I, _I, _I, _I], _Z),
+    "qattn_paged": ([_P, _P, _I, _P, _I, _I, _P, _I, _P, _P, _I, _Z, _I, _I, ctypes.c_float, _I, _P, _Z, _P], _I),
+    "qg_kv_evict": ([_P, _P, _I, _P, _I, _P, _I, _I, _I, _I, _I, _P, _P, _P], _I),
     "qg_encode_mq4v1": ([_P, _P, _I, _I, _P], _I),
     "qg_encode_mq4c": ([_P, _P, _I, _I, _P], _I),
     "qg_quantize_i4g": ([_P, _P, _P, _I, _I, _I, _P], _I),
@@ -276,3 +283,69 @@ def qg_encode_mq4v2(blocks, w, O, I, stream=None) -> int:
 
 def qg_fwht256(out, inp, signs, n_blocks, stream=None) -> int:
     return _lib.qg_fwht256(_ptr(out), _ptr(inp), _ptr(signs), n_blocks, _stream(stream))
+
+
+class KVCache(ctypes.Structure):
+    """qg_kv_cache: a paged key-value cache's pools, layout and element type."""
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("weight", _P),
+                ("page_stride", _Z), ("head_stride", _Z), ("token_stride", _Z), ("type", _I),
+                ("n_pages", _I), ("page_size", _I), ("n_heads", _I), ("head_dim", _I)]
+
+
+def kv_cache(k, v, k_scale=None, v_scale=None, weight=None, order="head"):
+    """A KVCache over torch tensors k and v, [n_pages, n_heads, page_size,
+    head_dim] (``order="head"``) or [n_pages, page_size, n_heads, head_dim]
+    (``order="token"``), any strides with the last one 1;
+    bfloat16, float16 or float8_e4m3fn.  Holds the tensors while it lives."""
+    if order not in ("head", "token"):
+        raise ValueError("order is 'head' or 'token'")
+    name = str(k.dtype).replace("torch.", "")
+    types = {"bfloat16": QG_BF16, "float16": QG_F16, "float8_e4m3fn": QG_E4M3}
+    if name not in types:
+        raise ValueError(f"a cache of {name} is not supported")
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride() or k.stride(3) != 1:
+        raise ValueError("k and v are [n_pages, ., ., head_dim] of one shape, type and strides, the last stride 1")
+    pages, a, b, dim = k.shape
+    heads, page = (a, b) if order == "head" else (b, a)
+    hs, ts = (k.stride(1), k.stride(2)) if order == "head" else (k.stride(2), k.stride(1))
+    if weight is not None and (tuple(weight.shape) != (pages, heads, page) or not weight.is_contiguous()
+                               or not str(weight.dtype).endswith("float32")):
+        raise ValueError("weight is contiguous float32 [n_pages, n_heads, page_size]")
+    for s in (k_scale, v_scale):
+        if s is not None and (s.numel() != heads or not s.is_contiguous() or not str(s.dtype).endswith("float32")):
+            raise ValueError("k_scale and v_scale are contiguous float32 [n_heads]")
+    c = KVCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(weight), k.stride(0), hs, ts, types[name],
+                pages, page, heads, dim)
+    c.tensors = (k, v, k_scale, v_scale, weight)
+    return c
+
+
+def _cache(c):
+    return ctypes.addressof(c) if c is not None else None
+
+
+def qg_rope_append(cache, table, table_stride, n_seq, seq, slot, T, q, q_type, qkv, qkv_type, qkv_stride, n_q_heads,
+                   pos, n_axes, axis, inv_freq, rotary_dim, style=QG_ROPE_HALF, stream=None) -> int:
+    """Rotary positions and the cache write; ``axis`` is bytes of length
+    rotary_dim/2 (host data) or None."""
+    return _lib.qg_rope_append(_cache(cache), _ptr(table), table_stride, n_seq, _ptr(seq), _ptr(slot), T, _ptr(q),
+                               q_type, _ptr(qkv), qkv_type, qkv_stride, n_q_heads, _ptr(pos), n_axes,
+                               axis if axis is None else ctypes.c_char_p(axis), _ptr(inv_freq), rotary_dim, style,
+                               _stream(stream))
+
+
+def qattn_workspace_bytes(cache, n_seq, max_len, S, n_q_heads, accumulate=0) -> int:
+    return _lib.qattn_workspace_bytes(_cache(cache), n_seq, max_len, S, n_q_heads, accumulate)
+
+
+def qattn_paged(cache, table, table_stride, lens, n_seq, max_len, o, o_type, lse, q, q_type, q_stride, S, n_q_heads,
+                scale, accumulate=0, ws=None, ws_bytes=0, stream=None) -> int:
+    return _lib.qattn_paged(_cache(cache), _ptr(table), table_stride, _ptr(lens), n_seq, max_len, _ptr(o), o_type,
+                            _ptr(lse), _ptr(q), q_type, q_stride, S, n_q_heads, scale, accumulate, _ptr(ws), ws_bytes,
+                            _stream(stream))
+
+
+def qg_kv_evict(cache, table, table_stride, dst_table, dst_stride, lens, n_seq, max_len, budget, sinks, recent, kept,
+                new_lens, stream=None) -> int:
+    return _lib.qg_kv_evict(_cache(cache), _ptr(table), table_stride, _ptr(dst_table), dst_stride, _ptr(lens), n_seq,
+                            max_len, budget, sinks, recent, _ptr(kept), _ptr(new_lens), _stream(stream))

@@ -48,12 +48,6 @@ namespace {
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
-#define QG_REFUSE(code, ...)              \
-    do {                                  \
-        set_error_detail(__VA_ARGS__);    \
-        return (code);                    \
-    } while (0)
-
 // Common checks of the shape arguments.
 int check_dims(const char *fn, const char *sname, int S, int I, int O) {
     if (S < 1) QG_REFUSE(kEInval, "%s: %s = %d, must be >= 1", fn, sname, S);
@@ -151,6 +145,7 @@ const char *qg_strerror(int status) {
         case QG_ECUDA: return "QG_ECUDA: CUDA runtime error";
         case QG_ETIMEOUT: return "QG_ETIMEOUT: a kernel gave up waiting on a barrier";
         case QG_EEXPERT: return "QG_EEXPERT: a routed slot named a missing expert or one with misaligned weights";
+        case QG_EPAGE: return "QG_EPAGE: a block table, length or slot in device memory names no place of the cache";
         case QG_EBOUNDS: return "QG_EBOUNDS: a kernel formed an index outside its arrays (bounds-checking build)";
         default: return "unknown qg_status";
     }

@@ -1,0 +1,188 @@
+// kv_cache.cuh -- device view of a paged key-value cache (qg_kv_cache in
+// include/qgemv.h) and what its kernels share: finding a slot, the element
+// types, programmatic launches.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "launch.h"
+#include "pipeline.cuh"
+
+namespace qg {
+
+int *device_error_word();
+int num_sms();
+
+constexpr int kErrPage = -10;
+
+// Element types (QG_F32 ... in include/qgemv.h).
+enum { kF32 = 0, kBf16 = 1, kF16 = 2, kE4m3 = 3 };
+
+struct KvView {
+    char *k, *v;
+    const float *k_scale, *v_scale;   // e4m3 only
+    float *weight;                    // [n_pages][n_heads][page], or NULL
+    long long page_b, head_b, token_b;   // strides of k and v in bytes
+    int n_pages, page, page_shift;    // page_shift: log2(page), -1 when page is no power of two
+    int n_heads, dim, type;
+};
+
+struct SlotRef { int page, off; };    // page of the pool (-1: none) and slot inside it
+
+// Page index of slot t in a sequence's table, and t's place in that page.
+__device__ __forceinline__ void split_slot(const KvView &c, int t, int *index, int *off) {
+    if (c.page_shift >= 0) {
+        *index = t >> c.page_shift;
+        *off = t & (c.page - 1);
+    } else {
+        *index = (int)((unsigned)t / (unsigned)c.page);
+        *off = t - *index * c.page;
+    }
+}
+
+// Slot t of the sequence whose table row is `row`; page -1 when the table
+// names no page of the pool.
+__device__ __forceinline__ SlotRef find_slot(const KvView &c, const int *row, int t) {
+    SlotRef r;
+    int index;
+    split_slot(c, t, &index, &r.off);
+    const int p = __ldg(row + index);
+    r.page = (unsigned)p < (unsigned)c.n_pages ? p : -1;
+    return r;
+}
+
+__device__ __forceinline__ long long slot_bytes(const KvView &c, SlotRef r, int head) {
+    return r.page * c.page_b + head * c.head_b + r.off * c.token_b;
+}
+__device__ __forceinline__ size_t slot_weight(const KvView &c, SlotRef r, int head) {
+    return ((size_t)r.page * c.n_heads + head) * c.page + r.off;
+}
+
+// Length of sequence b, held to [0, max_len]; a length outside raises the
+// error word (by the thread that asks with err != NULL).
+__device__ __forceinline__ int seq_len(const int *lens, int b, int max_len, int *err) {
+    const int n = __ldg(lens + b);
+    if ((unsigned)n <= (unsigned)max_len) return n;
+    raise_device_error(err, kErrPage);
+    return n < 0 ? 0 : max_len;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Two e4m3 codes, the nearest finite ones of lo and hi (NaN stays NaN).
+__device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    uint32_t w;
+    asm("cvt.u32.u16 %0, %1;" : "=r"(w) : "h"(r));
+    return w;
+}
+__device__ __forceinline__ uint32_t pack_16(int type, float lo, float hi) {
+    return type == kF16 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
+}
+// Two e4m3 codes (low 16 bits of w) as an exact f16 pair.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
+    uint32_t r;
+    asm("{.reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t;}" : "=r"(r) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t w) {
+    float2 r;
+    asm("{.reg .f16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}" : "=f"(r.x), "=f"(r.y) : "r"(w));
+    return r;
+}
+
+// Launch with programmatic stream serialization: the kernel may start while
+// its predecessor runs, and waits for it with griddep_wait().
+template <class... P, class... A>
+inline int launch_pdl(const char *what, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                      A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+    count_launch();
+    return check_launch(what);
+}
+
+// Arguments of the attention over the cache (qattn_paged).
+struct AttnArgs {
+    KvView c;
+    const int *table;
+    int table_stride;
+    const int *lens;
+    int n_seq, max_len;
+    void *o;
+    int o_type;
+    float *lse;                       // or NULL
+    const void *q;
+    int q_type;
+    size_t q_stride;
+    int S, n_q_heads, group;          // group = n_q_heads / c.n_heads
+    float scale;
+    int accumulate;
+    int *err;
+};
+
+// Arguments of the cache write with rotary positions (qg_rope_append).
+constexpr int kMaxPairs = 128;
+struct RopeArgs {
+    KvView c;
+    const int *table;
+    int table_stride, n_seq;
+    const int *seq, *slot;
+    int T;
+    void *q;
+    int q_type;
+    const void *qkv;
+    size_t qkv_stride;
+    int n_q_heads;
+    const int *pos;
+    int n_axes;
+    const float *inv_freq;
+    int rotary, interleaved;
+    int *err;
+    unsigned char axis[kMaxPairs];
+};
+
+// Arguments of the eviction (qg_kv_evict).
+struct EvictArgs {
+    KvView c;
+    const int *table;
+    int table_stride;
+    const int *dst_table;
+    int dst_stride;
+    const int *lens;
+    int n_seq, max_len, budget, sinks, recent;
+    int *kept, *new_lens;
+    int *err;
+};
+
+int run_rope_append(const RopeArgs &a, int qkv_type, cudaStream_t st);
+size_t ws_attn_paged(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int accumulate);
+int run_attn_paged(const AttnArgs &a, void *ws, cudaStream_t st);
+int run_kv_evict(const EvictArgs &a, cudaStream_t st);
+
+}  // namespace qg

@@ -17,6 +17,13 @@ enum { kOk = 0, kEInval = -1, kEGs = -2, kEShape = -3, kEAlign = -4, kEWorkspace
 // Records a refusal / error detail for qg_last_error() (thread-local).
 void set_error_detail(const char *fmt, ...);
 
+// Refuses a call: records the detail and returns the status.
+#define QG_REFUSE(code, ...)              \
+    do {                                  \
+        set_error_detail(__VA_ARGS__);    \
+        return (code);                    \
+    } while (0)
+
 // Reports launch errors of the kernels just enqueued.
 int check_launch(const char *what);
 
