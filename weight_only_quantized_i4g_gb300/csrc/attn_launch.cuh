@@ -1,0 +1,46 @@
+// attn_launch.cuh -- which instantiation of the attention kernel a call takes,
+// and its launch.
+#pragma once
+
+#include "attn_paged.cuh"
+
+namespace qg {
+
+struct AttnPlan {
+    int dp, nt;         // padded head size, tiles of 8 rows per segment
+    int warps;
+    size_t smem;        // without the lengths
+};
+
+// The smallest padded head size (the padding is not read from memory), and
+// one, two or four tiles of 8 rows: as many as hold the rows, so that K and V
+// are read once per segment; O's registers bound them (128 a thread).
+template <int TYPE, class Fn>
+auto attn_dispatch(int rows, int dim, Fn fn) {
+    const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+    if (dim <= 64) return nt == 1 ? fn(AttnCfg<TYPE, 64, 1>()) : nt == 2 ? fn(AttnCfg<TYPE, 64, 2>()) : fn(AttnCfg<TYPE, 64, 4>());
+    if (dim <= 128)
+        return nt == 1 ? fn(AttnCfg<TYPE, 128, 1>()) : nt == 2 ? fn(AttnCfg<TYPE, 128, 2>()) : fn(AttnCfg<TYPE, 128, 4>());
+    return nt == 1 ? fn(AttnCfg<TYPE, 256, 1>()) : fn(AttnCfg<TYPE, 256, 2>());
+}
+
+template <int TYPE>
+AttnPlan attn_plan(int rows, int dim) {
+    return attn_dispatch<TYPE>(rows, dim, [](auto cfg) {
+        using C = decltype(cfg);
+        return AttnPlan{C::DP, C::NT, C::W, attn_fixed_smem<C>()};
+    });
+}
+
+template <int TYPE>
+int launch_attn_stream(const AttnArgs &a, const AttnWork &w, const AttnPlan &pl, cudaStream_t st) {
+    return attn_dispatch<TYPE>(a.S * a.group, a.c.dim, [&](auto cfg) {
+        using C = decltype(cfg);
+        const size_t smem = pl.smem + (2 * (size_t)a.n_seq + 1) * sizeof(int);
+        auto *kernel = attn_stream_kernel<TYPE, C::DP, C::NT>;
+        set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), 232448);
+        return launch_pdl("qattn_paged", kernel, dim3(num_sms()), dim3(C::threads), smem, st, a, w);
+    });
+}
+
+}  // namespace qg

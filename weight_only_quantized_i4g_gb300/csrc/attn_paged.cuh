@@ -1,0 +1,734 @@
+// attn_paged.cuh -- attention of a few new tokens over a paged key-value cache
+// (qattn_paged): the streaming kernel.
+//
+// Row (b, s, h) sees the slots t < len_b - S + 1 + s:
+//   z_t = scale q . k_t,   o = sum_t exp(z_t - lse) v_t,   lse = log sum_t exp(z_t).
+// The cache is read once and little is computed per byte, so the call is bound
+// by HBM and everything serves keeping its reads in flight.
+//
+// Work.  The rows of one sequence that share a key-value head, R = S * group,
+// form tiles of 8 * NT rows; a (sequence, head, tile) is a segment of
+// ceil(len / 16) steps of 16 slots.  All segments' steps, laid end to end, are
+// cut into one equal range per block (one block an SM) and each range into one
+// per warp: unequal lengths balance without the host knowing them.  A warp
+// keeps the running maximum and sum of each row and O in registers (online
+// softmax).  A segment that ends inside its warp is finished there; pieces of
+// one that does not are joined in shared memory after the block's ranges are
+// done, and across blocks by a second kernel, always in slot order.
+//
+// Loads.  Every thread copies the 16-byte chunks that it will use itself into
+// a ring of its own in shared memory (cp.async), NS steps ahead: no barrier,
+// no exchange between threads, conflict-free 16-byte reads, and any strides
+// and page sizes.  The chunks are the fragments of the warp-level MMA as they
+// lie in memory: the contraction over d may run in any order, so a thread's
+// k indices are the 8 (or 16) consecutive elements of its chunk.
+//
+// Products.  S^T = K Q^T with the 16 slots as M and 8 rows as N (a decode step
+// has few rows), then O^T = V^T P^T; P^T's fragment is the transpose of
+// S^T's (movmatrix), V^T's pairs of slots are byte permutes of two loads.
+// mma.sync suffices: at the HBM rate 16 slots of 128 dimensions arrive per SM
+// every ~350 cycles and need 24 MMAs per 8 rows, a twelfth of its rate.
+// Precision: products of 16-bit operands are exact and summed in f32.  P is
+// not rounded to one 16-bit value but split into a sum of two (three for f32
+// output of a bf16 cache), so it keeps 16 to 24 bits; f16 parts are scaled by
+// 2^14 (as are the sums they are divided by) to stay out of its subnormals.
+// e4m3 codes are exact in f16; q over them is scaled per row by a power of two
+// into f16's range, which is exact for bf16 values within 2^29 of the largest.
+#pragma once
+
+#include "kv_cache.cuh"
+
+namespace qg {
+
+constexpr int kAttnMaxSeq = 2048;     // sequences per launch (their lengths sit in shared memory)
+
+// Workspace of one launch.
+struct AttnWork {
+    float *part_o;      // [ctas][2][rows][DP]: pieces a block leaves open, at its start (0) and end (1)
+    float2 *part_ml;    // [ctas][2][rows]: their maxima (log2 units) and sums
+    float *head_o;      // [ctas][warps][rows][DP]: pieces a warp finishes before its range ends
+    int2 *tail;         // [ctas]: {segment left open at the block's end or -1, blocks it spans}
+    float *scores;      // accumulate: z in log2 units, [segment][slot][rows]
+    int score_slots;    // slots per segment in scores
+    int row_tiles;
+};
+
+template <int TYPE, int DP_, int NT_>
+struct AttnCfg {
+    static constexpr int DP = DP_, NT = NT_;
+    static constexpr int ESZ = TYPE == kE4m3 ? 1 : 2;
+    static constexpr int rows = 8 * NT;
+    static constexpr int KE = 16 / ESZ;               // elements of a K chunk
+    static constexpr int NI = DP * ESZ / 64;          // K chunks a thread holds per slot (4 threads a slot)
+    static constexpr int E = DP / 8 < KE ? DP / 8 : KE;   // elements of a V chunk (8 threads a slot)
+    static constexpr int VB = E * ESZ;                // its bytes: 16, or 8
+    static constexpr int NQ = DP / (8 * E);           // V chunks a thread holds per slot
+    static constexpr int MT = DP / 16;                // 16-row tiles of O^T
+    static constexpr int k_bytes = 2 * NI * 512;
+    static constexpr int stage = k_bytes + NQ * 4 * 32 * VB;   // 16 slots of K and V: 32 * DP * ESZ
+    // 192 KB in flight per SM at most; eight warps, four where a stage is 16 KB
+    static constexpr int W = stage > 8192 ? 4 : 8;
+    static constexpr int NS0 = 196608 / (W * stage);
+    static constexpr int NS = NS0 > 8 ? 8 : NS0;
+    static constexpr int ring = NS * stage;           // per warp
+    static_assert(ring >= rows * DP * 4, "a warp's open piece takes the place of its ring");
+    static constexpr int threads = 32 * W;
+};
+
+// dynamic shared memory: rings, row statistics of open pieces, step masks,
+// piece descriptors, then prefix [n + 1] and lengths [n]
+template <class C>
+__host__ __device__ constexpr size_t attn_fixed_smem() {
+    return (size_t)C::W * C::ring + C::W * 2 * C::rows * sizeof(float2) + C::W * C::NS * 4 + C::W * 2 * 8;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+
+template <int TYPE>
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    if (TYPE == kBf16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// Elements 4 at a time of an output row: normalised, in the output's type.
+__device__ __forceinline__ void store_out4(const AttnArgs &a, size_t at, float4 v, float f) {
+    v.x *= f, v.y *= f, v.z *= f, v.w *= f;
+    if (a.o_type == kF32)
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + at) = v;
+    else
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.o) + at) =
+            make_uint2(pack_16(a.o_type, v.x, v.y), pack_16(a.o_type, v.z, v.w));
+}
+
+// What a row's statistics (maximum m in log2 units, sum l) say: the factor of
+// its O and its lse.  The f16 paths carry l and O times 2^14.
+template <int TYPE>
+__device__ __forceinline__ float row_factor(float l, float v_scale) {
+    return l == 0.f ? 0.f : v_scale / l;
+}
+template <int TYPE>
+__device__ __forceinline__ float row_lse(float m, float l) {
+    return l == 0.f ? -INFINITY : (m + (log2f(l) - (TYPE == kBf16 ? 0.f : 14.f))) * 0.69314718055994530942f;
+}
+
+// The place of row r (of a segment's tile) in q, o and lse.
+struct RowRef { bool real; int s; size_t head; };   // head: index of (b, s, q head)
+__device__ __forceinline__ RowRef row_ref(const AttnArgs &a, int b, int kh, int r) {
+    RowRef x;
+    x.real = r < a.S * a.group;
+    x.s = r / a.group;
+    x.head = ((size_t)b * a.S + x.s) * a.n_q_heads + kh * a.group + (r - x.s * a.group);
+    return x;
+}
+
+template <int TYPE, int DP_, int NT_>
+__global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
+    attn_stream_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnWork w) {
+    using C = AttnCfg<TYPE, DP_, NT_>;
+    constexpr int DP = C::DP, NT = C::NT, W = C::W, NS = C::NS, NI = C::NI, E = C::E, NQ = C::NQ, rows = C::rows;
+    extern __shared__ __align__(128) char smem[];
+    float2 *s_ml = reinterpret_cast<float2 *>(smem + W * C::ring);            // [W][2][rows]
+    uint32_t *s_mask = reinterpret_cast<uint32_t *>(s_ml + W * 2 * rows);     // [W][NS]
+    int2 *s_piece = reinterpret_cast<int2 *>(s_mask + W * NS);                // [W][2]: {segment or -1, ended}
+    int *s_prefix = reinterpret_cast<int *>(s_piece + W * 2);                 // [n + 1]
+    int *s_len = s_prefix + a.n_seq + 1;                                      // [n]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+    const int n = a.n_seq, D = a.c.dim;
+    const int tiles = a.c.n_heads * w.row_tiles;                              // segments per sequence
+
+    griddep_launch_dependents();
+    griddep_wait();
+
+    // ---- steps of every sequence, and their sums ----
+    {
+        const int per = (n + C::threads - 1) / C::threads;
+        int *s_sum = reinterpret_cast<int *>(smem);                           // the rings are not in use yet
+        int sum = 0;
+        for (int i = tid * per; i < (tid + 1) * per && i < n; ++i) {
+            const int len = seq_len(a.lens, i, a.max_len, blockIdx.x == 0 ? a.err : nullptr);
+            s_len[i] = len;
+            sum += (len + 15) >> 4;
+        }
+        int inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(~0u, inc, o);
+            if (lane >= o) inc += v;
+        }
+        if (lane == 31) s_sum[warp] = inc;
+        __syncthreads();
+        int base = 0;
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            if (i < warp) base += s_sum[i];
+        int at = base + inc - sum;
+        for (int i = tid * per; i < (tid + 1) * per && i < n; ++i) {
+            s_prefix[i] = at;
+            at += (s_len[i] + 15) >> 4;
+        }
+        if (tid == C::threads - 1) s_prefix[n] = at;
+        __syncthreads();
+    }
+    const int total = s_prefix[n] * tiles;
+    // one range per block, at least one step per warp
+    int chunk = (total + gridDim.x - 1) / gridDim.x;
+    if (chunk < W) chunk = W;
+    const int c0 = blockIdx.x * chunk < total ? blockIdx.x * chunk : total;
+    const int c1 = c0 + chunk < total ? c0 + chunk : total;
+
+    // sequences without a slot have no steps: their rows are empty
+    for (int b = blockIdx.x; b < n; b += gridDim.x) {
+        if (s_len[b] != 0) continue;
+        const int quads = D / 4, count = a.S * a.n_q_heads;
+        for (int i = tid; i < count * quads; i += C::threads)
+            store_out4(a, ((size_t)b * count) * D + 4 * (size_t)i, make_float4(0.f, 0.f, 0.f, 0.f), 1.f);
+        if (a.lse)
+            for (int i = tid; i < count; i += C::threads) a.lse[(size_t)b * count + i] = -INFINITY;
+    }
+    if (tid == 0) w.tail[blockIdx.x] = make_int2(-1, 0);
+    if (c0 >= c1) return;
+
+    const int w0 = c0 + (int)((long long)(c1 - c0) * warp / W);
+    const int w1 = c0 + (int)((long long)(c1 - c0) * (warp + 1) / W);
+    char *ring = smem + warp * C::ring;
+    const uint32_t ring_a = smem_addr(ring);
+    if (lane < 2) s_piece[2 * warp + lane] = make_int2(-1, 0);
+
+    // ---- place of a global step: sequence, segment of it, step of that ----
+    struct Place { int b, seg, i, n; };
+    auto locate = [&](int step) {
+        Place p;
+        const int x = step / tiles;
+        int lo = 0, hi = n - 1;                      // the last b with prefix[b] <= x
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (s_prefix[mid] <= x) lo = mid;
+            else hi = mid - 1;
+        }
+        p.b = lo;
+        p.n = s_prefix[lo + 1] - s_prefix[lo];
+        const int rem = step - s_prefix[lo] * tiles;
+        p.seg = rem / p.n;
+        p.i = rem - p.seg * p.n;
+        return p;
+    };
+    auto advance = [&](Place &p) {
+        if (++p.i < p.n) return;
+        p.i = 0;
+        if (++p.seg < tiles) return;
+        p.seg = 0;
+        do ++p.b;
+        while (p.b < n && s_prefix[p.b + 1] == s_prefix[p.b]);
+        p.n = p.b < n ? s_prefix[p.b + 1] - s_prefix[p.b] : 1;
+    };
+
+    // ---- loads ----
+    Place ip = locate(w0 < w1 ? w0 : c0);
+    int issued = w0, istage = 0;
+    // lanes 0-15 look up the 16 slots of the next step to load, one step early
+    int look_page = 0, look_off = 0;
+    auto look = [&]() {
+        if (lane < 16 && issued < w1) {
+            const int t = 16 * ip.i + lane;
+            if (t < s_len[ip.b]) {
+                int index;
+                split_slot(a.c, t, &index, &look_off);
+                look_page = __ldg(a.table + (size_t)ip.b * a.table_stride + index);
+            }
+        }
+    };
+    auto issue = [&]() {
+        if (issued < w1) {
+            const int t = 16 * ip.i + lane;
+            const bool in = lane < 16 && t < s_len[ip.b];
+            const bool ok = in && (unsigned)look_page < (unsigned)a.c.n_pages;
+            const uint32_t good = __ballot_sync(~0u, ok), bad = __ballot_sync(~0u, in && !ok);
+            if (lane == 0) {
+                s_mask[warp * NS + istage] = good | bad << 16;
+                if (bad) raise_device_error(a.err, kErrPage);
+            }
+            const int kh = ip.seg / w.row_tiles;
+            const long long off = ok ? look_page * a.c.page_b + kh * a.c.head_b + look_off * a.c.token_b : 0;
+            const uint32_t dst = ring_a + istage * C::stage + lane * 16;
+            const int row_b = D * C::ESZ;
+            // K: slots g and g + 8, chunks c, c + 4, ...
+            const char *k0 = a.c.k + __shfl_sync(~0u, off, g) + 16 * c;
+            const char *k1 = a.c.k + __shfl_sync(~0u, off, g + 8) + 16 * c;
+            const bool ok0 = good >> g & 1u, ok1 = good >> (g + 8) & 1u;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const bool in_row = 64 * i + 16 * c < row_b;
+                cp_async16(dst + (2 * i) * 512, in_row ? k0 + 64 * i : k0 - 16 * c, ok0 && in_row);
+                cp_async16(dst + (2 * i + 1) * 512, in_row ? k1 + 64 * i : k1 - 16 * c, ok1 && in_row);
+            }
+            // V: slots 2c, 2c + 1, 2c + 8, 2c + 9, chunks g, g + 8, ...
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int slot = 2 * c + (j & 1) + 8 * (j >> 1);
+                const char *v = a.c.v + __shfl_sync(~0u, off, slot);
+                const bool okv = good >> slot & 1u;
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    const int at = (8 * q + g) * C::VB;
+                    const bool in_row = at < row_b;
+                    if (C::VB == 16)
+                        cp_async16(dst + C::k_bytes + (4 * q + j) * 512, in_row ? v + at : v, okv && in_row);
+                    else
+                        cp_async8(dst + C::k_bytes + (4 * q + j) * 256 - lane * 8, in_row ? v + at : v,
+                                  okv && in_row);
+                }
+            }
+            ++issued;
+            advance(ip);
+            look();
+        }
+        cp_async_commit();
+        if (++istage == NS) istage = 0;
+    };
+    look();
+#pragma unroll 1
+    for (int i = 0; i < NS; ++i) issue();
+
+    // ---- the warp's range ----
+    Place p = locate(w0 < w1 ? w0 : c0);
+    float o[C::MT][NT][4];
+    float m[NT][2], l[NT][2];
+    uint32_t qf[NT][NI][C::ESZ == 1 ? 8 : 4];
+    float rs[NT][2];                                  // score factor of the thread's rows (e4m3: per row)
+    int lim[NT][2];                                   // slots they see
+    const float factor = a.scale * 1.44269504088896340736f;
+    const bool third = TYPE == kBf16 && a.o_type == kF32;
+    bool fresh = true;                                // at the start of a piece
+    int stage = 0;
+    bool began_here = false;
+
+#pragma unroll 1
+    for (int step = w0; step < w1; ++step) {
+        const int kh = p.seg / w.row_tiles, tile = p.seg - kh * w.row_tiles;
+        const int len = s_len[p.b];
+        if (fresh) {
+            fresh = false;
+            began_here = p.i == 0;
+            // Q as the B operand: row g of each 8, the thread's chunks
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const RowRef r = row_ref(a, p.b, kh, tile * rows + 8 * nt + g);
+                const size_t head = r.head % a.n_q_heads, bs = r.head / a.n_q_heads;
+                const uint16_t *q = static_cast<const uint16_t *>(a.q) + bs * a.q_stride + head * D;
+                if constexpr (TYPE != kE4m3) {
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) {
+                        const int d = (4 * i + c) * 8;
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (r.real && d < D) v = *reinterpret_cast<const uint4 *>(q + d);
+                        qf[nt][i][0] = v.x, qf[nt][i][1] = v.y, qf[nt][i][2] = v.z, qf[nt][i][3] = v.w;
+                    }
+                } else {
+                    float top = 0.f;
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) {
+                        const int d = (4 * i + c) * 16;
+                        uint4 v[2] = {};
+                        if (r.real && d < D)
+                            v[0] = *reinterpret_cast<const uint4 *>(q + d),
+                            v[1] = *reinterpret_cast<const uint4 *>(q + d + 8);
+                        const uint32_t x[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            qf[nt][i][u] = x[u];
+                            const float2 f = a.q_type == kF16 ? unpack_f16(x[u]) : unpack_bf16(x[u]);
+                            if (fabsf(f.x) < INFINITY) top = fmaxf(top, fabsf(f.x));
+                            if (fabsf(f.y) < INFINITY) top = fmaxf(top, fabsf(f.y));
+                        }
+                    }
+                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+                    // largest |q| of the row into [2^14, 2^15)
+                    int ex = 141 - (int)(__float_as_uint(top) >> 23);
+                    ex = top == 0.f ? 0 : ex > 100 ? 100 : ex < -100 ? -100 : ex;
+                    const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
+#pragma unroll
+                    for (int i = 0; i < NI; ++i)
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            const float2 f = a.q_type == kF16 ? unpack_f16(qf[nt][i][u]) : unpack_bf16(qf[nt][i][u]);
+                            qf[nt][i][u] = pack_f16(f.x * up, f.y * up);
+                        }
+                    const float down = factor * __ldg(a.c.k_scale + kh) * __uint_as_float((uint32_t)(127 - ex) << 23);
+                    rs[nt][0] = __shfl_sync(~0u, down, 8 * c);
+                    rs[nt][1] = __shfl_sync(~0u, down, 8 * c + 4);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int s = (tile * rows + 8 * nt + 2 * c + e) / a.group;
+                    lim[nt][e] = len - a.S + 1 + (s < a.S ? s : a.S - 1);
+                    m[nt][e] = -INFINITY;
+                    l[nt][e] = 0.f;
+                }
+#pragma unroll
+                for (int t = 0; t < C::MT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[t][nt][e] = 0.f;
+            }
+        }
+
+        cp_async_wait<NS - 1>();
+        __syncwarp();
+        const uint32_t mask = s_mask[warp * NS + stage];
+        const uint32_t src = ring_a + stage * C::stage + lane * 16;
+
+        // ---- S^T = K Q^T ----
+        float s[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const uint4 x = lds128(src + (2 * i) * 512), y = lds128(src + (2 * i + 1) * 512);
+            const uint32_t kx[4] = {x.x, x.y, x.z, x.w}, ky[4] = {y.x, y.y, y.z, y.w};
+            if constexpr (TYPE != kE4m3) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma16816<TYPE>(s[nt], kx[2 * u], ky[2 * u], kx[2 * u + 1], ky[2 * u + 1], qf[nt][i][2 * u],
+                                       qf[nt][i][2 * u + 1]);
+            } else {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint32_t a0 = e4m3x2_to_f16x2(kx[u]), a2 = e4m3x2_to_f16x2(kx[u] >> 16);
+                    const uint32_t a1 = e4m3x2_to_f16x2(ky[u]), a3 = e4m3x2_to_f16x2(ky[u] >> 16);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma16816<TYPE>(s[nt], a0, a1, a2, a3, qf[nt][i][2 * u], qf[nt][i][2 * u + 1]);
+                }
+            }
+        }
+        // scores in log2 units; thread: slots g, g + 8 by rows 2c, 2c + 1
+        const int t0 = 16 * p.i;
+        const bool partial = mask != 0xFFFFu || (a.S > 1 && t0 + 16 > len - a.S + 1);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[nt][e] *= TYPE == kE4m3 ? rs[nt][e & 1] : factor;
+        if (partial) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = g + 8 * (e >> 1);
+                    if (t0 + j >= lim[nt][e & 1]) s[nt][e] = -INFINITY;      // slots past the end are past every limit
+                    else if (mask >> (16 + j) & 1u) s[nt][e] = NAN;          // its page is not in the pool
+                }
+        }
+        if (a.accumulate) {
+            float *dst = w.scores + ((size_t)(p.b * tiles + p.seg) * w.score_slots + t0) * rows + 2 * c;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                *reinterpret_cast<float2 *>(dst + (size_t)g * rows + 8 * nt) = make_float2(s[nt][0], s[nt][1]);
+                *reinterpret_cast<float2 *>(dst + (size_t)(g + 8) * rows + 8 * nt) = make_float2(s[nt][2], s[nt][3]);
+            }
+        }
+
+        // ---- running maxima; O and l follow when one grows ----
+        uint32_t ph[NT][2], pl[NT][2], pt[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float x0 = fmaxf(s[nt][0], s[nt][2]), x1 = fmaxf(s[nt][1], s[nt][3]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+                x0 = fmaxf(x0, __shfl_xor_sync(~0u, x0, d));
+                x1 = fmaxf(x1, __shfl_xor_sync(~0u, x1, d));
+            }
+            if (__any_sync(~0u, x0 > m[nt][0] || x1 > m[nt][1])) {
+                const float n0 = fmaxf(m[nt][0], x0), n1 = fmaxf(m[nt][1], x1);
+                const float f0 = n0 == -INFINITY ? 1.f : exp2f(m[nt][0] - n0);
+                const float f1 = n1 == -INFINITY ? 1.f : exp2f(m[nt][1] - n1);
+                m[nt][0] = n0, m[nt][1] = n1;
+                l[nt][0] *= f0, l[nt][1] *= f1;
+#pragma unroll
+                for (int t = 0; t < C::MT; ++t) {
+                    o[t][nt][0] *= f0, o[t][nt][2] *= f0;
+                    o[t][nt][1] *= f1, o[t][nt][3] *= f1;
+                }
+            }
+            constexpr float shift = TYPE == kBf16 ? 0.f : 14.f;
+            const float r0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] - shift;
+            const float r1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] - shift;
+            const float p0 = exp2f(s[nt][0] - r0), p1 = exp2f(s[nt][1] - r1);
+            const float p2 = exp2f(s[nt][2] - r0), p3 = exp2f(s[nt][3] - r1);
+            l[nt][0] += p0 + p2;
+            l[nt][1] += p1 + p3;
+            // P as a sum of 16-bit parts, transposed into B fragments
+            auto split = [&](float x, float y, int half) {
+                uint32_t h, r, q = 0;
+                if constexpr (TYPE == kBf16) {
+                    h = pack_bf16(x, y);
+                    float2 f = unpack_bf16(h);
+                    x -= f.x, y -= f.y;
+                    r = pack_bf16(x, y);
+                    if (third) {
+                        f = unpack_bf16(r);
+                        q = pack_bf16(x - f.x, y - f.y);
+                    }
+                } else {
+                    h = pack_f16(x, y);
+                    const float2 f = unpack_f16(h);
+                    r = pack_f16(x - f.x, y - f.y);
+                }
+                ph[nt][half] = transpose8x8(h);
+                pl[nt][half] = transpose8x8(r);
+                if (TYPE == kBf16 && third) pt[nt][half] = transpose8x8(q);
+            };
+            split(p0, p1, 0);
+            split(p2, p3, 1);
+        }
+
+        // ---- O^T += V^T P^T ----
+        // V^T's A fragments: tile t of chunk q covers elements t (rows g) and t + E/2 (rows g + 8) of the chunk
+        auto v_chunk = [&](int q, uint32_t (&x)[4][4]) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (C::VB == 16) {
+                    const uint4 v = lds128(src + C::k_bytes + (4 * q + j) * 512);
+                    x[j][0] = v.x, x[j][1] = v.y, x[j][2] = v.z, x[j][3] = v.w;
+                } else {
+                    const uint2 v = lds64(src - lane * 8 + C::k_bytes + (4 * q + j) * 256);
+                    x[j][0] = v.x, x[j][1] = v.y, x[j][2] = x[j][3] = 0u;
+                }
+            }
+        };
+        auto v_pair = [&](uint32_t lo, uint32_t hi, int e) -> uint32_t {   // element e of two slots' words
+            if constexpr (TYPE != kE4m3) return __byte_perm(lo, hi, e & 1 ? 0x7632 : 0x5410);
+            const uint32_t two = __byte_perm(lo, hi, e & 2 ? 0x7362 : 0x5140);
+            return e4m3x2_to_f16x2(e & 1 ? two >> 16 : two);
+        };
+        constexpr int per_word = 4 / C::ESZ;
+        bool careful = false;
+        if (a.S > 1 && partial) {
+            // a slot hidden from some rows: 0 * NaN and 0 * inf must not reach them
+            bool odd = false;
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                uint32_t x[4][4];
+                v_chunk(q, x);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t v = x[j][e];
+                        if constexpr (TYPE == kE4m3) {
+                            const uint32_t y = ~v & 0x7F7F7F7Fu;          // a zero byte: NaN
+                            odd |= ((y - 0x01010101u) & ~y & 0x80808080u) != 0u;
+                        } else {
+                            constexpr uint32_t ex = TYPE == kBf16 ? 0x7F80u : 0x7C00u;
+                            odd |= (v & ex) == ex || (v >> 16 & ex) == ex;
+                        }
+                    }
+            }
+            careful = __any_sync(~0u, odd);
+        }
+        if (!careful) {
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                uint32_t x[4][4];
+                v_chunk(q, x);
+#pragma unroll
+                for (int t = 0; t < E / 2; ++t) {
+                    const int e0 = t, e1 = t + E / 2;
+                    const uint32_t a0 = v_pair(x[0][e0 / per_word], x[1][e0 / per_word], e0);
+                    const uint32_t a1 = v_pair(x[0][e1 / per_word], x[1][e1 / per_word], e1);
+                    const uint32_t a2 = v_pair(x[2][e0 / per_word], x[3][e0 / per_word], e0);
+                    const uint32_t a3 = v_pair(x[2][e1 / per_word], x[3][e1 / per_word], e1);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float(&acc)[4] = o[q * (E / 2) + t][nt];
+                        if (TYPE == kBf16 && third) mma16816<TYPE>(acc, a0, a1, a2, a3, pt[nt][0], pt[nt][1]);
+                        mma16816<TYPE>(acc, a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+                        mma16816<TYPE>(acc, a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+                    }
+                }
+            }
+        } else {
+            // one slot at a time, added only to the rows that see it
+#pragma unroll 1
+            for (int j = 0; j < 16; ++j) {
+                const uint32_t m0 = (j == 2 * c ? 0xFFFFu : 0u) | (j == 2 * c + 1 ? 0xFFFF0000u : 0u);
+                const uint32_t m1 = (j == 2 * c + 8 ? 0xFFFFu : 0u) | (j == 2 * c + 9 ? 0xFFFF0000u : 0u);
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    uint32_t x[4][4];
+                    v_chunk(q, x);
+#pragma unroll
+                    for (int t = 0; t < E / 2; ++t) {
+                        const int e0 = t, e1 = t + E / 2;
+                        const uint32_t a0 = v_pair(x[0][e0 / per_word], x[1][e0 / per_word], e0) & m0;
+                        const uint32_t a1 = v_pair(x[0][e1 / per_word], x[1][e1 / per_word], e1) & m0;
+                        const uint32_t a2 = v_pair(x[2][e0 / per_word], x[3][e0 / per_word], e0) & m1;
+                        const uint32_t a3 = v_pair(x[2][e1 / per_word], x[3][e1 / per_word], e1) & m1;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                            if (TYPE == kBf16 && third) mma16816<TYPE>(acc, a0, a1, a2, a3, pt[nt][0], pt[nt][1]);
+                            mma16816<TYPE>(acc, a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+                            mma16816<TYPE>(acc, a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (t0 + j < lim[nt][e & 1]) o[q * (E / 2) + t][nt][e] += acc[e];
+                        }
+                    }
+                }
+            }
+        }
+        __syncwarp();                                 // every lane has read the mask and its chunks
+        issue();
+        if (++stage == NS) stage = 0;
+
+        // ---- end of a piece ----
+        const bool ended = p.i + 1 == p.n;
+        if (ended || step + 1 == w1) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(~0u, l[nt][e], d);
+            const float vs = TYPE == kE4m3 ? __ldg(a.c.v_scale + kh) : 1.f;
+            const bool whole = ended && began_here;
+            // an open piece waits in the ring when the range is done with it, else in the workspace
+            float *keep = step + 1 == w1 ? reinterpret_cast<float *>(ring)
+                                         : w.head_o + ((size_t)blockIdx.x * W + warp) * rows * DP;
+            const int slot = began_here ? 1 : 0;
+            if (step + 1 == w1) {
+                cp_async_wait<0>();
+                __syncwarp();
+            }
+            if (!whole) {
+                if (lane == 0) s_piece[2 * warp + slot] = make_int2(p.b * tiles + p.seg, ended ? 1 : 0);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 8 * nt + 2 * c + e;
+                    const RowRef ref = row_ref(a, p.b, kh, tile * rows + r);
+                    if (!ref.real) continue;
+                    const float f = row_factor<TYPE>(l[nt][e], vs);
+                    if (g == 0) {
+                        if (whole) {
+                            if (a.lse) a.lse[ref.head] = row_lse<TYPE>(m[nt][e], l[nt][e]);
+                        } else {
+                            s_ml[(2 * warp + slot) * rows + r] = make_float2(m[nt][e], l[nt][e]);
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                        for (int x = 0; x < E; x += 4) {
+                            const int d = (8 * q + g) * E + x;
+                            auto at = [&](int y) {
+                                return y < E / 2 ? o[q * (E / 2) + y][nt][e] : o[q * (E / 2) + y - E / 2][nt][2 + e];
+                            };
+                            const float4 v = make_float4(at(x), at(x + 1), at(x + 2), at(x + 3));
+                            if (!whole) *reinterpret_cast<float4 *>(keep + r * DP + d) = v;
+                            else if (d < D) store_out4(a, ref.head * D + d, v, f);
+                        }
+                }
+            fresh = true;
+        }
+        advance(p);
+    }
+
+    // ---- join the block's open pieces, in order ----
+    __syncthreads();
+    int first = 0;
+    while (first < 2 * W) {
+        const int seg = s_piece[first].x;
+        if (seg < 0) {
+            ++first;
+            continue;
+        }
+        int last = first;                             // the last piece of this segment
+        for (int i = first + 1; i < 2 * W; ++i) {
+            if (s_piece[i].x == seg) last = i;
+            else if (s_piece[i].x >= 0) break;
+        }
+        const bool starts = first & 1, ends = s_piece[last].y != 0, whole = starts && ends;
+        const int b = seg / tiles, sg = seg - b * tiles, kh = sg / w.row_tiles, tile = sg - kh * w.row_tiles;
+        const float vs = TYPE == kE4m3 ? __ldg(a.c.v_scale + kh) : 1.f;
+        const size_t out = ((size_t)blockIdx.x * 2 + (starts ? 1 : 0)) * rows;
+        for (int i = tid; i < rows * (DP / 4); i += C::threads) {
+            const int r = i / (DP / 4), d = 4 * (i - r * (DP / 4));
+            const RowRef ref = row_ref(a, b, kh, tile * rows + r);
+            if (!ref.real) continue;
+            float mm = -INFINITY;
+            for (int x = first; x <= last; ++x)
+                if (s_piece[x].x == seg) mm = fmaxf(mm, s_ml[x * rows + r].x);
+            const float base = mm == -INFINITY ? 0.f : mm;
+            float ll = 0.f;
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int x = first; x <= last; ++x) {
+                if (s_piece[x].x != seg) continue;
+                const float2 ml = s_ml[x * rows + r];
+                const float f = exp2f(ml.x - base);
+                ll += ml.y * f;
+                // a piece that ended its segment before its warp's range did lies in the workspace
+                const int wx = x >> 1;
+                const int we = c0 + (int)((long long)(c1 - c0) * (wx + 1) / W);
+                const bool mid = s_piece[x].y != 0 && (s_prefix[b] * tiles + (sg + 1) * (s_prefix[b + 1] - s_prefix[b])) < we;
+                const float *src = mid ? w.head_o + ((size_t)blockIdx.x * W + wx) * rows * DP
+                                       : reinterpret_cast<const float *>(smem + wx * C::ring);
+                const float4 v = *reinterpret_cast<const float4 *>(src + r * DP + d);
+                sum.x += v.x * f, sum.y += v.y * f, sum.z += v.z * f, sum.w += v.w * f;
+            }
+            if (whole) {
+                if (d < D) store_out4(a, ref.head * D + d, sum, row_factor<TYPE>(ll, vs));
+                if (d == 0 && a.lse) a.lse[ref.head] = row_lse<TYPE>(mm, ll);
+            } else {
+                *reinterpret_cast<float4 *>(w.part_o + (out + r) * DP + d) = sum;
+                if (d == 0) w.part_ml[out + r] = make_float2(mm, ll);
+            }
+        }
+        if (!whole && starts && tid == 0) {
+            const int end = s_prefix[b] * tiles + (sg + 1) * (s_prefix[b + 1] - s_prefix[b]);
+            w.tail[blockIdx.x] = make_int2(seg, (end - 1) / chunk - (int)blockIdx.x + 1);
+        }
+        first = last + 1;
+    }
+}
+
+}  // namespace qg

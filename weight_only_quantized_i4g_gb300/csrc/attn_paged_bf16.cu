@@ -1,0 +1,7 @@
+// attn_paged_bf16.cu -- the attention kernels over a bf16 cache.
+#include "attn_launch.cuh"
+
+namespace qg {
+template int launch_attn_stream<kBf16>(const AttnArgs &, const AttnWork &, const AttnPlan &, cudaStream_t);
+template AttnPlan attn_plan<kBf16>(int rows, int dim);
+}

@@ -1,0 +1,7 @@
+// attn_paged_e4m3.cu -- the attention kernels over a e4m3 cache.
+#include "attn_launch.cuh"
+
+namespace qg {
+template int launch_attn_stream<kE4m3>(const AttnArgs &, const AttnWork &, const AttnPlan &, cudaStream_t);
+template AttnPlan attn_plan<kE4m3>(int rows, int dim);
+}

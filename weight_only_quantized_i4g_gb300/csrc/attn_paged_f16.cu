@@ -1,0 +1,7 @@
+// attn_paged_f16.cu -- the attention kernels over a f16 cache.
+#include "attn_launch.cuh"
+
+namespace qg {
+template int launch_attn_stream<kF16>(const AttnArgs &, const AttnWork &, const AttnPlan &, cudaStream_t);
+template AttnPlan attn_plan<kF16>(int rows, int dim);
+}
