@@ -39,19 +39,19 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     // one warp a row: largest maximum, then factors and the sum
     const int r = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool real = tile * rows + r0 + r < a.S * a.group;
-    float m = -INFINITY, l = 0.f;
+    float m = kNoRef, l = 0.f;
     for (int i = lane; i < pieces; i += 32) m = fmaxf(m, s_ml[8 * i + r].x);
     for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
     for (int i = lane; i < pieces; i += 32) {
         const float2 x = s_ml[8 * i + r];
-        const float f = exp2f(x.x - (m == -INFINITY ? 0.f : m));
+        const float f = ex2(x.x - m);
         s_ml[8 * i + r].x = f;
         l += x.y * f;
     }
     for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
     if (lane == 0) {
         s_l[r] = l;
-        if (real && a.lse) a.lse[row_ref(a, b, kh, tile * rows + r0 + r).head] = row_lse<TYPE>(m, l);
+        if (real && a.lse) a.lse[row_ref(a, b, kh, tile * rows + r0 + r).head] = row_lse(m, l);
     }
     __syncthreads();
     const float vs = TYPE == kE4m3 ? __ldg(a.c.v_scale + kh) : 1.f;
@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
             const float4 v = *reinterpret_cast<const float4 *>(w.part_o + (base(x) + row) * dp + d);
             sum.x += v.x * f, sum.y += v.y * f, sum.z += v.z * f, sum.w += v.w * f;
         }
-        store_out4(a, ref.head * a.c.dim + d, sum, row_factor<TYPE>(s_l[row], vs));
+        store_out4(a, ref.head * a.c.dim + d, sum, row_factor(s_l[row], vs));
     }
 }
 
@@ -97,8 +97,8 @@ __global__ void __launch_bounds__(kWeightThreads) attn_weight_kernel(const __gri
         const float *z = w.scores + (seg * w.score_slots + t) * rows;
         for (int r = 0; r < rows && tile * rows + r < R; r += 2) {
             const float2 x = *reinterpret_cast<const float2 *>(z + r);
-            if (s_lse[r] != -INFINITY) sum += exp2f(x.x - s_lse[r]);
-            if (s_lse[r + 1] != -INFINITY) sum += exp2f(x.y - s_lse[r + 1]);
+            if (s_lse[r] != -INFINITY) sum += ex2(x.x - s_lse[r]);
+            if (s_lse[r + 1] != -INFINITY) sum += ex2(x.y - s_lse[r + 1]);
         }
     }
     if (ref.page >= 0) a.c.weight[slot_weight(a.c, ref, kh)] += sum;

@@ -16,12 +16,14 @@
 // one that does not are joined in shared memory after the block's ranges are
 // done, and across blocks by a second kernel, always in slot order.
 //
-// Loads.  Every thread copies the 16-byte chunks that it will use itself into
-// a ring of its own in shared memory (cp.async), NS steps ahead: no barrier,
-// no exchange between threads, conflict-free 16-byte reads, and any strides
-// and page sizes.  The chunks are the fragments of the warp-level MMA as they
-// lie in memory: the contraction over d may run in any order, so a thread's
-// k indices are the 8 (or 16) consecutive elements of its chunk.
+// Loads.  Each warp copies its steps into a ring of its own in shared memory
+// (cp.async, NS steps ahead; no block barrier), 512 consecutive bytes of a
+// page per instruction.  Copying straight in fragment order (64 and 128 byte
+// pieces of many rows per instruction) read 5.2 TB/s where this order reads
+// 6.8.  The 16-byte chunks of a row are swizzled so that both the copies and
+// the fragment reads (16 bytes a thread) are free of bank conflicts.  A
+// fragment's k indices are the 8 (or 16) consecutive elements of a chunk: the
+// contraction over d may run in any order.
 //
 // Products.  S^T = K Q^T with the 16 slots as M and 8 rows as N (a decode step
 // has few rows), then O^T = V^T P^T; P^T's fragment is the transpose of
@@ -31,10 +33,15 @@
 // Precision: products of 16-bit operands are exact and summed in f32.  P is
 // not rounded to one 16-bit value but split into a sum of two (three for f32
 // output of a bf16 cache), so it keeps 16 to 24 bits; f16 parts are scaled by
-// 2^14 (as are the sums they are divided by) to stay out of its subnormals.
+// 2^6 (as are the sums they are divided by) against its subnormals.
+// Softmax.  Each row's exponents are taken against a reference that follows
+// the running maximum only when a score passes it by more than 2^8: a step
+// then needs one vote instead of a maximum over lanes, and p stays <= 2^14.
 // e4m3 codes are exact in f16; q over them is scaled per row by a power of two
 // into f16's range, which is exact for bf16 values within 2^29 of the largest.
 #pragma once
+
+#include <type_traits>
 
 #include "kv_cache.cuh"
 
@@ -64,8 +71,12 @@ struct AttnCfg {
     static constexpr int VB = E * ESZ;                // its bytes: 16, or 8
     static constexpr int NQ = DP / (8 * E);           // V chunks a thread holds per slot
     static constexpr int MT = DP / 16;                // 16-row tiles of O^T
-    static constexpr int k_bytes = 2 * NI * 512;
-    static constexpr int stage = k_bytes + NQ * 4 * 32 * VB;   // 16 slots of K and V: 32 * DP * ESZ
+    static constexpr int RB = DP * ESZ;               // bytes of a row
+    static constexpr int NC = RB / 16;                // 16-byte chunks of a row: 4, 8, 16 or 32
+    static constexpr int NL = NC / 2;                 // copies of 512 bytes for 16 rows
+    static constexpr int RPL = 32 / NC;               // rows one covers
+    static constexpr int k_bytes = 16 * RB;
+    static constexpr int stage = 2 * k_bytes;         // 16 slots of K and V
     // 192 KB in flight per SM at most; eight warps, four where a stage is 16 KB
     static constexpr int W = stage > 8192 ? 4 : 8;
     static constexpr int NS0 = 196608 / (W * stage);
@@ -77,17 +88,43 @@ struct AttnCfg {
 
 // dynamic shared memory: rings, row statistics of open pieces, step masks,
 // piece descriptors, then prefix [n + 1] and lengths [n]
+// Where chunk u = row * NC + chunk of a step sits: the low three bits (its bank
+// group) are exchanged by row.  A fragment read takes, per eight lanes, chunks
+// x .. x + 3 of two neighbouring rows of K, two neighbouring chunks of four
+// even (or odd) rows of V.
+template <class C>
+__device__ __forceinline__ constexpr int k_place(int row, int chunk) {
+    return (row * C::NC + chunk) ^ (C::NC >= 8 ? (row & 1) << 2 : 0);
+}
+template <class C>
+__device__ __forceinline__ constexpr int v_place(int row, int chunk) {
+    return (row * C::NC + chunk) ^ (row >> 1 & 3) << 1;
+}
+
 template <class C>
 __host__ __device__ constexpr size_t attn_fixed_smem() {
     return (size_t)C::W * C::ring + C::W * 2 * C::rows * sizeof(float2) + C::W * C::NS * 4 + C::W * 2 * 8;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool ok) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
-                 : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, bool ok) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
+template <int S>
+__device__ __forceinline__ void cp_async16_at(uint32_t dst, const char *src) {   // [dst] <- [src + S]
+    asm volatile("cp.async.cg.shared.global [%0], [%1 + %2], 16;" ::"r"(dst), "l"(src), "n"(S) : "memory");
+}
+// fn(integral_constant<int, 0>) .. fn(integral_constant<int, N - 1>): unrolled, with the index a constant
+template <int N, int I = 0, class Fn>
+__device__ __forceinline__ void unrolled(Fn fn) {
+    if constexpr (I < N) {
+        fn(std::integral_constant<int, I>());
+        unrolled<N, I + 1>(fn);
+    }
+}
+__device__ __forceinline__ float ex2(float x) {       // 2^x, 2 ulp; 2^-inf = 0
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -109,19 +146,19 @@ template <int TYPE>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
     if (TYPE == kBf16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                      "{%0,%1,%2,%3};"
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                      "{%0,%1,%2,%3};"
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
 
@@ -135,15 +172,12 @@ __device__ __forceinline__ void store_out4(const AttnArgs &a, size_t at, float4 
             make_uint2(pack_16(a.o_type, v.x, v.y), pack_16(a.o_type, v.z, v.w));
 }
 
-// What a row's statistics (maximum m in log2 units, sum l) say: the factor of
-// its O and its lse.  The f16 paths carry l and O times 2^14.
-template <int TYPE>
-__device__ __forceinline__ float row_factor(float l, float v_scale) {
-    return l == 0.f ? 0.f : v_scale / l;
-}
-template <int TYPE>
+// A row's statistics: reference m (log2 units) and sum l of 2^(z - m).  A row
+// that has seen nothing has l = 0 and m = kNoRef, whose differences are finite.
+constexpr float kNoRef = -3e38f;
+__device__ __forceinline__ float row_factor(float l, float v_scale) { return l == 0.f ? 0.f : v_scale / l; }
 __device__ __forceinline__ float row_lse(float m, float l) {
-    return l == 0.f ? -INFINITY : (m + (log2f(l) - (TYPE == kBf16 ? 0.f : 14.f))) * 0.69314718055994530942f;
+    return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }
 
 // The place of row r (of a segment's tile) in q, o and lse.
@@ -258,63 +292,74 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
     };
 
     // ---- loads ----
+    // `simple`: the 16 slots of a step lie in one page and rows fill the padded size
+    const bool simple = D == DP && a.c.page % 16 == 0;
     Place ip = locate(w0 < w1 ? w0 : c0);
+    int ip_kh = ip.seg / w.row_tiles;
     int issued = w0, istage = 0;
-    // lanes 0-15 look up the 16 slots of the next step to load, one step early
+    // the page of the next step to load is looked up one step early: of its
+    // first slot where the step is simple, else of slot `lane` by lanes 0-15
     int look_page = 0, look_off = 0;
     auto look = [&]() {
-        if (lane < 16 && issued < w1) {
-            const int t = 16 * ip.i + lane;
-            if (t < s_len[ip.b]) {
-                int index;
-                split_slot(a.c, t, &index, &look_off);
-                look_page = __ldg(a.table + (size_t)ip.b * a.table_stride + index);
-            }
+        if (issued >= w1) return;
+        const int t = 16 * ip.i + (simple ? 0 : lane);
+        if (simple || (lane < 16 && t < s_len[ip.b])) {
+            int index;
+            split_slot(a.c, t, &index, &look_off);
+            look_page = __ldg(a.table + (size_t)ip.b * a.table_stride + index);
         }
     };
+    // copy n of a step moves chunk lane % NC of row n * RPL + lane / NC
+    const int l_row = lane / C::NC, l_chunk = lane % C::NC;
+    const long long l_off = l_row * a.c.token_b + 16 * l_chunk, copy_b = C::RPL * a.c.token_b;
+    const bool in_row = 16 * l_chunk < D * C::ESZ;
     auto issue = [&]() {
         if (issued < w1) {
-            const int t = 16 * ip.i + lane;
-            const bool in = lane < 16 && t < s_len[ip.b];
-            const bool ok = in && (unsigned)look_page < (unsigned)a.c.n_pages;
-            const uint32_t good = __ballot_sync(~0u, ok), bad = __ballot_sync(~0u, in && !ok);
-            if (lane == 0) {
-                s_mask[warp * NS + istage] = good | bad << 16;
-                if (bad) raise_device_error(a.err, kErrPage);
-            }
-            const int kh = ip.seg / w.row_tiles;
-            const long long off = ok ? look_page * a.c.page_b + kh * a.c.head_b + look_off * a.c.token_b : 0;
-            const uint32_t dst = ring_a + istage * C::stage + lane * 16;
-            const int row_b = D * C::ESZ;
-            // K: slots g and g + 8, chunks c, c + 4, ...
-            const char *k0 = a.c.k + __shfl_sync(~0u, off, g) + 16 * c;
-            const char *k1 = a.c.k + __shfl_sync(~0u, off, g + 8) + 16 * c;
-            const bool ok0 = good >> g & 1u, ok1 = good >> (g + 8) & 1u;
+            const uint32_t dst = ring_a + istage * C::stage;
+            const int t0 = 16 * ip.i, len = s_len[ip.b];
+            if (simple && t0 + 16 <= len && (unsigned)look_page < (unsigned)a.c.n_pages) {
+                if (lane == 0) s_mask[warp * NS + istage] = 0xFFFFu;
+                const long long base =
+                    look_page * a.c.page_b + ip_kh * a.c.head_b + look_off * a.c.token_b + l_off;
+                const char *k = a.c.k + base, *v = a.c.v + base;
+                if (copy_b == 512) {
+                    unrolled<C::NL>([&](auto n) {
+                        cp_async16_at<512 * n>(dst + 16 * k_place<C>(n * C::RPL + l_row, l_chunk), k);
+                    });
+                    unrolled<C::NL>([&](auto n) {
+                        cp_async16_at<512 * n>(dst + C::k_bytes + 16 * v_place<C>(n * C::RPL + l_row, l_chunk), v);
+                    });
+                } else {
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const bool in_row = 64 * i + 16 * c < row_b;
-                cp_async16(dst + (2 * i) * 512, in_row ? k0 + 64 * i : k0 - 16 * c, ok0 && in_row);
-                cp_async16(dst + (2 * i + 1) * 512, in_row ? k1 + 64 * i : k1 - 16 * c, ok1 && in_row);
-            }
-            // V: slots 2c, 2c + 1, 2c + 8, 2c + 9, chunks g, g + 8, ...
+                    for (int n = 0; n < C::NL; ++n) {
+                        cp_async16_at<0>(dst + 16 * k_place<C>(n * C::RPL + l_row, l_chunk), k);
+                        cp_async16_at<0>(dst + C::k_bytes + 16 * v_place<C>(n * C::RPL + l_row, l_chunk), v);
+                        k += copy_b, v += copy_b;
+                    }
+                }
+            } else {
+                const bool in = lane < 16 && t0 + lane < len;
+                const bool ok = in && (unsigned)look_page < (unsigned)a.c.n_pages;
+                const uint32_t good = __ballot_sync(~0u, ok), bad = __ballot_sync(~0u, in && !ok);
+                if (lane == 0) {
+                    s_mask[warp * NS + istage] = good | bad << 16;
+                    if (bad) raise_device_error(a.err, kErrPage);
+                }
+                const long long off = ok ? look_page * a.c.page_b + ip_kh * a.c.head_b +
+                                               (look_off + (simple ? lane : 0)) * a.c.token_b
+                                         : 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int slot = 2 * c + (j & 1) + 8 * (j >> 1);
-                const char *v = a.c.v + __shfl_sync(~0u, off, slot);
-                const bool okv = good >> slot & 1u;
-#pragma unroll
-                for (int q = 0; q < NQ; ++q) {
-                    const int at = (8 * q + g) * C::VB;
-                    const bool in_row = at < row_b;
-                    if (C::VB == 16)
-                        cp_async16(dst + C::k_bytes + (4 * q + j) * 512, in_row ? v + at : v, okv && in_row);
-                    else
-                        cp_async8(dst + C::k_bytes + (4 * q + j) * 256 - lane * 8, in_row ? v + at : v,
-                                  okv && in_row);
+                for (int n = 0; n < C::NL; ++n) {
+                    const int row = n * C::RPL + l_row;
+                    const long long at = __shfl_sync(~0u, off, row) + (in_row ? 16 * l_chunk : 0);
+                    const bool take = in_row && (good >> row & 1u);
+                    cp_async16(dst + 16 * k_place<C>(row, l_chunk), a.c.k + at, take);
+                    cp_async16(dst + C::k_bytes + 16 * v_place<C>(row, l_chunk), a.c.v + at, take);
                 }
             }
             ++issued;
             advance(ip);
+            if (ip.i == 0) ip_kh = ip.seg / w.row_tiles;
             look();
         }
         cp_async_commit();
@@ -332,16 +377,18 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
     float rs[NT][2];                                  // score factor of the thread's rows (e4m3: per row)
     int lim[NT][2];                                   // slots they see
     const float factor = a.scale * 1.44269504088896340736f;
+    constexpr float shift = TYPE == kBf16 ? 0.f : 6.f;
     const bool third = TYPE == kBf16 && a.o_type == kF32;
+    int hidden_from = 0;                              // first slot that some row does not see
     bool fresh = true;                                // at the start of a piece
     int stage = 0;
     bool began_here = false;
 
 #pragma unroll 1
     for (int step = w0; step < w1; ++step) {
-        const int kh = p.seg / w.row_tiles, tile = p.seg - kh * w.row_tiles;
-        const int len = s_len[p.b];
         if (fresh) {
+            const int kh = p.seg / w.row_tiles, tile = p.seg - kh * w.row_tiles, len = s_len[p.b];
+            hidden_from = len - a.S + 1;
             fresh = false;
             began_here = p.i == 0;
             // Q as the B operand: row g of each 8, the thread's chunks
@@ -397,7 +444,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                 for (int e = 0; e < 2; ++e) {
                     const int s = (tile * rows + 8 * nt + 2 * c + e) / a.group;
                     lim[nt][e] = len - a.S + 1 + (s < a.S ? s : a.S - 1);
-                    m[nt][e] = -INFINITY;
+                    m[nt][e] = kNoRef;
                     l[nt][e] = 0.f;
                 }
 #pragma unroll
@@ -410,124 +457,121 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
         cp_async_wait<NS - 1>();
         __syncwarp();
         const uint32_t mask = s_mask[warp * NS + stage];
-        const uint32_t src = ring_a + stage * C::stage + lane * 16;
+        const uint32_t src = ring_a + stage * C::stage;
 
-        // ---- S^T = K Q^T ----
-        float s[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const uint4 x = lds128(src + (2 * i) * 512), y = lds128(src + (2 * i + 1) * 512);
-            const uint32_t kx[4] = {x.x, x.y, x.z, x.w}, ky[4] = {y.x, y.y, y.z, y.w};
-            if constexpr (TYPE != kE4m3) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma16816<TYPE>(s[nt], kx[2 * u], ky[2 * u], kx[2 * u + 1], ky[2 * u + 1], qf[nt][i][2 * u],
-                                       qf[nt][i][2 * u + 1]);
-            } else {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const uint32_t a0 = e4m3x2_to_f16x2(kx[u]), a2 = e4m3x2_to_f16x2(kx[u] >> 16);
-                    const uint32_t a1 = e4m3x2_to_f16x2(ky[u]), a3 = e4m3x2_to_f16x2(ky[u] >> 16);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma16816<TYPE>(s[nt], a0, a1, a2, a3, qf[nt][i][2 * u], qf[nt][i][2 * u + 1]);
-                }
-            }
-        }
-        // scores in log2 units; thread: slots g, g + 8 by rows 2c, 2c + 1
-        const int t0 = 16 * p.i;
-        const bool partial = mask != 0xFFFFu || (a.S > 1 && t0 + 16 > len - a.S + 1);
+        // ---- S^T = K Q^T, in two chains ----
+        float s[NT][4], s1[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[nt][e] *= TYPE == kE4m3 ? rs[nt][e & 1] : factor;
-        if (partial) {
+            for (int e = 0; e < 4; ++e) s[nt][e] = s1[nt][e] = 0.f;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+        for (int i = 0; i < NI; ++i) {
+            // slots g and g + 8, chunk c + 4 i
+            const uint4 x = lds128(src + 16 * k_place<C>(g, 4 * i + c)), y = lds128(src + 16 * k_place<C>(g + 8, 4 * i + c));
+            const uint32_t kx[4] = {x.x, x.y, x.z, x.w}, ky[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = g + 8 * (e >> 1);
-                    if (t0 + j >= lim[nt][e & 1]) s[nt][e] = -INFINITY;      // slots past the end are past every limit
-                    else if (mask >> (16 + j) & 1u) s[nt][e] = NAN;          // its page is not in the pool
+            for (int u = 0; u < C::KE / 4; ++u) {
+                uint32_t a0, a1, a2, a3;
+                if constexpr (TYPE != kE4m3) {
+                    a0 = kx[2 * u], a1 = ky[2 * u], a2 = kx[2 * u + 1], a3 = ky[2 * u + 1];
+                } else {
+                    a0 = e4m3x2_to_f16x2(kx[u]), a2 = e4m3x2_to_f16x2(kx[u] >> 16);
+                    a1 = e4m3x2_to_f16x2(ky[u]), a3 = e4m3x2_to_f16x2(ky[u] >> 16);
                 }
-        }
-        if (a.accumulate) {
-            float *dst = w.scores + ((size_t)(p.b * tiles + p.seg) * w.score_slots + t0) * rows + 2 * c;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                *reinterpret_cast<float2 *>(dst + (size_t)g * rows + 8 * nt) = make_float2(s[nt][0], s[nt][1]);
-                *reinterpret_cast<float2 *>(dst + (size_t)(g + 8) * rows + 8 * nt) = make_float2(s[nt][2], s[nt][3]);
+                for (int nt = 0; nt < NT; ++nt)
+                    mma16816<TYPE>(u & 1 ? s1[nt] : s[nt], a0, a1, a2, a3, qf[nt][i][2 * u], qf[nt][i][2 * u + 1]);
             }
         }
 
-        // ---- running maxima; O and l follow when one grows ----
+        // ---- exponents against the rows' references; thread: slots g, g + 8 by rows 2c, 2c + 1 ----
+        const int t0 = 16 * p.i;
+        const bool partial = mask != 0xFFFFu || (a.S > 1 && t0 + 16 > hidden_from);
+        // slots past the end are past every limit; NaN where the slot's page is not in the pool
+        auto masked = [&](float z, int nt, int e) {
+            const int j = g + 8 * (e >> 1);
+            if (t0 + j >= lim[nt][e & 1]) return -INFINITY;
+            return mask >> (16 + j) & 1u ? NAN : z;
+        };
         uint32_t ph[NT][2], pl[NT][2], pt[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float x0 = fmaxf(s[nt][0], s[nt][2]), x1 = fmaxf(s[nt][1], s[nt][3]);
+            float x[4];
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) {
-                x0 = fmaxf(x0, __shfl_xor_sync(~0u, x0, d));
-                x1 = fmaxf(x1, __shfl_xor_sync(~0u, x1, d));
+            for (int e = 0; e < 4; ++e) {
+                s[nt][e] += s1[nt][e];
+                x[e] = fmaf(s[nt][e], TYPE == kE4m3 ? rs[nt][e & 1] : factor, -m[nt][e & 1]);
+                if (partial) x[e] = masked(x[e], nt, e);
             }
-            if (__any_sync(~0u, x0 > m[nt][0] || x1 > m[nt][1])) {
-                const float n0 = fmaxf(m[nt][0], x0), n1 = fmaxf(m[nt][1], x1);
-                const float f0 = n0 == -INFINITY ? 1.f : exp2f(m[nt][0] - n0);
-                const float f1 = n1 == -INFINITY ? 1.f : exp2f(m[nt][1] - n1);
-                m[nt][0] = n0, m[nt][1] = n1;
-                l[nt][0] *= f0, l[nt][1] *= f1;
+            constexpr float most = shift + 8.f;
+            if (__any_sync(~0u, x[0] > most || x[1] > most || x[2] > most || x[3] > most)) {
+                // raise the references to the maxima; l and O follow
+                float z[4];
 #pragma unroll
-                for (int t = 0; t < C::MT; ++t) {
-                    o[t][nt][0] *= f0, o[t][nt][2] *= f0;
-                    o[t][nt][1] *= f1, o[t][nt][3] *= f1;
+                for (int e = 0; e < 4; ++e) {
+                    z[e] = s[nt][e] * (TYPE == kE4m3 ? rs[nt][e & 1] : factor);
+                    if (partial) z[e] = masked(z[e], nt, e);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float top = fmaxf(z[e], z[2 + e]);
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+                    const float ref = fmaxf(m[nt][e], top - shift), f = ex2(m[nt][e] - ref);
+                    m[nt][e] = ref;
+                    l[nt][e] *= f;
+#pragma unroll
+                    for (int t = 0; t < C::MT; ++t) o[t][nt][e] *= f, o[t][nt][2 + e] *= f;
+                    x[e] = z[e] - ref;
+                    x[2 + e] = z[2 + e] - ref;
                 }
             }
-            constexpr float shift = TYPE == kBf16 ? 0.f : 14.f;
-            const float r0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] - shift;
-            const float r1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] - shift;
-            const float p0 = exp2f(s[nt][0] - r0), p1 = exp2f(s[nt][1] - r1);
-            const float p2 = exp2f(s[nt][2] - r0), p3 = exp2f(s[nt][3] - r1);
-            l[nt][0] += p0 + p2;
-            l[nt][1] += p1 + p3;
+            if (a.accumulate) {
+                float *dst = w.scores + ((size_t)(p.b * tiles + p.seg) * w.score_slots + t0) * rows + 8 * nt + 2 * c;
+                *reinterpret_cast<float2 *>(dst + (size_t)g * rows) = make_float2(x[0] + m[nt][0], x[1] + m[nt][1]);
+                *reinterpret_cast<float2 *>(dst + (size_t)(g + 8) * rows) = make_float2(x[2] + m[nt][0], x[3] + m[nt][1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = ex2(x[e]);
+            l[nt][0] += x[0] + x[2];
+            l[nt][1] += x[1] + x[3];
             // P as a sum of 16-bit parts, transposed into B fragments
-            auto split = [&](float x, float y, int half) {
-                uint32_t h, r, q = 0;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float u = x[2 * half], v = x[2 * half + 1];
                 if constexpr (TYPE == kBf16) {
-                    h = pack_bf16(x, y);
+                    const uint32_t h = pack_bf16(u, v);
                     float2 f = unpack_bf16(h);
-                    x -= f.x, y -= f.y;
-                    r = pack_bf16(x, y);
+                    u -= f.x, v -= f.y;
+                    const uint32_t r = pack_bf16(u, v);
+                    ph[nt][half] = transpose8x8(h);
+                    pl[nt][half] = transpose8x8(r);
                     if (third) {
                         f = unpack_bf16(r);
-                        q = pack_bf16(x - f.x, y - f.y);
+                        pt[nt][half] = transpose8x8(pack_bf16(u - f.x, v - f.y));
                     }
                 } else {
-                    h = pack_f16(x, y);
+                    const uint32_t h = pack_f16(u, v);
                     const float2 f = unpack_f16(h);
-                    r = pack_f16(x - f.x, y - f.y);
+                    ph[nt][half] = transpose8x8(h);
+                    pl[nt][half] = transpose8x8(pack_f16(u - f.x, v - f.y));
                 }
-                ph[nt][half] = transpose8x8(h);
-                pl[nt][half] = transpose8x8(r);
-                if (TYPE == kBf16 && third) pt[nt][half] = transpose8x8(q);
-            };
-            split(p0, p1, 0);
-            split(p2, p3, 1);
+            }
         }
 
         // ---- O^T += V^T P^T ----
         // V^T's A fragments: tile t of chunk q covers elements t (rows g) and t + E/2 (rows g + 8) of the chunk
         auto v_chunk = [&](int q, uint32_t (&x)[4][4]) {
+            // slots 2c, 2c + 1, 2c + 8, 2c + 9, the thread's chunk 8 q + g (of 8 bytes where a row has but 64)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
+                const int row = 2 * c + (j & 1) + 8 * (j >> 1);
                 if (C::VB == 16) {
-                    const uint4 v = lds128(src + C::k_bytes + (4 * q + j) * 512);
+                    const uint4 v = lds128(src + C::k_bytes + 16 * v_place<C>(row, 8 * q + g));
                     x[j][0] = v.x, x[j][1] = v.y, x[j][2] = v.z, x[j][3] = v.w;
                 } else {
-                    const uint2 v = lds64(src - lane * 8 + C::k_bytes + (4 * q + j) * 256);
+                    const uint2 v = lds64(src + C::k_bytes + 16 * v_place<C>(row, g >> 1) + 8 * (g & 1));
                     x[j][0] = v.x, x[j][1] = v.y, x[j][2] = x[j][3] = 0u;
                 }
             }
@@ -562,7 +606,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
             }
             careful = __any_sync(~0u, odd);
         }
-        if (!careful) {
+        auto add_pv = [&](auto with_third) {
 #pragma unroll
             for (int q = 0; q < NQ; ++q) {
                 uint32_t x[4][4];
@@ -577,12 +621,16 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float(&acc)[4] = o[q * (E / 2) + t][nt];
-                        if (TYPE == kBf16 && third) mma16816<TYPE>(acc, a0, a1, a2, a3, pt[nt][0], pt[nt][1]);
+                        if constexpr (with_third) mma16816<TYPE>(acc, a0, a1, a2, a3, pt[nt][0], pt[nt][1]);
                         mma16816<TYPE>(acc, a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
                         mma16816<TYPE>(acc, a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
                     }
                 }
             }
+        };
+        if (!careful) {
+            if (TYPE == kBf16 && third) add_pv(std::true_type());
+            else add_pv(std::false_type());
         } else {
             // one slot at a time, added only to the rows that see it
 #pragma unroll 1
@@ -627,6 +675,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(~0u, l[nt][e], d);
+            const int kh = p.seg / w.row_tiles, tile = p.seg - kh * w.row_tiles;
             const float vs = TYPE == kE4m3 ? __ldg(a.c.v_scale + kh) : 1.f;
             const bool whole = ended && began_here;
             // an open piece waits in the ring when the range is done with it, else in the workspace
@@ -647,10 +696,10 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                     const int r = 8 * nt + 2 * c + e;
                     const RowRef ref = row_ref(a, p.b, kh, tile * rows + r);
                     if (!ref.real) continue;
-                    const float f = row_factor<TYPE>(l[nt][e], vs);
+                    const float f = row_factor(l[nt][e], vs);
                     if (g == 0) {
                         if (whole) {
-                            if (a.lse) a.lse[ref.head] = row_lse<TYPE>(m[nt][e], l[nt][e]);
+                            if (a.lse) a.lse[ref.head] = row_lse(m[nt][e], l[nt][e]);
                         } else {
                             s_ml[(2 * warp + slot) * rows + r] = make_float2(m[nt][e], l[nt][e]);
                         }
@@ -695,16 +744,15 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
             const int r = i / (DP / 4), d = 4 * (i - r * (DP / 4));
             const RowRef ref = row_ref(a, b, kh, tile * rows + r);
             if (!ref.real) continue;
-            float mm = -INFINITY;
+            float mm = kNoRef;
             for (int x = first; x <= last; ++x)
                 if (s_piece[x].x == seg) mm = fmaxf(mm, s_ml[x * rows + r].x);
-            const float base = mm == -INFINITY ? 0.f : mm;
             float ll = 0.f;
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int x = first; x <= last; ++x) {
                 if (s_piece[x].x != seg) continue;
                 const float2 ml = s_ml[x * rows + r];
-                const float f = exp2f(ml.x - base);
+                const float f = ex2(ml.x - mm);
                 ll += ml.y * f;
                 // a piece that ended its segment before its warp's range did lies in the workspace
                 const int wx = x >> 1;
@@ -716,8 +764,8 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                 sum.x += v.x * f, sum.y += v.y * f, sum.z += v.z * f, sum.w += v.w * f;
             }
             if (whole) {
-                if (d < D) store_out4(a, ref.head * D + d, sum, row_factor<TYPE>(ll, vs));
-                if (d == 0 && a.lse) a.lse[ref.head] = row_lse<TYPE>(mm, ll);
+                if (d < D) store_out4(a, ref.head * D + d, sum, row_factor(ll, vs));
+                if (d == 0 && a.lse) a.lse[ref.head] = row_lse(mm, ll);
             } else {
                 *reinterpret_cast<float4 *>(w.part_o + (out + r) * DP + d) = sum;
                 if (d == 0) w.part_ml[out + r] = make_float2(mm, ll);
