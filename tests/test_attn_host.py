@@ -37,7 +37,7 @@ def append(qg, c=None, **kw):
 
 
 def attn(qg, c=None, **kw):
-    d = dict(table=P, table_stride=8, lens=P, n_seq=2, max_len=100, o=P, o_type=qg.QG_F32, lse=P, q=P,
+    d = dict(table=P, table_stride=8, lens=P, n_seq=64, max_len=100, o=P, o_type=qg.QG_F32, lse=P, q=P,
              q_type=qg.QG_BF16, q_stride=8 * 128, S=1, n_q_heads=8, scale=0.1, accumulate=0, ws=P, ws_bytes=1 << 40,
              stream=0)
     d.update(kw)

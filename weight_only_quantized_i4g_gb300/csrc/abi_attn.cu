@@ -55,7 +55,7 @@ int check_cache(const char *fn, const qg_kv_cache *c, KvView *view) {
     view->token_b = (long long)(c->token_stride * esz);
     view->n_pages = c->n_pages;
     view->page = c->page_size;
-    view->page_shift = (c->page_size & (c->page_size - 1)) ? -1 : __builtin_ctz((unsigned)c->page_size);
+    view->page_div = fast_div(c->page_size);
     view->n_heads = c->n_heads;
     view->dim = c->head_dim;
     view->type = c->type;

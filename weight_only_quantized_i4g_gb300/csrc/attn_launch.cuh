@@ -39,7 +39,7 @@ int launch_attn_stream(const AttnArgs &a, const AttnWork &w, const AttnPlan &pl,
         const size_t smem = pl.smem + (2 * (size_t)a.n_seq + 1) * sizeof(int);
         auto *kernel = attn_stream_kernel<TYPE, C::DP, C::NT>;
         set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), 232448);
-        return launch_pdl("qattn_paged", kernel, dim3(num_sms()), dim3(C::threads), smem, st, a, w);
+        return launch_pdl("qattn_paged", kernel, dim3(w.ctas), dim3(C::threads), smem, st, a, w);
     });
 }
 

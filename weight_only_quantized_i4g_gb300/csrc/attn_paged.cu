@@ -1,6 +1,6 @@
-// attn_paged.cu -- attention over a paged cache: workspace, launches, the join
-// of segments that several blocks share, and the accumulation of attention
-// weights.  The streaming kernel is in attn_paged.cuh.
+// attn_paged.cu -- attention over a paged cache: workspace, launches, and the
+// second kernel: the join of segments that several blocks share, and the
+// accumulation of attention weights.  The streaming kernel is in attn_paged.cuh.
 #include "attn_launch.cuh"
 
 namespace qg {
@@ -14,87 +14,123 @@ extern template AttnPlan attn_plan<kE4m3>(int, int);
 
 namespace {
 
-constexpr int kJoinThreads = 256;
+constexpr long long kWholeBytes = 512 << 10;
+constexpr int kFinishThreads = 256;
+constexpr int kFinishWarps = kFinishThreads / 32;
 
-// Joins the pieces of the segment that block x of the streaming kernel left
-// open at its end: that block's last piece, then the first pieces of the
-// blocks after it.  Block (x, y) does rows 8y .. 8y + 7.
-template <int TYPE>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnArgs a,
-                                                                 const __grid_constant__ AttnWork w, int rows,
-                                                                 int dp) {
-    extern __shared__ float2 s_ml[];                  // [pieces][8]: factor, sum
-    __shared__ float s_l[8];
-    griddep_launch_dependents();
-    griddep_wait();
-    const int2 open = w.tail[blockIdx.x];
-    const int seg = open.x, pieces = open.y, r0 = 8 * blockIdx.y;
-    if (seg < 0) return;
-    const int tiles = a.c.n_heads * w.row_tiles;
-    const int b = seg / tiles, sg = seg - b * tiles, kh = sg / w.row_tiles, tile = sg - kh * w.row_tiles;
-    if (tile * rows + r0 >= a.S * a.group) return;
-    auto base = [&](int i) { return ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * rows + r0; };
-    for (int i = threadIdx.x; i < 8 * pieces; i += kJoinThreads) s_ml[i] = w.part_ml[base(i >> 3) + (i & 7)];
-    __syncthreads();
-    // one warp a row: largest maximum, then factors and the sum
-    const int r = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool real = tile * rows + r0 + r < a.S * a.group;
-    float m = kNoRef, l = 0.f;
-    for (int i = lane; i < pieces; i += 32) m = fmaxf(m, s_ml[8 * i + r].x);
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-    for (int i = lane; i < pieces; i += 32) {
-        const float2 x = s_ml[8 * i + r];
-        const float f = ex2(x.x - m);
-        s_ml[8 * i + r].x = f;
-        l += x.y * f;
-    }
-    for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
-    if (lane == 0) {
-        s_l[r] = l;
-        if (real && a.lse) a.lse[row_ref(a, b, kh, tile * rows + r0 + r).head] = row_lse(m, l);
-    }
-    __syncthreads();
-    const float vs = TYPE == kE4m3 ? __ldg(a.c.v_scale + kh) : 1.f;
-    for (int i = threadIdx.x; i < 8 * (dp / 4); i += kJoinThreads) {
-        const int row = i / (dp / 4), d = 4 * (i - row * (dp / 4));
-        const RowRef ref = row_ref(a, b, kh, tile * rows + r0 + row);
-        if (!ref.real || d >= a.c.dim) continue;
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int x = 0; x < pieces; ++x) {
-            const float f = s_ml[8 * x + row].x;
-            const float4 v = *reinterpret_cast<const float4 *>(w.part_o + (base(x) + row) * dp + d);
-            sum.x += v.x * f, sum.y += v.y * f, sum.z += v.z * f, sum.w += v.w * f;
-        }
-        store_out4(a, ref.head * a.c.dim + d, sum, row_factor(s_l[row], vs));
-    }
-}
-
-// weight[t] += sum over the rows of a key-value head of exp(z_t - lse), from
-// the scores that the streaming kernel left; a thread a slot.
-constexpr int kWeightThreads = 256;
-__global__ void __launch_bounds__(kWeightThreads) attn_weight_kernel(const __grid_constant__ AttnArgs a,
-                                                                     const __grid_constant__ AttnWork w, int rows) {
+// The second kernel of a call.  Its first w.ctas * rows blocks join segments
+// that several blocks of the streaming kernel share: block (x, r) does row r
+// of the segment that the streaming kernel's block x left open at its end (its
+// last piece, then the first pieces of the blocks after it).  Of its `dp / 4`
+// threads a piece, each takes every so many pieces, all loads in flight at
+// once.  The further blocks add up attention weights from the scores that the
+// streaming kernel left, a thread a slot:
+//   weight[t] += sum over the rows of a key-value head of 2^(z_t - lse).
+// Which segments are shared follows from the lengths, which are read before
+// the wait for the streaming kernel.
+__global__ void __launch_bounds__(kFinishThreads)
+    attn_finish_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnWork w, int rows, int dp,
+                       int warps, int join_blocks) {
+    extern __shared__ int s_prefix[];                 // [n + 1], then lengths [n]
+    __shared__ float4 s_acc[kFinishThreads];
     __shared__ float s_lse[64];
+    __shared__ int s_sum[kFinishWarps];
     griddep_launch_dependents();
-    griddep_wait();
-    const int kh = blockIdx.x % a.c.n_heads, b = blockIdx.x / a.c.n_heads;
-    const int len = seq_len(a.lens, b, a.max_len, nullptr);
-    if ((int)blockIdx.y * kWeightThreads >= len) return;
-    const int t = blockIdx.y * kWeightThreads + threadIdx.x, R = a.S * a.group;
+    const int tid = threadIdx.x, lane = tid & 31, n = a.n_seq;
+    int *s_len = s_prefix + n + 1;
+    scan_steps<kFinishThreads>(a, s_len, s_prefix, s_sum, nullptr);
+    const int total = s_prefix[n] * w.tiles, chunk = steps_per_block(total, w.ctas, warps);
+    // this kernel must not be complete before the streaming kernel is
+    if (blockIdx.x == 0) griddep_wait();
+
+    if ((int)blockIdx.x < join_blocks) {
+        const int x = blockIdx.x / rows, r = blockIdx.x - x * rows;
+        const int c0 = x * chunk, c1 = c0 + chunk;
+        if (c1 >= total) return;
+        const Place p = locate(c1 - 1, s_prefix, n, w);
+        const int start = c1 - 1 - p.i, end = start + p.n;
+        if (start < c0 || end <= c1) return;          // it begins before this block, or is not open
+        const int pieces = (end - 1) / chunk - x + 1;
+        const int kh = quotient(p.seg, w.row_tiles_div), tile = p.seg - kh * w.row_tiles;
+        const RowRef ref = row_ref(a, w, p.b, kh, tile * rows + r);
+        if (!ref.real) return;
+        const float vs = a.c.type == kE4m3 ? __ldg(a.c.v_scale + kh) : 1.f;
+        griddep_wait();
+
+        auto at = [&](int i) { return ((size_t)(x + i) * 2 + (i == 0 ? 1 : 0)) * rows + r; };
+        const int quads = dp / 4, set = tid / quads, d = 4 * (tid - set * quads), sets = kFinishThreads / quads;
+        constexpr int kAhead = 4;
+        float4 v[kAhead];
+        float f[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = set + k * sets;
+            f[k] = kNoRef;
+            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < pieces) v[k] = *reinterpret_cast<const float4 *>(w.part_o + at(i) * dp + d), f[k] = w.part_ml[at(i)].x;
+        }
+        // every warp: the row's reference and sum
+        float m = kNoRef, l = 0.f;
+        for (int i = lane; i < pieces; i += 32) m = fmaxf(m, w.part_ml[at(i)].x);
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+        for (int i = lane; i < pieces; i += 32) {
+            const float2 y = w.part_ml[at(i)];
+            l += y.y * ex2(y.x - m);
+        }
+        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](float4 y, float g) {
+            sum.x += y.x * g, sum.y += y.y * g, sum.z += y.z * g, sum.w += y.w * g;
+        };
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (set + k * sets < pieces) add(v[k], ex2(f[k] - m));
+        for (int i = set + kAhead * sets; i < pieces; i += sets)
+            add(*reinterpret_cast<const float4 *>(w.part_o + at(i) * dp + d), ex2(w.part_ml[at(i)].x - m));
+        s_acc[tid] = sum;
+        __syncthreads();
+        if (set > 0) return;
+        for (int k = 1; k < sets; ++k) add(s_acc[k * quads + tid], 1.f);
+        if (d < a.c.dim) store_out4(a, ref.head * a.c.dim + d, sum, row_factor(l, vs));
+        if (tid == 0 && a.lse) a.lse[ref.head] = row_lse(m, l);
+        return;
+    }
+
+    const int at = blockIdx.x - join_blocks, heads = n * a.c.n_heads;
+    const int bh = at % heads, part = at / heads, b = bh / a.c.n_heads, kh = bh - b * a.c.n_heads;
+    const int len = s_len[b];
+    if (part * kFinishThreads >= len) return;
+    const int t = part * kFinishThreads + tid, R = a.S * a.group;
     SlotRef ref{-1, 0};
     if (t < len) ref = find_slot(a.c, a.table + (size_t)b * a.table_stride, t);
+    griddep_wait();
     float sum = 0.f;
     for (int tile = 0; tile < w.row_tiles; ++tile) {
+        const int sg = kh * w.row_tiles + tile;
         __syncthreads();
-        if (threadIdx.x < rows) {
-            const RowRef r = row_ref(a, b, kh, tile * rows + threadIdx.x);
-            s_lse[threadIdx.x] = r.real ? a.lse[r.head] * 1.44269504088896340736f : -INFINITY;
+        if (tid < rows) {
+            const RowRef r = row_ref(a, w, b, kh, tile * rows + tid);
+            float lse = -INFINITY;                    // in log2 units
+            if (r.real) {
+                const int steps = s_prefix[b + 1] - s_prefix[b], start = s_prefix[b] * w.tiles + sg * steps;
+                const int i0 = w.whole ? 0 : start / chunk, i1 = w.whole ? 0 : (start + steps - 1) / chunk;
+                if (i0 == i1) {
+                    lse = a.lse[r.head] * 1.44269504088896340736f;
+                } else {                              // its pieces' statistics; the join may not have run yet
+                    auto stat = [&](int i) { return w.part_ml[((size_t)i * 2 + (i == i0 ? 1 : 0)) * rows + tid]; };
+                    float m = kNoRef, l = 0.f;
+#pragma unroll 4
+                    for (int i = i0; i <= i1; ++i) m = fmaxf(m, stat(i).x);
+#pragma unroll 4
+                    for (int i = i0; i <= i1; ++i) l += stat(i).y * ex2(stat(i).x - m);
+                    lse = l == 0.f ? -INFINITY : m + log2f(l);
+                }
+            }
+            s_lse[tid] = lse;
         }
         __syncthreads();
         if (ref.page < 0) continue;
-        const size_t seg = ((size_t)b * a.c.n_heads + kh) * w.row_tiles + tile;
-        const float *z = w.scores + (seg * w.score_slots + t) * rows;
+        const float *z = w.scores + (((size_t)b * w.tiles + sg) * w.score_slots + t) * rows;
         for (int r = 0; r < rows && tile * rows + r < R; r += 2) {
             const float2 x = *reinterpret_cast<const float2 *>(z + r);
             if (s_lse[r] != -INFINITY) sum += ex2(x.x - s_lse[r]);
@@ -116,16 +152,25 @@ AttnPlan plan_of(int type, int rows, int dim) {
 struct Layout {
     AttnPlan pl;
     int rows, row_tiles, seqs, score_slots;
-    size_t part_o, part_ml, head_o, tail, lse, scores, bytes;
+    int ctas, whole;
+    size_t part_o, part_ml, head_o, lse, scores, bytes;
 };
 Layout layout(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int accumulate) {
     Layout y;
-    const int R = S * (n_q_heads / c.n_heads), ctas = num_sms();
+    const int R = S * (n_q_heads / c.n_heads);
     y.pl = plan_of(c.type, R, c.dim);
     y.rows = 8 * y.pl.nt;
     y.row_tiles = (R + y.rows - 1) / y.rows;
     y.score_slots = (max_len + 15) / 16 * 16;
     y.seqs = n_seq < kAttnMaxSeq ? n_seq : kAttnMaxSeq;
+    // one block per segment where one wave of blocks holds them all and a
+    // segment is at most kWholeBytes of K and V: an SM streams that in less
+    // than the second kernel takes
+    const long long segments = (long long)y.seqs * c.n_heads * y.row_tiles;
+    const int esz = c.type == kE4m3 ? 1 : 2;
+    y.whole = segments <= num_sms() && (long long)max_len * c.dim * esz * 2 <= kWholeBytes;
+    y.ctas = y.whole ? (int)segments : num_sms();
+    const size_t ctas = y.ctas;
     const size_t tile_f = (size_t)y.rows * y.pl.dp * 4;
     const size_t seq_scores = (size_t)c.n_heads * y.row_tiles * y.score_slots * y.rows * 4;
     if (accumulate && seq_scores * y.seqs > ((size_t)1 << 30)) {
@@ -138,23 +183,13 @@ Layout layout(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int
         at += up256(n);
         return here;
     };
-    y.part_o = take(2 * ctas * tile_f);
-    y.part_ml = take((size_t)2 * ctas * y.rows * sizeof(float2));
-    y.head_o = take((size_t)ctas * y.pl.warps * tile_f);
-    y.tail = take((size_t)ctas * sizeof(int2));
+    y.part_o = take(y.whole ? 0 : 2 * ctas * tile_f);
+    y.part_ml = take(y.whole ? 0 : 2 * ctas * y.rows * sizeof(float2));
+    y.head_o = take(y.whole ? 0 : ctas * y.pl.warps * tile_f);
     y.lse = take(accumulate ? (size_t)y.seqs * S * n_q_heads * 4 : 0);
     y.scores = take(accumulate ? seq_scores * y.seqs : 0);
     y.bytes = at;
     return y;
-}
-
-template <int TYPE>
-int run(const AttnArgs &a, const AttnWork &w, const Layout &y, cudaStream_t st) {
-    int rc = launch_attn_stream<TYPE>(a, w, y.pl, st);
-    if (rc != kOk) return rc;
-    const int ctas = num_sms();
-    return launch_pdl("qattn_paged", attn_join_kernel<TYPE>, dim3(ctas, y.pl.nt), kJoinThreads,
-                      (size_t)8 * ctas * sizeof(float2), st, a, w, y.rows, y.pl.dp);
 }
 
 }  // namespace
@@ -170,10 +205,14 @@ int run_attn_paged(const AttnArgs &args, void *ws, cudaStream_t st) {
     w.part_o = reinterpret_cast<float *>(base + y.part_o);
     w.part_ml = reinterpret_cast<float2 *>(base + y.part_ml);
     w.head_o = reinterpret_cast<float *>(base + y.head_o);
-    w.tail = reinterpret_cast<int2 *>(base + y.tail);
     w.scores = reinterpret_cast<float *>(base + y.scores);
     w.score_slots = y.score_slots;
     w.row_tiles = y.row_tiles;
+    w.tiles = args.c.n_heads * y.row_tiles;
+    w.whole = y.whole;
+    w.tiles_div = fast_div(w.tiles);
+    w.row_tiles_div = fast_div(w.row_tiles);
+    w.group_div = fast_div(args.group);
     for (int b0 = 0; b0 < args.n_seq; b0 += y.seqs) {
         AttnArgs a = args;
         a.n_seq = args.n_seq - b0 < y.seqs ? args.n_seq - b0 : y.seqs;
@@ -184,12 +223,17 @@ int run_attn_paged(const AttnArgs &args, void *ws, cudaStream_t st) {
         a.o = static_cast<char *>(a.o) + rows * a.n_q_heads * a.c.dim * (a.o_type == kF32 ? 4 : 2);
         if (a.lse) a.lse += rows * a.n_q_heads;
         else if (a.accumulate) a.lse = reinterpret_cast<float *>(base + y.lse);
-        int rc = a.c.type == kBf16 ? run<kBf16>(a, w, y, st)
-                 : a.c.type == kF16 ? run<kF16>(a, w, y, st) : run<kE4m3>(a, w, y, st);
-        if (rc == kOk && a.accumulate && a.max_len > 0)
-            rc = launch_pdl("qattn_paged", attn_weight_kernel,
-                            dim3(a.n_seq * a.c.n_heads, (a.max_len + kWeightThreads - 1) / kWeightThreads),
-                            kWeightThreads, 0, st, a, w, y.rows);
+        w.ctas = y.whole ? a.n_seq * w.tiles : y.ctas;
+        int rc = a.c.type == kBf16 ? launch_attn_stream<kBf16>(a, w, y.pl, st)
+                 : a.c.type == kF16 ? launch_attn_stream<kF16>(a, w, y.pl, st)
+                                    : launch_attn_stream<kE4m3>(a, w, y.pl, st);
+        const int joins = y.whole ? 0 : w.ctas * y.rows;
+        const long long adds = a.accumulate ? (long long)a.n_seq * a.c.n_heads *
+                                                  ((a.max_len + kFinishThreads - 1) / kFinishThreads)
+                                            : 0;
+        if (rc == kOk && joins + adds > 0)
+            rc = launch_pdl("qattn_paged", attn_finish_kernel, dim3((unsigned)(joins + adds)), kFinishThreads,
+                            (2 * (size_t)a.n_seq + 1) * sizeof(int), st, a, w, y.rows, y.pl.dp, y.pl.warps, joins);
         if (rc != kOk) return rc;
     }
     return kOk;

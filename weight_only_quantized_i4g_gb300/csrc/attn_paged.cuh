@@ -14,7 +14,9 @@
 // keeps the running maximum and sum of each row and O in registers (online
 // softmax).  A segment that ends inside its warp is finished there; pieces of
 // one that does not are joined in shared memory after the block's ranges are
-// done, and across blocks by a second kernel, always in slot order.
+// done, and across blocks by a second kernel, always in slot order.  Where
+// every segment is short and has an SM to itself, each block takes one whole
+// segment instead and the second kernel is not needed.
 //
 // Loads.  Each warp copies its steps into a ring of its own in shared memory
 // (cp.async, NS steps ahead; no block barrier), 512 consecutive bytes of a
@@ -54,10 +56,13 @@ struct AttnWork {
     float *part_o;      // [ctas][2][rows][DP]: pieces a block leaves open, at its start (0) and end (1)
     float2 *part_ml;    // [ctas][2][rows]: their maxima (log2 units) and sums
     float *head_o;      // [ctas][warps][rows][DP]: pieces a warp finishes before its range ends
-    int2 *tail;         // [ctas]: {segment left open at the block's end or -1, blocks it spans}
     float *scores;      // accumulate: z in log2 units, [segment][slot][rows]
     int score_slots;    // slots per segment in scores
     int row_tiles;
+    int tiles;          // segments per sequence: heads times row tiles
+    int whole;          // one block per segment (else equal ranges of steps)
+    int ctas;           // blocks of the streaming kernel
+    FastDiv tiles_div, row_tiles_div, group_div;
 };
 
 template <int TYPE, int DP_, int NT_>
@@ -180,14 +185,74 @@ __device__ __forceinline__ float row_lse(float m, float l) {
     return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }
 
-// The place of row r (of a segment's tile) in q, o and lse.
-struct RowRef { bool real; int s; size_t head; };   // head: index of (b, s, q head)
-__device__ __forceinline__ RowRef row_ref(const AttnArgs &a, int b, int kh, int r) {
+// Row r of a (sequence, key-value head): new token s, q head, and their index
+// in q, o and lse.
+struct RowRef { bool real; int s, q_head; size_t head; };
+__device__ __forceinline__ RowRef row_ref(const AttnArgs &a, const AttnWork &w, int b, int kh, int r) {
     RowRef x;
     x.real = r < a.S * a.group;
-    x.s = r / a.group;
-    x.head = ((size_t)b * a.S + x.s) * a.n_q_heads + kh * a.group + (r - x.s * a.group);
+    x.s = quotient(r, w.group_div);
+    x.q_head = kh * a.group + (r - x.s * a.group);
+    x.head = ((size_t)b * a.S + x.s) * a.n_q_heads + x.q_head;
     return x;
+}
+
+// Steps of 16 slots of all sequences: lengths and their running sums (n + 1)
+// into shared memory; THREADS threads, `s_sum` one int per warp.
+template <int THREADS>
+__device__ __forceinline__ void scan_steps(const AttnArgs &a, int *s_len, int *s_prefix, int *s_sum, int *err) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.n_seq;
+    const int per = (n + THREADS - 1) / THREADS;
+    int sum = 0;
+    for (int i = tid * per; i < (tid + 1) * per && i < n; ++i) {
+        const int len = seq_len(a.lens, i, a.max_len, err);
+        s_len[i] = len;
+        sum += (len + 15) >> 4;
+    }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(~0u, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) s_sum[warp] = inc;
+    __syncthreads();
+    int base = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i)
+        if (i < warp) base += s_sum[i];
+    int at = base + inc - sum;
+    for (int i = tid * per; i < (tid + 1) * per && i < n; ++i) {
+        s_prefix[i] = at;
+        at += (s_len[i] + 15) >> 4;
+    }
+    if (tid == THREADS - 1) s_prefix[n] = at;
+    __syncthreads();
+}
+
+// Steps per block where all are cut into equal ranges: at least one per warp.
+__device__ __forceinline__ int steps_per_block(int total, int ctas, int warps) {
+    const int chunk = (total + ctas - 1) / ctas;
+    return chunk < warps ? warps : chunk;
+}
+
+// Place of a global step: its sequence, segment there, step of that and steps of the segment.
+struct Place { int b, seg, i, n; };
+__device__ __forceinline__ Place locate(int step, const int *s_prefix, int n, const AttnWork &w) {
+    Place p;
+    const int x = quotient(step, w.tiles_div);
+    int lo = 0, hi = n - 1;                          // the last b with prefix[b] <= x
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_prefix[mid] <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    p.b = lo;
+    p.n = s_prefix[lo + 1] - s_prefix[lo];
+    const int rem = step - s_prefix[lo] * w.tiles;
+    p.seg = rem / p.n;
+    p.i = rem - p.seg * p.n;
+    return p;
 }
 
 template <int TYPE, int DP_, int NT_>
@@ -198,52 +263,28 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
     extern __shared__ __align__(128) char smem[];
     float2 *s_ml = reinterpret_cast<float2 *>(smem + W * C::ring);            // [W][2][rows]
     uint32_t *s_mask = reinterpret_cast<uint32_t *>(s_ml + W * 2 * rows);     // [W][NS]
-    int2 *s_piece = reinterpret_cast<int2 *>(s_mask + W * NS);                // [W][2]: {segment or -1, ended}
+    int2 *s_piece = reinterpret_cast<int2 *>(s_mask + W * NS);                // [W][2]: {segment or -1, 1: ended | 2: in head_o}
     int *s_prefix = reinterpret_cast<int *>(s_piece + W * 2);                 // [n + 1]
     int *s_len = s_prefix + a.n_seq + 1;                                      // [n]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int n = a.n_seq, D = a.c.dim;
-    const int tiles = a.c.n_heads * w.row_tiles;                              // segments per sequence
+    const int tiles = w.tiles;
 
-    griddep_launch_dependents();
+    // dependents may start once the lengths are final: the second kernel reads them before its own wait
     griddep_wait();
+    griddep_launch_dependents();
 
-    // ---- steps of every sequence, and their sums ----
-    {
-        const int per = (n + C::threads - 1) / C::threads;
-        int *s_sum = reinterpret_cast<int *>(smem);                           // the rings are not in use yet
-        int sum = 0;
-        for (int i = tid * per; i < (tid + 1) * per && i < n; ++i) {
-            const int len = seq_len(a.lens, i, a.max_len, blockIdx.x == 0 ? a.err : nullptr);
-            s_len[i] = len;
-            sum += (len + 15) >> 4;
-        }
-        int inc = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(~0u, inc, o);
-            if (lane >= o) inc += v;
-        }
-        if (lane == 31) s_sum[warp] = inc;
-        __syncthreads();
-        int base = 0;
-#pragma unroll
-        for (int i = 0; i < W; ++i)
-            if (i < warp) base += s_sum[i];
-        int at = base + inc - sum;
-        for (int i = tid * per; i < (tid + 1) * per && i < n; ++i) {
-            s_prefix[i] = at;
-            at += (s_len[i] + 15) >> 4;
-        }
-        if (tid == C::threads - 1) s_prefix[n] = at;
-        __syncthreads();
+    scan_steps<C::threads>(a, s_len, s_prefix, reinterpret_cast<int *>(smem), blockIdx.x == 0 ? a.err : nullptr);
+    int c0, c1;
+    if (w.whole) {
+        const int b = quotient(blockIdx.x, w.tiles_div), steps = s_prefix[b + 1] - s_prefix[b];
+        c0 = s_prefix[b] * tiles + (blockIdx.x - b * tiles) * steps;
+        c1 = c0 + steps;
+    } else {
+        const int total = s_prefix[n] * tiles, chunk = steps_per_block(total, gridDim.x, W);
+        c0 = (int)(blockIdx.x * chunk) < total ? blockIdx.x * chunk : total;
+        c1 = c0 + chunk < total ? c0 + chunk : total;
     }
-    const int total = s_prefix[n] * tiles;
-    // one range per block, at least one step per warp
-    int chunk = (total + gridDim.x - 1) / gridDim.x;
-    if (chunk < W) chunk = W;
-    const int c0 = blockIdx.x * chunk < total ? blockIdx.x * chunk : total;
-    const int c1 = c0 + chunk < total ? c0 + chunk : total;
 
     // sequences without a slot have no steps: their rows are empty
     for (int b = blockIdx.x; b < n; b += gridDim.x) {
@@ -254,7 +295,6 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
         if (a.lse)
             for (int i = tid; i < count; i += C::threads) a.lse[(size_t)b * count + i] = -INFINITY;
     }
-    if (tid == 0) w.tail[blockIdx.x] = make_int2(-1, 0);
     if (c0 >= c1) return;
 
     const int w0 = c0 + (int)((long long)(c1 - c0) * warp / W);
@@ -263,24 +303,6 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
     const uint32_t ring_a = smem_addr(ring);
     if (lane < 2) s_piece[2 * warp + lane] = make_int2(-1, 0);
 
-    // ---- place of a global step: sequence, segment of it, step of that ----
-    struct Place { int b, seg, i, n; };
-    auto locate = [&](int step) {
-        Place p;
-        const int x = step / tiles;
-        int lo = 0, hi = n - 1;                      // the last b with prefix[b] <= x
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (s_prefix[mid] <= x) lo = mid;
-            else hi = mid - 1;
-        }
-        p.b = lo;
-        p.n = s_prefix[lo + 1] - s_prefix[lo];
-        const int rem = step - s_prefix[lo] * tiles;
-        p.seg = rem / p.n;
-        p.i = rem - p.seg * p.n;
-        return p;
-    };
     auto advance = [&](Place &p) {
         if (++p.i < p.n) return;
         p.i = 0;
@@ -294,8 +316,8 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
     // ---- loads ----
     // `simple`: the 16 slots of a step lie in one page and rows fill the padded size
     const bool simple = D == DP && a.c.page % 16 == 0;
-    Place ip = locate(w0 < w1 ? w0 : c0);
-    int ip_kh = ip.seg / w.row_tiles;
+    Place ip = locate(w0 < w1 ? w0 : c0, s_prefix, n, w), p = ip;
+    int ip_kh = quotient(ip.seg, w.row_tiles_div);
     int issued = w0, istage = 0;
     // the page of the next step to load is looked up one step early: of its
     // first slot where the step is simple, else of slot `lane` by lanes 0-15
@@ -359,7 +381,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
             }
             ++issued;
             advance(ip);
-            if (ip.i == 0) ip_kh = ip.seg / w.row_tiles;
+            if (ip.i == 0) ip_kh = quotient(ip.seg, w.row_tiles_div);
             look();
         }
         cp_async_commit();
@@ -370,7 +392,6 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
     for (int i = 0; i < NS; ++i) issue();
 
     // ---- the warp's range ----
-    Place p = locate(w0 < w1 ? w0 : c0);
     float o[C::MT][NT][4];
     float m[NT][2], l[NT][2];
     uint32_t qf[NT][NI][C::ESZ == 1 ? 8 : 4];
@@ -387,16 +408,16 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
 #pragma unroll 1
     for (int step = w0; step < w1; ++step) {
         if (fresh) {
-            const int kh = p.seg / w.row_tiles, tile = p.seg - kh * w.row_tiles, len = s_len[p.b];
+            const int kh = quotient(p.seg, w.row_tiles_div), tile = p.seg - kh * w.row_tiles, len = s_len[p.b];
             hidden_from = len - a.S + 1;
             fresh = false;
             began_here = p.i == 0;
             // Q as the B operand: row g of each 8, the thread's chunks
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const RowRef r = row_ref(a, p.b, kh, tile * rows + 8 * nt + g);
-                const size_t head = r.head % a.n_q_heads, bs = r.head / a.n_q_heads;
-                const uint16_t *q = static_cast<const uint16_t *>(a.q) + bs * a.q_stride + head * D;
+                const RowRef r = row_ref(a, w, p.b, kh, tile * rows + 8 * nt + g);
+                const uint16_t *q = static_cast<const uint16_t *>(a.q) + ((size_t)p.b * a.S + r.s) * a.q_stride +
+                                    (size_t)r.q_head * D;
                 if constexpr (TYPE != kE4m3) {
 #pragma unroll
                     for (int i = 0; i < NI; ++i) {
@@ -442,7 +463,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int s = (tile * rows + 8 * nt + 2 * c + e) / a.group;
+                    const int s = quotient(tile * rows + 8 * nt + 2 * c + e, w.group_div);
                     lim[nt][e] = len - a.S + 1 + (s < a.S ? s : a.S - 1);
                     m[nt][e] = kNoRef;
                     l[nt][e] = 0.f;
@@ -675,7 +696,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(~0u, l[nt][e], d);
-            const int kh = p.seg / w.row_tiles, tile = p.seg - kh * w.row_tiles;
+            const int kh = quotient(p.seg, w.row_tiles_div), tile = p.seg - kh * w.row_tiles;
             const float vs = TYPE == kE4m3 ? __ldg(a.c.v_scale + kh) : 1.f;
             const bool whole = ended && began_here;
             // an open piece waits in the ring when the range is done with it, else in the workspace
@@ -687,14 +708,15 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                 __syncwarp();
             }
             if (!whole) {
-                if (lane == 0) s_piece[2 * warp + slot] = make_int2(p.b * tiles + p.seg, ended ? 1 : 0);
+                if (lane == 0)
+                    s_piece[2 * warp + slot] = make_int2(p.b * tiles + p.seg, (ended ? 1 : 0) | (step + 1 == w1 ? 0 : 2));
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int r = 8 * nt + 2 * c + e;
-                    const RowRef ref = row_ref(a, p.b, kh, tile * rows + r);
+                    const RowRef ref = row_ref(a, w, p.b, kh, tile * rows + r);
                     if (!ref.real) continue;
                     const float f = row_factor(l[nt][e], vs);
                     if (g == 0) {
@@ -722,44 +744,42 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
         advance(p);
     }
 
-    // ---- join the block's open pieces, in order ----
+    // ---- join the block's open pieces, in order: a segment has at most one per warp ----
     __syncthreads();
-    int first = 0;
-    while (first < 2 * W) {
-        const int seg = s_piece[first].x;
-        if (seg < 0) {
-            ++first;
-            continue;
-        }
-        int last = first;                             // the last piece of this segment
-        for (int i = first + 1; i < 2 * W; ++i) {
-            if (s_piece[i].x == seg) last = i;
-            else if (s_piece[i].x >= 0) break;
-        }
-        const bool starts = first & 1, ends = s_piece[last].y != 0, whole = starts && ends;
-        const int b = seg / tiles, sg = seg - b * tiles, kh = sg / w.row_tiles, tile = sg - kh * w.row_tiles;
+    const int2 piece = lane < 2 * W ? s_piece[lane] : make_int2(-1, 0);
+    const uint32_t before = __ballot_sync(~0u, piece.x >= 0) & ((1u << lane) - 1u);
+    const int prior = __shfl_sync(~0u, piece.x, before ? 31 - __clz(before) : lane);
+    uint32_t leaders = __ballot_sync(~0u, piece.x >= 0 && (before == 0u || prior != piece.x));
+    const uint32_t in_work = __ballot_sync(~0u, piece.y & 2);
+    for (; leaders; leaders &= leaders - 1u) {
+        const int first = __ffs(leaders) - 1, seg = __shfl_sync(~0u, piece.x, first);
+        const uint32_t members = __ballot_sync(~0u, piece.x == seg);
+        const bool starts = first & 1, ends = __shfl_sync(~0u, piece.y, 31 - __clz(members)) & 1, whole = starts && ends;
+        const int b = quotient(seg, w.tiles_div), sg = seg - b * tiles;
+        const int kh = quotient(sg, w.row_tiles_div), tile = sg - kh * w.row_tiles;
         const float vs = TYPE == kE4m3 ? __ldg(a.c.v_scale + kh) : 1.f;
         const size_t out = ((size_t)blockIdx.x * 2 + (starts ? 1 : 0)) * rows;
         for (int i = tid; i < rows * (DP / 4); i += C::threads) {
             const int r = i / (DP / 4), d = 4 * (i - r * (DP / 4));
-            const RowRef ref = row_ref(a, b, kh, tile * rows + r);
+            const RowRef ref = row_ref(a, w, b, kh, tile * rows + r);
             if (!ref.real) continue;
-            float mm = kNoRef;
-            for (int x = first; x <= last; ++x)
-                if (s_piece[x].x == seg) mm = fmaxf(mm, s_ml[x * rows + r].x);
-            float ll = 0.f;
+            float2 ml[W];
+            float mm = kNoRef, ll = 0.f;
+#pragma unroll
+            for (int x = 0; x < W; ++x) {
+                const uint32_t has = members >> (2 * x) & 3u;
+                ml[x] = has ? s_ml[(2 * x + (has >> 1)) * rows + r] : make_float2(kNoRef, 0.f);
+                mm = fmaxf(mm, ml[x].x);
+            }
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int x = first; x <= last; ++x) {
-                if (s_piece[x].x != seg) continue;
-                const float2 ml = s_ml[x * rows + r];
-                const float f = ex2(ml.x - mm);
-                ll += ml.y * f;
-                // a piece that ended its segment before its warp's range did lies in the workspace
-                const int wx = x >> 1;
-                const int we = c0 + (int)((long long)(c1 - c0) * (wx + 1) / W);
-                const bool mid = s_piece[x].y != 0 && (s_prefix[b] * tiles + (sg + 1) * (s_prefix[b + 1] - s_prefix[b])) < we;
-                const float *src = mid ? w.head_o + ((size_t)blockIdx.x * W + wx) * rows * DP
-                                       : reinterpret_cast<const float *>(smem + wx * C::ring);
+#pragma unroll
+            for (int x = 0; x < W; ++x) {
+                if (!(members >> (2 * x) & 3u)) continue;
+                const float f = ex2(ml[x].x - mm);
+                ll += ml[x].y * f;
+                const float *src = in_work & members & 3u << (2 * x)
+                                       ? w.head_o + ((size_t)blockIdx.x * W + x) * rows * DP
+                                       : reinterpret_cast<const float *>(smem + x * C::ring);
                 const float4 v = *reinterpret_cast<const float4 *>(src + r * DP + d);
                 sum.x += v.x * f, sum.y += v.y * f, sum.z += v.z * f, sum.w += v.w * f;
             }
@@ -771,11 +791,6 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                 if (d == 0) w.part_ml[out + r] = make_float2(mm, ll);
             }
         }
-        if (!whole && starts && tid == 0) {
-            const int end = s_prefix[b] * tiles + (sg + 1) * (s_prefix[b + 1] - s_prefix[b]);
-            w.tail[blockIdx.x] = make_int2(seg, (end - 1) / chunk - (int)blockIdx.x + 1);
-        }
-        first = last + 1;
     }
 }
 

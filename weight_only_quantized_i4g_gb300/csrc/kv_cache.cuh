@@ -22,12 +22,26 @@ constexpr int kErrPage = -10;
 // Element types (QG_F32 ... in include/qgemv.h).
 enum { kF32 = 0, kBf16 = 1, kF16 = 2, kE4m3 = 3 };
 
+// x / d for 0 <= x < 2^31 by one multiplication: mul = ceil(2^(31+L) / d) with
+// 2^(L-1) < d <= 2^L errs by less than 2^L / 2^(31+L) per unit of x, under 1/d
+// in all.
+struct FastDiv { unsigned d, mul, shift; };
+inline FastDiv fast_div(int d) {
+    unsigned l = 0;
+    while ((1ull << l) < (unsigned long long)d) ++l;
+    return FastDiv{(unsigned)d, (unsigned)(((1ull << (31 + l)) + d - 1) / d), 31 + l};
+}
+__device__ __forceinline__ int quotient(int x, FastDiv f) {
+    return (int)(((unsigned long long)(unsigned)x * f.mul) >> f.shift);
+}
+
 struct KvView {
     char *k, *v;
     const float *k_scale, *v_scale;   // e4m3 only
     float *weight;                    // [n_pages][n_heads][page], or NULL
     long long page_b, head_b, token_b;   // strides of k and v in bytes
-    int n_pages, page, page_shift;    // page_shift: log2(page), -1 when page is no power of two
+    int n_pages, page;
+    FastDiv page_div;
     int n_heads, dim, type;
 };
 
@@ -35,13 +49,8 @@ struct SlotRef { int page, off; };    // page of the pool (-1: none) and slot in
 
 // Page index of slot t in a sequence's table, and t's place in that page.
 __device__ __forceinline__ void split_slot(const KvView &c, int t, int *index, int *off) {
-    if (c.page_shift >= 0) {
-        *index = t >> c.page_shift;
-        *off = t & (c.page - 1);
-    } else {
-        *index = (int)((unsigned)t / (unsigned)c.page);
-        *off = t - *index * c.page;
-    }
+    *index = quotient(t, c.page_div);
+    *off = t - *index * c.page;
 }
 
 // Slot t of the sequence whose table row is `row`; page -1 when the table
