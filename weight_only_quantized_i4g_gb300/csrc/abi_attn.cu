@@ -35,7 +35,7 @@ int check_cache(const char *fn, const qg_kv_cache *c, KvView *view) {
     const size_t dim = (size_t)c->head_dim;
     if (c->token_stride < dim || c->head_stride < dim || c->page_stride < dim)
         QG_REFUSE(kEInval, "%s: the cache's strides must be at least head_dim", fn);
-    const size_t most = (size_t)1 << 40;   // elements; keeps every byte offset far inside 63 bits
+    const size_t most = (size_t)1 << 38;   // elements: the copies' strides are below 2^40 bytes
     if (c->token_stride > most || c->head_stride > most || c->page_stride > most ||
         c->page_stride > ((size_t)1 << 60) / c->n_pages || c->head_stride > ((size_t)1 << 60) / c->n_heads ||
         c->token_stride > ((size_t)1 << 60) / c->page_size)
@@ -84,15 +84,15 @@ int check_max_len(const char *fn, int max_len, int stride, int page) {
     return kOk;
 }
 
-// Rows of all sequences, and 16-slot steps of all sequences and heads, must
-// be counted in 31 bits.
+// Rows of all sequences, and steps (up to 16 slots of a page) of all sequences
+// and heads, must be counted in 31 bits.
 int check_attn_sizes(const char *fn, const KvView &c, int n_seq, int max_len, int S, int n_q_heads) {
     if (S < 1 || S > 8) QG_REFUSE(kEInval, "%s: S = %d new tokens, must be in 1..8", fn, S);
     if (n_seq < 0) QG_REFUSE(kEInval, "%s: n_seq = %d, must be >= 0", fn, n_seq);
     const int rc = check_heads(fn, n_q_heads, c.n_heads);
     if (rc) return rc;
-    if ((double)n_seq * S * n_q_heads > (double)INT_MAX / 2 ||
-        (double)n_seq * n_q_heads * S * ((double)max_len / 16 + 1) > (double)INT_MAX / 2)
+    const double steps = ((double)max_len / c.page + 1) * ((c.page + 15) / 16);
+    if ((double)n_seq * S * n_q_heads > (double)INT_MAX / 2 || (double)n_seq * n_q_heads * S * steps > (double)INT_MAX / 2)
         QG_REFUSE(kEInval, "%s: sizes overflow", fn);
     return kOk;
 }

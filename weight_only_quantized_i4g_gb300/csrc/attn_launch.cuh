@@ -9,6 +9,7 @@ namespace qg {
 struct AttnPlan {
     int dp, nt;         // padded head size, tiles of 8 rows per segment
     int warps;
+    int box_bytes;      // bytes of a row that one copy moves
     size_t smem;        // without the lengths
 };
 
@@ -28,18 +29,19 @@ template <int TYPE>
 AttnPlan attn_plan(int rows, int dim) {
     return attn_dispatch<TYPE>(rows, dim, [](auto cfg) {
         using C = decltype(cfg);
-        return AttnPlan{C::DP, C::NT, C::W, attn_fixed_smem<C>()};
+        return AttnPlan{C::DP, C::NT, C::W, C::BB, attn_fixed_smem<C>()};
     });
 }
 
 template <int TYPE>
-int launch_attn_stream(const AttnArgs &a, const AttnWork &w, const AttnPlan &pl, cudaStream_t st) {
+int launch_attn_stream(const AttnArgs &a, const AttnWork &w, const AttnPlan &pl, const CUtensorMap (&maps)[2],
+                       cudaStream_t st) {
     return attn_dispatch<TYPE>(a.S * a.group, a.c.dim, [&](auto cfg) {
         using C = decltype(cfg);
         const size_t smem = pl.smem + (2 * (size_t)a.n_seq + 1) * sizeof(int);
         auto *kernel = attn_stream_kernel<TYPE, C::DP, C::NT>;
         set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), 232448);
-        return launch_pdl("qattn_paged", kernel, dim3(w.ctas), dim3(C::threads), smem, st, a, w);
+        return launch_pdl("qattn_paged", kernel, dim3(w.ctas), dim3(C::threads), smem, st, a, w, maps[0], maps[1]);
     });
 }
 

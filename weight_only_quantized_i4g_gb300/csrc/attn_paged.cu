@@ -1,13 +1,18 @@
 // attn_paged.cu -- attention over a paged cache: workspace, launches, and the
 // second kernel: the join of segments that several blocks share, and the
 // accumulation of attention weights.  The streaming kernel is in attn_paged.cuh.
+#include <cudaTypedefs.h>
+
 #include "attn_launch.cuh"
 
 namespace qg {
 
-extern template int launch_attn_stream<kBf16>(const AttnArgs &, const AttnWork &, const AttnPlan &, cudaStream_t);
-extern template int launch_attn_stream<kF16>(const AttnArgs &, const AttnWork &, const AttnPlan &, cudaStream_t);
-extern template int launch_attn_stream<kE4m3>(const AttnArgs &, const AttnWork &, const AttnPlan &, cudaStream_t);
+extern template int launch_attn_stream<kBf16>(const AttnArgs &, const AttnWork &, const AttnPlan &,
+                                              const CUtensorMap (&)[2], cudaStream_t);
+extern template int launch_attn_stream<kF16>(const AttnArgs &, const AttnWork &, const AttnPlan &,
+                                              const CUtensorMap (&)[2], cudaStream_t);
+extern template int launch_attn_stream<kE4m3>(const AttnArgs &, const AttnWork &, const AttnPlan &,
+                                              const CUtensorMap (&)[2], cudaStream_t);
 extern template AttnPlan attn_plan<kBf16>(int, int);
 extern template AttnPlan attn_plan<kF16>(int, int);
 extern template AttnPlan attn_plan<kE4m3>(int, int);
@@ -38,7 +43,7 @@ __global__ void __launch_bounds__(kFinishThreads)
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, n = a.n_seq;
     int *s_len = s_prefix + n + 1;
-    scan_steps<kFinishThreads>(a, s_len, s_prefix, s_sum, nullptr);
+    scan_steps<kFinishThreads>(a, w, s_len, s_prefix, s_sum, nullptr);
     const int total = s_prefix[n] * w.tiles, chunk = steps_per_block(total, w.ctas, warps);
     // this kernel must not be complete before the streaming kernel is
     if (blockIdx.x == 0) griddep_wait();
@@ -161,7 +166,7 @@ Layout layout(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int
     y.pl = plan_of(c.type, R, c.dim);
     y.rows = 8 * y.pl.nt;
     y.row_tiles = (R + y.rows - 1) / y.rows;
-    y.score_slots = (max_len + 15) / 16 * 16;
+    y.score_slots = max_len;
     y.seqs = n_seq < kAttnMaxSeq ? n_seq : kAttnMaxSeq;
     // one block per segment where one wave of blocks holds them all and a
     // segment is at most kWholeBytes of K and V: an SM streams that in less
@@ -192,6 +197,34 @@ Layout layout(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int
     return y;
 }
 
+// Tensor map of the k or v pool: [page][head][slot][dim] in boxes of a step's
+// slots by `box_bytes`, zeros where a box passes the end of a page or a row.
+int cache_map(CUtensorMap *map, const KvView &c, const char *base, int box_bytes, int box_rows) {
+    static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            fn = nullptr;
+        }
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    }();
+    if (!encode) QG_REFUSE(kECuda, "qattn_paged: cuTensorMapEncodeTiled is not available from the driver");
+    const int esz = c.type == kE4m3 ? 1 : 2;
+    const cuuint64_t dims[4] = {(cuuint64_t)c.dim, (cuuint64_t)c.page, (cuuint64_t)c.n_heads, (cuuint64_t)c.n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)c.token_b, (cuuint64_t)c.head_b, (cuuint64_t)c.page_b};
+    const cuuint32_t box[4] = {(cuuint32_t)(box_bytes / esz), (cuuint32_t)box_rows, 1, 1}, steps[4] = {1, 1, 1, 1};
+    const CUresult r = encode(
+        map, c.type == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+             : c.type == kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+        4, const_cast<char *>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) QG_REFUSE(kECuda, "qattn_paged: cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return kOk;
+}
+
 }  // namespace
 
 size_t ws_attn_paged(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int accumulate) {
@@ -213,6 +246,13 @@ int run_attn_paged(const AttnArgs &args, void *ws, cudaStream_t st) {
     w.tiles_div = fast_div(w.tiles);
     w.row_tiles_div = fast_div(w.row_tiles);
     w.group_div = fast_div(args.group);
+    w.page_steps = (args.c.page + 15) / 16;
+    w.page_steps_div = fast_div(w.page_steps);
+    w.box_rows = args.c.page < 16 ? args.c.page : 16;
+    CUtensorMap maps[2];
+    int rc = cache_map(&maps[0], args.c, args.c.k, y.pl.box_bytes, w.box_rows);
+    if (rc == kOk) rc = cache_map(&maps[1], args.c, args.c.v, y.pl.box_bytes, w.box_rows);
+    if (rc != kOk) return rc;
     for (int b0 = 0; b0 < args.n_seq; b0 += y.seqs) {
         AttnArgs a = args;
         a.n_seq = args.n_seq - b0 < y.seqs ? args.n_seq - b0 : y.seqs;
@@ -224,9 +264,9 @@ int run_attn_paged(const AttnArgs &args, void *ws, cudaStream_t st) {
         if (a.lse) a.lse += rows * a.n_q_heads;
         else if (a.accumulate) a.lse = reinterpret_cast<float *>(base + y.lse);
         w.ctas = y.whole ? a.n_seq * w.tiles : y.ctas;
-        int rc = a.c.type == kBf16 ? launch_attn_stream<kBf16>(a, w, y.pl, st)
-                 : a.c.type == kF16 ? launch_attn_stream<kF16>(a, w, y.pl, st)
-                                    : launch_attn_stream<kE4m3>(a, w, y.pl, st);
+        rc = a.c.type == kBf16 ? launch_attn_stream<kBf16>(a, w, y.pl, maps, st)
+             : a.c.type == kF16 ? launch_attn_stream<kF16>(a, w, y.pl, maps, st)
+                                : launch_attn_stream<kE4m3>(a, w, y.pl, maps, st);
         const int joins = y.whole ? 0 : w.ctas * y.rows;
         const long long adds = a.accumulate ? (long long)a.n_seq * a.c.n_heads *
                                                   ((a.max_len + kFinishThreads - 1) / kFinishThreads)

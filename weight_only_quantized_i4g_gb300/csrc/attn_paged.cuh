@@ -7,25 +7,27 @@
 // by HBM and everything serves keeping its reads in flight.
 //
 // Work.  The rows of one sequence that share a key-value head, R = S * group,
-// form tiles of 8 * NT rows; a (sequence, head, tile) is a segment of
-// ceil(len / 16) steps of 16 slots.  All segments' steps, laid end to end, are
-// cut into one equal range per block (one block an SM) and each range into one
-// per warp: unequal lengths balance without the host knowing them.  A warp
-// keeps the running maximum and sum of each row and O in registers (online
-// softmax).  A segment that ends inside its warp is finished there; pieces of
-// one that does not are joined in shared memory after the block's ranges are
-// done, and across blocks by a second kernel, always in slot order.  Where
-// every segment is short and has an SM to itself, each block takes one whole
-// segment instead and the second kernel is not needed.
+// form tiles of 8 * NT rows; a (sequence, head, tile) is a segment of steps of
+// up to 16 slots of one page.  All segments' steps, laid end to end, are cut
+// into one equal range per block (one block an SM) and each range into one per
+// warp: unequal lengths balance without the host knowing them.  A warp keeps
+// the running maximum and sum of each row and O in registers (online softmax).
+// A segment that ends inside its warp is finished there; pieces of one that
+// does not are joined in shared memory after the block's ranges are done, and
+// across blocks by a second kernel, always in slot order.  Where every segment
+// is short and has an SM to itself, each block takes one whole segment instead
+// and the second kernel is not needed.
 //
-// Loads.  Each warp copies its steps into a ring of its own in shared memory
-// (cp.async, NS steps ahead; no block barrier), 512 consecutive bytes of a
-// page per instruction.  Copying straight in fragment order (64 and 128 byte
-// pieces of many rows per instruction) read 5.2 TB/s where this order reads
-// 6.8.  The 16-byte chunks of a row are swizzled so that both the copies and
-// the fragment reads (16 bytes a thread) are free of bank conflicts.  A
-// fragment's k indices are the 8 (or 16) consecutive elements of a chunk: the
-// contraction over d may run in any order.
+// Loads.  Each warp keeps a ring of steps in shared memory, filled by TMA
+// tensor copies (boxes of 16 slots by 128 bytes, 128-byte swizzle) that one
+// lane issues NS steps ahead; the copies pad odd head sizes and page ends with
+// zeros and take any strides.  Fragments are read 16 bytes a thread without
+// bank conflicts: a fragment's k indices are the 8 (or 16) consecutive
+// elements of a chunk, since the contraction over d may run in any order, and
+// the chunks are dealt to the threads so that the swizzle spreads them.
+// (Before: cp.async in fragment order, 64 to 128 bytes a row, read 5.2 TB/s;
+// cp.async of 512 consecutive bytes read 6.8, but its issue cost a warp 450 to
+// 570 cycles a step, against the 350 that HBM gives an SM for one.)
 //
 // Products.  S^T = K Q^T with the 16 slots as M and 8 rows as N (a decode step
 // has few rows), then O^T = V^T P^T; P^T's fragment is the transpose of
@@ -42,6 +44,8 @@
 // e4m3 codes are exact in f16; q over them is scaled per row by a power of two
 // into f16's range, which is exact for bf16 values within 2^29 of the largest.
 #pragma once
+
+#include <cuda.h>
 
 #include <type_traits>
 
@@ -62,7 +66,9 @@ struct AttnWork {
     int tiles;          // segments per sequence: heads times row tiles
     int whole;          // one block per segment (else equal ranges of steps)
     int ctas;           // blocks of the streaming kernel
-    FastDiv tiles_div, row_tiles_div, group_div;
+    int page_steps;     // steps of a page
+    int box_rows;       // slots a copy moves: 16, or a smaller page
+    FastDiv tiles_div, row_tiles_div, group_div, page_steps_div;
 };
 
 template <int TYPE, int DP_, int NT_>
@@ -76,65 +82,63 @@ struct AttnCfg {
     static constexpr int VB = E * ESZ;                // its bytes: 16, or 8
     static constexpr int NQ = DP / (8 * E);           // V chunks a thread holds per slot
     static constexpr int MT = DP / 16;                // 16-row tiles of O^T
-    static constexpr int RB = DP * ESZ;               // bytes of a row
-    static constexpr int NC = RB / 16;                // 16-byte chunks of a row: 4, 8, 16 or 32
-    static constexpr int NL = NC / 2;                 // copies of 512 bytes for 16 rows
-    static constexpr int RPL = 32 / NC;               // rows one covers
-    static constexpr int k_bytes = 16 * RB;
-    static constexpr int stage = 2 * k_bytes;         // 16 slots of K and V
-    // 192 KB in flight per SM at most; eight warps, four where a stage is 16 KB
-    static constexpr int W = stage > 8192 ? 4 : 8;
+    static constexpr int BB = DP * ESZ < 128 ? DP * ESZ : 128;   // bytes of a row in one box: 64 or 128
+    static constexpr int NB = DP * ESZ / BB;          // boxes of a row
+    static constexpr int box = 16 * BB;
+    static constexpr int stage = 2 * NB * box;        // 16 slots of K, then of V
+    // as many warps as the registers of O, Q and S allow (16, 12 or 8 an SM)
+    static constexpr int regs = 70 + 4 * MT * NT + NT * NI * (ESZ == 1 ? 8 : 4) + 8 * NT;
+    static constexpr int W0 = regs <= 128 ? 16 : regs <= 168 ? 12 : 8;
+    static constexpr int W = stage > 8192 ? 4 : W0;
+    // up to 192 KB of copies in flight
     static constexpr int NS0 = 196608 / (W * stage);
-    static constexpr int NS = NS0 > 8 ? 8 : NS0;
+    static constexpr int NS = NS0 > 6 ? 6 : NS0;
     static constexpr int ring = NS * stage;           // per warp
     static_assert(ring >= rows * DP * 4, "a warp's open piece takes the place of its ring");
     static constexpr int threads = 32 * W;
 };
 
-// dynamic shared memory: rings, row statistics of open pieces, step masks,
-// piece descriptors, then prefix [n + 1] and lengths [n]
-// Where chunk u = row * NC + chunk of a step sits: the low three bits (its bank
-// group) are exchanged by row.  A fragment read takes, per eight lanes, chunks
-// x .. x + 3 of two neighbouring rows of K, two neighbouring chunks of four
-// even (or odd) rows of V.
+// The ring: byte offset of 16-byte chunk `chunk` of slot `row` in a step's K or
+// V, as the copies' swizzle leaves it.
 template <class C>
-__device__ __forceinline__ constexpr int k_place(int row, int chunk) {
-    return (row * C::NC + chunk) ^ (C::NC >= 8 ? (row & 1) << 2 : 0);
+__device__ __forceinline__ constexpr int chunk_place(int row, int chunk) {
+    constexpr int per = C::BB / 16;
+    const int b = chunk / per, x = chunk % per;
+    return b * C::box + row * C::BB + 16 * (per == 8 ? x ^ (row & 7) : x ^ (row >> 1 & 3));
 }
+// Which chunk of its slot a thread (c = lane % 4) holds as its i-th of K: with
+// rows of 128 bytes neighbouring ones, so that the swizzle of even and odd rows
+// parts the eight lanes of a read.
 template <class C>
-__device__ __forceinline__ constexpr int v_place(int row, int chunk) {
-    return (row * C::NC + chunk) ^ (row >> 1 & 3) << 1;
+__device__ __forceinline__ constexpr int k_chunk(int i, int c) {
+    return C::BB == 128 ? 8 * (i >> 1) + 2 * c + (i & 1) : 4 * i + c;
+}
+// Pieces of 8 rows of O in shared memory: place (in float4) of quad x of row r.
+// The exchange by row parts the eight lanes of a store (two g, four c).
+template <class C>
+__device__ __forceinline__ int slab_place(int r, int x) {
+    return r * (C::DP / 4) + (x ^ ((r >> 1 & 1) | (r >> 2 & 1) << 2));
 }
 
 template <class C>
 __host__ __device__ constexpr size_t attn_fixed_smem() {
-    return (size_t)C::W * C::ring + C::W * 2 * C::rows * sizeof(float2) + C::W * C::NS * 4 + C::W * 2 * 8;
+    // 1 KB for the copies' alignment, then as laid out in the kernel
+    return 1024 + (size_t)C::W * C::ring + C::W * C::NS * (8 + 4) + C::W * 2 * C::rows * sizeof(float2) + C::W * 2 * 8;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool ok) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
-template <int S>
-__device__ __forceinline__ void cp_async16_at(uint32_t dst, const char *src) {   // [dst] <- [src + S]
-    asm volatile("cp.async.cg.shared.global [%0], [%1 + %2], 16;" ::"r"(dst), "l"(src), "n"(S) : "memory");
-}
-// fn(integral_constant<int, 0>) .. fn(integral_constant<int, N - 1>): unrolled, with the index a constant
-template <int N, int I = 0, class Fn>
-__device__ __forceinline__ void unrolled(Fn fn) {
-    if constexpr (I < N) {
-        fn(std::integral_constant<int, I>());
-        unrolled<N, I + 1>(fn);
-    }
+// Box at element x, slot t, head h of page p.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int t, int h, int p,
+                                            uint64_t *bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+        "[%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(t), "r"(h), "r"(p), "r"(smem_addr(bar)), "l"(policy)
+        : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {       // 2^x, 2 ulp; 2^-inf = 0
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
@@ -197,17 +201,24 @@ __device__ __forceinline__ RowRef row_ref(const AttnArgs &a, const AttnWork &w, 
     return x;
 }
 
-// Steps of 16 slots of all sequences: lengths and their running sums (n + 1)
-// into shared memory; THREADS threads, `s_sum` one int per warp.
+// Steps of a sequence of len slots: 16 slots of a page each, fewer at the ends
+// of pages and of the sequence.
+__device__ __forceinline__ int seq_steps(const AttnArgs &a, const AttnWork &w, int len) {
+    const int full = quotient(len, a.c.page_div);
+    return full * w.page_steps + ((len - full * a.c.page + 15) >> 4);
+}
+
+// Lengths of all sequences and the running sums (n + 1) of their steps into
+// shared memory; THREADS threads, `s_sum` one int per warp.
 template <int THREADS>
-__device__ __forceinline__ void scan_steps(const AttnArgs &a, int *s_len, int *s_prefix, int *s_sum, int *err) {
+__device__ __forceinline__ void scan_steps(const AttnArgs &a, const AttnWork &w, int *s_len, int *s_prefix, int *s_sum, int *err) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.n_seq;
     const int per = (n + THREADS - 1) / THREADS;
     int sum = 0;
     for (int i = tid * per; i < (tid + 1) * per && i < n; ++i) {
         const int len = seq_len(a.lens, i, a.max_len, err);
         s_len[i] = len;
-        sum += (len + 15) >> 4;
+        sum += seq_steps(a, w, len);
     }
     int inc = sum;
 #pragma unroll
@@ -224,7 +235,7 @@ __device__ __forceinline__ void scan_steps(const AttnArgs &a, int *s_len, int *s
     int at = base + inc - sum;
     for (int i = tid * per; i < (tid + 1) * per && i < n; ++i) {
         s_prefix[i] = at;
-        at += (s_len[i] + 15) >> 4;
+        at += seq_steps(a, w, s_len[i]);
     }
     if (tid == THREADS - 1) s_prefix[n] = at;
     __syncthreads();
@@ -236,8 +247,9 @@ __device__ __forceinline__ int steps_per_block(int total, int ctas, int warps) {
     return chunk < warps ? warps : chunk;
 }
 
-// Place of a global step: its sequence, segment there, step of that and steps of the segment.
-struct Place { int b, seg, i, n; };
+// Place of a global step: its sequence, segment there, step of that (page of
+// the sequence and step inside it) and steps of the segment.
+struct Place { int b, seg, i, n, page, sub; };
 __device__ __forceinline__ Place locate(int step, const int *s_prefix, int n, const AttnWork &w) {
     Place p;
     const int x = quotient(step, w.tiles_div);
@@ -252,29 +264,38 @@ __device__ __forceinline__ Place locate(int step, const int *s_prefix, int n, co
     const int rem = step - s_prefix[lo] * w.tiles;
     p.seg = rem / p.n;
     p.i = rem - p.seg * p.n;
+    p.page = quotient(p.i, w.page_steps_div);
+    p.sub = p.i - p.page * w.page_steps;
     return p;
 }
 
 template <int TYPE, int DP_, int NT_>
 __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
-    attn_stream_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnWork w) {
+    attn_stream_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnWork w,
+                       const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using C = AttnCfg<TYPE, DP_, NT_>;
     constexpr int DP = C::DP, NT = C::NT, W = C::W, NS = C::NS, NI = C::NI, E = C::E, NQ = C::NQ, rows = C::rows;
-    extern __shared__ __align__(128) char smem[];
-    float2 *s_ml = reinterpret_cast<float2 *>(smem + W * C::ring);            // [W][2][rows]
-    uint32_t *s_mask = reinterpret_cast<uint32_t *>(s_ml + W * 2 * rows);     // [W][NS]
-    int2 *s_piece = reinterpret_cast<int2 *>(s_mask + W * NS);                // [W][2]: {segment or -1, 1: ended | 2: in head_o}
-    int *s_prefix = reinterpret_cast<int *>(s_piece + W * 2);                 // [n + 1]
+    constexpr int kMissing = 32;                      // flag of a step whose page is not in the pool
+    extern __shared__ char smem_raw[];
+    char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    uint64_t *s_bar = reinterpret_cast<uint64_t *>(smem + W * C::ring);       // [W][NS]
+    float2 *s_ml = reinterpret_cast<float2 *>(s_bar + W * NS);                // [W][2][rows]
+    int2 *s_piece = reinterpret_cast<int2 *>(s_ml + W * 2 * rows);            // [W][2]: {segment or -1, 1: ended | 2: in head_o}
+    int *s_state = reinterpret_cast<int *>(s_piece + W * 2);                  // [W][NS]: slots of the step, kMissing
+    int *s_prefix = s_state + W * NS;                                         // [n + 1]
     int *s_len = s_prefix + a.n_seq + 1;                                      // [n]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int n = a.n_seq, D = a.c.dim;
     const int tiles = w.tiles;
+    if (tid < W * NS) mbar_init(&s_bar[tid], 1);
+    if (tid < W * 2) s_piece[tid] = make_int2(-1, 0);
+    mbar_fence_init();
 
     // dependents may start once the lengths are final: the second kernel reads them before its own wait
     griddep_wait();
     griddep_launch_dependents();
 
-    scan_steps<C::threads>(a, s_len, s_prefix, reinterpret_cast<int *>(smem), blockIdx.x == 0 ? a.err : nullptr);
+    scan_steps<C::threads>(a, w, s_len, s_prefix, s_state, blockIdx.x == 0 ? a.err : nullptr);
     int c0, c1;
     if (w.whole) {
         const int b = quotient(blockIdx.x, w.tiles_div), steps = s_prefix[b + 1] - s_prefix[b];
@@ -287,9 +308,11 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
     }
 
     // sequences without a slot have no steps: their rows are empty
+#pragma unroll 1
     for (int b = blockIdx.x; b < n; b += gridDim.x) {
         if (s_len[b] != 0) continue;
         const int quads = D / 4, count = a.S * a.n_q_heads;
+#pragma unroll 1
         for (int i = tid; i < count * quads; i += C::threads)
             store_out4(a, ((size_t)b * count) * D + 4 * (size_t)i, make_float4(0.f, 0.f, 0.f, 0.f), 1.f);
         if (a.lse)
@@ -301,11 +324,11 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
     const int w1 = c0 + (int)((long long)(c1 - c0) * (warp + 1) / W);
     char *ring = smem + warp * C::ring;
     const uint32_t ring_a = smem_addr(ring);
-    if (lane < 2) s_piece[2 * warp + lane] = make_int2(-1, 0);
 
     auto advance = [&](Place &p) {
+        if (++p.sub == w.page_steps) p.sub = 0, ++p.page;
         if (++p.i < p.n) return;
-        p.i = 0;
+        p.i = p.page = p.sub = 0;
         if (++p.seg < tiles) return;
         p.seg = 0;
         do ++p.b;
@@ -313,78 +336,45 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
         p.n = p.b < n ? s_prefix[p.b + 1] - s_prefix[p.b] : 1;
     };
 
-    // ---- loads ----
-    // `simple`: the 16 slots of a step lie in one page and rows fill the padded size
-    const bool simple = D == DP && a.c.page % 16 == 0;
+    // ---- loads: the page of the next step is looked up one step early ----
+    // K and V are read once per row tile: marked first to leave L2 where there is but one
+    uint64_t policy;
+    if (w.row_tiles == 1) asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    else asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
     Place ip = locate(w0 < w1 ? w0 : c0, s_prefix, n, w), p = ip;
-    int ip_kh = quotient(ip.seg, w.row_tiles_div);
-    int issued = w0, istage = 0;
-    // the page of the next step to load is looked up one step early: of its
-    // first slot where the step is simple, else of slot `lane` by lanes 0-15
-    int look_page = 0, look_off = 0;
+    int issued = w0, istage = 0, look_page = 0;
     auto look = [&]() {
-        if (issued >= w1) return;
-        const int t = 16 * ip.i + (simple ? 0 : lane);
-        if (simple || (lane < 16 && t < s_len[ip.b])) {
-            int index;
-            split_slot(a.c, t, &index, &look_off);
-            look_page = __ldg(a.table + (size_t)ip.b * a.table_stride + index);
-        }
+        if (issued < w1) look_page = __ldg(a.table + (size_t)ip.b * a.table_stride + ip.page);
     };
-    // copy n of a step moves chunk lane % NC of row n * RPL + lane / NC
-    const int l_row = lane / C::NC, l_chunk = lane % C::NC;
-    const long long l_off = l_row * a.c.token_b + 16 * l_chunk, copy_b = C::RPL * a.c.token_b;
-    const bool in_row = 16 * l_chunk < D * C::ESZ;
     auto issue = [&]() {
         if (issued < w1) {
-            const uint32_t dst = ring_a + istage * C::stage;
-            const int t0 = 16 * ip.i, len = s_len[ip.b];
-            if (simple && t0 + 16 <= len && (unsigned)look_page < (unsigned)a.c.n_pages) {
-                if (lane == 0) s_mask[warp * NS + istage] = 0xFFFFu;
-                const long long base =
-                    look_page * a.c.page_b + ip_kh * a.c.head_b + look_off * a.c.token_b + l_off;
-                const char *k = a.c.k + base, *v = a.c.v + base;
-                if (copy_b == 512) {
-                    unrolled<C::NL>([&](auto n) {
-                        cp_async16_at<512 * n>(dst + 16 * k_place<C>(n * C::RPL + l_row, l_chunk), k);
-                    });
-                    unrolled<C::NL>([&](auto n) {
-                        cp_async16_at<512 * n>(dst + C::k_bytes + 16 * v_place<C>(n * C::RPL + l_row, l_chunk), v);
-                    });
+            if (lane == 0) {
+                const int slot = 16 * ip.sub, left = s_len[ip.b] - ip.page * a.c.page;
+                int count = (left < a.c.page ? left : a.c.page) - slot;
+                if (count > 16) count = 16;
+                uint64_t *bar = &s_bar[warp * NS + istage];
+                const uint32_t dst = ring_a + istage * C::stage;
+                const int kh = quotient(ip.seg, w.row_tiles_div);
+                const bool there = (unsigned)look_page < (unsigned)a.c.n_pages;
+                s_state[warp * NS + istage] = there ? count : count | kMissing;   // published by the arrival
+                if (there) {
+                    mbar_arrive_expect_tx(bar, 2 * C::NB * C::BB * w.box_rows);
+#pragma unroll
+                    for (int x = 0; x < C::NB; ++x)
+                        tma_load_4d(dst + x * C::box, &k_map, x * (C::BB / C::ESZ), slot, kh, look_page, bar, policy);
+#pragma unroll
+                    for (int x = 0; x < C::NB; ++x)
+                        tma_load_4d(dst + (C::NB + x) * C::box, &v_map, x * (C::BB / C::ESZ), slot, kh, look_page, bar,
+                                    policy);
                 } else {
-#pragma unroll
-                    for (int n = 0; n < C::NL; ++n) {
-                        cp_async16_at<0>(dst + 16 * k_place<C>(n * C::RPL + l_row, l_chunk), k);
-                        cp_async16_at<0>(dst + C::k_bytes + 16 * v_place<C>(n * C::RPL + l_row, l_chunk), v);
-                        k += copy_b, v += copy_b;
-                    }
-                }
-            } else {
-                const bool in = lane < 16 && t0 + lane < len;
-                const bool ok = in && (unsigned)look_page < (unsigned)a.c.n_pages;
-                const uint32_t good = __ballot_sync(~0u, ok), bad = __ballot_sync(~0u, in && !ok);
-                if (lane == 0) {
-                    s_mask[warp * NS + istage] = good | bad << 16;
-                    if (bad) raise_device_error(a.err, kErrPage);
-                }
-                const long long off = ok ? look_page * a.c.page_b + ip_kh * a.c.head_b +
-                                               (look_off + (simple ? lane : 0)) * a.c.token_b
-                                         : 0;
-#pragma unroll
-                for (int n = 0; n < C::NL; ++n) {
-                    const int row = n * C::RPL + l_row;
-                    const long long at = __shfl_sync(~0u, off, row) + (in_row ? 16 * l_chunk : 0);
-                    const bool take = in_row && (good >> row & 1u);
-                    cp_async16(dst + 16 * k_place<C>(row, l_chunk), a.c.k + at, take);
-                    cp_async16(dst + C::k_bytes + 16 * v_place<C>(row, l_chunk), a.c.v + at, take);
+                    raise_device_error(a.err, kErrPage);
+                    mbar_arrive(bar);
                 }
             }
             ++issued;
             advance(ip);
-            if (ip.i == 0) ip_kh = quotient(ip.seg, w.row_tiles_div);
             look();
         }
-        cp_async_commit();
         if (++istage == NS) istage = 0;
     };
     look();
@@ -402,8 +392,9 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
     const bool third = TYPE == kBf16 && a.o_type == kF32;
     int hidden_from = 0;                              // first slot that some row does not see
     bool fresh = true;                                // at the start of a piece
-    int stage = 0;
     bool began_here = false;
+    int stage = 0;
+    uint32_t phase = 0;
 
 #pragma unroll 1
     for (int step = w0; step < w1; ++step) {
@@ -421,7 +412,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                 if constexpr (TYPE != kE4m3) {
 #pragma unroll
                     for (int i = 0; i < NI; ++i) {
-                        const int d = (4 * i + c) * 8;
+                        const int d = k_chunk<C>(i, c) * 8;
                         uint4 v = make_uint4(0, 0, 0, 0);
                         if (r.real && d < D) v = *reinterpret_cast<const uint4 *>(q + d);
                         qf[nt][i][0] = v.x, qf[nt][i][1] = v.y, qf[nt][i][2] = v.z, qf[nt][i][3] = v.w;
@@ -430,7 +421,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                     float top = 0.f;
 #pragma unroll
                     for (int i = 0; i < NI; ++i) {
-                        const int d = (4 * i + c) * 16;
+                        const int d = k_chunk<C>(i, c) * 16;
                         uint4 v[2] = {};
                         if (r.real && d < D)
                             v[0] = *reinterpret_cast<const uint4 *>(q + d),
@@ -475,10 +466,17 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
             }
         }
 
-        cp_async_wait<NS - 1>();
-        __syncwarp();
-        const uint32_t mask = s_mask[warp * NS + stage];
-        const uint32_t src = ring_a + stage * C::stage;
+        if (!__all_sync(~0u, mbar_wait(&s_bar[warp * NS + stage], phase))) {
+            // a copy did not land in time: no result, but let those in flight land before the block ends
+            if (lane == 0) raise_device_error(a.err, kErrTimeout);
+            for (int x = step; x < issued; ++x) {
+                mbar_wait(&s_bar[warp * NS + stage], phase);
+                if (++stage == NS) stage = 0, phase ^= 1u;
+            }
+            break;
+        }
+        const int state = s_state[warp * NS + stage], count = state & 31;
+        const uint32_t src = ring_a + stage * C::stage, src_v = src + C::NB * C::box;
 
         // ---- S^T = K Q^T, in two chains ----
         float s[NT][4], s1[NT][4];
@@ -488,8 +486,9 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
             for (int e = 0; e < 4; ++e) s[nt][e] = s1[nt][e] = 0.f;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            // slots g and g + 8, chunk c + 4 i
-            const uint4 x = lds128(src + 16 * k_place<C>(g, 4 * i + c)), y = lds128(src + 16 * k_place<C>(g + 8, 4 * i + c));
+            // slots g and g + 8
+            const uint4 x = lds128(src + chunk_place<C>(g, k_chunk<C>(i, c)));
+            const uint4 y = lds128(src + chunk_place<C>(g + 8, k_chunk<C>(i, c)));
             const uint32_t kx[4] = {x.x, x.y, x.z, x.w}, ky[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int u = 0; u < C::KE / 4; ++u) {
@@ -507,13 +506,13 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
         }
 
         // ---- exponents against the rows' references; thread: slots g, g + 8 by rows 2c, 2c + 1 ----
-        const int t0 = 16 * p.i;
-        const bool partial = mask != 0xFFFFu || (a.S > 1 && t0 + 16 > hidden_from);
-        // slots past the end are past every limit; NaN where the slot's page is not in the pool
+        const int t0 = p.page * a.c.page + 16 * p.sub;
+        const bool partial = state != 16 || (a.S > 1 && t0 + 16 > hidden_from);
+        // no weight for slots that the step has not, or that the row does not see; NaN for a missing page
         auto masked = [&](float z, int nt, int e) {
             const int j = g + 8 * (e >> 1);
-            if (t0 + j >= lim[nt][e & 1]) return -INFINITY;
-            return mask >> (16 + j) & 1u ? NAN : z;
+            if (j >= count || t0 + j >= lim[nt][e & 1]) return -INFINITY;
+            return state & kMissing ? NAN : z;
         };
         uint32_t ph[NT][2], pl[NT][2], pt[NT][2];
 #pragma unroll
@@ -550,8 +549,10 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
             }
             if (a.accumulate) {
                 float *dst = w.scores + ((size_t)(p.b * tiles + p.seg) * w.score_slots + t0) * rows + 8 * nt + 2 * c;
-                *reinterpret_cast<float2 *>(dst + (size_t)g * rows) = make_float2(x[0] + m[nt][0], x[1] + m[nt][1]);
-                *reinterpret_cast<float2 *>(dst + (size_t)(g + 8) * rows) = make_float2(x[2] + m[nt][0], x[3] + m[nt][1]);
+                if (g < count)
+                    *reinterpret_cast<float2 *>(dst + g * rows) = make_float2(x[0] + m[nt][0], x[1] + m[nt][1]);
+                if (g + 8 < count)
+                    *reinterpret_cast<float2 *>(dst + (g + 8) * rows) = make_float2(x[2] + m[nt][0], x[3] + m[nt][1]);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[e] = ex2(x[e]);
@@ -589,12 +590,18 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
             for (int j = 0; j < 4; ++j) {
                 const int row = 2 * c + (j & 1) + 8 * (j >> 1);
                 if (C::VB == 16) {
-                    const uint4 v = lds128(src + C::k_bytes + 16 * v_place<C>(row, 8 * q + g));
+                    const uint4 v = lds128(src_v + chunk_place<C>(row, 8 * q + g));
                     x[j][0] = v.x, x[j][1] = v.y, x[j][2] = v.z, x[j][3] = v.w;
                 } else {
-                    const uint2 v = lds64(src + C::k_bytes + 16 * v_place<C>(row, g >> 1) + 8 * (g & 1));
+                    const uint2 v = lds64(src_v + chunk_place<C>(row, g >> 1) + 8 * (g & 1));
                     x[j][0] = v.x, x[j][1] = v.y, x[j][2] = x[j][3] = 0u;
                 }
+            }
+            if (state != 16) {   // what lies past the step's slots, or where no copy landed
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (state & kMissing || 2 * c + (j & 1) + 8 * (j >> 1) >= count)
+                        x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0u;
             }
         };
         auto v_pair = [&](uint32_t lo, uint32_t hi, int e) -> uint32_t {   // element e of two slots' words
@@ -683,104 +690,105 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                 }
             }
         }
-        __syncwarp();                                 // every lane has read the mask and its chunks
-        issue();
-        if (++stage == NS) stage = 0;
+        __syncwarp();                                 // every lane has read its chunks and the state
 
         // ---- end of a piece ----
-        const bool ended = p.i + 1 == p.n;
-        if (ended || step + 1 == w1) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(~0u, l[nt][e], d);
+        const bool ended = p.i + 1 == p.n, last = step + 1 == w1;
+        if (ended || last) {
+            fresh = true;
             const int kh = quotient(p.seg, w.row_tiles_div), tile = p.seg - kh * w.row_tiles;
             const float vs = TYPE == kE4m3 ? __ldg(a.c.v_scale + kh) : 1.f;
             const bool whole = ended && began_here;
-            // an open piece waits in the ring when the range is done with it, else in the workspace
-            float *keep = step + 1 == w1 ? reinterpret_cast<float *>(ring)
-                                         : w.head_o + ((size_t)blockIdx.x * W + warp) * rows * DP;
-            const int slot = began_here ? 1 : 0;
-            if (step + 1 == w1) {
-                cp_async_wait<0>();
-                __syncwarp();
-            }
-            if (!whole) {
-                if (lane == 0)
-                    s_piece[2 * warp + slot] = make_int2(p.b * tiles + p.seg, (ended ? 1 : 0) | (step + 1 == w1 ? 0 : 2));
-            }
+            const int slot = 2 * warp + (began_here ? 1 : 0);
+            if (!whole && lane == 0) s_piece[slot] = make_int2(p.b * tiles + p.seg, (ended ? 1 : 0) | (last ? 0 : 2));
+            // 8 rows at a time through shared memory: the stage just read, or, with
+            // the range done, the ring, where an open piece stays for the join
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+                float4 *slab = reinterpret_cast<float4 *>(last ? ring + nt * 32 * DP : ring + stage * C::stage);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int r = 8 * nt + 2 * c + e;
-                    const RowRef ref = row_ref(a, w, p.b, kh, tile * rows + r);
-                    if (!ref.real) continue;
-                    const float f = row_factor(l[nt][e], vs);
-                    if (g == 0) {
-                        if (whole) {
-                            if (a.lse) a.lse[ref.head] = row_lse(m[nt][e], l[nt][e]);
-                        } else {
-                            s_ml[(2 * warp + slot) * rows + r] = make_float2(m[nt][e], l[nt][e]);
-                        }
-                    }
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(~0u, l[nt][e], d);
+                    if (g == 0) s_ml[slot * rows + 8 * nt + 2 * c + e] = make_float2(m[nt][e], l[nt][e]);
 #pragma unroll
                     for (int q = 0; q < NQ; ++q)
 #pragma unroll
                         for (int x = 0; x < E; x += 4) {
-                            const int d = (8 * q + g) * E + x;
                             auto at = [&](int y) {
                                 return y < E / 2 ? o[q * (E / 2) + y][nt][e] : o[q * (E / 2) + y - E / 2][nt][2 + e];
                             };
-                            const float4 v = make_float4(at(x), at(x + 1), at(x + 2), at(x + 3));
-                            if (!whole) *reinterpret_cast<float4 *>(keep + r * DP + d) = v;
-                            else if (d < D) store_out4(a, ref.head * D + d, v, f);
+                            slab[slab_place<C>(2 * c + e, ((8 * q + g) * E + x) / 4)] =
+                                make_float4(at(x), at(x + 1), at(x + 2), at(x + 3));
                         }
                 }
-            fresh = true;
+                __syncwarp();
+                if (whole) {
+#pragma unroll 1
+                    for (int i = lane; i < 8 * (DP / 4); i += 32) {
+                        const int r = i / (DP / 4), d = 4 * (i - r * (DP / 4));
+                        const RowRef ref = row_ref(a, w, p.b, kh, tile * rows + 8 * nt + r);
+                        const float2 ml = s_ml[slot * rows + 8 * nt + r];
+                        if (!ref.real) continue;
+                        if (d < D) store_out4(a, ref.head * D + d, slab[slab_place<C>(r, d / 4)], row_factor(ml.y, vs));
+                        if (d == 0 && a.lse) a.lse[ref.head] = row_lse(ml.x, ml.y);
+                    }
+                } else if (!last) {
+                    float4 *keep = reinterpret_cast<float4 *>(w.head_o) +
+                                   (((size_t)blockIdx.x * W + warp) * NT + nt) * 2 * DP;
+#pragma unroll 1
+                    for (int i = lane; i < 2 * DP; i += 32) keep[i] = slab[i];
+                }
+                __syncwarp();
+            }
+            // the stage is written next by a copy, another proxy
+            if (!last) {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+            }
         }
+        issue();
         advance(p);
+        if (++stage == NS) stage = 0, phase ^= 1u;
     }
 
     // ---- join the block's open pieces, in order: a segment has at most one per warp ----
     __syncthreads();
-    const int2 piece = lane < 2 * W ? s_piece[lane] : make_int2(-1, 0);
+    const int2 piece = lane < 2 * W ? s_piece[lane] : make_int2(-1, 0);   // 2 W <= 32
     const uint32_t before = __ballot_sync(~0u, piece.x >= 0) & ((1u << lane) - 1u);
+    static_assert(2 * W <= 32, "a lane per piece");
     const int prior = __shfl_sync(~0u, piece.x, before ? 31 - __clz(before) : lane);
     uint32_t leaders = __ballot_sync(~0u, piece.x >= 0 && (before == 0u || prior != piece.x));
     const uint32_t in_work = __ballot_sync(~0u, piece.y & 2);
     for (; leaders; leaders &= leaders - 1u) {
         const int first = __ffs(leaders) - 1, seg = __shfl_sync(~0u, piece.x, first);
         const uint32_t members = __ballot_sync(~0u, piece.x == seg);
-        const bool starts = first & 1, ends = __shfl_sync(~0u, piece.y, 31 - __clz(members)) & 1, whole = starts && ends;
+        const bool starts = first & 1, ends = __shfl_sync(~0u, piece.y, 31 - __clz(members)) & 1;
+        const bool whole = starts && ends;
         const int b = quotient(seg, w.tiles_div), sg = seg - b * tiles;
         const int kh = quotient(sg, w.row_tiles_div), tile = sg - kh * w.row_tiles;
         const float vs = TYPE == kE4m3 ? __ldg(a.c.v_scale + kh) : 1.f;
         const size_t out = ((size_t)blockIdx.x * 2 + (starts ? 1 : 0)) * rows;
+#pragma unroll 1
         for (int i = tid; i < rows * (DP / 4); i += C::threads) {
             const int r = i / (DP / 4), d = 4 * (i - r * (DP / 4));
             const RowRef ref = row_ref(a, w, b, kh, tile * rows + r);
             if (!ref.real) continue;
-            float2 ml[W];
             float mm = kNoRef, ll = 0.f;
-#pragma unroll
-            for (int x = 0; x < W; ++x) {
-                const uint32_t has = members >> (2 * x) & 3u;
-                ml[x] = has ? s_ml[(2 * x + (has >> 1)) * rows + r] : make_float2(kNoRef, 0.f);
-                mm = fmaxf(mm, ml[x].x);
-            }
+#pragma unroll 1
+            for (uint32_t y = members; y; y &= y - 1u) mm = fmaxf(mm, s_ml[(__ffs(y) - 1) * rows + r].x);
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int x = 0; x < W; ++x) {
-                if (!(members >> (2 * x) & 3u)) continue;
-                const float f = ex2(ml[x].x - mm);
-                ll += ml[x].y * f;
-                const float *src = in_work & members & 3u << (2 * x)
-                                       ? w.head_o + ((size_t)blockIdx.x * W + x) * rows * DP
-                                       : reinterpret_cast<const float *>(smem + x * C::ring);
-                const float4 v = *reinterpret_cast<const float4 *>(src + r * DP + d);
+#pragma unroll 1
+            for (uint32_t y = members; y; y &= y - 1u) {
+                const int x = __ffs(y) - 1;
+                const float2 ml = s_ml[x * rows + r];
+                const float f = ex2(ml.x - mm);
+                ll += ml.y * f;
+                const float4 *src = in_work >> x & 1u
+                                        ? reinterpret_cast<const float4 *>(w.head_o) +
+                                              ((size_t)blockIdx.x * W + (x >> 1)) * rows * (DP / 4)
+                                        : reinterpret_cast<const float4 *>(smem + (x >> 1) * C::ring);
+                const float4 v = src[(r >> 3) * 2 * DP + slab_place<C>(r & 7, d / 4)];
                 sum.x += v.x * f, sum.y += v.y * f, sum.z += v.z * f, sum.w += v.w * f;
             }
             if (whole) {

@@ -2,6 +2,7 @@
 #include "attn_launch.cuh"
 
 namespace qg {
-template int launch_attn_stream<kBf16>(const AttnArgs &, const AttnWork &, const AttnPlan &, cudaStream_t);
+template int launch_attn_stream<kBf16>(const AttnArgs &, const AttnWork &, const AttnPlan &, const CUtensorMap (&)[2],
+                                cudaStream_t);
 template AttnPlan attn_plan<kBf16>(int rows, int dim);
 }
