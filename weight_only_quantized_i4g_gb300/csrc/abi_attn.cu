@@ -81,6 +81,7 @@ int check_max_len(const char *fn, int max_len, int stride, int page) {
     if (max_len < 0 || max_len > (long long)stride * page)
         QG_REFUSE(kEInval, "%s: max_len = %d must be in 0..%lld (the table's pages)", fn, max_len,
                   (long long)stride * page);
+    if (max_len > (1 << 30)) QG_REFUSE(kEInval, "%s: max_len = %d, must be <= 2^30", fn, max_len);
     return kOk;
 }
 
@@ -230,7 +231,7 @@ int qg_kv_evict(const qg_kv_cache *cache, const int *table, int table_stride, co
     if (sinks < 0 || recent < 0 || (long long)sinks + recent > budget)
         QG_REFUSE(kEInval, "%s: sinks = %d and recent = %d must be >= 0 and together at most budget = %d", fn, sinks,
                   recent, budget);
-    if ((double)n_seq * a.c.n_heads > (double)INT_MAX / 2) QG_REFUSE(kEInval, "%s: sizes overflow", fn);
+    if ((double)n_seq * a.c.n_heads > (double)INT_MAX / 16) QG_REFUSE(kEInval, "%s: sizes overflow", fn);
     if (n_seq == 0) return kOk;
     if ((rc = check_table(fn, "table", table, table_stride))) return rc;
     if ((rc = check_table(fn, "dst_table", dst_table, dst_stride))) return rc;

@@ -87,7 +87,7 @@ struct AttnCfg {
     static constexpr int box = 16 * BB;
     static constexpr int stage = 2 * NB * box;        // 16 slots of K, then of V
     // as many warps as the registers of O, Q and S allow (16, 12 or 8 an SM)
-    static constexpr int regs = 70 + 4 * MT * NT + NT * NI * (ESZ == 1 ? 8 : 4) + 8 * NT;
+    static constexpr int regs = (ESZ == 1 ? 85 : 70) + 4 * MT * NT + NT * NI * (ESZ == 1 ? 8 : 4) + 8 * NT;
     static constexpr int W0 = regs <= 128 ? 16 : regs <= 168 ? 12 : 8;
     static constexpr int W = stage > 8192 ? 4 : W0;
     // up to 192 KB of copies in flight

@@ -117,23 +117,32 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t w) {
 }
 
 // Launch with programmatic stream serialization: the kernel may start while
-// its predecessor runs, and waits for it with griddep_wait().
+// its predecessor runs, and waits for it with griddep_wait().  `cluster`
+// consecutive blocks of x form a thread-block cluster.
 template <class... P, class... A>
-inline int launch_pdl(const char *what, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                      A... args) {
+inline int launch_clusters(const char *what, void (*kernel)(P...), dim3 grid, dim3 block, int cluster, size_t smem,
+                           cudaStream_t st, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
     count_launch();
     return check_launch(what);
+}
+template <class... P, class... A>
+inline int launch_pdl(const char *what, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                      A... args) {
+    return launch_clusters(what, kernel, grid, block, 1, smem, st, args...);
 }
 
 // Arguments of the attention over the cache (qattn_paged).

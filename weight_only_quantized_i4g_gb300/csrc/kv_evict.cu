@@ -7,14 +7,20 @@
 // order; a move kernel copies K, V and weight of the kept slots to the new
 // pages.  Selection reads 4 bytes a slot; the copies, 4 D bytes a kept slot
 // and 16-bit element each way, are the bulk and bound by HBM.
+#include <cooperative_groups.h>
+
 #include "kv_cache.cuh"
 
 namespace qg {
 
+namespace cg = cooperative_groups;
+
 namespace {
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
 
 // Order of weights: every NaN above +inf, -0 equal to +0; larger key = larger weight.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -23,147 +29,228 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictArgs a) {
-    __shared__ int s_hist[2048];
-    __shared__ int s_gt[kSelWarps], s_eq[kSelWarps];
+// A cluster per sequence and head; its blocks share the slots in equal
+// stretches and keep their keys in shared memory (`cap` of them; a longer
+// stretch reads the rest again).  Three digits (11, 11, 10 bits) of the key of
+// the last slot to keep are found from the top: each block counts its keys'
+// digits, each rank adds up one slice of the bins over the blocks and hands
+// the sums to all, and every block finds the same bin.  One block per head
+// took 315 us for three sequences of 100k slots, 8 heads, two thirds of it
+// here; the clusters spread that over the SMs.
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictArgs a, int cap) {
+    extern __shared__ uint32_t s_key[];
+    __shared__ int s_hist[kBins], s_total[kBins];
+    __shared__ int s_warp[2][kSelWarps];
+    __shared__ int2 s_block[kMaxCluster];
     __shared__ int s_digit, s_need;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     griddep_launch_dependents();
     griddep_wait();
-    const int h = blockIdx.x % a.c.n_heads, b = blockIdx.x / a.c.n_heads;
+    const int bh = blockIdx.x / ranks, b = bh / a.c.n_heads, h = bh - b * a.c.n_heads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int L = seq_len(a.lens, b, a.max_len, tid == 0 ? a.err : nullptr);
+    const int L = seq_len(a.lens, b, a.max_len, tid == 0 && rank == 0 ? a.err : nullptr);
     const int N = L < a.budget ? L : a.budget;
-    int *kept = a.kept + (size_t)blockIdx.x * a.budget;
-    if (h == 0 && tid == 0) a.new_lens[b] = N;
-    for (int i = N + tid; i < a.budget; i += kSelThreads) kept[i] = -1;
-    if (L <= a.budget) {
-        for (int i = tid; i < N; i += kSelThreads) kept[i] = i;
+    int *kept = a.kept + (size_t)bh * a.budget;
+    const int first = rank * kSelThreads + tid, step = ranks * kSelThreads;
+    if (h == 0 && first == 0) a.new_lens[b] = N;
+    for (int i = N + first; i < a.budget; i += step) kept[i] = -1;
+    if (L <= a.budget) {                           // the same for every block of the cluster
+        for (int i = first; i < N; i += step) kept[i] = i;
         return;
     }
     // sinks + recent <= budget < L: the protected ends do not meet
     const int *row = a.table + (size_t)b * a.table_stride;
     const int lo = a.sinks, hi = L - a.recent;
     int need = N - a.sinks - a.recent;             // to take from [lo, hi)
-    auto key_at = [&](int t) -> uint32_t {
+    const bool any = need > 0;
+    // this block's stretch, and each warp's in it
+    const int per_warp = ((L + ranks * kSelWarps - 1) / (ranks * kSelWarps) + 31) & ~31, per = per_warp * kSelWarps;
+    const int r0 = rank * per < L ? rank * per : L, r1 = r0 + per < L ? r0 + per : L;
+    auto key_in_cache = [&](int t) -> uint32_t {
         const SlotRef r = find_slot(a.c, row, t);
         return r.page < 0 ? 0u : weight_key(__ldg(a.c.weight + slot_weight(a.c, r, h)));
     };
-    // radix select: the key of the need-th largest weight, digit by digit (11, 11, 10 bits)
+    auto key_at = [&](int t) { return t - r0 < cap ? s_key[t - r0] : key_in_cache(t); };
+    const int in_smem = r1 - r0 < cap ? r1 - r0 : cap;
+    if (any) {
+#pragma unroll 4
+        for (int i = tid; i < in_smem; i += kSelThreads) s_key[i] = key_in_cache(r0 + i);
+    }
+    __syncthreads();
+
     uint32_t prefix = 0;
-    if (need > 0) {
+    if (any) {
         for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-            const int bins = pass == 2 ? 1024 : 2048;
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
+            const int done = pass == 0 ? 32 : pass == 1 ? 21 : 10;            // low bits not yet fixed
             for (int i = tid; i < bins; i += kSelThreads) s_hist[i] = 0;
             __syncthreads();
-            const uint32_t above = pass == 0 ? 0u : prefix >> (pass == 1 ? 21 : 10);
-            for (int t = lo + tid; t < hi; t += kSelThreads) {
-                const uint32_t k = key_at(t);
-                if (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == above)
-                    atomicAdd(&s_hist[(k >> shift) & (bins - 1)], 1);
+            // equal digits of a warp are counted by one of its lanes: weights crowd into few bins
+            for (int t0 = r0 + 32 * warp; t0 < r1; t0 += kSelThreads) {
+                const int t = t0 + lane;
+                const uint32_t k = t < r1 ? key_at(t) : 0u;
+                const bool on = t < r1 && t >= lo && t < hi && (pass == 0 || k >> done == prefix >> done);
+                const unsigned all = __ballot_sync(~0u, on);
+                if (!on) continue;
+                const int bin = (k >> shift) & (bins - 1);
+                const unsigned same = __match_any_sync(all, bin);
+                if (lane == __ffs(same) - 1) atomicAdd(&s_hist[bin], __popc(same));
             }
+            int *total = s_hist;
+            if (ranks > 1) {
+                total = s_total;
+                cluster.sync();
+                const int slice = bins / ranks;
+                for (int i = tid; i < slice; i += kSelThreads) {
+                    const int bin = rank * slice + i;
+                    int sum = 0;
+                    for (int x = 0; x < ranks; ++x) sum += cluster.map_shared_rank(s_hist, x)[bin];
+                    for (int x = 0; x < ranks; ++x) cluster.map_shared_rank(s_total, x)[bin] = sum;
+                }
+                cluster.sync();
+            } else {
+                __syncthreads();
+            }
+            // from the top bin down: where the count reaches `need`
+            const int each = bins / kSelThreads;
+            int mine[kBins / kSelThreads], sum = 0;
+#pragma unroll
+            for (int i = 0; i < kBins / kSelThreads; ++i) {
+                mine[i] = i < each ? total[bins - 1 - (tid * each + i)] : 0;
+                sum += mine[i];
+            }
+            int inc = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(~0u, inc, o);
+                if (lane >= o) inc += v;
+            }
+            if (lane == 31) s_warp[0][warp] = inc;
             __syncthreads();
-            if (warp == 0) {   // from the top bin down: where the count passes `need`
-                int left = need;
-                for (int top = bins; top > 0; top -= 32) {
-                    const int bin = top - 1 - lane, c = s_hist[bin];
-                    int sum = c;
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const int v = __shfl_up_sync(~0u, sum, o);
-                        if (lane >= o) sum += v;
-                    }
-                    const unsigned hit = __ballot_sync(~0u, sum >= left);
-                    if (hit) {
-                        const int first = __ffs(hit) - 1;
-                        if (lane == first) s_digit = bin, s_need = left - (sum - c);
-                        break;
-                    }
-                    left -= __shfl_sync(~0u, sum, 31);
+            int before = inc - sum;
+#pragma unroll
+            for (int x = 0; x < kSelWarps; ++x)
+                if (x < warp) before += s_warp[0][x];
+            if (before < need && need <= before + sum) {
+#pragma unroll
+                for (int i = 0; i < kBins / kSelThreads; ++i) {
+                    if (before < need && need <= before + mine[i]) s_digit = bins - 1 - (tid * each + i), s_need = need - before;
+                    before += mine[i];
                 }
             }
             __syncthreads();
             prefix |= (uint32_t)s_digit << shift;
-            need = s_need;                        // slots of this digit still to take
+            need = s_need;                         // slots of this digit still to take
             __syncthreads();
         }
     }
-    // Emit in slot order.  Every warp takes one stretch of slots: it counts
-    // (protected or above the threshold) and (equal to it), the counts are
-    // summed over the warps before it, then it writes.
-    const bool any = N > a.sinks + a.recent;
-    const int per = ((L + kSelWarps - 1) / kSelWarps + 31) & ~31;
-    const int t0 = warp * per, t1 = t0 + per < L ? t0 + per : L;
-    int gt = 0, eq = 0;
-    for (int pass = 0; pass < 2; ++pass) {
-        int base_gt = 0, base_eq = 0;
-        if (pass) {
-            for (int w = 0; w < warp; ++w) base_gt += s_gt[w], base_eq += s_eq[w];
-        }
-        for (int t = t0 + lane; t - lane < t1; t += 32) {
-            const bool safe = t < t1 && (t < lo || t >= hi);
-            const uint32_t k = t < t1 && !safe && any ? key_at(t) : 0u;
-            const bool mid = t < t1 && !safe && any;
-            const unsigned g = __ballot_sync(~0u, safe || (mid && k > prefix));
-            const unsigned e = __ballot_sync(~0u, mid && k == prefix);
-            if (!pass) {
-                gt += __popc(g), eq += __popc(e);
-            } else {
-                const unsigned below = (1u << lane) - 1u;
-                const int rank_e = base_eq + __popc(e & below);     // equal ones before this slot
-                const int taken = rank_e < need ? rank_e : need;
-                const bool take = (g >> lane & 1u) || ((e >> lane & 1u) && rank_e < need);
-                if (take) kept[base_gt + __popc(g & below) + taken] = t;
-                base_gt += __popc(g), base_eq += __popc(e);
-            }
-        }
-        if (!pass) {
-            if (lane == 0) s_gt[warp] = gt, s_eq[warp] = eq;
-            __syncthreads();
-        }
+    // Emit in slot order: every warp counts its stretch (kept for sure, and
+    // equal to the threshold), the counts before it are summed, then it writes.
+    const int t0 = r0 + warp * per_warp, t1 = t0 + per_warp < r1 ? t0 + per_warp : r1;
+    auto flags = [&](int t, unsigned *sure, unsigned *tie) {
+        const bool in = t < t1, safe = in && (t < lo || t >= hi);
+        const uint32_t k = in && !safe && any ? key_at(t) : 0u;
+        *sure = __ballot_sync(~0u, safe || (in && any && k > prefix));
+        *tie = __ballot_sync(~0u, in && !safe && any && k == prefix);
+    };
+    int sure_n = 0, tie_n = 0;
+    for (int t = t0 + lane; t - lane < t1; t += 32) {
+        unsigned sure, tie;
+        flags(t, &sure, &tie);
+        sure_n += __popc(sure), tie_n += __popc(tie);
+    }
+    if (lane == 0) s_warp[0][warp] = sure_n, s_warp[1][warp] = tie_n;
+    __syncthreads();
+    int base_sure = 0, base_tie = 0, all_sure = 0, all_tie = 0;
+#pragma unroll
+    for (int x = 0; x < kSelWarps; ++x) {
+        const int s = s_warp[0][x], e = s_warp[1][x];
+        if (x < warp) base_sure += s, base_tie += e;
+        all_sure += s, all_tie += e;
+    }
+    if (ranks > 1) {
+        if (tid < ranks) cluster.map_shared_rank(s_block, tid)[rank] = make_int2(all_sure, all_tie);
+        cluster.sync();                            // also the last access to another block's memory
+        for (int x = 0; x < rank; ++x) base_sure += s_block[x].x, base_tie += s_block[x].y;
+    }
+    for (int t = t0 + lane; t - lane < t1; t += 32) {
+        unsigned sure, tie;
+        flags(t, &sure, &tie);
+        const unsigned below = (1u << lane) - 1u;
+        const int rank_tie = base_tie + __popc(tie & below);                // equal ones before this slot
+        const bool take = (sure >> lane & 1u) || ((tie >> lane & 1u) && rank_tie < need);
+        if (take) kept[base_sure + __popc(sure & below) + (rank_tie < need ? rank_tie : need)] = t;
+        base_sure += __popc(sure), base_tie += __popc(tie);
     }
 }
 
-// Copies kept slots: `lanes` threads a slot and side (K or V), 16 bytes a thread and step.
-constexpr int kMoveThreads = 256;
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a, int row_b,
-                                                                  int slots_per_block) {
+// Copies kept slots, 64 a block: their places are looked up once, then every
+// thread has eight 16-byte loads in flight before its stores.
+constexpr int kMoveThreads = 256, kMoveSlots = 64, kMoveAhead = 4;
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a, FastDiv chunks) {
+    __shared__ long long s_src[kMoveSlots], s_dst[kMoveSlots];
     griddep_launch_dependents();
     griddep_wait();
-    const int bh = blockIdx.x, h = bh % a.c.n_heads, b = bh / a.c.n_heads;
+    const int bh = blockIdx.x, b = bh / a.c.n_heads, h = bh - b * a.c.n_heads, tid = threadIdx.x;
     const int n = __ldg(a.new_lens + b);
-    const int i0 = blockIdx.y * slots_per_block;
-    const int i1 = i0 + slots_per_block < n ? i0 + slots_per_block : n;
-    const int *src_row = a.table + (size_t)b * a.table_stride;
-    const int *dst_row = a.dst_table + (size_t)b * a.dst_stride;
-    const int *kept = a.kept + (size_t)bh * a.budget;
-    const int chunks = row_b / 16;
-    for (int w = threadIdx.x; w < (i1 - i0) * chunks; w += kMoveThreads) {
-        const int i = i0 + w / chunks, c = w % chunks;
-        const SlotRef s = find_slot(a.c, src_row, __ldg(kept + i)), d = find_slot(a.c, dst_row, i);
-        if (s.page < 0 || d.page < 0) {
-            if (c == 0) raise_device_error(a.err, kErrPage);
-            continue;
+    for (long long i0 = (long long)blockIdx.y * kMoveSlots; i0 < n; i0 += (long long)gridDim.y * kMoveSlots) {
+        const int count = n - i0 < kMoveSlots ? (int)(n - i0) : kMoveSlots;
+        __syncthreads();
+        if (tid < count) {
+            const int i = (int)i0 + tid;
+            const SlotRef s = find_slot(a.c, a.table + (size_t)b * a.table_stride, __ldg(a.kept + (size_t)bh * a.budget + i));
+            const SlotRef d = find_slot(a.c, a.dst_table + (size_t)b * a.dst_stride, i);
+            const bool ok = s.page >= 0 && d.page >= 0;
+            s_src[tid] = ok ? slot_bytes(a.c, s, h) : -1;
+            s_dst[tid] = ok ? slot_bytes(a.c, d, h) : -1;
+            if (ok) a.c.weight[slot_weight(a.c, d, h)] = a.c.weight[slot_weight(a.c, s, h)];
+            else raise_device_error(a.err, kErrPage);
         }
-        const long long so = slot_bytes(a.c, s, h) + 16 * c, to = slot_bytes(a.c, d, h) + 16 * c;
-        const uint4 k = *reinterpret_cast<const uint4 *>(a.c.k + so), v = *reinterpret_cast<const uint4 *>(a.c.v + so);
-        *reinterpret_cast<uint4 *>(a.c.k + to) = k;
-        *reinterpret_cast<uint4 *>(a.c.v + to) = v;
-        if (c == 0) a.c.weight[slot_weight(a.c, d, h)] = a.c.weight[slot_weight(a.c, s, h)];
+        __syncthreads();
+        const int work = count * (int)chunks.d;
+        for (int w0 = tid; w0 < work; w0 += kMoveAhead * kMoveThreads) {
+            uint4 k[kMoveAhead], v[kMoveAhead];
+            long long to[kMoveAhead];
+#pragma unroll
+            for (int x = 0; x < kMoveAhead; ++x) {
+                const int w = w0 + x * kMoveThreads;
+                to[x] = -1;
+                if (w >= work) continue;
+                const int i = quotient(w, chunks), at = 16 * (w - i * (int)chunks.d);
+                if (s_src[i] < 0) continue;
+                to[x] = s_dst[i] + at;
+                k[x] = *reinterpret_cast<const uint4 *>(a.c.k + s_src[i] + at);
+                v[x] = *reinterpret_cast<const uint4 *>(a.c.v + s_src[i] + at);
+            }
+#pragma unroll
+            for (int x = 0; x < kMoveAhead; ++x) {
+                if (to[x] < 0) continue;
+                *reinterpret_cast<uint4 *>(a.c.k + to[x]) = k[x];
+                *reinterpret_cast<uint4 *>(a.c.v + to[x]) = v[x];
+            }
+        }
     }
 }
 
 }  // namespace
 
 int run_kv_evict(const EvictArgs &a, cudaStream_t st) {
-    int rc = launch_pdl("qg_kv_evict", evict_select_kernel, dim3(a.n_seq * a.c.n_heads), kSelThreads, 0, st, a);
-    if (rc != kOk) return rc;
-    const int row_b = a.c.dim * (a.c.type == kE4m3 ? 1 : 2);
+    // blocks per head: 2048 slots each until a cluster is full
+    int ranks = 1;
+    while (ranks < kMaxCluster && (long long)ranks * 2048 < a.max_len) ranks *= 2;
+    const long long stretch = ((long long)a.max_len + ranks * kSelWarps - 1) / (ranks * kSelWarps) + 31;
+    const long long keys = stretch / 32 * 32 * kSelWarps;
+    const int cap = keys < 49152 ? (int)keys : 49152;              // up to 192 KB of keys
+    set_max_dynamic_smem(reinterpret_cast<const void *>(evict_select_kernel), 4 * 49152);
+    int rc = launch_clusters("qg_kv_evict", evict_select_kernel, dim3(a.n_seq * a.c.n_heads * ranks), kSelThreads,
+                             ranks, (size_t)cap * 4, st, a, cap);
     const int most = a.max_len < a.budget ? a.max_len : a.budget;
-    if (most == 0) return kOk;
-    int per = 64;
-    while ((most + per - 1) / per > 65535) per *= 2;
-    return launch_pdl("qg_kv_evict", evict_move_kernel, dim3(a.n_seq * a.c.n_heads, (most + per - 1) / per),
-                      kMoveThreads, 0, st, a, row_b, per);
+    if (rc != kOk || most == 0) return rc;
+    const int row_b = a.c.dim * (a.c.type == kE4m3 ? 1 : 2);
+    const int blocks = (most + kMoveSlots - 1) / kMoveSlots;
+    return launch_pdl("qg_kv_evict", evict_move_kernel, dim3(a.n_seq * a.c.n_heads, blocks < 65535 ? blocks : 65535),
+                      kMoveThreads, 0, st, a, fast_div(row_b / 16));
 }
 
 }  // namespace qg
