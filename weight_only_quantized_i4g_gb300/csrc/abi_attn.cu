@@ -92,7 +92,7 @@ int check_attn_sizes(const char *fn, const KvView &c, int n_seq, int max_len, in
     if (n_seq < 0) QG_REFUSE(kEInval, "%s: n_seq = %d, must be >= 0", fn, n_seq);
     const int rc = check_heads(fn, n_q_heads, c.n_heads);
     if (rc) return rc;
-    const double steps = ((double)max_len / c.page + 1) * ((c.page + 15) / 16);
+    const double steps = ((double)max_len / c.page + 1) * ((c.page + 15) / 16) + 2;   // and a segment's own cost
     if ((double)n_seq * S * n_q_heads > (double)INT_MAX / 2 || (double)n_seq * n_q_heads * S * steps > (double)INT_MAX / 2)
         QG_REFUSE(kEInval, "%s: sizes overflow", fn);
     return kOk;

@@ -21,113 +21,108 @@ namespace {
 
 constexpr long long kWholeBytes = 512 << 10;
 constexpr int kFinishThreads = 256;
-constexpr int kFinishWarps = kFinishThreads / 32;
 
-// The second kernel of a call.  Its first w.ctas * rows blocks join segments
-// that several blocks of the streaming kernel share: block (x, r) does row r
-// of the segment that the streaming kernel's block x left open at its end (its
-// last piece, then the first pieces of the blocks after it).  Of its `dp / 4`
-// threads a piece, each takes every so many pieces, all loads in flight at
-// once.  The further blocks add up attention weights from the scores that the
-// streaming kernel left, a thread a slot:
+// The second kernel of a call.  Its first blocks join segments that several
+// blocks of the streaming kernel share: block (x, y) does `per` rows of the
+// segment that the streaming kernel's block x left open at its end (its last
+// piece, then the first pieces of the blocks after it).  A thread takes four
+// elements of a row of every so many pieces, four loads in flight.  The
+// further blocks add up attention weights from the scores that the streaming
+// kernel left, a thread a slot:
 //   weight[t] += sum over the rows of a key-value head of 2^(z_t - lse).
-// Which segments are shared follows from the lengths, which are read before
-// the wait for the streaming kernel.
 __global__ void __launch_bounds__(kFinishThreads)
     attn_finish_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnWork w, int rows, int dp,
-                       int warps, int join_blocks) {
-    extern __shared__ int s_prefix[];                 // [n + 1], then lengths [n]
+                       int per, int join_blocks) {
     __shared__ float4 s_acc[kFinishThreads];
     __shared__ float s_lse[64];
-    __shared__ int s_sum[kFinishWarps];
+    const int tid = threadIdx.x, R = a.S * a.group;
     griddep_launch_dependents();
-    const int tid = threadIdx.x, lane = tid & 31, n = a.n_seq;
-    int *s_len = s_prefix + n + 1;
-    scan_steps<kFinishThreads>(a, w, s_len, s_prefix, s_sum, nullptr);
-    const int total = s_prefix[n] * w.tiles, chunk = steps_per_block(total, w.ctas, warps);
-    // this kernel must not be complete before the streaming kernel is
-    if (blockIdx.x == 0) griddep_wait();
+    griddep_wait();
 
     if ((int)blockIdx.x < join_blocks) {
-        const int x = blockIdx.x / rows, r = blockIdx.x - x * rows;
-        const int c0 = x * chunk, c1 = c0 + chunk;
-        if (c1 >= total) return;
-        const Place p = locate(c1 - 1, s_prefix, n, w);
-        const int start = c1 - 1 - p.i, end = start + p.n;
-        if (start < c0 || end <= c1) return;          // it begins before this block, or is not open
-        const int pieces = (end - 1) / chunk - x + 1;
-        const int kh = quotient(p.seg, w.row_tiles_div), tile = p.seg - kh * w.row_tiles;
-        const RowRef ref = row_ref(a, w, p.b, kh, tile * rows + r);
-        if (!ref.real) return;
-        const float vs = a.c.type == kE4m3 ? __ldg(a.c.v_scale + kh) : 1.f;
-        griddep_wait();
-
+        const int groups = rows / per, x = blockIdx.x / groups;
+        const int2 open = w.open[x];
+        if (open.x < 0) return;
+        const int pieces = open.y, b = quotient(open.x, w.tiles_div), sg = open.x - b * w.tiles;
+        const int kh = quotient(sg, w.row_tiles_div), tile = sg - kh * w.row_tiles;
+        const int quads = dp / 4, sets = kFinishThreads / (quads * per);
+        const int set = tid / (quads * per), item = tid - set * quads * per, local = item / quads;
+        const int r = (blockIdx.x - x * groups) * per + local, d = 4 * (item - local * quads);
+        const RowRef ref = row_ref(a, w, b, kh, tile * rows + r);
         auto at = [&](int i) { return ((size_t)(x + i) * 2 + (i == 0 ? 1 : 0)) * rows + r; };
-        const int quads = dp / 4, set = tid / quads, d = 4 * (tid - set * quads), sets = kFinishThreads / quads;
-        constexpr int kAhead = 4;
-        float4 v[kAhead];
-        float f[kAhead];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int i = set + k * sets;
-            f[k] = kNoRef;
-            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i < pieces) v[k] = *reinterpret_cast<const float4 *>(w.part_o + at(i) * dp + d), f[k] = w.part_ml[at(i)].x;
-        }
-        // every warp: the row's reference and sum
         float m = kNoRef, l = 0.f;
-        for (int i = lane; i < pieces; i += 32) m = fmaxf(m, w.part_ml[at(i)].x);
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-        for (int i = lane; i < pieces; i += 32) {
-            const float2 y = w.part_ml[at(i)];
-            l += y.y * ex2(y.x - m);
-        }
-        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto add = [&](float4 y, float g) {
-            sum.x += y.x * g, sum.y += y.y * g, sum.z += y.z * g, sum.w += y.w * g;
-        };
+        if (ref.real) {
+            constexpr int kAhead = 4;
+            float4 v[kAhead];
+            float f[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (set + k * sets < pieces) add(v[k], ex2(f[k] - m));
-        for (int i = set + kAhead * sets; i < pieces; i += sets)
-            add(*reinterpret_cast<const float4 *>(w.part_o + at(i) * dp + d), ex2(w.part_ml[at(i)].x - m));
-        s_acc[tid] = sum;
-        __syncthreads();
-        if (set > 0) return;
-        for (int k = 1; k < sets; ++k) add(s_acc[k * quads + tid], 1.f);
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = set + k * sets;
+                f[k] = kNoRef;
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < pieces) v[k] = *reinterpret_cast<const float4 *>(w.part_o + at(i) * dp + d), f[k] = w.part_ml[at(i)].x;
+            }
+#pragma unroll 8
+            for (int i = 0; i < pieces; ++i) m = fmaxf(m, w.part_ml[at(i)].x);
+#pragma unroll 8
+            for (int i = 0; i < pieces; ++i) {
+                const float2 y = w.part_ml[at(i)];
+                l += y.y * ex2(y.x - m);
+            }
+            auto add = [&](float4 y, float g) {
+                sum.x += y.x * g, sum.y += y.y * g, sum.z += y.z * g, sum.w += y.w * g;
+            };
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (set + k * sets < pieces) add(v[k], ex2(f[k] - m));
+#pragma unroll 4
+            for (int i = set + kAhead * sets; i < pieces; i += sets)
+                add(*reinterpret_cast<const float4 *>(w.part_o + at(i) * dp + d), ex2(w.part_ml[at(i)].x - m));
+        }
+        if (sets > 1) {
+            s_acc[tid] = sum;
+            __syncthreads();
+            if (set > 0) return;
+            for (int k = 1; k < sets; ++k) {
+                const float4 y = s_acc[k * quads * per + tid];
+                sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
+            }
+        }
+        if (!ref.real || set >= sets) return;
+        const float vs = a.c.type == kE4m3 ? __ldg(a.c.v_scale + kh) : 1.f;
         if (d < a.c.dim) store_out4(a, ref.head * a.c.dim + d, sum, row_factor(l, vs));
-        if (tid == 0 && a.lse) a.lse[ref.head] = row_lse(m, l);
+        if (d == 0 && a.lse) a.lse[ref.head] = row_lse(m, l);
         return;
     }
 
-    const int at = blockIdx.x - join_blocks, heads = n * a.c.n_heads;
-    const int bh = at % heads, part = at / heads, b = bh / a.c.n_heads, kh = bh - b * a.c.n_heads;
-    const int len = s_len[b];
+    const int at = blockIdx.x - join_blocks, heads = a.n_seq * a.c.n_heads;
+    const int part = at / heads, bh = at - part * heads, b = bh / a.c.n_heads, kh = bh - b * a.c.n_heads;
+    const int len = seq_len(a.lens, b, a.max_len, nullptr);
     if (part * kFinishThreads >= len) return;
-    const int t = part * kFinishThreads + tid, R = a.S * a.group;
+    const int t = part * kFinishThreads + tid;
     SlotRef ref{-1, 0};
     if (t < len) ref = find_slot(a.c, a.table + (size_t)b * a.table_stride, t);
-    griddep_wait();
     float sum = 0.f;
     for (int tile = 0; tile < w.row_tiles; ++tile) {
-        const int sg = kh * w.row_tiles + tile;
+        const int seg = b * w.tiles + kh * w.row_tiles + tile;
         __syncthreads();
         if (tid < rows) {
             const RowRef r = row_ref(a, w, b, kh, tile * rows + tid);
             float lse = -INFINITY;                    // in log2 units
             if (r.real) {
-                const int steps = s_prefix[b + 1] - s_prefix[b], start = s_prefix[b] * w.tiles + sg * steps;
-                const int i0 = w.whole ? 0 : start / chunk, i1 = w.whole ? 0 : (start + steps - 1) / chunk;
-                if (i0 == i1) {
+                const int2 span = w.span[seg];
+                if (span.y == 1) {
                     lse = a.lse[r.head] * 1.44269504088896340736f;
-                } else {                              // its pieces' statistics; the join may not have run yet
-                    auto stat = [&](int i) { return w.part_ml[((size_t)i * 2 + (i == i0 ? 1 : 0)) * rows + tid]; };
+                } else {                              // its pieces' statistics: the join may not have run yet
+                    auto stat = [&](int i) {
+                        return w.part_ml[((size_t)(span.x + i) * 2 + (i == 0 ? 1 : 0)) * rows + tid];
+                    };
                     float m = kNoRef, l = 0.f;
-#pragma unroll 4
-                    for (int i = i0; i <= i1; ++i) m = fmaxf(m, stat(i).x);
-#pragma unroll 4
-                    for (int i = i0; i <= i1; ++i) l += stat(i).y * ex2(stat(i).x - m);
+#pragma unroll 8
+                    for (int i = 0; i < span.y; ++i) m = fmaxf(m, stat(i).x);
+#pragma unroll 8
+                    for (int i = 0; i < span.y; ++i) l += stat(i).y * ex2(stat(i).x - m);
                     lse = l == 0.f ? -INFINITY : m + log2f(l);
                 }
             }
@@ -135,7 +130,7 @@ __global__ void __launch_bounds__(kFinishThreads)
         }
         __syncthreads();
         if (ref.page < 0) continue;
-        const float *z = w.scores + (((size_t)b * w.tiles + sg) * w.score_slots + t) * rows;
+        const float *z = w.scores + ((size_t)seg * w.score_slots + t) * rows;
         for (int r = 0; r < rows && tile * rows + r < R; r += 2) {
             const float2 x = *reinterpret_cast<const float2 *>(z + r);
             if (s_lse[r] != -INFINITY) sum += ex2(x.x - s_lse[r]);
@@ -158,7 +153,7 @@ struct Layout {
     AttnPlan pl;
     int rows, row_tiles, seqs, score_slots;
     int ctas, whole;
-    size_t part_o, part_ml, head_o, lse, scores, bytes;
+    size_t part_o, part_ml, head_o, open, span, lse, scores, bytes;
 };
 Layout layout(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int accumulate) {
     Layout y;
@@ -191,6 +186,8 @@ Layout layout(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int
     y.part_o = take(y.whole ? 0 : 2 * ctas * tile_f);
     y.part_ml = take(y.whole ? 0 : 2 * ctas * y.rows * sizeof(float2));
     y.head_o = take(y.whole ? 0 : ctas * y.pl.warps * tile_f);
+    y.open = take(y.whole ? 0 : ctas * sizeof(int2));
+    y.span = take(accumulate ? (size_t)segments * sizeof(int2) : 0);
     y.lse = take(accumulate ? (size_t)y.seqs * S * n_q_heads * 4 : 0);
     y.scores = take(accumulate ? seq_scores * y.seqs : 0);
     y.bytes = at;
@@ -238,6 +235,8 @@ int run_attn_paged(const AttnArgs &args, void *ws, cudaStream_t st) {
     w.part_o = reinterpret_cast<float *>(base + y.part_o);
     w.part_ml = reinterpret_cast<float2 *>(base + y.part_ml);
     w.head_o = reinterpret_cast<float *>(base + y.head_o);
+    w.open = reinterpret_cast<int2 *>(base + y.open);
+    w.span = reinterpret_cast<int2 *>(base + y.span);
     w.scores = reinterpret_cast<float *>(base + y.scores);
     w.score_slots = y.score_slots;
     w.row_tiles = y.row_tiles;
@@ -267,13 +266,16 @@ int run_attn_paged(const AttnArgs &args, void *ws, cudaStream_t st) {
         rc = a.c.type == kBf16 ? launch_attn_stream<kBf16>(a, w, y.pl, maps, st)
              : a.c.type == kF16 ? launch_attn_stream<kF16>(a, w, y.pl, maps, st)
                                 : launch_attn_stream<kE4m3>(a, w, y.pl, maps, st);
-        const int joins = y.whole ? 0 : w.ctas * y.rows;
+        // a segment's pieces: few where there are many segments, and a block then does
+        // several rows; else one, its threads sharing the pieces
+        const int most = kFinishThreads / (y.pl.dp / 4), per = (long long)a.n_seq * w.tiles * 8 < w.ctas ? 1 : most < 8 ? most : 8;
+        const int joins = y.whole ? 0 : w.ctas * (y.rows / per);
         const long long adds = a.accumulate ? (long long)a.n_seq * a.c.n_heads *
                                                   ((a.max_len + kFinishThreads - 1) / kFinishThreads)
                                             : 0;
         if (rc == kOk && joins + adds > 0)
             rc = launch_pdl("qattn_paged", attn_finish_kernel, dim3((unsigned)(joins + adds)), kFinishThreads,
-                            (2 * (size_t)a.n_seq + 1) * sizeof(int), st, a, w, y.rows, y.pl.dp, y.pl.warps, joins);
+                            0, st, a, w, y.rows, y.pl.dp, per, joins);
         if (rc != kOk) return rc;
     }
     return kOk;

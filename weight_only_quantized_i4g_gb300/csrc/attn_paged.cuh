@@ -10,7 +10,8 @@
 // form tiles of 8 * NT rows; a (sequence, head, tile) is a segment of steps of
 // up to 16 slots of one page.  All segments' steps, laid end to end, are cut
 // into one equal range per block (one block an SM) and each range into one per
-// warp: unequal lengths balance without the host knowing them.  A warp keeps
+// warp: unequal lengths balance without the host knowing them.  A segment
+// counts kSegmentCost steps more than it has, for its Q and its end.  A warp keeps
 // the running maximum and sum of each row and O in registers (online softmax).
 // A segment that ends inside its warp is finished there; pieces of one that
 // does not are joined in shared memory after the block's ranges are done, and
@@ -54,12 +55,15 @@
 namespace qg {
 
 constexpr int kAttnMaxSeq = 2048;     // sequences per launch (their lengths sit in shared memory)
+constexpr int kSegmentCost = 2;       // what starting and ending a segment takes, in steps (~5000 cycles against ~2000)
 
 // Workspace of one launch.
 struct AttnWork {
     float *part_o;      // [ctas][2][rows][DP]: pieces a block leaves open, at its start (0) and end (1)
     float2 *part_ml;    // [ctas][2][rows]: their maxima (log2 units) and sums
     float *head_o;      // [ctas][warps][rows][DP]: pieces a warp finishes before its range ends
+    int2 *open;         // [ctas]: {segment a block leaves open at its end or -1, blocks it spans}
+    int2 *span;         // accumulate: [segment]: {its first block, blocks it spans}
     float *scores;      // accumulate: z in log2 units, [segment][slot][rows]
     int score_slots;    // slots per segment in scores
     int row_tiles;
@@ -123,7 +127,7 @@ __device__ __forceinline__ int slab_place(int r, int x) {
 template <class C>
 __host__ __device__ constexpr size_t attn_fixed_smem() {
     // 1 KB for the copies' alignment, then as laid out in the kernel
-    return 1024 + (size_t)C::W * C::ring + C::W * C::NS * (8 + 4) + C::W * 2 * C::rows * sizeof(float2) + C::W * 2 * 8;
+    return 1024 + (size_t)C::W * C::ring + C::W * C::NS * (8 + 16) + C::W * 2 * C::rows * sizeof(float2) + C::W * 2 * 8;
 }
 
 // Box at element x, slot t, head h of page p.
@@ -208,17 +212,18 @@ __device__ __forceinline__ int seq_steps(const AttnArgs &a, const AttnWork &w, i
     return full * w.page_steps + ((len - full * a.c.page + 15) >> 4);
 }
 
-// Lengths of all sequences and the running sums (n + 1) of their steps into
-// shared memory; THREADS threads, `s_sum` one int per warp.
+// Lengths of all sequences, and the running sums (n + 1) of their segments'
+// costs (a sequence without slots has none), into shared memory; THREADS
+// threads, `s_sum` one int per warp.
 template <int THREADS>
-__device__ __forceinline__ void scan_steps(const AttnArgs &a, const AttnWork &w, int *s_len, int *s_prefix, int *s_sum, int *err) {
+__device__ __forceinline__ void scan_costs(const AttnArgs &a, const AttnWork &w, int *s_len, int *s_prefix, int *s_sum, int *err) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.n_seq;
     const int per = (n + THREADS - 1) / THREADS;
     int sum = 0;
     for (int i = tid * per; i < (tid + 1) * per && i < n; ++i) {
         const int len = seq_len(a.lens, i, a.max_len, err);
         s_len[i] = len;
-        sum += seq_steps(a, w, len);
+        if (len > 0) sum += seq_steps(a, w, len) + kSegmentCost;
     }
     int inc = sum;
 #pragma unroll
@@ -235,35 +240,38 @@ __device__ __forceinline__ void scan_steps(const AttnArgs &a, const AttnWork &w,
     int at = base + inc - sum;
     for (int i = tid * per; i < (tid + 1) * per && i < n; ++i) {
         s_prefix[i] = at;
-        at += seq_steps(a, w, s_len[i]);
+        if (s_len[i] > 0) at += seq_steps(a, w, s_len[i]) + kSegmentCost;
     }
     if (tid == THREADS - 1) s_prefix[n] = at;
     __syncthreads();
 }
 
-// Steps per block where all are cut into equal ranges: at least one per warp.
-__device__ __forceinline__ int steps_per_block(int total, int ctas, int warps) {
+// Cost units per block where all are cut into equal ranges: a step per warp at least.
+__device__ __forceinline__ int units_per_block(int total, int ctas, int warps) {
     const int chunk = (total + ctas - 1) / ctas;
-    return chunk < warps ? warps : chunk;
+    return chunk < warps + kSegmentCost ? warps + kSegmentCost : chunk;
 }
 
-// Place of a global step: its sequence, segment there, step of that (page of
-// the sequence and step inside it) and steps of the segment.
+// A step: sequence, segment there, step of that (page of the sequence and step
+// inside it) and steps of the segment.
 struct Place { int b, seg, i, n, page, sub; };
-__device__ __forceinline__ Place locate(int step, const int *s_prefix, int n, const AttnWork &w) {
-    Place p;
-    const int x = quotient(step, w.tiles_div);
+// The first step at or after unit u; a segment's first kSegmentCost units have none.
+__device__ __forceinline__ Place locate(int u, const int *s_prefix, int n, const AttnWork &w) {
+    Place p = {n, 0, 0, 1, 0, 0};
+    const int x = quotient(u, w.tiles_div);
+    if (x >= s_prefix[n]) return p;
     int lo = 0, hi = n - 1;                          // the last b with prefix[b] <= x
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (s_prefix[mid] <= x) lo = mid;
         else hi = mid - 1;
     }
+    const int cost = s_prefix[lo + 1] - s_prefix[lo], rem = u - s_prefix[lo] * w.tiles;
     p.b = lo;
-    p.n = s_prefix[lo + 1] - s_prefix[lo];
-    const int rem = step - s_prefix[lo] * w.tiles;
-    p.seg = rem / p.n;
-    p.i = rem - p.seg * p.n;
+    p.n = cost - kSegmentCost;
+    p.seg = rem / cost;
+    p.i = rem - p.seg * cost - kSegmentCost;
+    if (p.i < 0) p.i = 0;
     p.page = quotient(p.i, w.page_steps_div);
     p.sub = p.i - p.page * w.page_steps;
     return p;
@@ -275,14 +283,17 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                        const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using C = AttnCfg<TYPE, DP_, NT_>;
     constexpr int DP = C::DP, NT = C::NT, W = C::W, NS = C::NS, NI = C::NI, E = C::E, NQ = C::NQ, rows = C::rows;
-    constexpr int kMissing = 32;                      // flag of a step whose page is not in the pool
+    // flags of a step: its page is not in the pool; first and last of its segment
+    constexpr int kMissing = 32, kFirst = 64, kLast = 128;
     extern __shared__ char smem_raw[];
     char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint64_t *s_bar = reinterpret_cast<uint64_t *>(smem + W * C::ring);       // [W][NS]
     float2 *s_ml = reinterpret_cast<float2 *>(s_bar + W * NS);                // [W][2][rows]
     int2 *s_piece = reinterpret_cast<int2 *>(s_ml + W * 2 * rows);            // [W][2]: {segment or -1, 1: ended | 2: in head_o}
-    int *s_state = reinterpret_cast<int *>(s_piece + W * 2);                  // [W][NS]: slots of the step, kMissing
-    int *s_prefix = s_state + W * NS;                                         // [n + 1]
+    // [W][NS] of a step in the ring: its slots and flags, its first slot, its
+    // segment, the first slot that some row of the sequence does not see
+    int4 *s_state = reinterpret_cast<int4 *>(s_piece + W * 2);
+    int *s_prefix = reinterpret_cast<int *>(s_state + W * NS);                // [n + 1]
     int *s_len = s_prefix + a.n_seq + 1;                                      // [n]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int n = a.n_seq, D = a.c.dim;
@@ -291,20 +302,22 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
     if (tid < W * 2) s_piece[tid] = make_int2(-1, 0);
     mbar_fence_init();
 
-    // dependents may start once the lengths are final: the second kernel reads them before its own wait
-    griddep_wait();
     griddep_launch_dependents();
+    griddep_wait();
 
-    scan_steps<C::threads>(a, w, s_len, s_prefix, s_state, blockIdx.x == 0 ? a.err : nullptr);
-    int c0, c1;
+    scan_costs<C::threads>(a, w, s_len, s_prefix, reinterpret_cast<int *>(s_state),
+                           blockIdx.x == 0 ? a.err : nullptr);
+    int c0, c1, chunk = 0;                                                    // in cost units
     if (w.whole) {
-        const int b = quotient(blockIdx.x, w.tiles_div), steps = s_prefix[b + 1] - s_prefix[b];
-        c0 = s_prefix[b] * tiles + (blockIdx.x - b * tiles) * steps;
-        c1 = c0 + steps;
+        const int b = quotient(blockIdx.x, w.tiles_div), cost = s_prefix[b + 1] - s_prefix[b];
+        c1 = s_prefix[b] * tiles + (blockIdx.x - b * tiles + 1) * cost;
+        c0 = cost ? c1 - cost + kSegmentCost : c1;
     } else {
-        const int total = s_prefix[n] * tiles, chunk = steps_per_block(total, gridDim.x, W);
+        const int total = s_prefix[n] * tiles;
+        chunk = units_per_block(total, gridDim.x, W);
         c0 = (int)(blockIdx.x * chunk) < total ? blockIdx.x * chunk : total;
         c1 = c0 + chunk < total ? c0 + chunk : total;
+        if (tid == 0) w.open[blockIdx.x] = make_int2(-1, 0);
     }
 
     // sequences without a slot have no steps: their rows are empty
@@ -320,43 +333,56 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
     }
     if (c0 >= c1) return;
 
-    const int w0 = c0 + (int)((long long)(c1 - c0) * warp / W);
-    const int w1 = c0 + (int)((long long)(c1 - c0) * (warp + 1) / W);
+    // the warp's first step, and how many it has
+    Place ip = locate(c0 + (int)((long long)(c1 - c0) * warp / W), s_prefix, n, w);
+    int left;
+    {
+        const Place end = locate(c0 + (int)((long long)(c1 - c0) * (warp + 1) / W), s_prefix, n, w);
+        left = end.seg * end.n + end.i - (ip.seg * ip.n + ip.i);
+        for (int b = ip.b; b < end.b; ++b) {
+            const int cost = s_prefix[b + 1] - s_prefix[b];
+            if (cost) left += tiles * (cost - kSegmentCost);
+        }
+    }
     char *ring = smem + warp * C::ring;
     const uint32_t ring_a = smem_addr(ring);
-
-    auto advance = [&](Place &p) {
-        if (++p.sub == w.page_steps) p.sub = 0, ++p.page;
-        if (++p.i < p.n) return;
-        p.i = p.page = p.sub = 0;
-        if (++p.seg < tiles) return;
-        p.seg = 0;
-        do ++p.b;
-        while (p.b < n && s_prefix[p.b + 1] == s_prefix[p.b]);
-        p.n = p.b < n ? s_prefix[p.b + 1] - s_prefix[p.b] : 1;
-    };
 
     // ---- loads: the page of the next step is looked up one step early ----
     // K and V are read once per row tile: marked first to leave L2 where there is but one
     uint64_t policy;
     if (w.row_tiles == 1) asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
     else asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
-    Place ip = locate(w0 < w1 ? w0 : c0, s_prefix, n, w), p = ip;
-    int issued = w0, istage = 0, look_page = 0;
+    int to_issue = left, istage = 0, look_page = 0;
     auto look = [&]() {
-        if (issued < w1) look_page = __ldg(a.table + (size_t)ip.b * a.table_stride + ip.page);
+        if (to_issue == 0) return;
+        look_page = __ldg(a.table + (size_t)ip.b * a.table_stride + ip.page);
+        if (ip.i == 0) {                              // a new segment: its rows of q, a line a lane
+            const int kh = quotient(ip.seg, w.row_tiles_div), tile = ip.seg - kh * w.row_tiles;
+            constexpr int lines = DP / 64;
+#pragma unroll 1
+            for (int x = lane; x < rows * lines; x += 32) {
+                const RowRef r = row_ref(a, w, ip.b, kh, tile * rows + x / lines);
+                const int d = 64 * (x % lines);
+                if (r.real && d < D)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint16_t *>(a.q) +
+                                                                  ((size_t)ip.b * a.S + r.s) * a.q_stride +
+                                                                  (size_t)r.q_head * D + d));
+            }
+        }
     };
     auto issue = [&]() {
-        if (issued < w1) {
+        if (to_issue > 0) {
             if (lane == 0) {
-                const int slot = 16 * ip.sub, left = s_len[ip.b] - ip.page * a.c.page;
-                int count = (left < a.c.page ? left : a.c.page) - slot;
+                const int slot = 16 * ip.sub, before = ip.page * a.c.page, len = s_len[ip.b];
+                int count = (len - before < a.c.page ? len - before : a.c.page) - slot;
                 if (count > 16) count = 16;
                 uint64_t *bar = &s_bar[warp * NS + istage];
                 const uint32_t dst = ring_a + istage * C::stage;
                 const int kh = quotient(ip.seg, w.row_tiles_div);
                 const bool there = (unsigned)look_page < (unsigned)a.c.n_pages;
-                s_state[warp * NS + istage] = there ? count : count | kMissing;   // published by the arrival
+                s_state[warp * NS + istage] =
+                    make_int4(count | (there ? 0 : kMissing) | (ip.i == 0 ? kFirst : 0) | (ip.i + 1 == ip.n ? kLast : 0),
+                              before + slot, ip.b * tiles + ip.seg, len - a.S + 1);
                 if (there) {
                     mbar_arrive_expect_tx(bar, 2 * C::NB * C::BB * w.box_rows);
 #pragma unroll
@@ -371,8 +397,17 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                     mbar_arrive(bar);
                 }
             }
-            ++issued;
-            advance(ip);
+            --to_issue;
+            if (++ip.sub == w.page_steps) ip.sub = 0, ++ip.page;
+            if (++ip.i == ip.n) {
+                ip.i = ip.page = ip.sub = 0;
+                if (++ip.seg == tiles) {
+                    ip.seg = 0;
+                    do ++ip.b;
+                    while (ip.b < n && s_prefix[ip.b + 1] == s_prefix[ip.b]);
+                    ip.n = ip.b < n ? s_prefix[ip.b + 1] - s_prefix[ip.b] - kSegmentCost : 1;
+                }
+            }
             look();
         }
         if (++istage == NS) istage = 0;
@@ -386,28 +421,30 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
     float m[NT][2], l[NT][2];
     uint32_t qf[NT][NI][C::ESZ == 1 ? 8 : 4];
     float rs[NT][2];                                  // score factor of the thread's rows (e4m3: per row)
-    int lim[NT][2];                                   // slots they see
     const float factor = a.scale * 1.44269504088896340736f;
     constexpr float shift = TYPE == kBf16 ? 0.f : 6.f;
     const bool third = TYPE == kBf16 && a.o_type == kF32;
-    int hidden_from = 0;                              // first slot that some row does not see
     bool fresh = true;                                // at the start of a piece
     bool began_here = false;
     int stage = 0;
     uint32_t phase = 0;
 
 #pragma unroll 1
-    for (int step = w0; step < w1; ++step) {
+    for (; left > 0; --left) {
+        __syncwarp();                                 // the state was written by lane 0
+        const int4 state = s_state[warp * NS + stage];
+        const int count = state.x & 31, t0 = state.y, hidden_from = state.w;
+        const uint32_t src = ring_a + stage * C::stage, src_v = src + C::NB * C::box;
         if (fresh) {
-            const int kh = quotient(p.seg, w.row_tiles_div), tile = p.seg - kh * w.row_tiles, len = s_len[p.b];
-            hidden_from = len - a.S + 1;
+            const int b = quotient(state.z, w.tiles_div), sg = state.z - b * tiles;
+            const int kh = quotient(sg, w.row_tiles_div), tile = sg - kh * w.row_tiles;
             fresh = false;
-            began_here = p.i == 0;
+            began_here = state.x & kFirst;
             // Q as the B operand: row g of each 8, the thread's chunks
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const RowRef r = row_ref(a, w, p.b, kh, tile * rows + 8 * nt + g);
-                const uint16_t *q = static_cast<const uint16_t *>(a.q) + ((size_t)p.b * a.S + r.s) * a.q_stride +
+                const RowRef r = row_ref(a, w, b, kh, tile * rows + 8 * nt + g);
+                const uint16_t *q = static_cast<const uint16_t *>(a.q) + ((size_t)b * a.S + r.s) * a.q_stride +
                                     (size_t)r.q_head * D;
                 if constexpr (TYPE != kE4m3) {
 #pragma unroll
@@ -454,8 +491,6 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int s = quotient(tile * rows + 8 * nt + 2 * c + e, w.group_div);
-                    lim[nt][e] = len - a.S + 1 + (s < a.S ? s : a.S - 1);
                     m[nt][e] = kNoRef;
                     l[nt][e] = 0.f;
                 }
@@ -469,14 +504,12 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
         if (!__all_sync(~0u, mbar_wait(&s_bar[warp * NS + stage], phase))) {
             // a copy did not land in time: no result, but let those in flight land before the block ends
             if (lane == 0) raise_device_error(a.err, kErrTimeout);
-            for (int x = step; x < issued; ++x) {
+            for (; left > to_issue; --left) {
                 mbar_wait(&s_bar[warp * NS + stage], phase);
                 if (++stage == NS) stage = 0, phase ^= 1u;
             }
             break;
         }
-        const int state = s_state[warp * NS + stage], count = state & 31;
-        const uint32_t src = ring_a + stage * C::stage, src_v = src + C::NB * C::box;
 
         // ---- S^T = K Q^T, in two chains ----
         float s[NT][4], s1[NT][4];
@@ -506,13 +539,19 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
         }
 
         // ---- exponents against the rows' references; thread: slots g, g + 8 by rows 2c, 2c + 1 ----
-        const int t0 = p.page * a.c.page + 16 * p.sub;
-        const bool partial = state != 16 || (a.S > 1 && t0 + 16 > hidden_from);
+        const bool partial = (state.x & 63) != 16 || (a.S > 1 && t0 + 16 > hidden_from);
+        // slots that row nt, e of the thread sees of this step and before it
+        auto limit = [&](int nt, int e) {
+            const int sg = state.z - quotient(state.z, w.tiles_div) * tiles;
+            const int tile = sg - quotient(sg, w.row_tiles_div) * w.row_tiles;
+            const int s = quotient(tile * rows + 8 * nt + 2 * c + (e & 1), w.group_div);
+            return hidden_from + (s < a.S ? s : a.S - 1);
+        };
         // no weight for slots that the step has not, or that the row does not see; NaN for a missing page
         auto masked = [&](float z, int nt, int e) {
             const int j = g + 8 * (e >> 1);
-            if (j >= count || t0 + j >= lim[nt][e & 1]) return -INFINITY;
-            return state & kMissing ? NAN : z;
+            if (j >= count || (a.S > 1 && t0 + j >= limit(nt, e))) return -INFINITY;
+            return state.x & kMissing ? NAN : z;
         };
         uint32_t ph[NT][2], pl[NT][2], pt[NT][2];
 #pragma unroll
@@ -548,7 +587,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                 }
             }
             if (a.accumulate) {
-                float *dst = w.scores + ((size_t)(p.b * tiles + p.seg) * w.score_slots + t0) * rows + 8 * nt + 2 * c;
+                float *dst = w.scores + ((size_t)state.z * w.score_slots + t0) * rows + 8 * nt + 2 * c;
                 if (g < count)
                     *reinterpret_cast<float2 *>(dst + g * rows) = make_float2(x[0] + m[nt][0], x[1] + m[nt][1]);
                 if (g + 8 < count)
@@ -597,10 +636,10 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                     x[j][0] = v.x, x[j][1] = v.y, x[j][2] = x[j][3] = 0u;
                 }
             }
-            if (state != 16) {   // what lies past the step's slots, or where no copy landed
+            if ((state.x & 63) != 16) {   // what lies past the step's slots, or where no copy landed
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (state & kMissing || 2 * c + (j & 1) + 8 * (j >> 1) >= count)
+                    if (state.x & kMissing || 2 * c + (j & 1) + 8 * (j >> 1) >= count)
                         x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0u;
             }
         };
@@ -684,7 +723,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                             mma16816<TYPE>(acc, a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                if (t0 + j < lim[nt][e & 1]) o[q * (E / 2) + t][nt][e] += acc[e];
+                                if (t0 + j < limit(nt, e)) o[q * (E / 2) + t][nt][e] += acc[e];
                         }
                     }
                 }
@@ -693,14 +732,16 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
         __syncwarp();                                 // every lane has read its chunks and the state
 
         // ---- end of a piece ----
-        const bool ended = p.i + 1 == p.n, last = step + 1 == w1;
+        const bool ended = state.x & kLast, last = left == 1;
         if (ended || last) {
             fresh = true;
-            const int kh = quotient(p.seg, w.row_tiles_div), tile = p.seg - kh * w.row_tiles;
+            const int here = state.z, b = quotient(here, w.tiles_div), sg = here - b * tiles;
+            const int kh = quotient(sg, w.row_tiles_div), tile = sg - kh * w.row_tiles;
             const float vs = TYPE == kE4m3 ? __ldg(a.c.v_scale + kh) : 1.f;
             const bool whole = ended && began_here;
             const int slot = 2 * warp + (began_here ? 1 : 0);
-            if (!whole && lane == 0) s_piece[slot] = make_int2(p.b * tiles + p.seg, (ended ? 1 : 0) | (last ? 0 : 2));
+            if (whole && a.accumulate && lane == 0) w.span[here] = make_int2(blockIdx.x, 1);
+            if (!whole && lane == 0) s_piece[slot] = make_int2(here, (ended ? 1 : 0) | (last ? 0 : 2));
             // 8 rows at a time through shared memory: the stage just read, or, with
             // the range done, the ring, where an open piece stays for the join
 #pragma unroll
@@ -727,7 +768,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
 #pragma unroll 1
                     for (int i = lane; i < 8 * (DP / 4); i += 32) {
                         const int r = i / (DP / 4), d = 4 * (i - r * (DP / 4));
-                        const RowRef ref = row_ref(a, w, p.b, kh, tile * rows + 8 * nt + r);
+                        const RowRef ref = row_ref(a, w, b, kh, tile * rows + 8 * nt + r);
                         const float2 ml = s_ml[slot * rows + 8 * nt + r];
                         if (!ref.real) continue;
                         if (d < D) store_out4(a, ref.head * D + d, slab[slab_place<C>(r, d / 4)], row_factor(ml.y, vs));
@@ -748,7 +789,6 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
             }
         }
         issue();
-        advance(p);
         if (++stage == NS) stage = 0, phase ^= 1u;
     }
 
@@ -798,6 +838,12 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                 *reinterpret_cast<float4 *>(w.part_o + (out + r) * DP + d) = sum;
                 if (d == 0) w.part_ml[out + r] = make_float2(mm, ll);
             }
+        }
+        if (tid == 0 && starts) {
+            const int end_unit = s_prefix[b] * tiles + (sg + 1) * (s_prefix[b + 1] - s_prefix[b]);
+            const int2 span = make_int2(blockIdx.x, whole ? 1 : (end_unit - 1) / chunk - (int)blockIdx.x + 1);
+            if (!whole) w.open[blockIdx.x] = make_int2(seg, span.y);
+            if (a.accumulate) w.span[seg] = span;
         }
     }
 }

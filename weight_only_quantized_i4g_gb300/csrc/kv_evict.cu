@@ -17,8 +17,6 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 
@@ -37,7 +35,9 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // the sums to all, and every block finds the same bin.  One block per head
 // took 315 us for three sequences of 100k slots, 8 heads, two thirds of it
 // here; the clusters spread that over the SMs.
+template <int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictArgs a, int cap) {
+    constexpr int kSelWarps = kSelThreads / 32;
     extern __shared__ uint32_t s_key[];
     __shared__ int s_hist[kBins], s_total[kBins];
     __shared__ int s_warp[2][kSelWarps];
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     auto key_at = [&](int t) { return t - r0 < cap ? s_key[t - r0] : key_in_cache(t); };
     const int in_smem = r1 - r0 < cap ? r1 - r0 : cap;
     if (any) {
-#pragma unroll 4
+#pragma unroll 8
         for (int i = tid; i < in_smem; i += kSelThreads) s_key[i] = key_in_cache(r0 + i);
     }
     __syncthreads();
@@ -86,16 +86,12 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
             const int done = pass == 0 ? 32 : pass == 1 ? 21 : 10;            // low bits not yet fixed
             for (int i = tid; i < bins; i += kSelThreads) s_hist[i] = 0;
             __syncthreads();
-            // equal digits of a warp are counted by one of its lanes: weights crowd into few bins
-            for (int t0 = r0 + 32 * warp; t0 < r1; t0 += kSelThreads) {
-                const int t = t0 + lane;
-                const uint32_t k = t < r1 ? key_at(t) : 0u;
-                const bool on = t < r1 && t >= lo && t < hi && (pass == 0 || k >> done == prefix >> done);
-                const unsigned all = __ballot_sync(~0u, on);
-                if (!on) continue;
-                const int bin = (k >> shift) & (bins - 1);
-                const unsigned same = __match_any_sync(all, bin);
-                if (lane == __ffs(same) - 1) atomicAdd(&s_hist[bin], __popc(same));
+            // additions of one to an address that a warp shares are combined in hardware
+#pragma unroll 4
+            for (int t = r0 + tid; t < r1; t += kSelThreads) {
+                const uint32_t k = key_at(t);
+                if (t >= lo && t < hi && (pass == 0 || k >> done == prefix >> done))
+                    atomicAdd(&s_hist[(k >> shift) & (bins - 1)], 1);
             }
             int *total = s_hist;
             if (ranks > 1) {
@@ -105,8 +101,12 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
                 for (int i = tid; i < slice; i += kSelThreads) {
                     const int bin = rank * slice + i;
                     int sum = 0;
-                    for (int x = 0; x < ranks; ++x) sum += cluster.map_shared_rank(s_hist, x)[bin];
-                    for (int x = 0; x < ranks; ++x) cluster.map_shared_rank(s_total, x)[bin] = sum;
+#pragma unroll
+                    for (int x = 0; x < kMaxCluster; ++x)
+                        if (x < ranks) sum += cluster.map_shared_rank(s_hist, x)[bin];
+#pragma unroll
+                    for (int x = 0; x < kMaxCluster; ++x)
+                        if (x < ranks) cluster.map_shared_rank(s_total, x)[bin] = sum;
                 }
                 cluster.sync();
             } else {
@@ -235,16 +235,23 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
 
 }  // namespace
 
-int run_kv_evict(const EvictArgs &a, cudaStream_t st) {
-    // blocks per head: 2048 slots each until a cluster is full
-    int ranks = 1;
-    while (ranks < kMaxCluster && (long long)ranks * 2048 < a.max_len) ranks *= 2;
-    const long long stretch = ((long long)a.max_len + ranks * kSelWarps - 1) / (ranks * kSelWarps) + 31;
-    const long long keys = stretch / 32 * 32 * kSelWarps;
+template <int THREADS>
+int launch_select(const EvictArgs &a, int ranks, cudaStream_t st) {
+    const int warps = ranks * (THREADS / 32);
+    const long long keys = (((long long)a.max_len + warps - 1) / warps + 31) / 32 * THREADS;   // a block's stretch
     const int cap = keys < 49152 ? (int)keys : 49152;              // up to 192 KB of keys
-    set_max_dynamic_smem(reinterpret_cast<const void *>(evict_select_kernel), 4 * 49152);
-    int rc = launch_clusters("qg_kv_evict", evict_select_kernel, dim3(a.n_seq * a.c.n_heads * ranks), kSelThreads,
-                             ranks, (size_t)cap * 4, st, a, cap);
+    set_max_dynamic_smem(reinterpret_cast<const void *>(evict_select_kernel<THREADS>), 4 * 49152);
+    return launch_clusters("qg_kv_evict", evict_select_kernel<THREADS>, dim3(a.n_seq * a.c.n_heads * ranks), THREADS,
+                           ranks, (size_t)cap * 4, st, a, cap);
+}
+
+int run_kv_evict(const EvictArgs &a, cudaStream_t st) {
+    // As many blocks per head as have an SM each and 1024 slots or more; 1024
+    // threads where a block has an SM to itself, else 512 (up to four an SM).
+    const long long heads = (long long)a.n_seq * a.c.n_heads;
+    int ranks = 1;
+    while (ranks < kMaxCluster && heads * ranks * 2 <= num_sms() + num_sms() / 4 && ranks * 2048LL <= a.max_len) ranks *= 2;
+    int rc = heads * ranks <= num_sms() ? launch_select<1024>(a, ranks, st) : launch_select<512>(a, ranks, st);
     const int most = a.max_len < a.budget ? a.max_len : a.budget;
     if (rc != kOk || most == 0) return rc;
     const int row_b = a.c.dim * (a.c.type == kE4m3 ? 1 : 2);
