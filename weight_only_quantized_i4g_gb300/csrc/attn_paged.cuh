@@ -356,19 +356,6 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
     auto look = [&]() {
         if (to_issue == 0) return;
         look_page = __ldg(a.table + (size_t)ip.b * a.table_stride + ip.page);
-        if (ip.i == 0) {                              // a new segment: its rows of q, a line a lane
-            const int kh = quotient(ip.seg, w.row_tiles_div), tile = ip.seg - kh * w.row_tiles;
-            constexpr int lines = DP / 64;
-#pragma unroll 1
-            for (int x = lane; x < rows * lines; x += 32) {
-                const RowRef r = row_ref(a, w, ip.b, kh, tile * rows + x / lines);
-                const int d = 64 * (x % lines);
-                if (r.real && d < D)
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint16_t *>(a.q) +
-                                                                  ((size_t)ip.b * a.S + r.s) * a.q_stride +
-                                                                  (size_t)r.q_head * D + d));
-            }
-        }
     };
     auto issue = [&]() {
         if (to_issue > 0) {
@@ -431,11 +418,9 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
 
 #pragma unroll 1
     for (; left > 0; --left) {
-        __syncwarp();                                 // the state was written by lane 0
-        const int4 state = s_state[warp * NS + stage];
-        const int count = state.x & 31, t0 = state.y, hidden_from = state.w;
-        const uint32_t src = ring_a + stage * C::stage, src_v = src + C::NB * C::box;
         if (fresh) {
+            __syncwarp();                             // lane 0 wrote the state
+            const int4 state = s_state[warp * NS + stage];
             const int b = quotient(state.z, w.tiles_div), sg = state.z - b * tiles;
             const int kh = quotient(sg, w.row_tiles_div), tile = sg - kh * w.row_tiles;
             fresh = false;
@@ -510,6 +495,10 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
             }
             break;
         }
+        // published by the arrival that the wait has seen
+        const int4 state = s_state[warp * NS + stage];
+        const int count = state.x & 31, t0 = state.y, hidden_from = state.w;
+        const uint32_t src = ring_a + stage * C::stage, src_v = src + C::NB * C::box;
 
         // ---- S^T = K Q^T, in two chains ----
         float s[NT][4], s1[NT][4];
@@ -529,8 +518,8 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                 if constexpr (TYPE != kE4m3) {
                     a0 = kx[2 * u], a1 = ky[2 * u], a2 = kx[2 * u + 1], a3 = ky[2 * u + 1];
                 } else {
-                    a0 = e4m3x2_to_f16x2(kx[u]), a2 = e4m3x2_to_f16x2(kx[u] >> 16);
-                    a1 = e4m3x2_to_f16x2(ky[u]), a3 = e4m3x2_to_f16x2(ky[u] >> 16);
+                    e4m3x4_to_f16x2(kx[u], &a0, &a2);
+                    e4m3x4_to_f16x2(ky[u], &a1, &a3);
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -643,10 +632,10 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                         x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0u;
             }
         };
-        auto v_pair = [&](uint32_t lo, uint32_t hi, int e) -> uint32_t {   // element e of two slots' words
-            if constexpr (TYPE != kE4m3) return __byte_perm(lo, hi, e & 1 ? 0x7632 : 0x5410);
-            const uint32_t two = __byte_perm(lo, hi, e & 2 ? 0x7362 : 0x5140);
-            return e4m3x2_to_f16x2(e & 1 ? two >> 16 : two);
+        // elements e and e + 1 (e even) of two slots, each pair a half-word pair of an A fragment
+        auto v_pairs = [&](uint32_t lo, uint32_t hi, int e, uint32_t *x0, uint32_t *x1) {
+            if constexpr (TYPE != kE4m3) *x0 = __byte_perm(lo, hi, 0x5410), *x1 = __byte_perm(lo, hi, 0x7632);
+            else e4m3x4_to_f16x2(__byte_perm(lo, hi, e & 2 ? 0x7362 : 0x5140), x0, x1);
         };
         constexpr int per_word = 4 / C::ESZ;
         bool careful = false;
@@ -679,19 +668,23 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                 uint32_t x[4][4];
                 v_chunk(q, x);
 #pragma unroll
-                for (int t = 0; t < E / 2; ++t) {
+                for (int t = 0; t < E / 2; t += 2) {
                     const int e0 = t, e1 = t + E / 2;
-                    const uint32_t a0 = v_pair(x[0][e0 / per_word], x[1][e0 / per_word], e0);
-                    const uint32_t a1 = v_pair(x[0][e1 / per_word], x[1][e1 / per_word], e1);
-                    const uint32_t a2 = v_pair(x[2][e0 / per_word], x[3][e0 / per_word], e0);
-                    const uint32_t a3 = v_pair(x[2][e1 / per_word], x[3][e1 / per_word], e1);
+                    uint32_t f[2][4];
+                    v_pairs(x[0][e0 / per_word], x[1][e0 / per_word], e0, &f[0][0], &f[1][0]);
+                    v_pairs(x[0][e1 / per_word], x[1][e1 / per_word], e1, &f[0][1], &f[1][1]);
+                    v_pairs(x[2][e0 / per_word], x[3][e0 / per_word], e0, &f[0][2], &f[1][2]);
+                    v_pairs(x[2][e1 / per_word], x[3][e1 / per_word], e1, &f[0][3], &f[1][3]);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float(&acc)[4] = o[q * (E / 2) + t][nt];
-                        if constexpr (with_third) mma16816<TYPE>(acc, a0, a1, a2, a3, pt[nt][0], pt[nt][1]);
-                        mma16816<TYPE>(acc, a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
-                        mma16816<TYPE>(acc, a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-                    }
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float(&acc)[4] = o[q * (E / 2) + t + y][nt];
+                            const uint32_t(&v)[4] = f[y];
+                            if constexpr (with_third) mma16816<TYPE>(acc, v[0], v[1], v[2], v[3], pt[nt][0], pt[nt][1]);
+                            mma16816<TYPE>(acc, v[0], v[1], v[2], v[3], pl[nt][0], pl[nt][1]);
+                            mma16816<TYPE>(acc, v[0], v[1], v[2], v[3], ph[nt][0], ph[nt][1]);
+                        }
                 }
             }
         };
@@ -709,22 +702,26 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                     uint32_t x[4][4];
                     v_chunk(q, x);
 #pragma unroll
-                    for (int t = 0; t < E / 2; ++t) {
+                    for (int t = 0; t < E / 2; t += 2) {
                         const int e0 = t, e1 = t + E / 2;
-                        const uint32_t a0 = v_pair(x[0][e0 / per_word], x[1][e0 / per_word], e0) & m0;
-                        const uint32_t a1 = v_pair(x[0][e1 / per_word], x[1][e1 / per_word], e1) & m0;
-                        const uint32_t a2 = v_pair(x[2][e0 / per_word], x[3][e0 / per_word], e0) & m1;
-                        const uint32_t a3 = v_pair(x[2][e1 / per_word], x[3][e1 / per_word], e1) & m1;
+                        uint32_t f[2][4];
+                        v_pairs(x[0][e0 / per_word], x[1][e0 / per_word], e0, &f[0][0], &f[1][0]);
+                        v_pairs(x[0][e1 / per_word], x[1][e1 / per_word], e1, &f[0][1], &f[1][1]);
+                        v_pairs(x[2][e0 / per_word], x[3][e0 / per_word], e0, &f[0][2], &f[1][2]);
+                        v_pairs(x[2][e1 / per_word], x[3][e1 / per_word], e1, &f[0][3], &f[1][3]);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                            if (TYPE == kBf16 && third) mma16816<TYPE>(acc, a0, a1, a2, a3, pt[nt][0], pt[nt][1]);
-                            mma16816<TYPE>(acc, a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
-                            mma16816<TYPE>(acc, a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+                        for (int y = 0; y < 2; ++y)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (t0 + j < limit(nt, e)) o[q * (E / 2) + t][nt][e] += acc[e];
-                        }
+                            for (int nt = 0; nt < NT; ++nt) {
+                                const uint32_t a0 = f[y][0] & m0, a1 = f[y][1] & m0, a2 = f[y][2] & m1, a3 = f[y][3] & m1;
+                                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                                if (TYPE == kBf16 && third) mma16816<TYPE>(acc, a0, a1, a2, a3, pt[nt][0], pt[nt][1]);
+                                mma16816<TYPE>(acc, a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+                                mma16816<TYPE>(acc, a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (t0 + j < limit(nt, e)) o[q * (E / 2) + t + y][nt][e] += acc[e];
+                            }
                     }
                 }
             }

@@ -107,6 +107,12 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
     asm("{.reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t;}" : "=r"(r) : "r"(w));
     return r;
 }
+// Four codes as two pairs.
+__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t w, uint32_t *lo, uint32_t *hi) {
+    asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b;}"
+        : "=r"(*lo), "=r"(*hi)
+        : "r"(w));
+}
 __device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
