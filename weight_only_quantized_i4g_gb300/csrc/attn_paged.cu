@@ -103,9 +103,13 @@ __global__ void __launch_bounds__(kFinishThreads)
     const int t = part * kFinishThreads + tid;
     SlotRef ref{-1, 0};
     if (t < len) ref = find_slot(a.c, a.table + (size_t)b * a.table_stride, t);
-    float sum = 0.f;
+    float sum = 0.f, had = 0.f;
+    if (ref.page >= 0) had = a.c.weight[slot_weight(a.c, ref, kh)];
     for (int tile = 0; tile < w.row_tiles; ++tile) {
         const int seg = b * w.tiles + kh * w.row_tiles + tile;
+        const float *z = w.scores + ((size_t)seg * w.score_slots + t) * rows;
+        float4 z0 = make_float4(0.f, 0.f, 0.f, 0.f), z1 = z0;          // the first rows' scores, while lse comes
+        if (t < len) z0 = reinterpret_cast<const float4 *>(z)[0], z1 = reinterpret_cast<const float4 *>(z)[1];
         __syncthreads();
         if (tid < rows) {
             const RowRef r = row_ref(a, w, b, kh, tile * rows + tid);
@@ -130,14 +134,17 @@ __global__ void __launch_bounds__(kFinishThreads)
         }
         __syncthreads();
         if (ref.page < 0) continue;
-        const float *z = w.scores + ((size_t)seg * w.score_slots + t) * rows;
-        for (int r = 0; r < rows && tile * rows + r < R; r += 2) {
-            const float2 x = *reinterpret_cast<const float2 *>(z + r);
-            if (s_lse[r] != -INFINITY) sum += ex2(x.x - s_lse[r]);
-            if (s_lse[r + 1] != -INFINITY) sum += ex2(x.y - s_lse[r + 1]);
+        auto add = [&](float x, int r) {
+            if (s_lse[r] != -INFINITY) sum += ex2(x - s_lse[r]);
+        };
+        add(z0.x, 0), add(z0.y, 1), add(z0.z, 2), add(z0.w, 3), add(z1.x, 4), add(z1.y, 5), add(z1.z, 6), add(z1.w, 7);
+#pragma unroll 2
+        for (int r = 8; r < rows && tile * rows + r < R; r += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(z + r);
+            add(x.x, r), add(x.y, r + 1), add(x.z, r + 2), add(x.w, r + 3);
         }
     }
-    if (ref.page >= 0) a.c.weight[slot_weight(a.c, ref, kh)] += sum;
+    if (ref.page >= 0) a.c.weight[slot_weight(a.c, ref, kh)] = had + sum;
 }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }

@@ -542,19 +542,22 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
             if (j >= count || (a.S > 1 && t0 + j >= limit(nt, e))) return -INFINITY;
             return state.x & kMissing ? NAN : z;
         };
-        uint32_t ph[NT][2], pl[NT][2], pt[NT][2];
+        // one vote for all rows: the tiles' chains then run side by side
+        float x[NT][4];
+        bool over = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float x[4];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 s[nt][e] += s1[nt][e];
-                x[e] = fmaf(s[nt][e], TYPE == kE4m3 ? rs[nt][e & 1] : factor, -m[nt][e & 1]);
-                if (partial) x[e] = masked(x[e], nt, e);
+                x[nt][e] = fmaf(s[nt][e], TYPE == kE4m3 ? rs[nt][e & 1] : factor, -m[nt][e & 1]);
+                if (partial) x[nt][e] = masked(x[nt][e], nt, e);
+                over |= x[nt][e] > shift + 8.f;
             }
-            constexpr float most = shift + 8.f;
-            if (__any_sync(~0u, x[0] > most || x[1] > most || x[2] > most || x[3] > most)) {
-                // raise the references to the maxima; l and O follow
+        if (__any_sync(~0u, over)) {
+            // raise the references to the maxima; l and O follow
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
                 float z[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -571,25 +574,34 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                     l[nt][e] *= f;
 #pragma unroll
                     for (int t = 0; t < C::MT; ++t) o[t][nt][e] *= f, o[t][nt][2 + e] *= f;
-                    x[e] = z[e] - ref;
-                    x[2 + e] = z[2 + e] - ref;
+                    x[nt][e] = z[e] - ref;
+                    x[nt][2 + e] = z[2 + e] - ref;
                 }
             }
-            if (a.accumulate) {
-                float *dst = w.scores + ((size_t)state.z * w.score_slots + t0) * rows + 8 * nt + 2 * c;
-                if (g < count)
-                    *reinterpret_cast<float2 *>(dst + g * rows) = make_float2(x[0] + m[nt][0], x[1] + m[nt][1]);
-                if (g + 8 < count)
-                    *reinterpret_cast<float2 *>(dst + (g + 8) * rows) = make_float2(x[2] + m[nt][0], x[3] + m[nt][1]);
-            }
+        }
+        if (a.accumulate) {
+            float *dst = w.scores + ((size_t)state.z * w.score_slots + t0) * rows + 2 * c;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = ex2(x[e]);
-            l[nt][0] += x[0] + x[2];
-            l[nt][1] += x[1] + x[3];
+            for (int nt = 0; nt < NT; ++nt) {
+                if (g < count)
+                    *reinterpret_cast<float2 *>(dst + g * rows + 8 * nt) =
+                        make_float2(x[nt][0] + m[nt][0], x[nt][1] + m[nt][1]);
+                if (g + 8 < count)
+                    *reinterpret_cast<float2 *>(dst + (g + 8) * rows + 8 * nt) =
+                        make_float2(x[nt][2] + m[nt][0], x[nt][3] + m[nt][1]);
+            }
+        }
+        uint32_t ph[NT][2], pl[NT][2], pt[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[nt][e] = ex2(x[nt][e]);
+            l[nt][0] += x[nt][0] + x[nt][2];
+            l[nt][1] += x[nt][1] + x[nt][3];
             // P as a sum of 16-bit parts, transposed into B fragments
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                float u = x[2 * half], v = x[2 * half + 1];
+                float u = x[nt][2 * half], v = x[nt][2 * half + 1];
                 if constexpr (TYPE == kBf16) {
                     const uint32_t h = pack_bf16(u, v);
                     float2 f = unpack_bf16(h);

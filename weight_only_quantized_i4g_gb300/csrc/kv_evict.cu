@@ -80,6 +80,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     __syncthreads();
 
     uint32_t prefix = 0;
+    if (tid == 0) s_digit = s_need = 0;
     if (any) {
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
@@ -180,7 +181,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
         const unsigned below = (1u << lane) - 1u;
         const int rank_tie = base_tie + __popc(tie & below);                // equal ones before this slot
         const bool take = (sure >> lane & 1u) || ((tie >> lane & 1u) && rank_tie < need);
-        if (take) kept[base_sure + __popc(sure & below) + (rank_tie < need ? rank_tie : need)] = t;
+        const int at = base_sure + __popc(sure & below) + (rank_tie < need ? rank_tie : need);
+        if (take && at < N) kept[at] = t;          // at < N always, unless the weights change under the call
         base_sure += __popc(sure), base_tie += __popc(tie);
     }
 }
@@ -193,13 +195,15 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     griddep_launch_dependents();
     griddep_wait();
     const int bh = blockIdx.x, b = bh / a.c.n_heads, h = bh - b * a.c.n_heads, tid = threadIdx.x;
-    const int n = __ldg(a.new_lens + b);
+    const int n = __ldg(a.new_lens + b), len = seq_len(a.lens, b, a.max_len, nullptr);
     for (long long i0 = (long long)blockIdx.y * kMoveSlots; i0 < n; i0 += (long long)gridDim.y * kMoveSlots) {
         const int count = n - i0 < kMoveSlots ? (int)(n - i0) : kMoveSlots;
         __syncthreads();
         if (tid < count) {
             const int i = (int)i0 + tid;
-            const SlotRef s = find_slot(a.c, a.table + (size_t)b * a.table_stride, __ldg(a.kept + (size_t)bh * a.budget + i));
+            const int t = __ldg(a.kept + (size_t)bh * a.budget + i);
+            SlotRef s{-1, 0};
+            if ((unsigned)t < (unsigned)len) s = find_slot(a.c, a.table + (size_t)b * a.table_stride, t);
             const SlotRef d = find_slot(a.c, a.dst_table + (size_t)b * a.dst_stride, i);
             const bool ok = s.page >= 0 && d.page >= 0;
             s_src[tid] = ok ? slot_bytes(a.c, s, h) : -1;
