@@ -87,11 +87,12 @@ class QGError(RuntimeError):
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    try:
+        return t.data_ptr()
+    except AttributeError:
+        if t is None or isinstance(t, int):
+            return t
+        raise
 
 
 _current_stream = None     # how to ask torch for the current stream, once CUDA has been seen to be available

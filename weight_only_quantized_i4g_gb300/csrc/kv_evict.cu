@@ -38,7 +38,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 template <int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictArgs a, int cap) {
     constexpr int kSelWarps = kSelThreads / 32;
-    extern __shared__ uint32_t s_key[];
+    extern __shared__ __align__(16) uint32_t s_key[];
     __shared__ int s_hist[kBins], s_total[kBins];
     __shared__ int s_warp[2][kSelWarps];
     __shared__ int2 s_block[kMaxCluster];
@@ -71,11 +71,38 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
         const SlotRef r = find_slot(a.c, row, t);
         return r.page < 0 ? 0u : weight_key(__ldg(a.c.weight + slot_weight(a.c, r, h)));
     };
-    auto key_at = [&](int t) { return t - r0 < cap ? s_key[t - r0] : key_in_cache(t); };
+    // four keys from t on (t - r0 and cap are multiples of four), 0 past the stretch
+    auto keys_at = [&](int t, uint32_t (&k)[4]) {
+        if (t - r0 < cap) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(s_key + (t - r0));
+            k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
+        } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) k[x] = t + x < r1 ? key_in_cache(t + x) : 0u;
+        }
+    };
     const int in_smem = r1 - r0 < cap ? r1 - r0 : cap;
     if (any) {
-#pragma unroll 8
-        for (int i = tid; i < in_smem; i += kSelThreads) s_key[i] = key_in_cache(r0 + i);
+        constexpr int kAhead = 8;                  // pages, then weights, eight of each in flight
+        for (int i = tid; i < in_smem; i += kAhead * kSelThreads) {
+            int page[kAhead], off[kAhead];
+            float wt[kAhead];
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) {
+                int index;
+                split_slot(a.c, r0 + i + x * kSelThreads, &index, &off[x]);
+                page[x] = i + x * kSelThreads < in_smem ? __ldg(row + index) : -1;
+            }
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) {
+                const bool ok = (unsigned)page[x] < (unsigned)a.c.n_pages;
+                wt[x] = ok ? __ldg(a.c.weight + slot_weight(a.c, SlotRef{page[x], off[x]}, h)) : 0.f;
+            }
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x)
+                if (i + x * kSelThreads < in_smem)
+                    s_key[i + x * kSelThreads] = (unsigned)page[x] < (unsigned)a.c.n_pages ? weight_key(wt[x]) : 0u;
+        }
     }
     __syncthreads();
 
@@ -88,11 +115,13 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
             for (int i = tid; i < bins; i += kSelThreads) s_hist[i] = 0;
             __syncthreads();
             // additions of one to an address that a warp shares are combined in hardware
-#pragma unroll 4
-            for (int t = r0 + tid; t < r1; t += kSelThreads) {
-                const uint32_t k = key_at(t);
-                if (t >= lo && t < hi && (pass == 0 || k >> done == prefix >> done))
-                    atomicAdd(&s_hist[(k >> shift) & (bins - 1)], 1);
+            for (int t = r0 + 4 * tid; t < r1; t += 4 * kSelThreads) {
+                uint32_t k[4];
+                keys_at(t, k);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if (t + x < r1 && t + x >= lo && t + x < hi && (pass == 0 || k[x] >> done == prefix >> done))
+                        atomicAdd(&s_hist[(k[x] >> shift) & (bins - 1)], 1);
             }
             int *total = s_hist;
             if (ranks > 1) {
@@ -129,10 +158,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
             }
             if (lane == 31) s_warp[0][warp] = inc;
             __syncthreads();
-            int before = inc - sum;
+            int before = inc - sum, others = lane < warp && lane < kSelWarps ? s_warp[0][lane] : 0;
 #pragma unroll
-            for (int x = 0; x < kSelWarps; ++x)
-                if (x < warp) before += s_warp[0][x];
+            for (int o = 16; o; o >>= 1) others += __shfl_xor_sync(~0u, others, o);
+            before += others;
             if (before < need && need <= before + sum) {
 #pragma unroll
                 for (int i = 0; i < kBins / kSelThreads; ++i) {
@@ -146,20 +175,32 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
             __syncthreads();
         }
     }
-    // Emit in slot order: every warp counts its stretch (kept for sure, and
-    // equal to the threshold), the counts before it are summed, then it writes.
+    // Emit in slot order, four neighbouring slots a lane: every warp counts its
+    // stretch (kept for sure, and equal to the threshold), the counts before it
+    // are summed, then it writes.
     const int t0 = r0 + warp * per_warp, t1 = t0 + per_warp < r1 ? t0 + per_warp : r1;
-    auto flags = [&](int t, unsigned *sure, unsigned *tie) {
-        const bool in = t < t1, safe = in && (t < lo || t >= hi);
-        const uint32_t k = in && !safe && any ? key_at(t) : 0u;
-        *sure = __ballot_sync(~0u, safe || (in && any && k > prefix));
-        *tie = __ballot_sync(~0u, in && !safe && any && k == prefix);
+    // bits 0-3: slot t + x is kept for sure; bits 4-7: it ties with the threshold
+    auto flags = [&](int t) {
+        uint32_t k[4] = {0u, 0u, 0u, 0u};
+        if (any && t < t1) keys_at(t, k);
+        unsigned f = 0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const bool in = t + x < t1, safe = t + x < lo || t + x >= hi;
+            if (in && (safe || (any && k[x] > prefix))) f |= 1u << x;
+            if (in && !safe && any && k[x] == prefix) f |= 16u << x;
+        }
+        return f;
     };
     int sure_n = 0, tie_n = 0;
-    for (int t = t0 + lane; t - lane < t1; t += 32) {
-        unsigned sure, tie;
-        flags(t, &sure, &tie);
-        sure_n += __popc(sure), tie_n += __popc(tie);
+    for (int t = t0 + 4 * lane; t < t1; t += 128) {
+        const unsigned f = flags(t);
+        sure_n += __popc(f & 15u), tie_n += __popc(f >> 4);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        sure_n += __shfl_xor_sync(~0u, sure_n, o);
+        tie_n += __shfl_xor_sync(~0u, tie_n, o);
     }
     if (lane == 0) s_warp[0][warp] = sure_n, s_warp[1][warp] = tie_n;
     __syncthreads();
@@ -175,29 +216,42 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
         cluster.sync();                            // also the last access to another block's memory
         for (int x = 0; x < rank; ++x) base_sure += s_block[x].x, base_tie += s_block[x].y;
     }
-    for (int t = t0 + lane; t - lane < t1; t += 32) {
-        unsigned sure, tie;
-        flags(t, &sure, &tie);
-        const unsigned below = (1u << lane) - 1u;
-        const int rank_tie = base_tie + __popc(tie & below);                // equal ones before this slot
-        const bool take = (sure >> lane & 1u) || ((tie >> lane & 1u) && rank_tie < need);
-        const int at = base_sure + __popc(sure & below) + (rank_tie < need ? rank_tie : need);
-        if (take && at < N) kept[at] = t;          // at < N always, unless the weights change under the call
-        base_sure += __popc(sure), base_tie += __popc(tie);
+    for (int t = t0 + 4 * lane; t - 4 * lane < t1; t += 128) {
+        const unsigned f = flags(t);
+        // both counts of the lanes before this one: up to 128 each
+        const int mine = __popc(f & 15u) | __popc(f >> 4) << 16;
+        int inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(~0u, inc, o);
+            if (lane >= o) inc += v;
+        }
+        int sure = base_sure + ((inc - mine) & 0xFFFF), tie = base_tie + ((inc - mine) >> 16);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int at = sure + (tie < need ? tie : need);
+            const bool is_sure = f >> x & 1u, is_tie = f >> (4 + x) & 1u;
+            // at < N always, unless the weights change under the call
+            if ((is_sure || (is_tie && tie < need)) && at < N) kept[at] = t + x;
+            sure += is_sure, tie += is_tie;
+        }
+        const int all = __shfl_sync(~0u, inc, 31);
+        base_sure += all & 0xFFFF, base_tie += all >> 16;
     }
 }
 
-// Copies kept slots, 64 a block: their places are looked up once, then every
-// thread has eight 16-byte loads in flight before its stores.
-constexpr int kMoveThreads = 256, kMoveSlots = 64, kMoveAhead = 4;
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a, FastDiv chunks) {
+// Copies kept slots, `slots` a block: their places are looked up once, then
+// every thread has eight 16-byte loads in flight before its stores.
+constexpr int kMoveThreads = 256, kMoveSlots = 256, kMoveAhead = 4;
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a, FastDiv chunks,
+                                                                  int slots) {
     __shared__ long long s_src[kMoveSlots], s_dst[kMoveSlots];
     griddep_launch_dependents();
     griddep_wait();
     const int bh = blockIdx.x, b = bh / a.c.n_heads, h = bh - b * a.c.n_heads, tid = threadIdx.x;
     const int n = __ldg(a.new_lens + b), len = seq_len(a.lens, b, a.max_len, nullptr);
-    for (long long i0 = (long long)blockIdx.y * kMoveSlots; i0 < n; i0 += (long long)gridDim.y * kMoveSlots) {
-        const int count = n - i0 < kMoveSlots ? (int)(n - i0) : kMoveSlots;
+    for (long long i0 = (long long)blockIdx.y * slots; i0 < n; i0 += (long long)gridDim.y * slots) {
+        const int count = n - i0 < slots ? (int)(n - i0) : slots;
         __syncthreads();
         if (tid < count) {
             const int i = (int)i0 + tid;
@@ -250,18 +304,26 @@ int launch_select(const EvictArgs &a, int ranks, cudaStream_t st) {
 }
 
 int run_kv_evict(const EvictArgs &a, cudaStream_t st) {
-    // As many blocks per head as have an SM each and 1024 slots or more; 1024
-    // threads where a block has an SM to itself, else 512 (up to four an SM).
+    // As many blocks per head as have an SM each and 1024 slots or more (two
+    // an SM did not all start at once as clusters of eight: three sequences of
+    // 100k slots 143 us against 130).  1024 threads where a block has many
+    // slots (24 sequences of up to 8191, 8 heads: the longest heads took 30 us
+    // with 512); else 512, or 256, four blocks an SM, where there are more
+    // heads than SMs (200 sequences of 1000 slots, 8 heads: 187 us a call with
+    // 512, 168 with 256; one of 1280: 11.7 and 13.0).
     const long long heads = (long long)a.n_seq * a.c.n_heads;
     int ranks = 1;
-    while (ranks < kMaxCluster && heads * ranks * 2 <= num_sms() + num_sms() / 4 && ranks * 2048LL <= a.max_len) ranks *= 2;
-    int rc = heads * ranks <= num_sms() ? launch_select<1024>(a, ranks, st) : launch_select<512>(a, ranks, st);
+    while (ranks < kMaxCluster && heads * ranks * 2 <= num_sms() && ranks * 2048LL <= a.max_len) ranks *= 2;
+    int rc = a.max_len / ranks > 2048 ? launch_select<1024>(a, ranks, st)
+             : heads * ranks <= num_sms() ? launch_select<512>(a, ranks, st) : launch_select<256>(a, ranks, st);
     const int most = a.max_len < a.budget ? a.max_len : a.budget;
     if (rc != kOk || most == 0) return rc;
-    const int row_b = a.c.dim * (a.c.type == kE4m3 ? 1 : 2);
-    const int blocks = (most + kMoveSlots - 1) / kMoveSlots;
+    const int chunks = a.c.dim * (a.c.type == kE4m3 ? 1 : 2) / 16;
+    int slots = kMoveAhead * kMoveThreads / chunks;               // one round of loads a block
+    if (slots > kMoveSlots) slots = kMoveSlots;
+    const int blocks = (most + slots - 1) / slots;
     return launch_pdl("qg_kv_evict", evict_move_kernel, dim3(a.n_seq * a.c.n_heads, blocks < 65535 ? blocks : 65535),
-                      kMoveThreads, 0, st, a, fast_div(row_b / 16));
+                      kMoveThreads, 0, st, a, fast_div(chunks), slots);
 }
 
 }  // namespace qg
