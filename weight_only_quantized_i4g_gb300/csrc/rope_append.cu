@@ -56,11 +56,11 @@ __device__ __forceinline__ void store1(char *base, int type, int d, float x, flo
     }
 }
 
-// VEC: rows, sizes and pointers allow four elements per access (every thread
-// then takes 8 elements of a head, two such groups); otherwise a pair.
+// VEC: rows, sizes and pointers allow four elements per access; a thread then
+// takes units of 8 elements of a head (two such groups), otherwise of a pair.
 template <int IN, bool VEC>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeArgs a,
-                                                                   int heads_per_block) {
+                                                                   int heads_per_block, FastDiv units_div) {
     __shared__ float s_cos[kMaxPairs], s_sin[kMaxPairs];
     griddep_launch_dependents();
     griddep_wait();
@@ -69,6 +69,37 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
     const int heads = a.n_q_heads + 2 * a.c.n_heads;
     const int h0 = blockIdx.y * heads_per_block;
     const int h1 = h0 + heads_per_block < heads ? h0 + heads_per_block : heads;
+
+    // units of work: kUnit elements of a head, two halves of kHalf
+    constexpr int kUnit = VEC ? 8 : 2, kHalf = kUnit / 2;
+    const size_t row = (size_t)t * a.qkv_stride;
+    const int units = D / kUnit, work = (h1 - h0) * units;
+    struct Unit { float x[kHalf], y[kHalf]; };
+    // where unit u's halves start, and the first pair it holds (-1: none)
+    auto halves = [&](int u, int *d0, int *d1) {
+        *d0 = kUnit * u, *d1 = *d0 + kHalf;
+        if (*d0 >= a.rotary) return -1;
+        const int j = kHalf * u;
+        if (!a.interleaved) *d0 = j, *d1 = j + half;
+        return j;
+    };
+    auto load = [&](int i) {
+        Unit v;
+        const int hh = quotient(i, units_div), u = i - hh * units;
+        const size_t at = row + (size_t)(h0 + hh) * D;
+        int d0, d1;
+        halves(u, &d0, &d1);
+        if constexpr (VEC) {
+            load4<IN>(a.qkv, at + d0, v.x);
+            load4<IN>(a.qkv, at + d1, v.y);
+        } else {
+            v.x[0] = load1<IN>(a.qkv, at + d0), v.y[0] = load1<IN>(a.qkv, at + d1);
+        }
+        return v;
+    };
+    // the first unit is on its way while the angles and the slot are found
+    Unit next = {};
+    if ((int)threadIdx.x < work) next = load(threadIdx.x);
 
     // The angle is formed and reduced to one turn in 64 bits: in binary32 it
     // would be off by pos * 2^-24 radians, 0.06 at position 2^20.
@@ -90,67 +121,45 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
     }
     __syncthreads();
 
-    const size_t row = (size_t)t * a.qkv_stride;
-    constexpr int kUnit = VEC ? 8 : 2;
-    const int units = D / kUnit, work = (h1 - h0) * units;
     for (int i = threadIdx.x; i < work; i += kRopeThreads) {
-        const int hh = i / units, u = i - hh * units, h = h0 + hh;
-        const size_t at = row + (size_t)h * D;
-        const bool turn = h < a.n_q_heads + a.c.n_heads;
+        Unit v = next;
+        if (i + kRopeThreads < work) next = load(i + kRopeThreads);
+        const int hh = quotient(i, units_div), u = i - hh * units, h = h0 + hh;
+        const bool is_q = h < a.n_q_heads, is_v = h >= a.n_q_heads + a.c.n_heads;
+        int d0, d1;
+        const int j = halves(u, &d0, &d1);
+        if (j >= 0 && !is_v) {
+#pragma unroll
+            for (int e = 0; e < kHalf; ++e) {
+                // pair e is (x[e], y[e]), or elements 2e, 2e + 1 of the unit
+                const int at = 2 * e % kHalf;
+                const bool split = !VEC || !a.interleaved, low = 2 * e < kHalf;
+                float &p = split ? v.x[e] : low ? v.x[at] : v.y[at];
+                float &q = split ? v.y[e] : low ? v.x[(at + 1) % kHalf] : v.y[(at + 1) % kHalf];
+                const float p0 = p, cs = s_cos[j + e], sn = s_sin[j + e];
+                p = p0 * cs - q * sn;
+                q = q * cs + p0 * sn;
+            }
+        }
         char *base;
         float scale = 1.f;
         int type = a.c.type;
-        if (h < a.n_q_heads) {
+        if (is_q) {
             base = static_cast<char *>(a.q) + ((size_t)t * a.n_q_heads + h) * D * 2;
             type = a.q_type;
         } else {
             if (ref.page < 0) continue;
-            const bool is_k = h < a.n_q_heads + a.c.n_heads;
-            const int kh = h - a.n_q_heads - (is_k ? 0 : a.c.n_heads);
-            base = (is_k ? a.c.k : a.c.v) + slot_bytes(a.c, ref, kh);
-            if (type == kE4m3) scale = __ldg((is_k ? a.c.k_scale : a.c.v_scale) + kh);
-            if (is_k && u == 0 && a.c.weight) a.c.weight[slot_weight(a.c, ref, kh)] = 0.f;
+            const int kh = h - a.n_q_heads - (is_v ? a.c.n_heads : 0);
+            base = (is_v ? a.c.v : a.c.k) + slot_bytes(a.c, ref, kh);
+            if (type == kE4m3) scale = __ldg((is_v ? a.c.v_scale : a.c.k_scale) + kh);
+            if (!is_v && u == 0 && a.c.weight) a.c.weight[slot_weight(a.c, ref, kh)] = 0.f;
         }
-        if (VEC) {
-            // first and second group of four, and the pair of the first element
-            int d0 = 8 * u, d1 = d0 + 4, j = -1;
-            if (d0 < a.rotary) {
-                j = 4 * u;
-                if (!a.interleaved) d0 = j, d1 = j + half;
-            }
-            float x[4], y[4];
-            load4<IN>(a.qkv, at + d0, x);
-            load4<IN>(a.qkv, at + d1, y);
-            if (turn && j >= 0) {
-                const float4 c = *reinterpret_cast<const float4 *>(&s_cos[j]);
-                const float4 s = *reinterpret_cast<const float4 *>(&s_sin[j]);
-                const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    // pair e is (x[e], y[e]), or elements 2e, 2e + 1 of the eight
-                    float &p = !a.interleaved ? x[e] : e < 2 ? x[2 * e & 3] : y[2 * e & 3];
-                    float &q = !a.interleaved ? y[e] : e < 2 ? x[(2 * e + 1) & 3] : y[(2 * e + 1) & 3];
-                    const float p0 = p;
-                    p = p0 * cc[e] - q * ss[e];
-                    q = q * cc[e] + p0 * ss[e];
-                }
-            }
-            store4(base, type, d0, x, scale);
-            store4(base, type, d1, y, scale);
+        if constexpr (VEC) {
+            store4(base, type, d0, v.x, scale);
+            store4(base, type, d1, v.y, scale);
         } else {
-            int d0 = 2 * u, d1 = d0 + 1, j = -1;
-            if (d0 < a.rotary) {
-                j = u;
-                if (!a.interleaved) d0 = j, d1 = j + half;
-            }
-            float p = load1<IN>(a.qkv, at + d0), q = load1<IN>(a.qkv, at + d1);
-            if (turn && j >= 0) {
-                const float p0 = p, c = s_cos[j], s = s_sin[j];
-                p = p0 * c - q * s;
-                q = q * c + p0 * s;
-            }
-            store1(base, type, d0, p, scale);
-            store1(base, type, d1, q, scale);
+            store1(base, type, d0, v.x[0], scale);
+            store1(base, type, d1, v.y[0], scale);
         }
     }
 }
@@ -163,8 +172,9 @@ int launch(const RopeArgs &a, bool vec, cudaStream_t st) {
     if (groups > heads) groups = heads;
     const int per = (int)((heads + groups - 1) / groups);
     const dim3 grid(a.T, (heads + per - 1) / per);
-    return vec ? launch_pdl("qg_rope_append", rope_append_kernel<IN, true>, grid, kRopeThreads, 0, st, a, per)
-               : launch_pdl("qg_rope_append", rope_append_kernel<IN, false>, grid, kRopeThreads, 0, st, a, per);
+    const FastDiv units = fast_div(a.c.dim / (vec ? 8 : 2));
+    return vec ? launch_pdl("qg_rope_append", rope_append_kernel<IN, true>, grid, kRopeThreads, 0, st, a, per, units)
+               : launch_pdl("qg_rope_append", rope_append_kernel<IN, false>, grid, kRopeThreads, 0, st, a, per, units);
 }
 
 }  // namespace
