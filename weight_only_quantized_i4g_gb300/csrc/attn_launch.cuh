@@ -7,31 +7,37 @@
 namespace qg {
 
 struct AttnPlan {
-    int dp, nt;         // padded head size, tiles of 8 rows per segment
-    int warps;
+    int dp, rows;       // padded head size, rows of a segment
     int box_bytes;      // bytes of a row that one copy moves
+    size_t piece_rows;  // rows of O that all warps of a block hold
     size_t smem;        // without the lengths
 };
 
-// The smallest padded head size (the padding is not read from memory), and
-// one, two or (64 dimensions) four tiles of 8 rows a warp.  More rows make
-// several segments that read K and V each: at 128 dimensions four tiles spill
-// (48 bf16 sequences, 32 rows: 321 us against 272 with two segments of two
-// tiles; 64 rows: 632 against 543; e4m3, 32 rows: 367 against 263).
+// The smallest padded head size (the padding is not read from memory); then as
+// many tiles of 8 rows a warp as its registers take (four at 64 dimensions,
+// two at 128, one at 256: four at 128 spill), and groups of two or four warps
+// for more rows.  More than a group's rows are further segments.  48 ragged
+// bf16 sequences, 128 dimensions, 8 cache heads, 32 and 64 rows: 272 and 543 us
+// with segments of 16 rows, 321 and 632 with four tiles a warp.
 template <int TYPE, class Fn>
 auto attn_dispatch(int rows, int dim, Fn fn) {
-    const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
     if (dim <= 64)
-        return nt == 1 ? fn(AttnCfg<TYPE, 64, 1>()) : nt == 2 ? fn(AttnCfg<TYPE, 64, 2>()) : fn(AttnCfg<TYPE, 64, 4>());
-    if (dim <= 128) return nt == 1 ? fn(AttnCfg<TYPE, 128, 1>()) : fn(AttnCfg<TYPE, 128, 2>());
-    return nt == 1 ? fn(AttnCfg<TYPE, 256, 1>()) : fn(AttnCfg<TYPE, 256, 2>());
+        return rows <= 8    ? fn(AttnCfg<TYPE, 64, 1, 1>())
+               : rows <= 16 ? fn(AttnCfg<TYPE, 64, 2, 1>())
+               : rows <= 32 ? fn(AttnCfg<TYPE, 64, 4, 1>()) : fn(AttnCfg<TYPE, 64, 4, 2>());
+    if (dim <= 128)
+        return rows <= 8    ? fn(AttnCfg<TYPE, 128, 1, 1>())
+               : rows <= 16 ? fn(AttnCfg<TYPE, 128, 2, 1>())
+               : rows <= 32 ? fn(AttnCfg<TYPE, 128, 2, 2>()) : fn(AttnCfg<TYPE, 128, 2, 4>());
+    return rows <= 8    ? fn(AttnCfg<TYPE, 256, 1, 1>())
+           : rows <= 16 ? fn(AttnCfg<TYPE, 256, 1, 2>()) : fn(AttnCfg<TYPE, 256, 1, 4>());
 }
 
 template <int TYPE>
 AttnPlan attn_plan(int rows, int dim) {
     return attn_dispatch<TYPE>(rows, dim, [](auto cfg) {
         using C = decltype(cfg);
-        return AttnPlan{C::DP, C::NT, C::W, C::BB, attn_fixed_smem<C>()};
+        return AttnPlan{C::DP, C::rows, C::BB, (size_t)C::W * C::warp_rows, attn_fixed_smem<C>()};
     });
 }
 
@@ -41,7 +47,7 @@ int launch_attn_stream(const AttnArgs &a, const AttnWork &w, const AttnPlan &pl,
     return attn_dispatch<TYPE>(a.S * a.group, a.c.dim, [&](auto cfg) {
         using C = decltype(cfg);
         const size_t smem = pl.smem + (2 * (size_t)a.n_seq + 1) * sizeof(int);
-        auto *kernel = attn_stream_kernel<TYPE, C::DP, C::NT>;
+        auto *kernel = attn_stream_kernel<TYPE, C::DP, C::NT, C::GW>;
         set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), 232448);
         return launch_pdl("qattn_paged", kernel, dim3(w.ctas), dim3(C::threads), smem, st, a, w, maps[0], maps[1]);
     });

@@ -166,7 +166,7 @@ Layout layout(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int
     Layout y;
     const int R = S * (n_q_heads / c.n_heads);
     y.pl = plan_of(c.type, R, c.dim);
-    y.rows = 8 * y.pl.nt;
+    y.rows = y.pl.rows;
     y.row_tiles = (R + y.rows - 1) / y.rows;
     y.score_slots = max_len;
     y.seqs = n_seq < kAttnMaxSeq ? n_seq : kAttnMaxSeq;
@@ -193,7 +193,7 @@ Layout layout(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int
     };
     y.part_o = take(y.whole ? 0 : 2 * ctas * tile_f);
     y.part_ml = take(y.whole ? 0 : 2 * ctas * y.rows * sizeof(float2));
-    y.head_o = take(y.whole ? 0 : ctas * y.pl.warps * tile_f);
+    y.head_o = take(y.whole ? 0 : ctas * y.pl.piece_rows * y.pl.dp * 4);
     y.open = take(y.whole ? 0 : ctas * sizeof(int2));
     y.span = take(accumulate ? (size_t)segments * sizeof(int2) : 0);
     y.lse = take(accumulate ? (size_t)y.seqs * S * n_q_heads * 4 : 0);

@@ -7,8 +7,10 @@
 // by HBM and everything serves keeping its reads in flight.
 //
 // Work.  The rows of one sequence that share a key-value head, R = S * group,
-// form tiles of 8 * NT rows; a (sequence, head, tile) is a segment of steps of
-// up to 16 slots of one page.  All segments' steps, laid end to end, are cut
+// form tiles; a (sequence, head, tile) is a segment of steps of up to 16 slots
+// of one page.  A warp does 8 * NT rows; where there are more, GW warps share a
+// ring and each does its rows of the same steps (so K and V come from HBM and
+// L2 once for up to 64 rows).  Below, a warp stands for such a group.  All segments' steps, laid end to end, are cut
 // into one equal range per block (one block an SM) and each range into one per
 // warp: unequal lengths balance without the host knowing them.  A segment
 // counts kSegmentCost steps more than it has, for its Q and its end.  A warp keeps
@@ -61,7 +63,7 @@ constexpr int kSegmentCost = 2;       // what starting and ending a segment take
 struct AttnWork {
     float *part_o;      // [ctas][2][rows][DP]: pieces a block leaves open, at its start (0) and end (1)
     float2 *part_ml;    // [ctas][2][rows]: their maxima (log2 units) and sums
-    float *head_o;      // [ctas][warps][rows][DP]: pieces a warp finishes before its range ends
+    float *head_o;      // [ctas][warps][its rows][DP]: pieces a warp finishes before its range ends
     int2 *open;         // [ctas]: {segment a block leaves open at its end or -1, blocks it spans}
     int2 *span;         // accumulate: [segment]: {its first block, blocks it spans}
     float *scores;      // accumulate: z in log2 units, [segment][slot][rows]
@@ -75,11 +77,11 @@ struct AttnWork {
     FastDiv tiles_div, row_tiles_div, group_div, page_steps_div;
 };
 
-template <int TYPE, int DP_, int NT_>
+template <int TYPE, int DP_, int NT_, int GW_>
 struct AttnCfg {
-    static constexpr int DP = DP_, NT = NT_;
+    static constexpr int DP = DP_, NT = NT_, GW = GW_;
     static constexpr int ESZ = TYPE == kE4m3 ? 1 : 2;
-    static constexpr int rows = 8 * NT;
+    static constexpr int warp_rows = 8 * NT, rows = GW * warp_rows;   // of a warp, of a segment
     static constexpr int KE = 16 / ESZ;               // elements of a K chunk
     static constexpr int NI = DP * ESZ / 64;          // K chunks a thread holds per slot (4 threads a slot)
     static constexpr int E = DP / 8 < KE ? DP / 8 : KE;   // elements of a V chunk (8 threads a slot)
@@ -93,12 +95,15 @@ struct AttnCfg {
     // as many warps as the registers of O, Q and S allow (16, 12 or 8 an SM)
     static constexpr int regs = (ESZ == 1 ? 85 : 70) + 4 * MT * NT + NT * NI * (ESZ == 1 ? 8 : 4) + 8 * NT;
     static constexpr int W0 = regs <= 128 ? 16 : regs <= 168 ? 12 : 8;
-    static constexpr int W = stage > 8192 ? 4 : W0;
+    static constexpr int W = GW > 1 ? 8 : stage > 8192 ? 4 : W0;
+    static constexpr int G = W / GW;                  // groups, a ring each
+    // 8 rows of O on their way out; a lone warp takes the stage it has just read
+    static constexpr int slab = GW > 1 ? 32 * DP : 0;
     // up to 192 KB of copies in flight
-    static constexpr int NS0 = 196608 / (W * stage);
-    static constexpr int NS = NS0 > 6 ? 6 : NS0;
-    static constexpr int ring = NS * stage;           // per warp
-    static_assert(ring >= rows * DP * 4, "a warp's open piece takes the place of its ring");
+    static constexpr int NS0 = (196608 - W * slab) / (G * stage);
+    static constexpr int NS = GW == 1 ? (NS0 > 6 ? 6 : NS0) : (NS0 > 8 ? 8 : NS0);
+    static constexpr int ring = NS * stage;           // per group
+    static_assert(ring >= rows * DP * 4, "an open piece takes the place of its ring");
     static constexpr int threads = 32 * W;
 };
 
@@ -127,7 +132,8 @@ __device__ __forceinline__ int slab_place(int r, int x) {
 template <class C>
 __host__ __device__ constexpr size_t attn_fixed_smem() {
     // 1 KB for the copies' alignment, then as laid out in the kernel
-    return 1024 + (size_t)C::W * C::ring + C::W * C::NS * (8 + 16) + C::W * 2 * C::rows * sizeof(float2) + C::W * 2 * 8;
+    return 1024 + (size_t)C::G * C::ring + C::W * C::slab + C::G * C::NS * (8 + 8 + 16) +
+           C::G * 2 * C::rows * sizeof(float2) + C::G * 2 * 8;
 }
 
 // Box at element x, slot t, head h of page p.
@@ -277,29 +283,32 @@ __device__ __forceinline__ Place locate(int u, const int *s_prefix, int n, const
     return p;
 }
 
-template <int TYPE, int DP_, int NT_>
-__global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
+template <int TYPE, int DP_, int NT_, int GW_>
+__global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
     attn_stream_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnWork w,
                        const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
-    using C = AttnCfg<TYPE, DP_, NT_>;
-    constexpr int DP = C::DP, NT = C::NT, W = C::W, NS = C::NS, NI = C::NI, E = C::E, NQ = C::NQ, rows = C::rows;
+    using C = AttnCfg<TYPE, DP_, NT_, GW_>;
+    constexpr int DP = C::DP, NT = C::NT, W = C::W, GW = C::GW, G = C::G, NS = C::NS, NI = C::NI, E = C::E, NQ = C::NQ;
+    constexpr int rows = C::rows, warp_rows = C::warp_rows;
     // flags of a step: its page is not in the pool; first and last of its segment
     constexpr int kMissing = 32, kFirst = 64, kLast = 128;
     extern __shared__ char smem_raw[];
     char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    uint64_t *s_bar = reinterpret_cast<uint64_t *>(smem + W * C::ring);       // [W][NS]
-    float2 *s_ml = reinterpret_cast<float2 *>(s_bar + W * NS);                // [W][2][rows]
-    int2 *s_piece = reinterpret_cast<int2 *>(s_ml + W * 2 * rows);            // [W][2]: {segment or -1, 1: ended | 2: in head_o}
-    // [W][NS] of a step in the ring: its slots and flags, its first slot, its
+    uint64_t *s_bar = reinterpret_cast<uint64_t *>(smem + G * C::ring + W * C::slab);   // [G][NS]: a step has landed
+    uint64_t *s_free = s_bar + G * NS;                                        // [G][NS]: all warps have read it
+    float2 *s_ml = reinterpret_cast<float2 *>(s_free + G * NS);               // [G][2][rows]
+    int2 *s_piece = reinterpret_cast<int2 *>(s_ml + G * 2 * rows);            // [G][2]: {segment or -1, 1: ended | 2: in head_o}
+    // [G][NS] of a step in the ring: its slots and flags, its first slot, its
     // segment, the first slot that some row of the sequence does not see
-    int4 *s_state = reinterpret_cast<int4 *>(s_piece + W * 2);
-    int *s_prefix = reinterpret_cast<int *>(s_state + W * NS);                // [n + 1]
+    int4 *s_state = reinterpret_cast<int4 *>(s_piece + G * 2);
+    int *s_prefix = reinterpret_cast<int *>(s_state + G * NS);                // [n + 1]
     int *s_len = s_prefix + a.n_seq + 1;                                      // [n]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int n = a.n_seq, D = a.c.dim;
     const int tiles = w.tiles;
-    if (tid < W * NS) mbar_init(&s_bar[tid], 1);
-    if (tid < W * 2) s_piece[tid] = make_int2(-1, 0);
+    const int group = warp / GW, mate = warp % GW, my_rows = mate * warp_rows;   // rows of the segment before the warp's
+    if (tid < G * NS) mbar_init(&s_bar[tid], 1), mbar_init(&s_free[tid], GW);
+    if (tid < G * 2) s_piece[tid] = make_int2(-1, 0);
     mbar_fence_init();
 
     griddep_launch_dependents();
@@ -314,7 +323,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
         c0 = cost ? c1 - cost + kSegmentCost : c1;
     } else {
         const int total = s_prefix[n] * tiles;
-        chunk = units_per_block(total, gridDim.x, W);
+        chunk = units_per_block(total, gridDim.x, G);
         c0 = (int)(blockIdx.x * chunk) < total ? blockIdx.x * chunk : total;
         c1 = c0 + chunk < total ? c0 + chunk : total;
         if (tid == 0) w.open[blockIdx.x] = make_int2(-1, 0);
@@ -334,17 +343,17 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
     if (c0 >= c1) return;
 
     // the warp's first step, and how many it has
-    Place ip = locate(c0 + (int)((long long)(c1 - c0) * warp / W), s_prefix, n, w);
+    Place ip = locate(c0 + (int)((long long)(c1 - c0) * group / G), s_prefix, n, w);
     int left;
     {
-        const Place end = locate(c0 + (int)((long long)(c1 - c0) * (warp + 1) / W), s_prefix, n, w);
+        const Place end = locate(c0 + (int)((long long)(c1 - c0) * (group + 1) / G), s_prefix, n, w);
         left = end.seg * end.n + end.i - (ip.seg * ip.n + ip.i);
         for (int b = ip.b; b < end.b; ++b) {
             const int cost = s_prefix[b + 1] - s_prefix[b];
             if (cost) left += tiles * (cost - kSegmentCost);
         }
     }
-    char *ring = smem + warp * C::ring;
+    char *ring = smem + group * C::ring;
     const uint32_t ring_a = smem_addr(ring);
 
     // ---- loads: the page of the next step is looked up one step early ----
@@ -352,22 +361,23 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
     uint64_t policy;
     if (w.row_tiles == 1) asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
     else asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
-    int to_issue = left, istage = 0, look_page = 0;
+    int to_issue = mate == 0 ? left : 0, istage = 0, look_page = 0;
     auto look = [&]() {
         if (to_issue == 0) return;
         look_page = __ldg(a.table + (size_t)ip.b * a.table_stride + ip.page);
     };
-    auto issue = [&]() {
+    // reuse: wait until the group's other warps have read what the stage held
+    auto issue = [&](bool reuse, uint32_t phase) {
         if (to_issue > 0) {
-            if (lane == 0) {
+            if (lane == 0 && (GW == 1 || !reuse || mbar_wait(&s_free[group * NS + istage], phase))) {
                 const int slot = 16 * ip.sub, before = ip.page * a.c.page, len = s_len[ip.b];
                 int count = (len - before < a.c.page ? len - before : a.c.page) - slot;
                 if (count > 16) count = 16;
-                uint64_t *bar = &s_bar[warp * NS + istage];
+                uint64_t *bar = &s_bar[group * NS + istage];
                 const uint32_t dst = ring_a + istage * C::stage;
                 const int kh = quotient(ip.seg, w.row_tiles_div);
                 const bool there = (unsigned)look_page < (unsigned)a.c.n_pages;
-                s_state[warp * NS + istage] =
+                s_state[group * NS + istage] =
                     make_int4(count | (there ? 0 : kMissing) | (ip.i == 0 ? kFirst : 0) | (ip.i + 1 == ip.n ? kLast : 0),
                               before + slot, ip.b * tiles + ip.seg, len - a.S + 1);
                 if (there) {
@@ -401,7 +411,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
     };
     look();
 #pragma unroll 1
-    for (int i = 0; i < NS; ++i) issue();
+    for (int i = 0; i < NS; ++i) issue(false, 0u);
 
     // ---- the warp's range ----
     float o[C::MT][NT][4];
@@ -418,9 +428,12 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
 
 #pragma unroll 1
     for (; left > 0; --left) {
-        if (fresh) {
+        // a lone warp can load Q while the step is on its way
+        bool landed = true;
+        if (GW > 1) landed = __all_sync(~0u, mbar_wait(&s_bar[group * NS + stage], phase));
+        if (fresh && landed) {
             __syncwarp();                             // lane 0 wrote the state
-            const int4 state = s_state[warp * NS + stage];
+            const int4 state = s_state[group * NS + stage];
             const int b = quotient(state.z, w.tiles_div), sg = state.z - b * tiles;
             const int kh = quotient(sg, w.row_tiles_div), tile = sg - kh * w.row_tiles;
             fresh = false;
@@ -428,7 +441,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
             // Q as the B operand: row g of each 8, the thread's chunks
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const RowRef r = row_ref(a, w, b, kh, tile * rows + 8 * nt + g);
+                const RowRef r = row_ref(a, w, b, kh, tile * rows + my_rows + 8 * nt + g);
                 const uint16_t *q = static_cast<const uint16_t *>(a.q) + ((size_t)b * a.S + r.s) * a.q_stride +
                                     (size_t)r.q_head * D;
                 if constexpr (TYPE != kE4m3) {
@@ -486,17 +499,18 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
             }
         }
 
-        if (!__all_sync(~0u, mbar_wait(&s_bar[warp * NS + stage], phase))) {
+        if (GW == 1) landed = __all_sync(~0u, mbar_wait(&s_bar[group * NS + stage], phase));
+        if (!landed) {
             // a copy did not land in time: no result, but let those in flight land before the block ends
             if (lane == 0) raise_device_error(a.err, kErrTimeout);
-            for (; left > to_issue; --left) {
-                mbar_wait(&s_bar[warp * NS + stage], phase);
+            for (; mate == 0 && left > to_issue; --left) {
+                mbar_wait(&s_bar[group * NS + stage], phase);
                 if (++stage == NS) stage = 0, phase ^= 1u;
             }
             break;
         }
         // published by the arrival that the wait has seen
-        const int4 state = s_state[warp * NS + stage];
+        const int4 state = s_state[group * NS + stage];
         const int count = state.x & 31, t0 = state.y, hidden_from = state.w;
         const uint32_t src = ring_a + stage * C::stage, src_v = src + C::NB * C::box;
 
@@ -533,7 +547,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
         auto limit = [&](int nt, int e) {
             const int sg = state.z - quotient(state.z, w.tiles_div) * tiles;
             const int tile = sg - quotient(sg, w.row_tiles_div) * w.row_tiles;
-            const int s = quotient(tile * rows + 8 * nt + 2 * c + (e & 1), w.group_div);
+            const int s = quotient(tile * rows + my_rows + 8 * nt + 2 * c + (e & 1), w.group_div);
             return hidden_from + (s < a.S ? s : a.S - 1);
         };
         // no weight for slots that the step has not, or that the row does not see; NaN for a missing page
@@ -580,7 +594,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
             }
         }
         if (a.accumulate) {
-            float *dst = w.scores + ((size_t)state.z * w.score_slots + t0) * rows + 2 * c;
+            float *dst = w.scores + ((size_t)state.z * w.score_slots + t0) * rows + my_rows + 2 * c;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 if (g < count)
@@ -739,6 +753,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
             }
         }
         __syncwarp();                                 // every lane has read its chunks and the state
+        if (GW > 1 && lane == 0) mbar_arrive(&s_free[group * NS + stage]);
 
         // ---- end of a piece ----
         const bool ended = state.x & kLast, last = left == 1;
@@ -748,19 +763,24 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
             const int kh = quotient(sg, w.row_tiles_div), tile = sg - kh * w.row_tiles;
             const float vs = TYPE == kE4m3 ? __ldg(a.c.v_scale + kh) : 1.f;
             const bool whole = ended && began_here;
-            const int slot = 2 * warp + (began_here ? 1 : 0);
-            if (whole && a.accumulate && lane == 0) w.span[here] = make_int2(blockIdx.x, 1);
-            if (!whole && lane == 0) s_piece[slot] = make_int2(here, (ended ? 1 : 0) | (last ? 0 : 2));
-            // 8 rows at a time through shared memory: the stage just read, or, with
-            // the range done, the ring, where an open piece stays for the join
+            const int slot = 2 * group + (began_here ? 1 : 0), row0 = slot * rows + my_rows;
+            if (whole && a.accumulate && lane == 0 && mate == 0) w.span[here] = make_int2(blockIdx.x, 1);
+            if (!whole && lane == 0 && mate == 0) s_piece[slot] = make_int2(here, (ended ? 1 : 0) | (last ? 0 : 2));
+            // 8 rows at a time through shared memory: the stage just read (a group's
+            // warps: a place of their own), or, with the range done and read by the
+            // whole group, the ring, where an open piece stays for the join
+            if (GW > 1 && last && !mbar_wait(&s_free[group * NS + stage], phase) && lane == 0)
+                raise_device_error(a.err, kErrTimeout);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float4 *slab = reinterpret_cast<float4 *>(last ? ring + nt * 32 * DP : ring + stage * C::stage);
+                float4 *slab = reinterpret_cast<float4 *>(last     ? ring + my_rows * DP * 4 + nt * 32 * DP
+                                                          : GW > 1 ? smem + G * C::ring + warp * C::slab
+                                                                   : ring + stage * C::stage);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(~0u, l[nt][e], d);
-                    if (g == 0) s_ml[slot * rows + 8 * nt + 2 * c + e] = make_float2(m[nt][e], l[nt][e]);
+                    if (g == 0) s_ml[row0 + 8 * nt + 2 * c + e] = make_float2(m[nt][e], l[nt][e]);
 #pragma unroll
                     for (int q = 0; q < NQ; ++q)
 #pragma unroll
@@ -777,8 +797,8 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
 #pragma unroll 1
                     for (int i = lane; i < 8 * (DP / 4); i += 32) {
                         const int r = i / (DP / 4), d = 4 * (i - r * (DP / 4));
-                        const RowRef ref = row_ref(a, w, b, kh, tile * rows + 8 * nt + r);
-                        const float2 ml = s_ml[slot * rows + 8 * nt + r];
+                        const RowRef ref = row_ref(a, w, b, kh, tile * rows + my_rows + 8 * nt + r);
+                        const float2 ml = s_ml[row0 + 8 * nt + r];
                         if (!ref.real) continue;
                         if (d < D) store_out4(a, ref.head * D + d, slab[slab_place<C>(r, d / 4)], row_factor(ml.y, vs));
                         if (d == 0 && a.lse) a.lse[ref.head] = row_lse(ml.x, ml.y);
@@ -792,20 +812,20 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                 __syncwarp();
             }
             // the stage is written next by a copy, another proxy
-            if (!last) {
+            if (GW == 1 && !last) {
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
             }
         }
-        issue();
+        issue(true, phase);
         if (++stage == NS) stage = 0, phase ^= 1u;
     }
 
-    // ---- join the block's open pieces, in order: a segment has at most one per warp ----
+    // ---- join the block's open pieces, in order: a segment has at most one per group ----
     __syncthreads();
-    const int2 piece = lane < 2 * W ? s_piece[lane] : make_int2(-1, 0);   // 2 W <= 32
+    const int2 piece = lane < 2 * G ? s_piece[lane] : make_int2(-1, 0);
     const uint32_t before = __ballot_sync(~0u, piece.x >= 0) & ((1u << lane) - 1u);
-    static_assert(2 * W <= 32, "a lane per piece");
+    static_assert(2 * G <= 32, "a lane per piece");
     const int prior = __shfl_sync(~0u, piece.x, before ? 31 - __clz(before) : lane);
     uint32_t leaders = __ballot_sync(~0u, piece.x >= 0 && (before == 0u || prior != piece.x));
     const uint32_t in_work = __ballot_sync(~0u, piece.y & 2);
@@ -833,9 +853,10 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_>::threads, 1)
                 const float2 ml = s_ml[x * rows + r];
                 const float f = ex2(ml.x - mm);
                 ll += ml.y * f;
+                // rows lie as the group's warps left them, 8 at a time
                 const float4 *src = in_work >> x & 1u
                                         ? reinterpret_cast<const float4 *>(w.head_o) +
-                                              ((size_t)blockIdx.x * W + (x >> 1)) * rows * (DP / 4)
+                                              ((size_t)blockIdx.x * G + (x >> 1)) * rows * (DP / 4)
                                         : reinterpret_cast<const float4 *>(smem + (x >> 1) * C::ring);
                 const float4 v = src[(r >> 3) * 2 * DP + slab_place<C>(r & 7, d / 4)];
                 sum.x += v.x * f, sum.y += v.y * f, sum.z += v.z * f, sum.w += v.w * f;
