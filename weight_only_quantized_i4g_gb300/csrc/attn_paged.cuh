@@ -175,6 +175,21 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// d = A B, nothing added.
+template <int TYPE>
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+    if (TYPE == kBf16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -517,10 +532,6 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
         // ---- S^T = K Q^T, in two chains ----
         float s[NT][4], s1[NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[nt][e] = s1[nt][e] = 0.f;
-#pragma unroll
         for (int i = 0; i < NI; ++i) {
             // slots g and g + 8
             const uint4 x = lds128(src + chunk_place<C>(g, k_chunk<C>(i, c)));
@@ -536,8 +547,11 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
                     e4m3x4_to_f16x2(ky[u], &a1, &a3);
                 }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma16816<TYPE>(u & 1 ? s1[nt] : s[nt], a0, a1, a2, a3, qf[nt][i][2 * u], qf[nt][i][2 * u + 1]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    float(&d)[4] = u & 1 ? s1[nt] : s[nt];
+                    if (i == 0 && u < 2) mma16816_first<TYPE>(d, a0, a1, a2, a3, qf[nt][i][2 * u], qf[nt][i][2 * u + 1]);
+                    else mma16816<TYPE>(d, a0, a1, a2, a3, qf[nt][i][2 * u], qf[nt][i][2 * u + 1]);
+                }
             }
         }
 
@@ -565,10 +579,10 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
             for (int e = 0; e < 4; ++e) {
                 s[nt][e] += s1[nt][e];
                 x[nt][e] = fmaf(s[nt][e], TYPE == kE4m3 ? rs[nt][e & 1] : factor, -m[nt][e & 1]);
-                if (partial) x[nt][e] = masked(x[nt][e], nt, e);
+                if (__builtin_expect(partial, 0)) x[nt][e] = masked(x[nt][e], nt, e);
                 over |= x[nt][e] > shift + 8.f;
             }
-        if (__any_sync(~0u, over)) {
+        if (__builtin_expect(__any_sync(~0u, over), 0)) {
             // raise the references to the maxima; l and O follow
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -593,7 +607,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
                 }
             }
         }
-        if (a.accumulate) {
+        if (__builtin_expect(a.accumulate, 0)) {
             float *dst = w.scores + ((size_t)state.z * w.score_slots + t0) * rows + my_rows + 2 * c;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -651,7 +665,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
                     x[j][0] = v.x, x[j][1] = v.y, x[j][2] = x[j][3] = 0u;
                 }
             }
-            if ((state.x & 63) != 16) {   // what lies past the step's slots, or where no copy landed
+            if (__builtin_expect((state.x & 63) != 16, 0)) {   // what lies past the step's slots, or where no copy landed
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (state.x & kMissing || 2 * c + (j & 1) + 8 * (j >> 1) >= count)
@@ -665,7 +679,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
         };
         constexpr int per_word = 4 / C::ESZ;
         bool careful = false;
-        if (a.S > 1 && partial) {
+        if (__builtin_expect(a.S > 1 && partial, 0)) {
             // a slot hidden from some rows: 0 * NaN and 0 * inf must not reach them
             bool odd = false;
 #pragma unroll
@@ -714,7 +728,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
                 }
             }
         };
-        if (!careful) {
+        if (__builtin_expect(!careful, 1)) {
             if (TYPE == kBf16 && third) add_pv(std::true_type());
             else add_pv(std::false_type());
         } else {
@@ -757,7 +771,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
 
         // ---- end of a piece ----
         const bool ended = state.x & kLast, last = left == 1;
-        if (ended || last) {
+        if (__builtin_expect(ended || last, 0)) {
             fresh = true;
             const int here = state.z, b = quotient(here, w.tiles_div), sg = here - b * tiles;
             const int kh = quotient(sg, w.row_tiles_div), tile = sg - kh * w.row_tiles;
