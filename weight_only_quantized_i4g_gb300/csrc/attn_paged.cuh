@@ -110,7 +110,7 @@ struct AttnCfg {
 // The ring: byte offset of 16-byte chunk `chunk` of slot `row` in a step's K or
 // V, as the copies' swizzle leaves it.
 template <class C>
-__device__ __forceinline__ constexpr int chunk_place(int row, int chunk) {
+__host__ __device__ __forceinline__ constexpr int chunk_place(int row, int chunk) {
     constexpr int per = C::BB / 16;
     const int b = chunk / per, x = chunk % per;
     return b * C::box + row * C::BB + 16 * (per == 8 ? x ^ (row & 7) : x ^ (row >> 1 & 3));
@@ -119,13 +119,13 @@ __device__ __forceinline__ constexpr int chunk_place(int row, int chunk) {
 // rows of 128 bytes neighbouring ones, so that the swizzle of even and odd rows
 // parts the eight lanes of a read.
 template <class C>
-__device__ __forceinline__ constexpr int k_chunk(int i, int c) {
+__host__ __device__ __forceinline__ constexpr int k_chunk(int i, int c) {
     return C::BB == 128 ? 8 * (i >> 1) + 2 * c + (i & 1) : 4 * i + c;
 }
 // Pieces of 8 rows of O in shared memory: place (in float4) of quad x of row r.
 // The exchange by row parts the eight lanes of a store (two g, four c).
 template <class C>
-__device__ __forceinline__ int slab_place(int r, int x) {
+__host__ __device__ __forceinline__ constexpr int slab_place(int r, int x) {
     return r * (C::DP / 4) + (x ^ ((r >> 1 & 1) | (r >> 2 & 1) << 2));
 }
 
@@ -228,9 +228,9 @@ __device__ __forceinline__ RowRef row_ref(const AttnArgs &a, const AttnWork &w, 
 
 // Steps of a sequence of len slots: 16 slots of a page each, fewer at the ends
 // of pages and of the sequence.
-__device__ __forceinline__ int seq_steps(const AttnArgs &a, const AttnWork &w, int len) {
-    const int full = quotient(len, a.c.page_div);
-    return full * w.page_steps + ((len - full * a.c.page + 15) >> 4);
+__host__ __device__ __forceinline__ int seq_steps(const KvView &c, const AttnWork &w, int len) {
+    const int full = quotient(len, c.page_div);
+    return full * w.page_steps + ((len - full * c.page + 15) >> 4);
 }
 
 // Lengths of all sequences, and the running sums (n + 1) of their segments'
@@ -244,7 +244,7 @@ __device__ __forceinline__ void scan_costs(const AttnArgs &a, const AttnWork &w,
     for (int i = tid * per; i < (tid + 1) * per && i < n; ++i) {
         const int len = seq_len(a.lens, i, a.max_len, err);
         s_len[i] = len;
-        if (len > 0) sum += seq_steps(a, w, len) + kSegmentCost;
+        if (len > 0) sum += seq_steps(a.c, w, len) + kSegmentCost;
     }
     int inc = sum;
 #pragma unroll
@@ -261,14 +261,14 @@ __device__ __forceinline__ void scan_costs(const AttnArgs &a, const AttnWork &w,
     int at = base + inc - sum;
     for (int i = tid * per; i < (tid + 1) * per && i < n; ++i) {
         s_prefix[i] = at;
-        if (s_len[i] > 0) at += seq_steps(a, w, s_len[i]) + kSegmentCost;
+        if (s_len[i] > 0) at += seq_steps(a.c, w, s_len[i]) + kSegmentCost;
     }
     if (tid == THREADS - 1) s_prefix[n] = at;
     __syncthreads();
 }
 
 // Cost units per block where all are cut into equal ranges: a step per warp at least.
-__device__ __forceinline__ int units_per_block(int total, int ctas, int warps) {
+__host__ __device__ __forceinline__ int units_per_block(int total, int ctas, int warps) {
     const int chunk = (total + ctas - 1) / ctas;
     return chunk < warps + kSegmentCost ? warps + kSegmentCost : chunk;
 }
@@ -277,7 +277,7 @@ __device__ __forceinline__ int units_per_block(int total, int ctas, int warps) {
 // inside it) and steps of the segment.
 struct Place { int b, seg, i, n, page, sub; };
 // The first step at or after unit u; a segment's first kSegmentCost units have none.
-__device__ __forceinline__ Place locate(int u, const int *s_prefix, int n, const AttnWork &w) {
+__host__ __device__ __forceinline__ Place locate(int u, const int *s_prefix, int n, const AttnWork &w) {
     Place p = {n, 0, 0, 1, 0, 0};
     const int x = quotient(u, w.tiles_div);
     if (x >= s_prefix[n]) return p;
@@ -296,6 +296,36 @@ __device__ __forceinline__ Place locate(int u, const int *s_prefix, int n, const
     p.page = quotient(p.i, w.page_steps_div);
     p.sub = p.i - p.page * w.page_steps;
     return p;
+}
+// Steps from place x up to place y.
+__host__ __device__ __forceinline__ int steps_between(const Place &x, const Place &y, const int *s_prefix, int tiles) {
+    int steps = y.seg * y.n + y.i - (x.seg * x.n + x.i);
+    for (int b = x.b; b < y.b; ++b) {
+        const int cost = s_prefix[b + 1] - s_prefix[b];
+        if (cost) steps += tiles * (cost - kSegmentCost);
+    }
+    return steps;
+}
+// The step after p (the sequence n, segment 0, step 0 after the last).
+__host__ __device__ __forceinline__ void advance(Place &p, const int *s_prefix, int n, const AttnWork &w) {
+    if (++p.sub == w.page_steps) p.sub = 0, ++p.page;
+    if (++p.i < p.n) return;
+    p.i = p.page = p.sub = 0;
+    if (++p.seg < w.tiles) return;
+    p.seg = 0;
+    do ++p.b;
+    while (p.b < n && s_prefix[p.b + 1] == s_prefix[p.b]);
+    p.n = p.b < n ? s_prefix[p.b + 1] - s_prefix[p.b] - kSegmentCost : 1;
+}
+// Unit where part x of `parts` of the range [c0, c1) begins.
+__host__ __device__ __forceinline__ int part_of(int c0, int c1, int x, int parts) {
+    return c0 + (int)((long long)(c1 - c0) * x / parts);
+}
+// Blocks that the segment (sequence b, number sg) spans, from the block that holds its first step.
+__host__ __device__ __forceinline__ int blocks_spanned(int b, int sg, int first, int chunk, const int *s_prefix,
+                                                       int tiles) {
+    const int end_unit = s_prefix[b] * tiles + (sg + 1) * (s_prefix[b + 1] - s_prefix[b]);
+    return (end_unit - 1) / chunk - first + 1;
 }
 
 template <int TYPE, int DP_, int NT_, int GW_>
@@ -358,16 +388,8 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
     if (c0 >= c1) return;
 
     // the warp's first step, and how many it has
-    Place ip = locate(c0 + (int)((long long)(c1 - c0) * group / G), s_prefix, n, w);
-    int left;
-    {
-        const Place end = locate(c0 + (int)((long long)(c1 - c0) * (group + 1) / G), s_prefix, n, w);
-        left = end.seg * end.n + end.i - (ip.seg * ip.n + ip.i);
-        for (int b = ip.b; b < end.b; ++b) {
-            const int cost = s_prefix[b + 1] - s_prefix[b];
-            if (cost) left += tiles * (cost - kSegmentCost);
-        }
-    }
+    Place ip = locate(part_of(c0, c1, group, G), s_prefix, n, w);
+    int left = steps_between(ip, locate(part_of(c0, c1, group + 1, G), s_prefix, n, w), s_prefix, tiles);
     char *ring = smem + group * C::ring;
     const uint32_t ring_a = smem_addr(ring);
 
@@ -410,16 +432,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
                 }
             }
             --to_issue;
-            if (++ip.sub == w.page_steps) ip.sub = 0, ++ip.page;
-            if (++ip.i == ip.n) {
-                ip.i = ip.page = ip.sub = 0;
-                if (++ip.seg == tiles) {
-                    ip.seg = 0;
-                    do ++ip.b;
-                    while (ip.b < n && s_prefix[ip.b + 1] == s_prefix[ip.b]);
-                    ip.n = ip.b < n ? s_prefix[ip.b + 1] - s_prefix[ip.b] - kSegmentCost : 1;
-                }
-            }
+            advance(ip, s_prefix, n, w);
             look();
         }
         if (++istage == NS) istage = 0;
@@ -884,8 +897,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
             }
         }
         if (tid == 0 && starts) {
-            const int end_unit = s_prefix[b] * tiles + (sg + 1) * (s_prefix[b + 1] - s_prefix[b]);
-            const int2 span = make_int2(blockIdx.x, whole ? 1 : (end_unit - 1) / chunk - (int)blockIdx.x + 1);
+            const int2 span = make_int2(blockIdx.x, whole ? 1 : blocks_spanned(b, sg, blockIdx.x, chunk, s_prefix, tiles));
             if (!whole) w.open[blockIdx.x] = make_int2(seg, span.y);
             if (a.accumulate) w.span[seg] = span;
         }

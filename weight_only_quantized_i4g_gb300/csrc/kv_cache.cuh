@@ -31,7 +31,7 @@ inline FastDiv fast_div(int d) {
     while ((1ull << l) < (unsigned long long)d) ++l;
     return FastDiv{(unsigned)d, (unsigned)(((1ull << (31 + l)) + d - 1) / d), 31 + l};
 }
-__device__ __forceinline__ int quotient(int x, FastDiv f) {
+__host__ __device__ __forceinline__ int quotient(int x, FastDiv f) {
     return (int)(((unsigned long long)(unsigned)x * f.mul) >> f.shift);
 }
 
