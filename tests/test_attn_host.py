@@ -150,5 +150,7 @@ def test_binding_checks_its_tensors(qg):
         a.update(bad)
         with pytest.raises(ValueError):
             qg.kv_cache(**a)
+    with pytest.raises(ValueError):
+        append(qg, axis=bytes(63))
     assert ctypes.sizeof(qg.KVCache) == 8 * 8 + 5 * 4 + 4
     assert qg.strerror(qg.QG_EPAGE).startswith("QG_EPAGE")

@@ -117,6 +117,45 @@ def test_weights_are_accumulated(qg, kv, S, group):
     check_attention(pc, q, S, 2 * group, 0.088, accumulate=True, lse=False)
 
 
+@pytest.mark.parametrize("dim,S,group", [(64, 8, 7), (64, 8, 9), (128, 4, 6), (128, 8, 9), (256, 2, 5), (256, 8, 5)])
+def test_weights_of_many_rows(qg, dim, S, group):
+    """Rows that several warps, or several segments, share out."""
+    lens = [0, 5, 77, 700]
+    pc = Paged(qg, lens, 2, dim, "bf16", seed=dim + S, weight=True).fill()
+    q = queries(pc, len(lens), S, 2 * group, "bf16")
+    check_attention(pc, q, S, 2 * group, dim ** -0.5, accumulate=True)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_more_sequences_than_a_launch_takes(qg, accumulate):
+    """Their lengths sit in shared memory, 2048 at a time."""
+    B = 4100
+    lens = [(i * 7) % 23 for i in range(B)]
+    lens[2047], lens[2048], lens[4099] = 300, 290, 280
+    pc = Paged(qg, lens, 1, 16, "bf16", page=16, seed=41, weight=accumulate, fill=0.0)
+    n = sum(lens)
+    for name in ("k", "v"):                       # one write for all sequences
+        at = torch.cat([torch.arange(x) for x in lens]).to(DEV)
+        seq = torch.repeat_interleave(torch.arange(B), torch.tensor(lens)).to(DEV)
+        getattr(pc, name)[pc.table[seq, at // 16].long(), 0, at % 16] = pc.randn(n, 16).bfloat16()
+    q = queries(pc, B, 1, 2, "bf16")
+    o, lse = run_attention(pc, q, 1, 2, 0.25, accumulate=accumulate)
+    torch.cuda.synchronize()
+    assert qg.qg_device_status() == (0, 0)
+    for b in (0, 1, 22, 23, 2046, 2047, 2048, 2049, 3000, 4098, 4099):
+        if lens[b] == 0:
+            assert bool((o[b] == 0).all())
+            continue
+        k, v = pc.get("k", b, 0), pc.get("v", b, 0)
+        z = q[b].double().view(2, 16) @ k.T * 0.25
+        p = torch.softmax(z, -1)
+        assert float((o[b].double() - p @ v).abs().max()) < 1e-4
+        assert float((lse[b].double() - torch.logsumexp(z, -1)).abs().max()) < 1e-4
+        if accumulate:
+            at, i = pc.where(b)
+            assert float((pc.weight[at, 0, i].double() - 0.25 - p.sum(0)).abs().max()) < 1e-4
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("kv", ["bf16", "f16", "e4m3"])
 @pytest.mark.parametrize("S", [2, 4, 8])

@@ -347,6 +347,8 @@ def qg_rope_append(cache, table, table_stride, n_seq, seq, slot, T, q, q_type, q
                    pos, n_axes, axis, inv_freq, rotary_dim, style=QG_ROPE_HALF, stream=None) -> int:
     """Rotary positions and the cache write; ``axis`` is bytes of length
     rotary_dim/2 (host data) or None."""
+    if axis is not None and len(axis) < rotary_dim // 2:
+        raise ValueError("axis names the position of each of the rotary_dim/2 pairs")
     return _lib.qg_rope_append(_cache(cache), _ptr(table), table_stride, n_seq, _ptr(seq), _ptr(slot), T, _ptr(q),
                                q_type, _ptr(qkv), qkv_type, qkv_stride, n_q_heads, _ptr(pos), n_axes,
                                axis if axis is None else ctypes.c_char_p(axis), _ptr(inv_freq), rotary_dim, style,
