@@ -14,9 +14,11 @@ struct AttnPlan {
 };
 
 // The smallest padded head size (the padding is not read from memory); then as
-// many tiles of 8 rows a warp as its registers take (four at 64 dimensions,
-// two at 128, one at 256: four at 128 spill), and groups of two or four warps
-// for more rows.  More than a group's rows are further segments.  48 ragged
+// many tiles of 8 rows a warp as its registers take (two, or four at 64
+// dimensions, one at 256: four at 128 spill), and groups of two or four warps
+// for more rows (64 dimensions: 32 rows of 16 f16 sequences 25.6 us with two
+// warps of two tiles, 27.4 with one of four; 64 rows of 48 bf16 sequences 324 us
+// with four of two, 311 with two of four).  More than a group's rows are further segments.  48 ragged
 // bf16 sequences, 128 dimensions, 8 cache heads, 32 and 64 rows: 272 and 543 us
 // with segments of 16 rows, 321 and 632 with four tiles a warp.
 template <int TYPE, class Fn>
@@ -24,7 +26,7 @@ auto attn_dispatch(int rows, int dim, Fn fn) {
     if (dim <= 64)
         return rows <= 8    ? fn(AttnCfg<TYPE, 64, 1, 1>())
                : rows <= 16 ? fn(AttnCfg<TYPE, 64, 2, 1>())
-               : rows <= 32 ? fn(AttnCfg<TYPE, 64, 4, 1>()) : fn(AttnCfg<TYPE, 64, 4, 2>());
+               : rows <= 32 ? fn(AttnCfg<TYPE, 64, 2, 2>()) : fn(AttnCfg<TYPE, 64, 4, 2>());
     if (dim <= 128)
         return rows <= 8    ? fn(AttnCfg<TYPE, 128, 1, 1>())
                : rows <= 16 ? fn(AttnCfg<TYPE, 128, 2, 1>())
@@ -47,7 +49,9 @@ int launch_attn_stream(const AttnArgs &a, const AttnWork &w, const AttnPlan &pl,
     return attn_dispatch<TYPE>(a.S * a.group, a.c.dim, [&](auto cfg) {
         using C = decltype(cfg);
         const size_t smem = pl.smem + (2 * (size_t)a.n_seq + 1) * sizeof(int);
-        auto *kernel = attn_stream_kernel<TYPE, C::DP, C::NT, C::GW>;
+        auto *kernel = attn_stream_kernel<TYPE, C::DP, C::NT, C::GW, true>;
+        if constexpr (C::GW == 1)
+            if (a.S == 1) kernel = attn_stream_kernel<TYPE, C::DP, C::NT, C::GW, false>;
         set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), 232448);
         return launch_pdl("qattn_paged", kernel, dim3(w.ctas), dim3(C::threads), smem, st, a, w, maps[0], maps[1]);
     });

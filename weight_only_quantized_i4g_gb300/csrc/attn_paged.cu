@@ -37,9 +37,9 @@ __global__ void __launch_bounds__(kFinishThreads)
     __shared__ float s_lse[64];
     const int tid = threadIdx.x, R = a.S * a.group;
     griddep_launch_dependents();
-    griddep_wait();
 
     if ((int)blockIdx.x < join_blocks) {
+        griddep_wait();
         const int groups = rows / per, x = blockIdx.x / groups;
         const int2 open = w.open[x];
         if (open.x < 0) return;
@@ -99,12 +99,16 @@ __global__ void __launch_bounds__(kFinishThreads)
     const int at = blockIdx.x - join_blocks, heads = a.n_seq * a.c.n_heads;
     const int part = at / heads, bh = at - part * heads, b = bh / a.c.n_heads, kh = bh - b * a.c.n_heads;
     const int len = seq_len(a.lens, b, a.max_len, nullptr);
-    if (part * kFinishThreads >= len) return;
+    if (part * kFinishThreads >= len) {
+        if (blockIdx.x == 0) griddep_wait();          // this kernel must not be complete before the streaming kernel is
+        return;
+    }
     const int t = part * kFinishThreads + tid;
     SlotRef ref{-1, 0};
     if (t < len) ref = find_slot(a.c, a.table + (size_t)b * a.table_stride, t);
     float sum = 0.f, had = 0.f;
     if (ref.page >= 0) had = a.c.weight[slot_weight(a.c, ref, kh)];
+    griddep_wait();
     for (int tile = 0; tile < w.row_tiles; ++tile) {
         const int seg = b * w.tiles + kh * w.row_tiles + tile;
         const float *z = w.scores + ((size_t)seg * w.score_slots + t) * rows;

@@ -95,7 +95,7 @@ struct AttnCfg {
     // as many warps as the registers of O, Q and S allow (16, 12 or 8 an SM)
     static constexpr int regs = (ESZ == 1 ? 85 : 70) + 4 * MT * NT + NT * NI * (ESZ == 1 ? 8 : 4) + 8 * NT;
     static constexpr int W0 = regs <= 128 ? 16 : regs <= 168 ? 12 : 8;
-    static constexpr int W = GW > 1 ? 8 : stage > 8192 ? 4 : W0;
+    static constexpr int W = GW == 1 && stage > 8192 ? 4 : W0;
     static constexpr int G = W / GW;                  // groups, a ring each
     // 8 rows of O on their way out; a lone warp takes the stage it has just read
     static constexpr int slab = GW > 1 ? 32 * DP : 0;
@@ -328,7 +328,9 @@ __host__ __device__ __forceinline__ int blocks_spanned(int b, int sg, int first,
     return (end_unit - 1) / chunk - first + 1;
 }
 
-template <int TYPE, int DP_, int NT_, int GW_>
+// DRAFT: several new tokens a sequence, the last of which some rows do not see.
+// (Without the code for those the calls of one token are 2% faster.)
+template <int TYPE, int DP_, int NT_, int GW_, bool DRAFT>
 __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
     attn_stream_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnWork w,
                        const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
@@ -355,9 +357,14 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
     if (tid < G * NS) mbar_init(&s_bar[tid], 1), mbar_init(&s_free[tid], GW);
     if (tid < G * 2) s_piece[tid] = make_int2(-1, 0);
     mbar_fence_init();
+    if (tid == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&k_map)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&v_map)) : "memory");
+    }
 
-    griddep_launch_dependents();
+    // the second kernel may start once lengths, tables and weights are final: it reads them before its own wait
     griddep_wait();
+    griddep_launch_dependents();
 
     scan_costs<C::threads>(a, w, s_len, s_prefix, reinterpret_cast<int *>(s_state),
                            blockIdx.x == 0 ? a.err : nullptr);
@@ -569,7 +576,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
         }
 
         // ---- exponents against the rows' references; thread: slots g, g + 8 by rows 2c, 2c + 1 ----
-        const bool partial = (state.x & 63) != 16 || (a.S > 1 && t0 + 16 > hidden_from);
+        const bool partial = (state.x & 63) != 16 || (DRAFT && a.S > 1 && t0 + 16 > hidden_from);
         // slots that row nt, e of the thread sees of this step and before it
         auto limit = [&](int nt, int e) {
             const int sg = state.z - quotient(state.z, w.tiles_div) * tiles;
@@ -580,7 +587,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
         // no weight for slots that the step has not, or that the row does not see; NaN for a missing page
         auto masked = [&](float z, int nt, int e) {
             const int j = g + 8 * (e >> 1);
-            if (j >= count || (a.S > 1 && t0 + j >= limit(nt, e))) return -INFINITY;
+            if (j >= count || (DRAFT && a.S > 1 && t0 + j >= limit(nt, e))) return -INFINITY;
             return state.x & kMissing ? NAN : z;
         };
         // one vote for all rows: the tiles' chains then run side by side
@@ -692,7 +699,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
         };
         constexpr int per_word = 4 / C::ESZ;
         bool careful = false;
-        if (__builtin_expect(a.S > 1 && partial, 0)) {
+        if (DRAFT && __builtin_expect(a.S > 1 && partial, 0)) {
             // a slot hidden from some rows: 0 * NaN and 0 * inf must not reach them
             bool odd = false;
 #pragma unroll
@@ -741,7 +748,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
                 }
             }
         };
-        if (__builtin_expect(!careful, 1)) {
+        if (!DRAFT || __builtin_expect(!careful, 1)) {
             if (TYPE == kBf16 && third) add_pv(std::true_type());
             else add_pv(std::false_type());
         } else {

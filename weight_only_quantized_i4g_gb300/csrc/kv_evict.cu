@@ -193,8 +193,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
         return f;
     };
     int sure_n = 0, tie_n = 0;
-    for (int t = t0 + 4 * lane; t < t1; t += 128) {
+    unsigned long long seen = 0;                   // the flags of the first eight rounds
+    int round = 0;
+    for (int t = t0 + 4 * lane; t < t1; t += 128, ++round) {
         const unsigned f = flags(t);
+        if (round < 8) seen |= (unsigned long long)f << (8 * round);
         sure_n += __popc(f & 15u), tie_n += __popc(f >> 4);
     }
 #pragma unroll
@@ -216,8 +219,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
         cluster.sync();                            // also the last access to another block's memory
         for (int x = 0; x < rank; ++x) base_sure += s_block[x].x, base_tie += s_block[x].y;
     }
-    for (int t = t0 + 4 * lane; t - 4 * lane < t1; t += 128) {
-        const unsigned f = flags(t);
+    round = 0;
+    for (int t = t0 + 4 * lane; t - 4 * lane < t1; t += 128, ++round) {
+        const unsigned f = round < 8 ? (unsigned)(seen >> (8 * round)) & 255u : flags(t);
         // both counts of the lanes before this one: up to 128 each
         const int mine = __popc(f & 15u) | __popc(f >> 4) << 16;
         int inc = mine;
