@@ -53,7 +53,8 @@ int launch_attn_stream(const AttnArgs &a, const AttnWork &w, const AttnPlan &pl,
         if constexpr (C::GW == 1)
             if (a.S == 1) kernel = attn_stream_kernel<TYPE, C::DP, C::NT, C::GW, false>;
         set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), 232448);
-        return launch_pdl("qattn_paged", kernel, dim3(w.ctas), dim3(C::threads), smem, st, a, w, maps[0], maps[1]);
+        return launch_clusters("qattn_paged", kernel, dim3(w.ctas), dim3(C::threads), w.ranks > 1 ? w.ranks : 1, smem, st, a, w,
+                               maps[0], maps[1]);
     });
 }
 

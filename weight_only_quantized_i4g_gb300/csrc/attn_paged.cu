@@ -163,7 +163,7 @@ AttnPlan plan_of(int type, int rows, int dim) {
 struct Layout {
     AttnPlan pl;
     int rows, row_tiles, seqs, score_slots;
-    int ctas, whole;
+    int ctas, ranks;
     size_t part_o, part_ml, head_o, open, span, lse, scores, bytes;
 };
 Layout layout(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int accumulate) {
@@ -174,14 +174,19 @@ Layout layout(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int
     y.row_tiles = (R + y.rows - 1) / y.rows;
     y.score_slots = max_len;
     y.seqs = n_seq < kAttnMaxSeq ? n_seq : kAttnMaxSeq;
-    // one block per segment where one wave of blocks holds them all and a
-    // segment is at most kWholeBytes of K and V: an SM streams that in less
-    // than the second kernel takes (8 heads of 128 bf16: 520 slots 11.0 us
-    // whole, 12.3 in equal ranges; 1000 slots 13.2 and 12.7; 2000 19.0 and 12.6)
+    // One block, or a cluster of two, four or eight, per segment, where all
+    // run at once and a block has at most kWholeBytes of K and V: an SM streams
+    // that in less than the second kernel takes (8 heads of 128 bf16: 520 slots
+    // 11.0 us in a block each, 12.3 in equal ranges; 1000 slots 13.2 and 12.7).
+    // Blocks of one SM each: 76 clusters of two run at once, 36 of four, 15 of
+    // eight.
     const long long segments = (long long)y.seqs * c.n_heads * y.row_tiles;
-    const int esz = c.type == kE4m3 ? 1 : 2;
-    y.whole = segments <= num_sms() && (long long)max_len * c.dim * esz * 2 <= kWholeBytes;
-    y.ctas = y.whole ? (int)segments : num_sms();
+    const long long bytes = (long long)max_len * c.dim * (c.type == kE4m3 ? 1 : 2) * 2;
+    const int sms = num_sms(), at_once[4] = {sms, sms / 2, sms * 36 / 152, sms * 15 / 152};
+    y.ranks = 0;
+    for (int k = 3; k >= 0; --k)
+        if (segments <= at_once[k] && bytes <= kWholeBytes << k) y.ranks = 1 << k;
+    y.ctas = y.ranks ? (int)segments * y.ranks : sms;
     const size_t ctas = y.ctas;
     const size_t tile_f = (size_t)y.rows * y.pl.dp * 4;
     const size_t seq_scores = (size_t)c.n_heads * y.row_tiles * y.score_slots * y.rows * 4;
@@ -195,10 +200,10 @@ Layout layout(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int
         at += up256(n);
         return here;
     };
-    y.part_o = take(y.whole ? 0 : 2 * ctas * tile_f);
-    y.part_ml = take(y.whole ? 0 : 2 * ctas * y.rows * sizeof(float2));
-    y.head_o = take(y.whole ? 0 : ctas * y.pl.piece_rows * y.pl.dp * 4);
-    y.open = take(y.whole ? 0 : ctas * sizeof(int2));
+    y.part_o = take(y.ranks == 1 ? 0 : 2 * ctas * tile_f);
+    y.part_ml = take(y.ranks == 1 ? 0 : 2 * ctas * y.rows * sizeof(float2));
+    y.head_o = take(y.ranks ? 0 : ctas * y.pl.piece_rows * y.pl.dp * 4);
+    y.open = take(y.ranks ? 0 : ctas * sizeof(int2));
     y.span = take(accumulate ? (size_t)segments * sizeof(int2) : 0);
     y.lse = take(accumulate ? (size_t)y.seqs * S * n_q_heads * 4 : 0);
     y.scores = take(accumulate ? seq_scores * y.seqs : 0);
@@ -253,7 +258,7 @@ int run_attn_paged(const AttnArgs &args, void *ws, cudaStream_t st) {
     w.score_slots = y.score_slots;
     w.row_tiles = y.row_tiles;
     w.tiles = args.c.n_heads * y.row_tiles;
-    w.whole = y.whole;
+    w.ranks = y.ranks;
     w.tiles_div = fast_div(w.tiles);
     w.row_tiles_div = fast_div(w.row_tiles);
     w.group_div = fast_div(args.group);
@@ -274,14 +279,14 @@ int run_attn_paged(const AttnArgs &args, void *ws, cudaStream_t st) {
         a.o = static_cast<char *>(a.o) + rows * a.n_q_heads * a.c.dim * (a.o_type == kF32 ? 4 : 2);
         if (a.lse) a.lse += rows * a.n_q_heads;
         else if (a.accumulate) a.lse = reinterpret_cast<float *>(base + y.lse);
-        w.ctas = y.whole ? a.n_seq * w.tiles : y.ctas;
+        w.ctas = y.ranks ? a.n_seq * w.tiles * y.ranks : y.ctas;
         rc = a.c.type == kBf16 ? launch_attn_stream<kBf16>(a, w, y.pl, maps, st)
              : a.c.type == kF16 ? launch_attn_stream<kF16>(a, w, y.pl, maps, st)
                                 : launch_attn_stream<kE4m3>(a, w, y.pl, maps, st);
         // a segment's pieces: few where there are many segments, and a block then does
         // several rows; else one, its threads sharing the pieces
         const int most = kFinishThreads / (y.pl.dp / 4), per = (long long)a.n_seq * w.tiles * 8 < w.ctas ? 1 : most < 8 ? most : 8;
-        const int joins = y.whole ? 0 : w.ctas * (y.rows / per);
+        const int joins = y.ranks ? 0 : w.ctas * (y.rows / per);
         const long long adds = a.accumulate ? (long long)a.n_seq * a.c.n_heads *
                                                   ((a.max_len + kFinishThreads - 1) / kFinishThreads)
                                             : 0;

@@ -18,8 +18,9 @@
 // A segment that ends inside its warp is finished there; pieces of one that
 // does not are joined in shared memory after the block's ranges are done, and
 // across blocks by a second kernel, always in slot order.  Where every segment
-// is short and has an SM to itself, each block takes one whole segment instead
-// and the second kernel is not needed.
+// is short and has an SM or several to itself, a block or a thread-block cluster
+// takes one whole segment instead, the cluster's blocks join their pieces over
+// the workspace, and the second kernel is not needed.
 //
 // Loads.  Each warp keeps a ring of steps in shared memory, filled by TMA
 // tensor copies (boxes of 16 slots by 128 bytes, 128-byte swizzle) that one
@@ -57,6 +58,7 @@
 namespace qg {
 
 constexpr int kAttnMaxSeq = 2048;     // sequences per launch (their lengths sit in shared memory)
+constexpr int kMaxRanks = 8;          // blocks of a cluster
 constexpr int kSegmentCost = 2;       // what starting and ending a segment takes, in steps (~5000 cycles against ~2000)
 
 // Workspace of one launch.
@@ -70,7 +72,7 @@ struct AttnWork {
     int score_slots;    // slots per segment in scores
     int row_tiles;
     int tiles;          // segments per sequence: heads times row tiles
-    int whole;          // one block per segment (else equal ranges of steps)
+    int ranks;          // blocks (a cluster) that take one whole segment; 0: equal ranges of all steps
     int ctas;           // blocks of the streaming kernel
     int page_steps;     // steps of a page
     int box_rows;       // slots a copy moves: 16, or a smaller page
@@ -321,6 +323,12 @@ __host__ __device__ __forceinline__ void advance(Place &p, const int *s_prefix, 
 __host__ __device__ __forceinline__ int part_of(int c0, int c1, int x, int parts) {
     return c0 + (int)((long long)(c1 - c0) * x / parts);
 }
+// Steps per block where `ranks` of them take a segment of n steps: a step per
+// warp (or group of warps) at least.
+__host__ __device__ __forceinline__ int steps_per_rank(int n, int ranks, int groups) {
+    const int each = (n + ranks - 1) / ranks;
+    return each < groups ? groups : each;
+}
 // Blocks that the segment (sequence b, number sg) spans, from the block that holds its first step.
 __host__ __device__ __forceinline__ int blocks_spanned(int b, int sg, int first, int chunk, const int *s_prefix,
                                                        int tiles) {
@@ -368,11 +376,15 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
 
     scan_costs<C::threads>(a, w, s_len, s_prefix, reinterpret_cast<int *>(s_state),
                            blockIdx.x == 0 ? a.err : nullptr);
-    int c0, c1, chunk = 0;                                                    // in cost units
-    if (w.whole) {
-        const int b = quotient(blockIdx.x, w.tiles_div), cost = s_prefix[b + 1] - s_prefix[b];
-        c1 = s_prefix[b] * tiles + (blockIdx.x - b * tiles + 1) * cost;
-        c0 = cost ? c1 - cost + kSegmentCost : c1;
+    int c0, c1, chunk, shared_by = 1;                                         // in cost units
+    const int rank = w.ranks > 1 ? blockIdx.x % w.ranks : 0;
+    if (w.ranks > 0) {
+        const int seg = blockIdx.x / w.ranks, b = quotient(seg, w.tiles_div), cost = s_prefix[b + 1] - s_prefix[b];
+        const int steps = cost ? cost - kSegmentCost : 0, base = s_prefix[b] * tiles + (seg - b * tiles + 1) * cost - steps;
+        chunk = steps_per_rank(steps, w.ranks, G);
+        shared_by = (steps + chunk - 1) / chunk;
+        c0 = base + (rank * chunk < steps ? rank * chunk : steps);
+        c1 = base + ((rank + 1) * chunk < steps ? (rank + 1) * chunk : steps);
     } else {
         const int total = s_prefix[n] * tiles;
         chunk = units_per_block(total, gridDim.x, G);
@@ -392,7 +404,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
         if (a.lse)
             for (int i = tid; i < count; i += C::threads) a.lse[(size_t)b * count + i] = -INFINITY;
     }
-    if (c0 >= c1) return;
+    if (c0 >= c1 && w.ranks <= 1) return;
 
     // the warp's first step, and how many it has
     Place ip = locate(part_of(c0, c1, group, G), s_prefix, n, w);
@@ -904,9 +916,50 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
             }
         }
         if (tid == 0 && starts) {
-            const int2 span = make_int2(blockIdx.x, whole ? 1 : blocks_spanned(b, sg, blockIdx.x, chunk, s_prefix, tiles));
-            if (!whole) w.open[blockIdx.x] = make_int2(seg, span.y);
+            const int2 span = make_int2(blockIdx.x, whole       ? 1
+                                                    : w.ranks > 0 ? shared_by
+                                                                  : blocks_spanned(b, sg, blockIdx.x, chunk, s_prefix, tiles));
+            if (!whole && w.ranks == 0) w.open[blockIdx.x] = make_int2(seg, span.y);
             if (a.accumulate) w.span[seg] = span;
+        }
+    }
+
+    // ---- a cluster's blocks join their pieces of the segment, some rows each ----
+    if (w.ranks > 1) {
+        asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+        if (shared_by < 2) return;
+        const int seg = blockIdx.x / w.ranks, b = quotient(seg, w.tiles_div), sg = seg - b * tiles;
+        const int kh = quotient(sg, w.row_tiles_div), tile = sg - kh * w.row_tiles;
+        const float vs = TYPE == kE4m3 ? __ldg(a.c.v_scale + kh) : 1.f;
+#pragma unroll 1
+        for (int i = tid; i < (rows + w.ranks - 1 - rank) / w.ranks * (DP / 4); i += C::threads) {
+            const int y = i / (DP / 4), r = rank + y * w.ranks, d = 4 * (i - y * (DP / 4));
+            const RowRef ref = row_ref(a, w, b, kh, tile * rows + r);
+            if (!ref.real) continue;
+            float2 ml[kMaxRanks];
+            float4 v[kMaxRanks];
+            float mm = kNoRef, ll = 0.f;
+#pragma unroll
+            for (int x = 0; x < kMaxRanks; ++x) {
+                const size_t at = ((size_t)(blockIdx.x - rank + x) * 2 + (x == 0 ? 1 : 0)) * rows + r;
+                ml[x] = make_float2(kNoRef, 0.f);
+                v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (x < shared_by) {
+                    ml[x] = __ldcg(w.part_ml + at);
+                    v[x] = __ldcg(reinterpret_cast<const float4 *>(w.part_o + at * DP + d));
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < kMaxRanks; ++x) mm = fmaxf(mm, ml[x].x);
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int x = 0; x < kMaxRanks; ++x) {
+                const float f = ex2(ml[x].x - mm);
+                ll += ml[x].y * f;
+                sum.x += v[x].x * f, sum.y += v[x].y * f, sum.z += v[x].z * f, sum.w += v[x].w * f;
+            }
+            if (d < D) store_out4(a, ref.head * D + d, sum, row_factor(ll, vs));
+            if (d == 0 && a.lse) a.lse[ref.head] = row_lse(mm, ll);
         }
     }
 }
