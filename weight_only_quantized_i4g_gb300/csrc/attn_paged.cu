@@ -19,7 +19,7 @@ extern template AttnPlan attn_plan<kE4m3>(int, int);
 
 namespace {
 
-constexpr long long kWholeBytes = 384 << 10;
+constexpr long long kEnoughBytes = 128 << 10, kWholeBytes = 384 << 10;
 constexpr int kFinishThreads = 256;
 
 // The second kernel of a call.  Its first blocks join segments that several
@@ -175,16 +175,21 @@ Layout layout(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int
     y.score_slots = max_len;
     y.seqs = n_seq < kAttnMaxSeq ? n_seq : kAttnMaxSeq;
     // One block, or a cluster of two, four or eight, per segment, where all
-    // run at once and a block has at most kWholeBytes of K and V: an SM streams
-    // that in less than the second kernel takes (8 heads of 128 bf16: 520 slots
-    // 11.0 us in a block each, 12.3 in equal ranges; 1000 slots 13.2 and 12.7).
-    // Blocks of one SM each: 76 clusters of two run at once, 36 of four, 15 of
-    // eight.
+    // run at once: the fewest blocks of at most kEnoughBytes of K and V each,
+    // else the most of at most kWholeBytes (an SM streams that in less than the
+    // second kernel takes).  Clusters of one-block SMs that run at once: 76 of
+    // two, 36 of four, 15 of eight.  8 heads of 128 bf16, by blocks a segment:
+    //   520 slots: 10.2 us with one, 10.3 with two, 9.7 with four; equal ranges 12.3
+    //   1000: 13.2 with one, 11.2 with two, 9.7 with four; 12.7
+    //   2000: 11.2 with four, 9.8 with eight; 12.6
+    //   4000: 11.3 with eight; 14.2
     const long long segments = (long long)y.seqs * c.n_heads * y.row_tiles;
     const long long bytes = (long long)max_len * c.dim * (c.type == kE4m3 ? 1 : 2) * 2;
     const int sms = num_sms(), at_once[4] = {sms, sms / 2, sms * 36 / 152, sms * 15 / 152};
     y.ranks = 0;
-    for (int k = 3; k >= 0; --k)
+    for (int k = 0; k < 4 && !y.ranks; ++k)
+        if (segments <= at_once[k] && bytes <= kEnoughBytes << k) y.ranks = 1 << k;
+    for (int k = 3; k >= 0 && !y.ranks; --k)
         if (segments <= at_once[k] && bytes <= kWholeBytes << k) y.ranks = 1 << k;
     y.ctas = y.ranks ? (int)segments * y.ranks : sms;
     const size_t ctas = y.ctas;
