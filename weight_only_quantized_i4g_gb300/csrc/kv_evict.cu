@@ -34,7 +34,8 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // digits, each rank adds up one slice of the bins over the blocks and hands
 // the sums to all, and every block finds the same bin.  One block per head
 // took 315 us for three sequences of 100k slots, 8 heads, two thirds of it
-// here; the clusters spread that over the SMs.
+// here; the clusters spread that over the SMs.  A digit whose slots are all
+// kept ends the search (distinct weights: mostly the second).
 template <int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictArgs a, int cap) {
     constexpr int kSelWarps = kSelThreads / 32;
@@ -42,7 +43,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     __shared__ int s_hist[kBins], s_total[kBins];
     __shared__ int s_warp[2][kSelWarps];
     __shared__ int2 s_block[kMaxCluster];
-    __shared__ int s_digit, s_need;
+    __shared__ int s_digit, s_need, s_bin;
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     griddep_launch_dependents();
@@ -107,7 +108,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     __syncthreads();
 
     uint32_t prefix = 0;
-    if (tid == 0) s_digit = s_need = 0;
+    if (tid == 0) s_digit = s_need = s_bin = 0;
     if (any) {
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
@@ -165,14 +166,21 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
             if (before < need && need <= before + sum) {
 #pragma unroll
                 for (int i = 0; i < kBins / kSelThreads; ++i) {
-                    if (before < need && need <= before + mine[i]) s_digit = bins - 1 - (tid * each + i), s_need = need - before;
+                    if (before < need && need <= before + mine[i])
+                        s_digit = bins - 1 - (tid * each + i), s_need = need - before, s_bin = mine[i];
                     before += mine[i];
                 }
             }
             __syncthreads();
             prefix |= (uint32_t)s_digit << shift;
             need = s_need;                         // slots of this digit still to take
+            const bool all_of_it = need == s_bin;
             __syncthreads();
+            if (all_of_it && prefix > 0) {         // then those above the last key below the digit
+                --prefix;
+                need = 0;
+                break;
+            }
         }
     }
     // Emit in slot order, four neighbouring slots a lane: every warp counts its
