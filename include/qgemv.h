@@ -1,7 +1,8 @@
 /*
  * qgemv.h -- C ABI of libqgemv: dequantize-fused weight-only quantized GEMV
  * (decode, a handful of tokens) and dequant-GEMM (batched prefill) for three
- * packed weight formats, on one NVIDIA GB300 (sm_103a).
+ * packed weight formats, and the attention block between a decode step's
+ * projections, on one NVIDIA GB300 (sm_103a).
  *
  * Sources of each format's definition (page title, section):
  *   fmt=4  grouped int4     colibri PR #457 "metal: grouped-int4 (fmt=4) GEMV
