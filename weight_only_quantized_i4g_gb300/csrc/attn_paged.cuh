@@ -10,11 +10,12 @@
 // form tiles; a (sequence, head, tile) is a segment of steps of up to 16 slots
 // of one page.  A warp does 8 * NT rows; where there are more, GW warps share a
 // ring and each does its rows of the same steps (so K and V come from HBM and
-// L2 once for up to 64 rows).  Below, a warp stands for such a group.  All segments' steps, laid end to end, are cut
-// into one equal range per block (one block an SM) and each range into one per
-// warp: unequal lengths balance without the host knowing them.  A segment
-// counts kSegmentCost steps more than it has, for its Q and its end.  A warp keeps
-// the running maximum and sum of each row and O in registers (online softmax).
+// L2 once for up to 64 rows).  Below, a warp stands for such a group.
+// All segments' steps, laid end to end, are cut into one equal range per block
+// (one block an SM) and each range into one per warp: unequal lengths balance
+// without the host knowing them.  A segment counts kSegmentCost steps more than
+// it has, for its Q and its end.  A warp keeps the running maximum and sum of
+// each row and O in registers (online softmax).
 // A segment that ends inside its warp is finished there; pieces of one that
 // does not are joined in shared memory after the block's ranges are done, and
 // across blocks by a second kernel, always in slot order.  Where every segment
@@ -29,9 +30,10 @@
 // bank conflicts: a fragment's k indices are the 8 (or 16) consecutive
 // elements of a chunk, since the contraction over d may run in any order, and
 // the chunks are dealt to the threads so that the swizzle spreads them.
-// (Before: cp.async in fragment order, 64 to 128 bytes a row, read 5.2 TB/s;
-// cp.async of 512 consecutive bytes read 6.8, but its issue cost a warp 450 to
-// 570 cycles a step, against the 350 that HBM gives an SM for one.)
+// (cp.async in fragment order, 64 to 128 bytes a row and instruction, read 5.2
+// TB/s; in runs of 512 bytes 6.8, but it took a code path each for pages that
+// end inside a step, strides and padded heads, at the same issue cost, 450 to
+// 600 cycles a warp and step.)
 //
 // Products.  S^T = K Q^T with the 16 slots as M and 8 rows as N (a decode step
 // has few rows), then O^T = V^T P^T; P^T's fragment is the transpose of
