@@ -52,9 +52,9 @@ static int conflicts(const std::vector<int> &at, int size) {
     return worst;
 }
 
-template <int TYPE, int DP, int NT, int GW>
+template <int TYPE, int DP, int NT, int GW, bool THIRD>
 static void layout() {
-    using C = AttnCfg<TYPE, DP, NT, GW>;
+    using C = AttnCfg<TYPE, DP, NT, GW, THIRD>;
     const char *what = "layout";
     printf("type %d dp %d nt %d gw %d: W %d G %d NS %d stage %d smem %zu\n", TYPE, DP, NT, GW, C::W, C::G, C::NS, C::stage,
            attn_fixed_smem<C>());
@@ -105,14 +105,14 @@ static void layout() {
         }
 }
 
-template <int TYPE>
+template <int TYPE, bool THIRD>
 static void layouts() {
     std::set<int> done;
     for (int dim : {64, 128, 256})
         for (int rows : {1, 9, 17, 33}) {
-            attn_dispatch<TYPE>(rows, dim, [&](auto cfg) {
+            attn_dispatch<TYPE, THIRD>(rows, dim, [&](auto cfg) {
                 using C = decltype(cfg);
-                if (done.insert(C::DP * 100 + C::NT * 10 + C::GW).second) layout<TYPE, C::DP, C::NT, C::GW>();
+                if (done.insert(C::DP * 100 + C::NT * 10 + C::GW).second) layout<TYPE, C::DP, C::NT, C::GW, THIRD>();
                 CHECK(C::rows >= (rows < 33 ? rows : 32), "rows %d at %d", rows, dim);
                 return 0;
             });
@@ -183,9 +183,10 @@ static void share(const std::vector<int> &lens, int tiles, int page, int ctas, i
 
 int main() {
     divisions();
-    layouts<kBf16>();
-    layouts<kF16>();
-    layouts<kE4m3>();
+    layouts<kBf16, false>();
+    layouts<kBf16, true>();
+    layouts<kF16, false>();
+    layouts<kE4m3, false>();
     unsigned x = 7u;
     auto rnd = [&](int m) {
         x = x * 1664525u + 1013904223u;

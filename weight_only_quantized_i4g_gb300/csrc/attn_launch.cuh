@@ -9,8 +9,7 @@ namespace qg {
 struct AttnPlan {
     int dp, rows;       // padded head size, rows of a segment
     int box_bytes;      // bytes of a row that one copy moves
-    size_t piece_rows;  // rows of O that all warps of a block hold
-    size_t smem;        // without the lengths
+    size_t piece_rows;  // rows of O that all warps of a block hold, at most
 };
 
 // The smallest padded head size (the padding is not read from memory); then as
@@ -21,37 +20,38 @@ struct AttnPlan {
 // with four of two, 311 with two of four).  More than a group's rows are further segments.  48 ragged
 // bf16 sequences, 128 dimensions, 8 cache heads, 32 and 64 rows: 272 and 543 us
 // with segments of 16 rows, 321 and 632 with four tiles a warp.
-template <int TYPE, class Fn>
+template <int TYPE, bool THIRD, class Fn>
 auto attn_dispatch(int rows, int dim, Fn fn) {
     if (dim <= 64)
-        return rows <= 8    ? fn(AttnCfg<TYPE, 64, 1, 1>())
-               : rows <= 16 ? fn(AttnCfg<TYPE, 64, 2, 1>())
-               : rows <= 32 ? fn(AttnCfg<TYPE, 64, 2, 2>()) : fn(AttnCfg<TYPE, 64, 4, 2>());
+        return rows <= 8    ? fn(AttnCfg<TYPE, 64, 1, 1, THIRD>())
+               : rows <= 16 ? fn(AttnCfg<TYPE, 64, 2, 1, THIRD>())
+               : rows <= 32 ? fn(AttnCfg<TYPE, 64, 2, 2, THIRD>()) : fn(AttnCfg<TYPE, 64, 4, 2, THIRD>());
     if (dim <= 128)
-        return rows <= 8    ? fn(AttnCfg<TYPE, 128, 1, 1>())
-               : rows <= 16 ? fn(AttnCfg<TYPE, 128, 2, 1>())
-               : rows <= 32 ? fn(AttnCfg<TYPE, 128, 2, 2>()) : fn(AttnCfg<TYPE, 128, 2, 4>());
-    return rows <= 8    ? fn(AttnCfg<TYPE, 256, 1, 1>())
-           : rows <= 16 ? fn(AttnCfg<TYPE, 256, 1, 2>()) : fn(AttnCfg<TYPE, 256, 1, 4>());
+        return rows <= 8    ? fn(AttnCfg<TYPE, 128, 1, 1, THIRD>())
+               : rows <= 16 ? fn(AttnCfg<TYPE, 128, 2, 1, THIRD>())
+               : rows <= 32 ? fn(AttnCfg<TYPE, 128, 2, 2, THIRD>()) : fn(AttnCfg<TYPE, 128, 2, 4, THIRD>());
+    return rows <= 8    ? fn(AttnCfg<TYPE, 256, 1, 1, THIRD>())
+           : rows <= 16 ? fn(AttnCfg<TYPE, 256, 1, 2, THIRD>()) : fn(AttnCfg<TYPE, 256, 1, 4, THIRD>());
 }
 
+// The same for both forms of THIRD, but for the warps of a block.
 template <int TYPE>
 AttnPlan attn_plan(int rows, int dim) {
-    return attn_dispatch<TYPE>(rows, dim, [](auto cfg) {
+    return attn_dispatch<TYPE, false>(rows, dim, [](auto cfg) {
         using C = decltype(cfg);
-        return AttnPlan{C::DP, C::rows, C::BB, (size_t)C::W * C::warp_rows, attn_fixed_smem<C>()};
+        return AttnPlan{C::DP, C::rows, C::BB, (size_t)(C::GW > 1 ? 12 : C::W) * C::warp_rows};
     });
 }
 
-template <int TYPE>
-int launch_attn_stream(const AttnArgs &a, const AttnWork &w, const AttnPlan &pl, const CUtensorMap (&maps)[2],
-                       cudaStream_t st) {
-    return attn_dispatch<TYPE>(a.S * a.group, a.c.dim, [&](auto cfg) {
+template <int TYPE, bool THIRD>
+int launch_attn_stream(const AttnArgs &a, const AttnWork &w, const CUtensorMap (&maps)[2], cudaStream_t st) {
+    return attn_dispatch<TYPE, THIRD>(a.S * a.group, a.c.dim, [&](auto cfg) {
         using C = decltype(cfg);
-        const size_t smem = pl.smem + (2 * (size_t)a.n_seq + 1) * sizeof(int);
-        auto *kernel = attn_stream_kernel<TYPE, C::DP, C::NT, C::GW, true>;
+        static_assert(C::GW == 1 || C::W <= 12, "the plan's piece_rows");
+        const size_t smem = attn_fixed_smem<C>() + (2 * (size_t)a.n_seq + 1) * sizeof(int);
+        auto *kernel = attn_stream_kernel<TYPE, C::DP, C::NT, C::GW, THIRD, true>;
         if constexpr (C::GW == 1)
-            if (a.S == 1) kernel = attn_stream_kernel<TYPE, C::DP, C::NT, C::GW, false>;
+            if (a.S == 1) kernel = attn_stream_kernel<TYPE, C::DP, C::NT, C::GW, THIRD, false>;
         set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), 232448);
         return launch_clusters("qattn_paged", kernel, dim3(w.ctas), dim3(C::threads), w.ranks > 1 ? w.ranks : 1, smem, st, a, w,
                                maps[0], maps[1]);

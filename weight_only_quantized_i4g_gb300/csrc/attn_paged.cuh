@@ -81,9 +81,11 @@ struct AttnWork {
     FastDiv tiles_div, row_tiles_div, group_div, page_steps_div;
 };
 
-template <int TYPE, int DP_, int NT_, int GW_>
+// THIRD: P as three parts (a bf16 cache, f32 output).
+template <int TYPE, int DP_, int NT_, int GW_, bool THIRD_>
 struct AttnCfg {
     static constexpr int DP = DP_, NT = NT_, GW = GW_;
+    static constexpr bool THIRD = THIRD_;
     static constexpr int ESZ = TYPE == kE4m3 ? 1 : 2;
     static constexpr int warp_rows = 8 * NT, rows = GW * warp_rows;   // of a warp, of a segment
     static constexpr int KE = 16 / ESZ;               // elements of a K chunk
@@ -96,15 +98,21 @@ struct AttnCfg {
     static constexpr int NB = DP * ESZ / BB;          // boxes of a row
     static constexpr int box = 16 * BB;
     static constexpr int stage = 2 * NB * box;        // 16 slots of K, then of V
-    // as many warps as the registers of O, Q and S allow (16, 12 or 8 an SM)
-    static constexpr int regs = (ESZ == 1 ? 85 : 70) + 4 * MT * NT + NT * NI * (ESZ == 1 ? 8 : 4) + 8 * NT;
+    // as many warps as the registers of O, Q and S allow (16, 12 or 8 an SM);
+    // groups that would get 8 keep Q in shared memory, which makes it 12 (48
+    // ragged f16 sequences, 32 rows at 128 dimensions: 254 -> 224 us; e4m3 236 ->
+    // 209) unless that spills as it does with a third part of P (261 -> 273)
+    static constexpr int regs0 = (ESZ == 1 ? 85 : 70) + 4 * MT * NT + 8 * NT, regs_q = NT * NI * (ESZ == 1 ? 8 : 4);
+    static constexpr bool QS = GW > 1 && DP == 128 && !THIRD && regs0 + regs_q > 168;
+    static constexpr int regs = regs0 + (QS ? 0 : regs_q);
     static constexpr int W0 = regs <= 128 ? 16 : regs <= 168 ? 12 : 8;
     static constexpr int W = GW == 1 && stage > 8192 ? 4 : W0;
+    static constexpr int q_bytes = QS ? NT * NI * (ESZ == 1 ? 2 : 1) * 512 : 0;   // of a warp
     static constexpr int G = W / GW;                  // groups, a ring each
     // 8 rows of O on their way out; a lone warp takes the stage it has just read
     static constexpr int slab = GW > 1 ? 32 * DP : 0;
     // up to 192 KB of copies in flight
-    static constexpr int NS0 = (196608 - W * slab) / (G * stage);
+    static constexpr int NS0 = (196608 - W * (slab + q_bytes)) / (G * stage);
     static constexpr int NS = GW == 1 ? (NS0 > 6 ? 6 : NS0) : (NS0 > 8 ? 8 : NS0);
     static constexpr int ring = NS * stage;           // per group
     static_assert(ring >= rows * DP * 4, "an open piece takes the place of its ring");
@@ -136,7 +144,7 @@ __host__ __device__ __forceinline__ constexpr int slab_place(int r, int x) {
 template <class C>
 __host__ __device__ constexpr size_t attn_fixed_smem() {
     // 1 KB for the copies' alignment, then as laid out in the kernel
-    return 1024 + (size_t)C::G * C::ring + C::W * C::slab + C::G * C::NS * (8 + 8 + 16) +
+    return 1024 + (size_t)C::G * C::ring + C::W * (C::slab + C::q_bytes) + C::G * C::NS * (8 + 8 + 16) +
            C::G * 2 * C::rows * sizeof(float2) + C::G * 2 * 8;
 }
 
@@ -340,18 +348,18 @@ __host__ __device__ __forceinline__ int blocks_spanned(int b, int sg, int first,
 
 // DRAFT: several new tokens a sequence, the last of which some rows do not see.
 // (Without the code for those the calls of one token are 2% faster.)
-template <int TYPE, int DP_, int NT_, int GW_, bool DRAFT>
-__global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
+template <int TYPE, int DP_, int NT_, int GW_, bool THIRD, bool DRAFT>
+__global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, THIRD>::threads, 1)
     attn_stream_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnWork w,
                        const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
-    using C = AttnCfg<TYPE, DP_, NT_, GW_>;
+    using C = AttnCfg<TYPE, DP_, NT_, GW_, THIRD>;
     constexpr int DP = C::DP, NT = C::NT, W = C::W, GW = C::GW, G = C::G, NS = C::NS, NI = C::NI, E = C::E, NQ = C::NQ;
     constexpr int rows = C::rows, warp_rows = C::warp_rows;
     // flags of a step: its page is not in the pool; first and last of its segment
     constexpr int kMissing = 32, kFirst = 64, kLast = 128;
     extern __shared__ char smem_raw[];
     char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    uint64_t *s_bar = reinterpret_cast<uint64_t *>(smem + G * C::ring + W * C::slab);   // [G][NS]: a step has landed
+    uint64_t *s_bar = reinterpret_cast<uint64_t *>(smem + G * C::ring + W * (C::slab + C::q_bytes));   // [G][NS]: a step has landed
     uint64_t *s_free = s_bar + G * NS;                                        // [G][NS]: all warps have read it
     float2 *s_ml = reinterpret_cast<float2 *>(s_free + G * NS);               // [G][2][rows]
     int2 *s_piece = reinterpret_cast<int2 *>(s_ml + G * 2 * rows);            // [G][2]: {segment or -1, 1: ended | 2: in head_o}
@@ -465,11 +473,12 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
     // ---- the warp's range ----
     float o[C::MT][NT][4];
     float m[NT][2], l[NT][2];
-    uint32_t qf[NT][NI][C::ESZ == 1 ? 8 : 4];
+    constexpr int QW = C::ESZ == 1 ? 8 : 4;           // words of Q per chunk
+    uint32_t qf[C::QS ? 1 : NT][NI][QW];              // or in shared memory, each lane's own
+    const uint32_t q_mem = smem_addr(smem) + G * C::ring + W * C::slab + warp * C::q_bytes + lane * 16;
     float rs[NT][2];                                  // score factor of the thread's rows (e4m3: per row)
     const float factor = a.scale * 1.44269504088896340736f;
     constexpr float shift = TYPE == kBf16 ? 0.f : 6.f;
-    const bool third = TYPE == kBf16 && a.o_type == kF32;
     bool fresh = true;                                // at the start of a piece
     bool began_here = false;
     int stage = 0;
@@ -490,6 +499,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
             // Q as the B operand: row g of each 8, the thread's chunks
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
+                uint32_t(&qn)[NI][QW] = qf[C::QS ? 0 : nt];
                 const RowRef r = row_ref(a, w, b, kh, tile * rows + my_rows + 8 * nt + g);
                 const uint16_t *q = static_cast<const uint16_t *>(a.q) + ((size_t)b * a.S + r.s) * a.q_stride +
                                     (size_t)r.q_head * D;
@@ -499,7 +509,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
                         const int d = k_chunk<C>(i, c) * 8;
                         uint4 v = make_uint4(0, 0, 0, 0);
                         if (r.real && d < D) v = *reinterpret_cast<const uint4 *>(q + d);
-                        qf[nt][i][0] = v.x, qf[nt][i][1] = v.y, qf[nt][i][2] = v.z, qf[nt][i][3] = v.w;
+                        qn[i][0] = v.x, qn[i][1] = v.y, qn[i][2] = v.z, qn[i][3] = v.w;
                     }
                 } else {
                     float top = 0.f;
@@ -513,7 +523,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
                         const uint32_t x[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
 #pragma unroll
                         for (int u = 0; u < 8; ++u) {
-                            qf[nt][i][u] = x[u];
+                            qn[i][u] = x[u];
                             const float2 f = a.q_type == kF16 ? unpack_f16(x[u]) : unpack_bf16(x[u]);
                             if (fabsf(f.x) < INFINITY) top = fmaxf(top, fabsf(f.x));
                             if (fabsf(f.y) < INFINITY) top = fmaxf(top, fabsf(f.y));
@@ -529,12 +539,21 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
                     for (int i = 0; i < NI; ++i)
 #pragma unroll
                         for (int u = 0; u < 8; ++u) {
-                            const float2 f = a.q_type == kF16 ? unpack_f16(qf[nt][i][u]) : unpack_bf16(qf[nt][i][u]);
-                            qf[nt][i][u] = pack_f16(f.x * up, f.y * up);
+                            const float2 f = a.q_type == kF16 ? unpack_f16(qn[i][u]) : unpack_bf16(qn[i][u]);
+                            qn[i][u] = pack_f16(f.x * up, f.y * up);
                         }
                     const float down = factor * __ldg(a.c.k_scale + kh) * __uint_as_float((uint32_t)(127 - ex) << 23);
                     rs[nt][0] = __shfl_sync(~0u, down, 8 * c);
                     rs[nt][1] = __shfl_sync(~0u, down, 8 * c + 4);
+                }
+                if constexpr (C::QS) {
+#pragma unroll
+                    for (int i = 0; i < NI; ++i)
+#pragma unroll
+                        for (int u = 0; u < QW; u += 4)
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(q_mem + ((nt * NI + i) * QW + u) * 128),
+                                         "r"(qn[i][u]), "r"(qn[i][u + 1]), "r"(qn[i][u + 2]), "r"(qn[i][u + 3])
+                                         : "memory");
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -571,6 +590,19 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
             const uint4 x = lds128(src + chunk_place<C>(g, k_chunk<C>(i, c)));
             const uint4 y = lds128(src + chunk_place<C>(g + 8, k_chunk<C>(i, c)));
             const uint32_t kx[4] = {x.x, x.y, x.z, x.w}, ky[4] = {y.x, y.y, y.z, y.w};
+            uint32_t qi[NT][QW];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int u = 0; u < QW; u += 4) {
+                    if constexpr (C::QS) {
+                        const uint4 v = lds128(q_mem + ((nt * NI + i) * QW + u) * 128);
+                        qi[nt][u] = v.x, qi[nt][u + 1] = v.y, qi[nt][u + 2] = v.z, qi[nt][u + 3] = v.w;
+                    } else {
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) qi[nt][u + z] = qf[nt][i][u + z];
+                    }
+                }
 #pragma unroll
             for (int u = 0; u < C::KE / 4; ++u) {
                 uint32_t a0, a1, a2, a3;
@@ -583,8 +615,8 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float(&d)[4] = u & 1 ? s1[nt] : s[nt];
-                    if (i == 0 && u < 2) mma16816_first<TYPE>(d, a0, a1, a2, a3, qf[nt][i][2 * u], qf[nt][i][2 * u + 1]);
-                    else mma16816<TYPE>(d, a0, a1, a2, a3, qf[nt][i][2 * u], qf[nt][i][2 * u + 1]);
+                    if (i == 0 && u < 2) mma16816_first<TYPE>(d, a0, a1, a2, a3, qi[nt][2 * u], qi[nt][2 * u + 1]);
+                    else mma16816<TYPE>(d, a0, a1, a2, a3, qi[nt][2 * u], qi[nt][2 * u + 1]);
                 }
             }
         }
@@ -671,7 +703,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
                     const uint32_t r = pack_bf16(u, v);
                     ph[nt][half] = transpose8x8(h);
                     pl[nt][half] = transpose8x8(r);
-                    if (third) {
+                    if constexpr (THIRD) {
                         f = unpack_bf16(r);
                         pt[nt][half] = transpose8x8(pack_bf16(u - f.x, v - f.y));
                     }
@@ -736,7 +768,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
             }
             careful = __any_sync(~0u, odd);
         }
-        auto add_pv = [&](auto with_third) {
+        if (!DRAFT || __builtin_expect(!careful, 1)) {
 #pragma unroll
             for (int q = 0; q < NQ; ++q) {
                 uint32_t x[4][4];
@@ -755,16 +787,12 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
                         for (int nt = 0; nt < NT; ++nt) {
                             float(&acc)[4] = o[q * (E / 2) + t + y][nt];
                             const uint32_t(&v)[4] = f[y];
-                            if constexpr (with_third) mma16816<TYPE>(acc, v[0], v[1], v[2], v[3], pt[nt][0], pt[nt][1]);
+                            if constexpr (THIRD) mma16816<TYPE>(acc, v[0], v[1], v[2], v[3], pt[nt][0], pt[nt][1]);
                             mma16816<TYPE>(acc, v[0], v[1], v[2], v[3], pl[nt][0], pl[nt][1]);
                             mma16816<TYPE>(acc, v[0], v[1], v[2], v[3], ph[nt][0], ph[nt][1]);
                         }
                 }
             }
-        };
-        if (!DRAFT || __builtin_expect(!careful, 1)) {
-            if (TYPE == kBf16 && third) add_pv(std::true_type());
-            else add_pv(std::false_type());
         } else {
             // one slot at a time, added only to the rows that see it
 #pragma unroll 1
@@ -789,7 +817,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_>::threads, 1)
                             for (int nt = 0; nt < NT; ++nt) {
                                 const uint32_t a0 = f[y][0] & m0, a1 = f[y][1] & m0, a2 = f[y][2] & m1, a3 = f[y][3] & m1;
                                 float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                                if (TYPE == kBf16 && third) mma16816<TYPE>(acc, a0, a1, a2, a3, pt[nt][0], pt[nt][1]);
+                                if constexpr (THIRD) mma16816<TYPE>(acc, a0, a1, a2, a3, pt[nt][0], pt[nt][1]);
                                 mma16816<TYPE>(acc, a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
                                 mma16816<TYPE>(acc, a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
 #pragma unroll

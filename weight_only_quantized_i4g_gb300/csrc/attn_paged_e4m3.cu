@@ -2,7 +2,6 @@
 #include "attn_launch.cuh"
 
 namespace qg {
-template int launch_attn_stream<kE4m3>(const AttnArgs &, const AttnWork &, const AttnPlan &, const CUtensorMap (&)[2],
-                                cudaStream_t);
+template int launch_attn_stream<kE4m3, false>(const AttnArgs &, const AttnWork &, const CUtensorMap (&)[2], cudaStream_t);
 template AttnPlan attn_plan<kE4m3>(int rows, int dim);
 }
