@@ -100,16 +100,23 @@ __global__ void __launch_bounds__(kFinishThreads)
 
     const int at = blockIdx.x - join_blocks, heads = a.n_seq * a.c.n_heads;
     const int part = at / heads, bh = at - part * heads, b = bh / a.c.n_heads, kh = bh - b * a.c.n_heads;
-    const int len = seq_len(a.lens, b, a.max_len, nullptr);
+    // before the wait, past L1: the lengths, the tables and the weights so far
+    int len = __ldcg(a.lens + b);
+    len = len < 0 ? 0 : len < a.max_len ? len : a.max_len;
     if (part * kFinishThreads >= len) {
         if (blockIdx.x == 0) griddep_wait();          // this kernel must not be complete before the streaming kernel is
         return;
     }
     const int t = part * kFinishThreads + tid;
     SlotRef ref{-1, 0};
-    if (t < len) ref = find_slot(a.c, a.table + (size_t)b * a.table_stride, t);
+    if (t < len) {
+        int index;
+        split_slot(a.c, t, &index, &ref.off);
+        const int page = __ldcg(a.table + (size_t)b * a.table_stride + index);
+        if ((unsigned)page < (unsigned)a.c.n_pages) ref.page = page;
+    }
     float sum = 0.f, had = 0.f;
-    if (ref.page >= 0) had = a.c.weight[slot_weight(a.c, ref, kh)];
+    if (ref.page >= 0) had = __ldcg(a.c.weight + slot_weight(a.c, ref, kh));
     griddep_wait();
     for (int tile = 0; tile < w.row_tiles; ++tile) {
         const int seg = b * w.tiles + kh * w.row_tiles + tile;
