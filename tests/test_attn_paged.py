@@ -45,7 +45,7 @@ def test_e4m3_cache_with_f16_queries(qg):
     check_attention(pc, q, 1, 8, 0.09)
 
 
-@pytest.mark.parametrize("heads,group", [(1, 1), (1, 7), (8, 5), (3, 8), (2, 9), (1, 16), (2, 17), (1, 33), (1, 71)])
+@pytest.mark.parametrize("heads,group", [(1, 1), (1, 7), (8, 5), (3, 7), (2, 9), (1, 16), (2, 17), (1, 33), (1, 71)])
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_head_layouts(qg, heads, group, dim):
     pc = Paged(qg, [0, 3, 200, 47], heads, dim, "bf16", seed=group).fill()
