@@ -27,6 +27,13 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+// The ones of the low half of each byte, in that byte.
+__device__ __forceinline__ unsigned ones_of_nibbles(unsigned v) {
+    v &= 0x0F0F0F0Fu;
+    v -= v >> 1 & 0x05050505u;
+    return (v & 0x03030303u) + (v >> 2 & 0x03030303u);
+}
+
 // A cluster per sequence and head; its blocks share the slots in equal
 // stretches and keep their keys in shared memory (`cap` of them; a longer
 // stretch reads the rest again).  Three digits (11, 11, 10 bits) of the key of
@@ -65,6 +72,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     const int lo = a.sinks, hi = L - a.recent;
     int need = N - a.sinks - a.recent;             // to take from [lo, hi)
     const bool any = need > 0;
+    const bool quads = a.c.page % 4 == 0 && reinterpret_cast<uintptr_t>(a.c.weight) % 16 == 0;
     // this block's stretch, and each warp's in it
     const int per_warp = ((L + ranks * kSelWarps - 1) / (ranks * kSelWarps) + 31) & ~31, per = per_warp * kSelWarps;
     const int r0 = rank * per < L ? rank * per : L, r1 = r0 + per < L ? r0 + per : L;
@@ -83,27 +91,58 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
         }
     };
     const int in_smem = r1 - r0 < cap ? r1 - r0 : cap;
+    // of this block's stretch, the slots to choose from: m0 to m0 + m_n
+    const int m0 = r0 > lo ? r0 : lo, m_n = (r1 < hi ? r1 : hi) > m0 ? (r1 < hi ? r1 : hi) - m0 : 0;
+    auto count = [&](int t, uint32_t digit) {      // additions of one that a warp shares are combined in hardware
+        if ((unsigned)(t - m0) < (unsigned)m_n) atomicAdd(&s_hist[digit], 1);
+    };
     if (any) {
-        constexpr int kAhead = 8;                  // pages, then weights, eight of each in flight
-        for (int i = tid; i < in_smem; i += kAhead * kSelThreads) {
-            int page[kAhead], off[kAhead];
-            float wt[kAhead];
+        // the keys, and the first digit's counts with them
+        for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
+        __syncthreads();
+        if (quads) {
+            // a page holds whole fours: one look-up and one load for four slots,
+            // eight look-ups, then four loads in flight
+            constexpr int kAhead = 8, kLoads = 4;
+            for (int i = 4 * tid; i < in_smem; i += 4 * kAhead * kSelThreads) {
+                int page[kAhead], off[kAhead];
 #pragma unroll
-            for (int x = 0; x < kAhead; ++x) {
-                int index;
-                split_slot(a.c, r0 + i + x * kSelThreads, &index, &off[x]);
-                page[x] = i + x * kSelThreads < in_smem ? __ldg(row + index) : -1;
+                for (int x = 0; x < kAhead; ++x) {
+                    int index;
+                    split_slot(a.c, r0 + i + x * 4 * kSelThreads, &index, &off[x]);
+                    page[x] = i + x * 4 * kSelThreads < in_smem ? __ldg(row + index) : -1;
+                }
+#pragma unroll
+                for (int x0 = 0; x0 < kAhead; x0 += kLoads) {
+                    float4 wt[kLoads];
+#pragma unroll
+                    for (int x = 0; x < kLoads; ++x) {
+                        const SlotRef r{page[x0 + x], off[x0 + x]};
+                        if ((unsigned)r.page < (unsigned)a.c.n_pages)
+                            wt[x] = __ldg(reinterpret_cast<const float4 *>(a.c.weight + slot_weight(a.c, r, h)));
+                    }
+#pragma unroll
+                    for (int x = 0; x < kLoads; ++x) {
+                        const int at = i + (x0 + x) * 4 * kSelThreads;
+                        if (at >= in_smem) break;
+                        const bool ok = (unsigned)page[x0 + x] < (unsigned)a.c.n_pages;
+                        const uint4 k = ok ? make_uint4(weight_key(wt[x].x), weight_key(wt[x].y), weight_key(wt[x].z),
+                                                        weight_key(wt[x].w))
+                                           : make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4 *>(s_key + at) = k;
+                        count(r0 + at, k.x >> 21), count(r0 + at + 1, k.y >> 21);
+                        count(r0 + at + 2, k.z >> 21), count(r0 + at + 3, k.w >> 21);
+                    }
+                }
             }
-#pragma unroll
-            for (int x = 0; x < kAhead; ++x) {
-                const bool ok = (unsigned)page[x] < (unsigned)a.c.n_pages;
-                wt[x] = ok ? __ldg(a.c.weight + slot_weight(a.c, SlotRef{page[x], off[x]}, h)) : 0.f;
+        } else {
+            for (int i = tid; i < in_smem; i += kSelThreads) {
+                const uint32_t k = key_in_cache(r0 + i);
+                s_key[i] = k;
+                count(r0 + i, k >> 21);
             }
-#pragma unroll
-            for (int x = 0; x < kAhead; ++x)
-                if (i + x * kSelThreads < in_smem)
-                    s_key[i + x * kSelThreads] = (unsigned)page[x] < (unsigned)a.c.n_pages ? weight_key(wt[x]) : 0u;
         }
+        for (int i = in_smem + tid; i < r1 - r0; i += kSelThreads) count(r0 + i, key_in_cache(r0 + i) >> 21);
     }
     __syncthreads();
 
@@ -112,17 +151,17 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     if (any) {
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
-            const int done = pass == 0 ? 32 : pass == 1 ? 21 : 10;            // low bits not yet fixed
-            for (int i = tid; i < bins; i += kSelThreads) s_hist[i] = 0;
-            __syncthreads();
-            // additions of one to an address that a warp shares are combined in hardware
-            for (int t = r0 + 4 * tid; t < r1; t += 4 * kSelThreads) {
-                uint32_t k[4];
-                keys_at(t, k);
+            if (pass > 0) {
+                const int done = pass == 1 ? 21 : 10;                         // low bits not yet fixed
+                for (int i = tid; i < bins; i += kSelThreads) s_hist[i] = 0;
+                __syncthreads();
+                for (int t = r0 + 4 * tid; t < r1; t += 4 * kSelThreads) {
+                    uint32_t k[4];
+                    keys_at(t, k);
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (t + x < r1 && t + x >= lo && t + x < hi && (pass == 0 || k[x] >> done == prefix >> done))
-                        atomicAdd(&s_hist[(k[x] >> shift) & (bins - 1)], 1);
+                    for (int x = 0; x < 4; ++x)
+                        if ((k[x] ^ prefix) >> done == 0) count(t + x, (k[x] >> shift) & (bins - 1));
+                }
             }
             int *total = s_hist;
             if (ranks > 1) {
@@ -194,14 +233,14 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
         unsigned f = 0;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            const bool in = t + x < t1, safe = t + x < lo || t + x >= hi;
-            if (in && (safe || (any && k[x] > prefix))) f |= 1u << x;
-            if (in && !safe && any && k[x] == prefix) f |= 16u << x;
+            const bool safe = (unsigned)(t + x - lo) >= (unsigned)(hi - lo);
+            if (t + x < t1 && (safe || k[x] > prefix)) f |= 1u << x;
+            if (t + x < t1 && !safe && k[x] == prefix) f |= 16u << x;
         }
         return f;
     };
     int sure_n = 0, tie_n = 0;
-    unsigned long long seen = 0;                   // the flags of the first eight rounds
+    unsigned long long seen = 0;                   // the flags of the first eight rounds of 128 slots
     int round = 0;
     for (int t = t0 + 4 * lane; t < t1; t += 128, ++round) {
         const unsigned f = flags(t);
@@ -227,28 +266,44 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
         cluster.sync();                            // also the last access to another block's memory
         for (int x = 0; x < rank; ++x) base_sure += s_block[x].x, base_tie += s_block[x].y;
     }
-    round = 0;
-    for (int t = t0 + 4 * lane; t - 4 * lane < t1; t += 128, ++round) {
-        const unsigned f = round < 8 ? (unsigned)(seen >> (8 * round)) & 255u : flags(t);
-        // both counts of the lanes before this one: up to 128 each
-        const int mine = __popc(f & 15u) | __popc(f >> 4) << 16;
-        int inc = mine;
+    // four rounds at a time: a count of a round is 128 at most and takes a byte
+    const bool ties = need > 0 && tie_n > 0;       // the same in every lane
+    for (int g = 0; t0 + 128 * g < t1; g += 4) {
+        const int t = t0 + 128 * g + 4 * lane;
+        unsigned f4 = 0;
+        if (g < 8) {
+            f4 = (unsigned)(seen >> (8 * g));
+        } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) f4 |= flags(t + 128 * x) << (8 * x);
+        }
+        const unsigned sure4 = ones_of_nibbles(f4), tie4 = ties ? ones_of_nibbles(f4 >> 4) : 0u;
+        unsigned sure_in = sure4, tie_in = tie4;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(~0u, inc, o);
-            if (lane >= o) inc += v;
+            const unsigned v = __shfl_up_sync(~0u, sure_in, o);
+            if (lane >= o) sure_in += v;
         }
-        int sure = base_sure + ((inc - mine) & 0xFFFF), tie = base_tie + ((inc - mine) >> 16);
+        if (ties)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int at = sure + (tie < need ? tie : need);
-            const bool is_sure = f >> x & 1u, is_tie = f >> (4 + x) & 1u;
-            // at < N always, unless the weights change under the call
-            if ((is_sure || (is_tie && tie < need)) && at < N) kept[at] = t + x;
-            sure += is_sure, tie += is_tie;
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned v = __shfl_up_sync(~0u, tie_in, o);
+                if (lane >= o) tie_in += v;
+            }
+        const unsigned sure_all = __shfl_sync(~0u, sure_in, 31), tie_all = __shfl_sync(~0u, tie_in, 31);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            int sure = base_sure + ((sure_in - sure4) >> (8 * r) & 255u), tie = base_tie + ((tie_in - tie4) >> (8 * r) & 255u);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int at = sure + (tie < need ? tie : need);
+                const bool is_sure = f4 >> (8 * r + x) & 1u, is_tie = ties && (f4 >> (8 * r + 4 + x) & 1u);
+                // at < N always, unless the weights change under the call
+                if ((is_sure || (is_tie && tie < need)) && at < N) kept[at] = t + 128 * r + x;
+                sure += is_sure, tie += is_tie;
+            }
+            base_sure += sure_all >> (8 * r) & 255u, base_tie += tie_all >> (8 * r) & 255u;
         }
-        const int all = __shfl_sync(~0u, inc, 31);
-        base_sure += all & 0xFFFF, base_tie += all >> 16;
     }
 }
 
