@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
                     keys_at(t, k);
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
-                        if ((k[x] ^ prefix) >> done == 0) count(t + x, (k[x] >> shift) & (bins - 1));
+                        if ((k[x] ^ prefix) < 1u << done) count(t + x, (k[x] >> shift) & (bins - 1));
                 }
             }
             int *total = s_hist;
@@ -198,10 +198,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
             }
             if (lane == 31) s_warp[0][warp] = inc;
             __syncthreads();
-            int before = inc - sum, others = lane < warp && lane < kSelWarps ? s_warp[0][lane] : 0;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) others += __shfl_xor_sync(~0u, others, o);
-            before += others;
+            int before = inc - sum + __reduce_add_sync(~0u, lane < warp ? s_warp[0][lane] : 0);
             if (before < need && need <= before + sum) {
 #pragma unroll
                 for (int i = 0; i < kBins / kSelThreads; ++i) {
@@ -247,20 +244,13 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
         if (round < 8) seen |= (unsigned long long)f << (8 * round);
         sure_n += __popc(f & 15u), tie_n += __popc(f >> 4);
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        sure_n += __shfl_xor_sync(~0u, sure_n, o);
-        tie_n += __shfl_xor_sync(~0u, tie_n, o);
-    }
+    sure_n = __reduce_add_sync(~0u, sure_n), tie_n = __reduce_add_sync(~0u, tie_n);
     if (lane == 0) s_warp[0][warp] = sure_n, s_warp[1][warp] = tie_n;
     __syncthreads();
-    int base_sure = 0, base_tie = 0, all_sure = 0, all_tie = 0;
-#pragma unroll
-    for (int x = 0; x < kSelWarps; ++x) {
-        const int s = s_warp[0][x], e = s_warp[1][x];
-        if (x < warp) base_sure += s, base_tie += e;
-        all_sure += s, all_tie += e;
-    }
+    const int of_sure = lane < kSelWarps ? s_warp[0][lane] : 0, of_tie = lane < kSelWarps ? s_warp[1][lane] : 0;
+    const int all_sure = __reduce_add_sync(~0u, of_sure), all_tie = __reduce_add_sync(~0u, of_tie);
+    int base_sure = __reduce_add_sync(~0u, lane < warp ? of_sure : 0);
+    int base_tie = __reduce_add_sync(~0u, lane < warp ? of_tie : 0);
     if (ranks > 1) {
         if (tid < ranks) cluster.map_shared_rank(s_block, tid)[rank] = make_int2(all_sure, all_tie);
         cluster.sync();                            // also the last access to another block's memory
@@ -294,13 +284,20 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             int sure = base_sure + ((sure_in - sure4) >> (8 * r) & 255u), tie = base_tie + ((tie_in - tie4) >> (8 * r) & 255u);
+            // at < N always, unless the weights change under the call
+            if (ties) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int at = sure + (tie < need ? tie : need);
-                const bool is_sure = f4 >> (8 * r + x) & 1u, is_tie = ties && (f4 >> (8 * r + 4 + x) & 1u);
-                // at < N always, unless the weights change under the call
-                if ((is_sure || (is_tie && tie < need)) && at < N) kept[at] = t + 128 * r + x;
-                sure += is_sure, tie += is_tie;
+                for (int x = 0; x < 4; ++x) {
+                    const int at = sure + (tie < need ? tie : need);
+                    const bool is_sure = f4 >> (8 * r + x) & 1u, is_tie = f4 >> (8 * r + 4 + x) & 1u;
+                    if ((is_sure || (is_tie && tie < need)) && at < N) kept[at] = t + 128 * r + x;
+                    sure += is_sure, tie += is_tie;
+                }
+            } else {
+                int at = sure + (tie < need ? tie : need);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if ((f4 >> (8 * r + x) & 1u) && at < N) kept[at++] = t + 128 * r + x;
             }
             base_sure += sure_all >> (8 * r) & 255u, base_tie += tie_all >> (8 * r) & 255u;
         }
