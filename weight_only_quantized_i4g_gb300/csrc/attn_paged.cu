@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kFinishThreads)
             }
         }
         if (!ref.real || set >= sets) return;
-        const float vs = a.c.type == kE4m3 ? __ldg(a.c.v_scale + kh) : 1.f;
+        const float vs = a.c.type == kE4m3 ? a.c.v_scale[kh] : 1.f;
         if (d < a.c.dim) store_out4(a, ref.head * a.c.dim + d, sum, row_factor(l, vs));
         if (d == 0 && a.lse) a.lse[ref.head] = row_lse(m, l);
         return;

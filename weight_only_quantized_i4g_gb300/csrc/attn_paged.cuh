@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, THIRD>::threads, 
     int to_issue = mate == 0 ? left : 0, istage = 0, look_page = 0;
     auto look = [&]() {
         if (to_issue == 0) return;
-        look_page = __ldg(a.table + (size_t)ip.b * a.table_stride + ip.page);
+        look_page = a.table[(size_t)ip.b * a.table_stride + ip.page];
     };
     // reuse: wait until the group's other warps have read what the stage held
     auto issue = [&](bool reuse, uint32_t phase) {
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, THIRD>::threads, 
                             const float2 f = a.q_type == kF16 ? unpack_f16(qn[i][u]) : unpack_bf16(qn[i][u]);
                             qn[i][u] = pack_f16(f.x * up, f.y * up);
                         }
-                    const float down = factor * __ldg(a.c.k_scale + kh) * __uint_as_float((uint32_t)(127 - ex) << 23);
+                    const float down = factor * a.c.k_scale[kh] * __uint_as_float((uint32_t)(127 - ex) << 23);
                     rs[nt][0] = __shfl_sync(~0u, down, 8 * c);
                     rs[nt][1] = __shfl_sync(~0u, down, 8 * c + 4);
                 }
@@ -837,7 +837,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, THIRD>::threads, 
             fresh = true;
             const int here = state.z, b = quotient(here, w.tiles_div), sg = here - b * tiles;
             const int kh = quotient(sg, w.row_tiles_div), tile = sg - kh * w.row_tiles;
-            const float vs = TYPE == kE4m3 ? __ldg(a.c.v_scale + kh) : 1.f;
+            const float vs = TYPE == kE4m3 ? a.c.v_scale[kh] : 1.f;
             const bool whole = ended && began_here;
             const int slot = 2 * group + (began_here ? 1 : 0), row0 = slot * rows + my_rows;
             if (whole && a.accumulate && lane == 0 && mate == 0) w.span[here] = make_int2(blockIdx.x, 1);
@@ -912,7 +912,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, THIRD>::threads, 
         const bool whole = starts && ends;
         const int b = quotient(seg, w.tiles_div), sg = seg - b * tiles;
         const int kh = quotient(sg, w.row_tiles_div), tile = sg - kh * w.row_tiles;
-        const float vs = TYPE == kE4m3 ? __ldg(a.c.v_scale + kh) : 1.f;
+        const float vs = TYPE == kE4m3 ? a.c.v_scale[kh] : 1.f;
         const size_t out = ((size_t)blockIdx.x * 2 + (starts ? 1 : 0)) * rows;
 #pragma unroll 1
         for (int i = tid; i < rows * (DP / 4); i += C::threads) {
@@ -960,7 +960,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, THIRD>::threads, 
         if (shared_by < 2) return;
         const int seg = blockIdx.x / w.ranks, b = quotient(seg, w.tiles_div), sg = seg - b * tiles;
         const int kh = quotient(sg, w.row_tiles_div), tile = sg - kh * w.row_tiles;
-        const float vs = TYPE == kE4m3 ? __ldg(a.c.v_scale + kh) : 1.f;
+        const float vs = TYPE == kE4m3 ? a.c.v_scale[kh] : 1.f;
 #pragma unroll 1
         for (int i = tid; i < (rows + w.ranks - 1 - rank) / w.ranks * (DP / 4); i += C::threads) {
             const int y = i / (DP / 4), r = rank + y * w.ranks, d = 4 * (i - y * (DP / 4));

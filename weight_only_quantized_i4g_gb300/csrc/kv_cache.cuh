@@ -59,7 +59,7 @@ __device__ __forceinline__ SlotRef find_slot(const KvView &c, const int *row, in
     SlotRef r;
     int index;
     split_slot(c, t, &index, &r.off);
-    const int p = __ldg(row + index);
+    const int p = row[index];
     r.page = (unsigned)p < (unsigned)c.n_pages ? p : -1;
     return r;
 }
@@ -74,7 +74,7 @@ __device__ __forceinline__ size_t slot_weight(const KvView &c, SlotRef r, int he
 // Length of sequence b, held to [0, max_len]; a length outside raises the
 // error word (by the thread that asks with err != NULL).
 __device__ __forceinline__ int seq_len(const int *lens, int b, int max_len, int *err) {
-    const int n = __ldg(lens + b);
+    const int n = lens[b];
     if ((unsigned)n <= (unsigned)max_len) return n;
     raise_device_error(err, kErrPage);
     return n < 0 ? 0 : max_len;

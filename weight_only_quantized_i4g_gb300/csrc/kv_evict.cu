@@ -53,8 +53,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     __shared__ int s_digit, s_need, s_bin;
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();                   // after the wait: the copies' kernel reads lengths and tables before its own
     const int bh = blockIdx.x / ranks, b = bh / a.c.n_heads, h = bh - b * a.c.n_heads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int L = seq_len(a.lens, b, a.max_len, tid == 0 && rank == 0 ? a.err : nullptr);
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     const int r0 = rank * per < L ? rank * per : L, r1 = r0 + per < L ? r0 + per : L;
     auto key_in_cache = [&](int t) -> uint32_t {
         const SlotRef r = find_slot(a.c, row, t);
-        return r.page < 0 ? 0u : weight_key(__ldg(a.c.weight + slot_weight(a.c, r, h)));
+        return r.page < 0 ? 0u : weight_key(a.c.weight[slot_weight(a.c, r, h)]);
     };
     // four keys from t on (t - r0 and cap are multiples of four), 0 past the stretch
     auto keys_at = [&](int t, uint32_t (&k)[4]) {
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
                 for (int x = 0; x < kAhead; ++x) {
                     int index;
                     split_slot(a.c, r0 + i + x * 4 * kSelThreads, &index, &off[x]);
-                    page[x] = i + x * 4 * kSelThreads < in_smem ? __ldg(row + index) : -1;
+                    page[x] = i + x * 4 * kSelThreads < in_smem ? row[index] : -1;
                 }
 #pragma unroll
                 for (int x0 = 0; x0 < kAhead; x0 += kLoads) {
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
                     for (int x = 0; x < kLoads; ++x) {
                         const SlotRef r{page[x0 + x], off[x0 + x]};
                         if ((unsigned)r.page < (unsigned)a.c.n_pages)
-                            wt[x] = __ldg(reinterpret_cast<const float4 *>(a.c.weight + slot_weight(a.c, r, h)));
+                            wt[x] = *reinterpret_cast<const float4 *>(a.c.weight + slot_weight(a.c, r, h));
                     }
 #pragma unroll
                     for (int x = 0; x < kLoads; ++x) {
@@ -311,22 +311,36 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
                                                                   int slots) {
     __shared__ long long s_src[kMoveSlots], s_dst[kMoveSlots];
     griddep_launch_dependents();
-    griddep_wait();
     const int bh = blockIdx.x, b = bh / a.c.n_heads, h = bh - b * a.c.n_heads, tid = threadIdx.x;
-    const int n = __ldg(a.new_lens + b), len = seq_len(a.lens, b, a.max_len, nullptr);
+    // before the wait, past L1: all but `kept` stands
+    int len = __ldcg(a.lens + b);
+    len = len < 0 ? 0 : len < a.max_len ? len : a.max_len;
+    const int n = len < a.budget ? len : a.budget;
+    auto place = [&](long long i) {                // of kept slot i in the new pages
+        SlotRef r{-1, 0};
+        if (tid < slots && i < n) {
+            int index;
+            split_slot(a.c, (int)i, &index, &r.off);
+            const int page = __ldcg(a.dst_table + (size_t)b * a.dst_stride + index);
+            if ((unsigned)page < (unsigned)a.c.n_pages) r.page = page;
+        }
+        return r;
+    };
+    SlotRef d = place((long long)blockIdx.y * slots + tid);
+    griddep_wait();
     for (long long i0 = (long long)blockIdx.y * slots; i0 < n; i0 += (long long)gridDim.y * slots) {
         const int count = n - i0 < slots ? (int)(n - i0) : slots;
+        float weight = 0.f;
+        bool ok = false;
         __syncthreads();
         if (tid < count) {
-            const int i = (int)i0 + tid;
-            const int t = __ldg(a.kept + (size_t)bh * a.budget + i);
+            const int t = a.kept[(size_t)bh * a.budget + (int)i0 + tid];
             SlotRef s{-1, 0};
             if ((unsigned)t < (unsigned)len) s = find_slot(a.c, a.table + (size_t)b * a.table_stride, t);
-            const SlotRef d = find_slot(a.c, a.dst_table + (size_t)b * a.dst_stride, i);
-            const bool ok = s.page >= 0 && d.page >= 0;
+            ok = s.page >= 0 && d.page >= 0;
             s_src[tid] = ok ? slot_bytes(a.c, s, h) : -1;
             s_dst[tid] = ok ? slot_bytes(a.c, d, h) : -1;
-            if (ok) a.c.weight[slot_weight(a.c, d, h)] = a.c.weight[slot_weight(a.c, s, h)];
+            if (ok) weight = a.c.weight[slot_weight(a.c, s, h)];
             else raise_device_error(a.err, kErrPage);
         }
         __syncthreads();
@@ -352,6 +366,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
                 *reinterpret_cast<uint4 *>(a.c.v + to[x]) = v[x];
             }
         }
+        if (ok) a.c.weight[slot_weight(a.c, d, h)] = weight;
+        d = place(i0 + (long long)gridDim.y * slots + tid);
     }
 }
 

@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_append_kernel(const __gr
     // The angle is formed and reduced to one turn in 64 bits: in binary32 it
     // would be off by pos * 2^-24 radians, 0.06 at position 2^20.
     for (int j = threadIdx.x; j < half; j += kRopeThreads) {
-        const double x = (double)__ldg(a.pos + (size_t)t * a.n_axes + a.axis[j]) * (double)__ldg(a.inv_freq + j) *
+        const double x = (double)a.pos[(size_t)t * a.n_axes + a.axis[j]] * (double)a.inv_freq[j] *
                          0.15915494309189533577;   // 1 / (2 pi): turns
         sincospif(2.0f * (float)(x - rint(x)), &s_sin[j], &s_cos[j]);
     }
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_append_kernel(const __gr
     // where this token's k and v go
     SlotRef ref{-1, 0};
     if (h1 > a.n_q_heads) {
-        const int b = __ldg(a.seq + t), slot = __ldg(a.slot + t);
+        const int b = a.seq[t], slot = a.slot[t];
         if (slot >= 0) {
             if ((unsigned)b < (unsigned)a.n_seq && slot < (long long)a.table_stride * a.c.page)
                 ref = find_slot(a.c, a.table + (size_t)b * a.table_stride, slot);
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_append_kernel(const __gr
             if (ref.page < 0) continue;
             const int kh = h - a.n_q_heads - (is_v ? a.c.n_heads : 0);
             base = (is_v ? a.c.v : a.c.k) + slot_bytes(a.c, ref, kh);
-            if (type == kE4m3) scale = __ldg((is_v ? a.c.v_scale : a.c.k_scale) + kh);
+            if (type == kE4m3) scale = *((is_v ? a.c.v_scale : a.c.k_scale) + kh);
             if (!is_v && u == 0 && a.c.weight) a.c.weight[slot_weight(a.c, ref, kh)] = 0.f;
         }
         if constexpr (VEC) {
