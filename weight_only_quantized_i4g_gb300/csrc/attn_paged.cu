@@ -22,7 +22,11 @@ extern template AttnPlan attn_plan<kE4m3>(int, int);
 namespace {
 
 constexpr long long kEnoughBytes = 128 << 10, kWholeBytes = 384 << 10;
-constexpr int kFinishThreads = 256;
+// Slots a thread adds weights for: its chain of dependent reads, not bytes,
+// bounds the second kernel (9 sequences of 500 to 8192 slots, 8 heads, 40 query
+// heads: 42.4 us a call with one, 39.8 with two, 41.0 with four; 40 sequences
+// of 2000 and more: 178, 165, 168).
+constexpr int kFinishThreads = 256, kFinishSlots = 2;
 
 // The second kernel of a call.  Its first blocks join segments that several
 // blocks of the streaming kernel share: block (x, y) does `per` rows of the
@@ -30,7 +34,7 @@ constexpr int kFinishThreads = 256;
 // piece, then the first pieces of the blocks after it).  A thread takes four
 // elements of a row of every so many pieces, four loads in flight.  The
 // further blocks add up attention weights from the scores that the streaming
-// kernel left, a thread a slot:
+// kernel left, a thread two slots:
 //   weight[t] += sum over the rows of a key-value head of 2^(z_t - lse).
 __global__ void __launch_bounds__(kFinishThreads)
     attn_finish_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnWork w, int rows, int dp,
@@ -100,35 +104,51 @@ __global__ void __launch_bounds__(kFinishThreads)
 
     const int at = blockIdx.x - join_blocks, heads = a.n_seq * a.c.n_heads;
     const int part = at / heads, bh = at - part * heads, b = bh / a.c.n_heads, kh = bh - b * a.c.n_heads;
-    // before the wait, past L1: the lengths, the tables and the weights so far
+    // before the wait, past L1: lengths and tables; then all loads that depend on no other
     int len = __ldcg(a.lens + b);
     len = len < 0 ? 0 : len < a.max_len ? len : a.max_len;
-    if (part * kFinishThreads >= len) {
+    const int t0 = part * kFinishThreads * kFinishSlots + tid;
+    if (t0 - tid >= len) {
         if (blockIdx.x == 0) griddep_wait();          // this kernel must not be complete before the streaming kernel is
         return;
     }
-    const int t = part * kFinishThreads + tid;
-    SlotRef ref{-1, 0};
-    if (t < len) {
-        int index;
-        split_slot(a.c, t, &index, &ref.off);
-        const int page = __ldcg(a.table + (size_t)b * a.table_stride + index);
-        if ((unsigned)page < (unsigned)a.c.n_pages) ref.page = page;
+    SlotRef ref[kFinishSlots];
+    float sum[kFinishSlots], had[kFinishSlots];
+#pragma unroll
+    for (int x = 0; x < kFinishSlots; ++x) {
+        const int t = t0 + x * kFinishThreads;
+        ref[x].page = -1, sum[x] = had[x] = 0.f;
+        if (t < len) {
+            int index;
+            split_slot(a.c, t, &index, &ref[x].off);
+            ref[x].page = __ldcg(a.table + (size_t)b * a.table_stride + index);
+        }
     }
-    float sum = 0.f, had = 0.f;
-    if (ref.page >= 0) had = __ldcg(a.c.weight + slot_weight(a.c, ref, kh));
     griddep_wait();
     for (int tile = 0; tile < w.row_tiles; ++tile) {
         const int seg = b * w.tiles + kh * w.row_tiles + tile;
-        const float *z = w.scores + ((size_t)seg * w.score_slots + t) * rows;
-        float4 z0 = make_float4(0.f, 0.f, 0.f, 0.f), z1 = z0;          // the first rows' scores, while lse comes
-        if (t < len) z0 = reinterpret_cast<const float4 *>(z)[0], z1 = reinterpret_cast<const float4 *>(z)[1];
+        const float *z = w.scores + ((size_t)seg * w.score_slots + t0) * w.score_rows;
+        const size_t next = (size_t)kFinishThreads * w.score_rows;
+        const int2 span = tid < rows ? w.span[seg] : make_int2(0, 0);
+        float4 z0[kFinishSlots], z1[kFinishSlots];    // the first rows' scores, while lse comes
+#pragma unroll
+        for (int x = 0; x < kFinishSlots; ++x)
+            if (t0 + x * kFinishThreads < len) {
+                z0[x] = reinterpret_cast<const float4 *>(z + x * next)[0];
+                if (w.score_rows > 4) z1[x] = reinterpret_cast<const float4 *>(z + x * next)[1];
+            }
+        if (tile == 0) {
+#pragma unroll
+            for (int x = 0; x < kFinishSlots; ++x) {
+                if ((unsigned)ref[x].page >= (unsigned)a.c.n_pages) ref[x].page = -1;
+                if (ref[x].page >= 0) had[x] = a.c.weight[slot_weight(a.c, ref[x], kh)];
+            }
+        }
         __syncthreads();
         if (tid < rows) {
             const RowRef r = row_ref(a, w, b, kh, tile * rows + tid);
             float lse = -INFINITY;                    // in log2 units
             if (r.real) {
-                const int2 span = w.span[seg];
                 if (span.y == 1) {
                     lse = a.lse[r.head] * 1.44269504088896340736f;
                 } else {                              // its pieces' statistics: the join may not have run yet
@@ -146,18 +166,24 @@ __global__ void __launch_bounds__(kFinishThreads)
             s_lse[tid] = lse;
         }
         __syncthreads();
-        if (ref.page < 0) continue;
-        auto add = [&](float x, int r) {
-            if (s_lse[r] != -INFINITY) sum += ex2(x - s_lse[r]);
-        };
-        add(z0.x, 0), add(z0.y, 1), add(z0.z, 2), add(z0.w, 3), add(z1.x, 4), add(z1.y, 5), add(z1.z, 6), add(z1.w, 7);
+#pragma unroll
+        for (int x = 0; x < kFinishSlots; ++x) {
+            if (ref[x].page < 0) continue;
+            auto add = [&](float y, int r) {
+                if (s_lse[r] != -INFINITY) sum[x] += ex2(y - s_lse[r]);
+            };
+            add(z0[x].x, 0), add(z0[x].y, 1), add(z0[x].z, 2), add(z0[x].w, 3);
+            if (w.score_rows > 4) add(z1[x].x, 4), add(z1[x].y, 5), add(z1[x].z, 6), add(z1[x].w, 7);
 #pragma unroll 2
-        for (int r = 8; r < rows && tile * rows + r < R; r += 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(z + r);
-            add(x.x, r), add(x.y, r + 1), add(x.z, r + 2), add(x.w, r + 3);
+            for (int r = 8; r < rows && tile * rows + r < R; r += 4) {
+                const float4 y = *reinterpret_cast<const float4 *>(z + x * next + r);
+                add(y.x, r), add(y.y, r + 1), add(y.z, r + 2), add(y.w, r + 3);
+            }
         }
     }
-    if (ref.page >= 0) a.c.weight[slot_weight(a.c, ref, kh)] = had + sum;
+#pragma unroll
+    for (int x = 0; x < kFinishSlots; ++x)
+        if (ref[x].page >= 0) a.c.weight[slot_weight(a.c, ref[x], kh)] = had[x] + sum[x];
 }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -171,7 +197,7 @@ AttnPlan plan_of(int type, int rows, int dim) {
 // kept for the weights stay within 1 GiB where one sequence's do.
 struct Layout {
     AttnPlan pl;
-    int rows, row_tiles, seqs, score_slots;
+    int rows, row_tiles, seqs, score_slots, score_rows;
     int ctas, ranks;
     size_t part_o, part_ml, head_o, open, span, lse, scores, bytes;
 };
@@ -182,6 +208,8 @@ Layout layout(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int
     y.rows = y.pl.rows;
     y.row_tiles = (R + y.rows - 1) / y.rows;
     y.score_slots = max_len;
+    // whole 16 bytes a slot: 32 query heads over 8 (9 sequences as above) 37.1 us, 39.9 with all 8 rows
+    y.score_rows = y.row_tiles == 1 ? (R + 3) & ~3 : y.rows;
     y.seqs = n_seq < kAttnMaxSeq ? n_seq : kAttnMaxSeq;
     // One block, or a cluster of two, four or eight, per segment, where all
     // run at once: the fewest blocks of at most kEnoughBytes of K and V each,
@@ -203,7 +231,7 @@ Layout layout(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int
     y.ctas = y.ranks ? (int)segments * y.ranks : sms;
     const size_t ctas = y.ctas;
     const size_t tile_f = (size_t)y.rows * y.pl.dp * 4;
-    const size_t seq_scores = (size_t)c.n_heads * y.row_tiles * y.score_slots * y.rows * 4;
+    const size_t seq_scores = (size_t)c.n_heads * y.row_tiles * y.score_slots * y.score_rows * 4;
     if (accumulate && seq_scores * y.seqs > ((size_t)1 << 30)) {
         const size_t fit = ((size_t)1 << 30) / seq_scores;
         y.seqs = fit < 1 ? 1 : (int)fit;
@@ -270,6 +298,7 @@ int run_attn_paged(const AttnArgs &args, void *ws, cudaStream_t st) {
     w.span = reinterpret_cast<int2 *>(base + y.span);
     w.scores = reinterpret_cast<float *>(base + y.scores);
     w.score_slots = y.score_slots;
+    w.score_rows = y.score_rows;
     w.row_tiles = y.row_tiles;
     w.tiles = args.c.n_heads * y.row_tiles;
     w.ranks = y.ranks;
@@ -303,7 +332,7 @@ int run_attn_paged(const AttnArgs &args, void *ws, cudaStream_t st) {
         const int most = kFinishThreads / (y.pl.dp / 4), per = (long long)a.n_seq * w.tiles * 8 < w.ctas ? 1 : most < 8 ? most : 8;
         const int joins = y.ranks ? 0 : w.ctas * (y.rows / per);
         const long long adds = a.accumulate ? (long long)a.n_seq * a.c.n_heads *
-                                                  ((a.max_len + kFinishThreads - 1) / kFinishThreads)
+                                                  ((a.max_len - 1) / (kFinishThreads * kFinishSlots) + 1)
                                             : 0;
         if (rc == kOk && joins + adds > 0)
             rc = launch_pdl("qattn_paged", attn_finish_kernel, dim3((unsigned)(joins + adds)), kFinishThreads,

@@ -70,8 +70,8 @@ struct AttnWork {
     float *head_o;      // [ctas][warps][its rows][DP]: pieces a warp finishes before its range ends
     int2 *open;         // [ctas]: {segment a block leaves open at its end or -1, blocks it spans}
     int2 *span;         // accumulate: [segment]: {its first block, blocks it spans}
-    float *scores;      // accumulate: z in log2 units, [segment][slot][rows]
-    int score_slots;    // slots per segment in scores
+    float *scores;      // accumulate: z in log2 units, [segment][slot][score_rows]
+    int score_slots, score_rows;   // slots per segment; rows, a multiple of four
     int row_tiles;
     int tiles;          // segments per sequence: heads times row tiles
     int ranks;          // blocks (a cluster) that take one whole segment; 0: equal ranges of all steps
@@ -674,14 +674,15 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, THIRD>::threads, 
             }
         }
         if (__builtin_expect(a.accumulate, 0)) {
-            float *dst = w.scores + ((size_t)state.z * w.score_slots + t0) * rows + my_rows + 2 * c;
+            float *dst = w.scores + ((size_t)state.z * w.score_slots + t0) * w.score_rows + my_rows + 2 * c;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
+                if (my_rows + 8 * nt + 2 * c >= w.score_rows) continue;
                 if (g < count)
-                    *reinterpret_cast<float2 *>(dst + g * rows + 8 * nt) =
+                    *reinterpret_cast<float2 *>(dst + g * w.score_rows + 8 * nt) =
                         make_float2(x[nt][0] + m[nt][0], x[nt][1] + m[nt][1]);
                 if (g + 8 < count)
-                    *reinterpret_cast<float2 *>(dst + (g + 8) * rows + 8 * nt) =
+                    *reinterpret_cast<float2 *>(dst + (g + 8) * w.score_rows + 8 * nt) =
                         make_float2(x[nt][2] + m[nt][0], x[nt][3] + m[nt][1]);
             }
         }
