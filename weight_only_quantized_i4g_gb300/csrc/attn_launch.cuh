@@ -39,7 +39,7 @@ template <int TYPE>
 AttnPlan attn_plan(int rows, int dim) {
     return attn_dispatch<TYPE, false>(rows, dim, [](auto cfg) {
         using C = decltype(cfg);
-        return AttnPlan{C::DP, C::rows, C::BB, (size_t)(C::GW > 1 ? 12 : C::W) * C::warp_rows};
+        return AttnPlan{C::DP, C::rows, C::BB, (size_t)(C::GW > 1 ? 16 : C::W) * C::warp_rows};
     });
 }
 
@@ -47,7 +47,7 @@ template <int TYPE, bool THIRD>
 int launch_attn_stream(const AttnArgs &a, const AttnWork &w, const CUtensorMap (&maps)[2], cudaStream_t st) {
     return attn_dispatch<TYPE, THIRD>(a.S * a.group, a.c.dim, [&](auto cfg) {
         using C = decltype(cfg);
-        static_assert(C::GW == 1 || C::W <= 12, "the plan's piece_rows");
+        static_assert(C::W <= 16, "the plan's piece_rows");
         const size_t smem = attn_fixed_smem<C>() + (2 * (size_t)a.n_seq + 1) * sizeof(int);
         auto *kernel = attn_stream_kernel<TYPE, C::DP, C::NT, C::GW, THIRD, true>;
         if constexpr (C::GW == 1)

@@ -81,6 +81,8 @@ struct AttnWork {
     FastDiv tiles_div, row_tiles_div, group_div, page_steps_div;
 };
 
+constexpr int warps_for(int regs) { return regs <= 128 ? 16 : regs <= 168 ? 12 : 8; }
+
 // THIRD: P as three parts (a bf16 cache, f32 output).
 template <int TYPE, int DP_, int NT_, int GW_, bool THIRD_>
 struct AttnCfg {
@@ -99,13 +101,14 @@ struct AttnCfg {
     static constexpr int box = 16 * BB;
     static constexpr int stage = 2 * NB * box;        // 16 slots of K, then of V
     // as many warps as the registers of O, Q and S allow (16, 12 or 8 an SM);
-    // groups that would get 8 keep Q in shared memory, which makes it 12 (48
+    // groups keep Q in shared memory where that makes it more: 12 for 8 (48
     // ragged f16 sequences, 32 rows at 128 dimensions: 254 -> 224 us; e4m3 236 ->
-    // 209) unless that spills as it does with a third part of P (261 -> 273)
+    // 209), 16 for 12 (16 sequences of 8000, 32 rows at 64 dimensions: 94.8 ->
+    // 89.0 us; with four drafted tokens, lengths to 4099, 25.6 -> 23.8).  Not with
+    // a third part of P, which then spills (261 -> 273; 30.4 -> 32.2)
     static constexpr int regs0 = (ESZ == 1 ? 85 : 70) + 4 * MT * NT + 8 * NT, regs_q = NT * NI * (ESZ == 1 ? 8 : 4);
-    static constexpr bool QS = GW > 1 && DP == 128 && !THIRD && regs0 + regs_q > 168;
-    static constexpr int regs = regs0 + (QS ? 0 : regs_q);
-    static constexpr int W0 = regs <= 128 ? 16 : regs <= 168 ? 12 : 8;
+    static constexpr bool QS = GW > 1 && DP <= 128 && NT == 2 && !THIRD && warps_for(regs0) > warps_for(regs0 + regs_q);
+    static constexpr int W0 = warps_for(regs0 + (QS ? 0 : regs_q));
     static constexpr int W = GW == 1 && stage > 8192 ? 4 : W0;
     static constexpr int q_bytes = QS ? NT * NI * (ESZ == 1 ? 2 : 1) * 512 : 0;   // of a warp
     static constexpr int G = W / GW;                  // groups, a ring each
