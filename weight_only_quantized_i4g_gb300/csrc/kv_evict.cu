@@ -44,7 +44,7 @@ __device__ __forceinline__ unsigned ones_of_nibbles(unsigned v) {
 // here; the clusters spread that over the SMs.  A digit whose slots are all
 // kept ends the search (distinct weights: mostly the second).
 template <int kSelThreads>
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictArgs a, int cap) {
+__global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_kernel(const __grid_constant__ EvictArgs a, int cap) {
     constexpr int kSelWarps = kSelThreads / 32;
     extern __shared__ __align__(16) uint32_t s_key[];
     __shared__ int s_hist[kBins], s_total[kBins];
@@ -386,16 +386,22 @@ int launch_select(const EvictArgs &a, int ranks, cudaStream_t st) {
 int run_kv_evict(const EvictArgs &a, cudaStream_t st) {
     // As many blocks per head as have an SM each and 1024 slots or more (two
     // an SM did not all start at once as clusters of eight: three sequences of
-    // 100k slots 143 us against 130).  1024 threads where a block has many
-    // slots (24 sequences of up to 8191, 8 heads: the longest heads took 30 us
-    // with 512); else 512, or 256, four blocks an SM, where there are more
-    // heads than SMs (200 sequences of 1000 slots, 8 heads: 187 us a call with
-    // 512, 168 with 256; one of 1280: 11.7 and 13.0).
+    // 100k slots 143 us against 130).  Their threads, where every head has an SM:
+    // 1024 for many slots, else 512 (8 heads, 30000 slots on eight blocks each:
+    // 14.0 us a call with 1024, 12.5 with 512).  With more heads than SMs several
+    // blocks share one, the more the shorter they are; 8 heads a sequence, with
+    // 1024 / 512 / 256 threads:
+    //   200 sequences of 1000 slots: - / 173 / 156 us, 64 of 2000: - / 59 / 55
+    //   24 of 3000 to 6000: 34.8 / 28.9 / 32.7, 64: 77 / 64 / 61
+    //   40 of 1500 to 8191: 199 / 192 / 229, 24: 119.7 / 121.0 / 138.6
+    //   64 of 16000: 92 / 79 / -, 24 of 30000: 54 / 64 / 92
     const long long heads = (long long)a.n_seq * a.c.n_heads;
+    const bool room = heads <= num_sms();
     int ranks = 1;
     while (ranks < kMaxCluster && heads * ranks * 2 <= num_sms() && ranks * 2048LL <= a.max_len) ranks *= 2;
-    int rc = a.max_len / ranks > 2048 ? launch_select<1024>(a, ranks, st)
-             : heads * ranks <= num_sms() ? launch_select<512>(a, ranks, st) : launch_select<256>(a, ranks, st);
+    const int stretch = a.max_len / ranks;
+    int rc = stretch > (room ? 4096 : 16384) ? launch_select<1024>(a, ranks, st)
+             : room || stretch > 2048        ? launch_select<512>(a, ranks, st) : launch_select<256>(a, ranks, st);
     const int most = a.max_len < a.budget ? a.max_len : a.budget;
     if (rc != kOk || most == 0) return rc;
     const int chunks = a.c.dim * (a.c.type == kE4m3 ? 1 : 2) / 16;
