@@ -187,6 +187,7 @@ int main() {
     layouts<kBf16, true>();
     layouts<kF16, false>();
     layouts<kE4m3, false>();
+    layouts<kE4m3, true>();
     unsigned x = 7u;
     auto rnd = [&](int m) {
         x = x * 1664525u + 1013904223u;

@@ -52,6 +52,36 @@ def test_head_layouts(qg, heads, group, dim):
     check_attention(pc, queries(pc, 4, 1, heads * group, "bf16"), 1, heads * group, dim ** -0.5)
 
 
+@pytest.mark.parametrize("group", [9, 17, 33])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("kv,out", [("bf16", "bf16"), ("f16", "f16"), ("e4m3", "bf16"), ("e4m3", "f32")])
+def test_many_rows_by_output_type(qg, kv, out, dim, group):
+    pc = Paged(qg, [0, 3, 200, 47], 2, dim, kv, seed=group).fill()
+    check_attention(pc, queries(pc, 4, 1, 2 * group, kv), 1, 2 * group, dim ** -0.5, out)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "f16", "e4m3"])
+@pytest.mark.parametrize("group,dim", [(8, 128), (16, 64), (32, 64), (32, 128)])
+def test_long_sums_do_not_shrink(qg, kv, group, dim):
+    """With positive V, sums rounded to nearest are off by a random walk, which
+    the mean over all outputs leaves far below a unit.  What does not average
+    out: a matrix instruction rounds towards zero, up to three a step of 16
+    slots, each by 2^-23 of that step's own sum, and the parts of P leave 2^-22
+    at most: 6e-7, taken as 1e-6.  Sums in the instruction's accumulators were
+    2e-6 too small after 50 steps of a warp; here it has 60 and more."""
+    B, n, heads = 48, 6000, 8
+    pc = Paged(qg, [n], heads, dim, kv, seed=group)
+    for h in range(heads):
+        pc.put("k", 0, h, (20.0 if kv == "e4m3" else 1.0) * pc.randn(n, dim))
+        pc.put("v", 0, h, (64.0 if kv == "e4m3" else 1.0) * (0.5 + torch.rand(n, dim, generator=pc.gen).to(DEV)))
+    pc.table, pc.lens, pc.lens_list = pc.table.repeat(B, 1), ints([n] * B), [n] * B      # all read the same pages
+    q = queries(pc, B, 1, heads * group, kv, 0.5)
+    o, _ = run_attention(pc, q, 1, heads * group, dim ** -0.5)
+    ref = attention(pc, q, 1, heads * group, dim ** -0.5)[0]
+    bias = ((o.double().view_as(ref) - ref) / ref).mean().item()
+    assert abs(bias) <= 1e-6, bias
+
+
 @pytest.mark.parametrize("S", [1, 2, 3, 4, 5, 6, 7, 8])
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 def test_drafted_tokens(qg, S, kv):

@@ -15,6 +15,8 @@ extern template int launch_attn_stream<kF16, false>(const AttnArgs &, const Attn
                                                     cudaStream_t);
 extern template int launch_attn_stream<kE4m3, false>(const AttnArgs &, const AttnWork &, const CUtensorMap (&)[2],
                                                      cudaStream_t);
+extern template int launch_attn_stream<kE4m3, true>(const AttnArgs &, const AttnWork &, const CUtensorMap (&)[2],
+                                                    cudaStream_t);
 extern template AttnPlan attn_plan<kBf16>(int, int);
 extern template AttnPlan attn_plan<kF16>(int, int);
 extern template AttnPlan attn_plan<kE4m3>(int, int);
@@ -324,8 +326,9 @@ int run_attn_paged(const AttnArgs &args, void *ws, cudaStream_t st) {
         else if (a.accumulate) a.lse = reinterpret_cast<float *>(base + y.lse);
         w.ctas = y.ranks ? a.n_seq * w.tiles * y.ranks : y.ctas;
         rc = a.c.type == kF16    ? launch_attn_stream<kF16, false>(a, w, maps, st)
-             : a.c.type == kE4m3 ? launch_attn_stream<kE4m3, false>(a, w, maps, st)
-             : a.o_type == kF32  ? launch_attn_stream<kBf16, true>(a, w, maps, st)
+             : a.c.type == kE4m3 ? (a.o_type == kBf16 ? launch_attn_stream<kE4m3, false>(a, w, maps, st)
+                                                      : launch_attn_stream<kE4m3, true>(a, w, maps, st))
+             : a.o_type != kBf16 ? launch_attn_stream<kBf16, true>(a, w, maps, st)
                                  : launch_attn_stream<kBf16, false>(a, w, maps, st);
         // a segment's pieces: few where there are many segments, and a block then does
         // several rows; else one, its threads sharing the pieces

@@ -83,11 +83,21 @@ struct AttnWork {
 
 constexpr int warps_for(int regs) { return regs <= 128 ? 16 : regs <= 168 ? 12 : 8; }
 
-// THIRD: P as three parts (a bf16 cache, f32 output).
-template <int TYPE, int DP_, int NT_, int GW_, bool THIRD_>
+// FINE: the output is of more bits than a bf16 or e4m3 cache's kernels have
+// otherwise (f32, f16).  With bf16 P then has three parts.
+template <int TYPE, int DP_, int NT_, int GW_, bool FINE>
 struct AttnCfg {
     static constexpr int DP = DP_, NT = NT_, GW = GW_;
-    static constexpr bool THIRD = THIRD_;
+    static constexpr bool THIRD = FINE && TYPE == kBf16;
+    // An MMA rounds its sum towards zero: O shrinks by about 2^-24.4 a step that
+    // is summed in the accumulators (measured: 2.2e-6 after 50 steps, 1e-7
+    // without).  So a step's product is summed alone and then added
+    // to O, which rounds to nearest.  Only where a warp has 16 rows and more and
+    // the output is bf16 the sum stays in the accumulators: 600,000 slots of one
+    // warp would make that half a unit of bf16, and 48 ragged sequences take
+    // 216 us for 232 (32 rows at 128 dimensions; 413 for 445 with 64 rows; with
+    // e4m3 199 for 265).  With 8 rows there is no difference in time.
+    static constexpr bool fresh = FINE || TYPE == kF16 || (NT == 1 && GW == 1);
     static constexpr int ESZ = TYPE == kE4m3 ? 1 : 2;
     static constexpr int warp_rows = 8 * NT, rows = GW * warp_rows;   // of a warp, of a segment
     static constexpr int KE = 16 / ESZ;               // elements of a K chunk
@@ -102,12 +112,12 @@ struct AttnCfg {
     static constexpr int stage = 2 * NB * box;        // 16 slots of K, then of V
     // as many warps as the registers of O, Q and S allow (16, 12 or 8 an SM);
     // groups keep Q in shared memory where that makes it more: 12 for 8 (48
-    // ragged f16 sequences, 32 rows at 128 dimensions: 254 -> 224 us; e4m3 236 ->
-    // 209), 16 for 12 (16 sequences of 8000, 32 rows at 64 dimensions: 94.8 ->
-    // 89.0 us; with four drafted tokens, lengths to 4099, 25.6 -> 23.8).  Not with
-    // a third part of P, which then spills (261 -> 273; 30.4 -> 32.2)
+    // ragged f16 sequences, 32 rows at 128 dimensions: 251 -> 232 us; e4m3 236 ->
+    // 199), 16 for 12 (64 dimensions: 158 -> 143; with four drafted tokens,
+    // lengths to 4099, 26.2 -> 24.6).  Not where FINE needs more registers, which
+    // then spill (e4m3 236 -> 271, bf16 with its third part of P 261 -> 273)
     static constexpr int regs0 = (ESZ == 1 ? 85 : 70) + 4 * MT * NT + 8 * NT, regs_q = NT * NI * (ESZ == 1 ? 8 : 4);
-    static constexpr bool QS = GW > 1 && DP <= 128 && NT == 2 && !THIRD && warps_for(regs0) > warps_for(regs0 + regs_q);
+    static constexpr bool QS = GW > 1 && DP <= 128 && NT == 2 && !FINE && warps_for(regs0) > warps_for(regs0 + regs_q);
     static constexpr int W0 = warps_for(regs0 + (QS ? 0 : regs_q));
     static constexpr int W = GW == 1 && stage > 8192 ? 4 : W0;
     static constexpr int q_bytes = QS ? NT * NI * (ESZ == 1 ? 2 : 1) * 512 : 0;   // of a warp
@@ -351,11 +361,11 @@ __host__ __device__ __forceinline__ int blocks_spanned(int b, int sg, int first,
 
 // DRAFT: several new tokens a sequence, the last of which some rows do not see.
 // (Without the code for those the calls of one token are 2% faster.)
-template <int TYPE, int DP_, int NT_, int GW_, bool THIRD, bool DRAFT>
-__global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, THIRD>::threads, 1)
+template <int TYPE, int DP_, int NT_, int GW_, bool FINE, bool DRAFT>
+__global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, FINE>::threads, 1)
     attn_stream_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnWork w,
                        const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
-    using C = AttnCfg<TYPE, DP_, NT_, GW_, THIRD>;
+    using C = AttnCfg<TYPE, DP_, NT_, GW_, FINE>;
     constexpr int DP = C::DP, NT = C::NT, W = C::W, GW = C::GW, G = C::G, NS = C::NS, NI = C::NI, E = C::E, NQ = C::NQ;
     constexpr int rows = C::rows, warp_rows = C::warp_rows;
     // flags of a step: its page is not in the pool; first and last of its segment
@@ -707,7 +717,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, THIRD>::threads, 
                     const uint32_t r = pack_bf16(u, v);
                     ph[nt][half] = transpose8x8(h);
                     pl[nt][half] = transpose8x8(r);
-                    if constexpr (THIRD) {
+                    if constexpr (C::THIRD) {
                         f = unpack_bf16(r);
                         pt[nt][half] = transpose8x8(pack_bf16(u - f.x, v - f.y));
                     }
@@ -791,9 +801,14 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, THIRD>::threads, 
                         for (int nt = 0; nt < NT; ++nt) {
                             float(&acc)[4] = o[q * (E / 2) + t + y][nt];
                             const uint32_t(&v)[4] = f[y];
-                            if constexpr (THIRD) mma16816<TYPE>(acc, v[0], v[1], v[2], v[3], pt[nt][0], pt[nt][1]);
-                            mma16816<TYPE>(acc, v[0], v[1], v[2], v[3], pl[nt][0], pl[nt][1]);
-                            mma16816<TYPE>(acc, v[0], v[1], v[2], v[3], ph[nt][0], ph[nt][1]);
+                            float part[4] = {0.f, 0.f, 0.f, 0.f};
+                            float(&sum)[4] = C::fresh ? part : acc;
+                            if constexpr (C::THIRD) mma16816<TYPE>(sum, v[0], v[1], v[2], v[3], pt[nt][0], pt[nt][1]);
+                            mma16816<TYPE>(sum, v[0], v[1], v[2], v[3], pl[nt][0], pl[nt][1]);
+                            mma16816<TYPE>(sum, v[0], v[1], v[2], v[3], ph[nt][0], ph[nt][1]);
+                            if (C::fresh)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) acc[e] += part[e];
                         }
                 }
             }
@@ -821,7 +836,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, THIRD>::threads, 
                             for (int nt = 0; nt < NT; ++nt) {
                                 const uint32_t a0 = f[y][0] & m0, a1 = f[y][1] & m0, a2 = f[y][2] & m1, a3 = f[y][3] & m1;
                                 float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                                if constexpr (THIRD) mma16816<TYPE>(acc, a0, a1, a2, a3, pt[nt][0], pt[nt][1]);
+                                if constexpr (C::THIRD) mma16816<TYPE>(acc, a0, a1, a2, a3, pt[nt][0], pt[nt][1]);
                                 mma16816<TYPE>(acc, a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
                                 mma16816<TYPE>(acc, a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
 #pragma unroll

@@ -1,4 +1,4 @@
-// attn_paged_bf16.cu -- the attention kernels over a bf16 cache.
+// attn_paged_bf16.cu -- the attention kernels over a bf16 cache, bf16 output.
 #include "attn_launch.cuh"
 
 namespace qg {

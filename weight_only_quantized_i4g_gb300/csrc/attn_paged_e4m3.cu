@@ -1,4 +1,4 @@
-// attn_paged_e4m3.cu -- the attention kernels over a e4m3 cache.
+// attn_paged_e4m3.cu -- the attention kernels over an e4m3 cache, bf16 output.
 #include "attn_launch.cuh"
 
 namespace qg {

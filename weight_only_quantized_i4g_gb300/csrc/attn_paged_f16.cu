@@ -1,4 +1,4 @@
-// attn_paged_f16.cu -- the attention kernels over a f16 cache.
+// attn_paged_f16.cu -- the attention kernels over an f16 cache.
 #include "attn_launch.cuh"
 
 namespace qg {
