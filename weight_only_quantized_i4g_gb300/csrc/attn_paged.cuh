@@ -42,8 +42,9 @@
 // every ~350 cycles and need 24 MMAs per 8 rows, a twelfth of its rate.
 // Precision: products of 16-bit operands are exact and summed in f32.  P is
 // not rounded to one 16-bit value but split into a sum of two (three for f32
-// output of a bf16 cache), so it keeps 16 to 24 bits; f16 parts are scaled by
-// 2^6 (as are the sums they are divided by) against its subnormals.
+// or f16 output of a bf16 cache), so it keeps 16 to 24 bits; f16 parts are
+// scaled by 2^6 (as are the sums they are divided by) against its subnormals.
+// Where `fresh`, O itself is summed outside the MMAs, which round towards zero.
 // Softmax.  Each row's exponents are taken against a reference that follows
 // the running maximum only when a score passes it by more than 2^8: a step
 // then needs one vote instead of a maximum over lanes, and p stays <= 2^14.

@@ -1,4 +1,4 @@
-// attn_paged_bf16_f32.cu -- the attention kernels over a bf16 cache, f32 output.
+// attn_paged_bf16_f32.cu -- the attention kernels over a bf16 cache, f32 or f16 output.
 #include "attn_launch.cuh"
 
 namespace qg {
