@@ -1,0 +1,77 @@
+"""Eviction where several blocks share a head: windows without a middle to
+choose from."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from attn_util import DEV, Paged, ints  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def qg():
+    import weight_only_quantized_i4g_gb300 as m
+    return m
+
+
+def definition(w, n, budget, sinks, recent):
+    """Kept slots of every head, w f32 [heads, n] on the CPU: protected ends,
+    then a stable sort (NaN above +inf, ties to the lower slot)."""
+    heads = w.shape[0]
+    if n <= budget:
+        return torch.arange(n).repeat(heads, 1)
+    mid = w[:, sinks:n - recent].double()
+    by_value = torch.sort(torch.where(mid.isnan(), math.inf, mid), dim=-1, descending=True, stable=True).indices
+    nan_first = torch.sort(mid.isnan().gather(1, by_value).byte(), dim=-1, descending=True, stable=True).indices
+    best = by_value.gather(1, nan_first)[:, :budget - sinks - recent]
+    ends = torch.cat([torch.arange(sinks), torch.arange(n - recent, n)]).repeat(heads, 1)
+    return torch.cat([ends, best + sinks], -1).sort(-1).values
+
+
+def run(qg, lens, heads, budget, sinks, recent, kv="e4m3", page=16, kind="ties", max_len=None):
+    kept_pages = [-(-min(n, budget) // page) for n in lens]
+    pc = Paged(qg, lens, heads, 16, kv, page=page, weight=True, extra=sum(kept_pages) + 1, fill=0.0, seed=budget)
+    bits = torch.uint8 if kv == "e4m3" else torch.int16
+    for pool in (pc.k, pc.v):
+        raw = pool.view(bits)
+        raw.copy_(torch.randint(0, 100, raw.shape, generator=pc.gen, dtype=torch.int32).to(DEV).to(bits))
+    w = torch.rand(pc.weight.shape, generator=pc.gen)
+    if kind == "ties":
+        w = (w ** 4 * 200).floor() / 8
+    elif kind == "special":
+        w = torch.where(w < 0.01, math.nan, torch.where(w < 0.02, math.inf, w))
+    pc.weight.copy_(w.to(DEV))
+    width = max(max(kept_pages), 1)
+    dst = ints([[pc.free.pop() for _ in range(c)] + [-1] * (width - c) for c in kept_pages])
+    before = [pc.k.clone(), pc.v.clone(), pc.weight.clone()]
+    kept = torch.full((len(lens), heads, budget), 77, dtype=torch.int32, device=DEV)
+    new = torch.full((len(lens),), 77, dtype=torch.int32, device=DEV)
+    qg.check(qg.qg_kv_evict(pc.cache, pc.table, pc.width, dst, width, pc.lens, len(lens),
+                            max(lens) if max_len is None else max_len, budget, sinks, recent, kept, new))
+    torch.cuda.synchronize()
+    assert qg.qg_device_status() == (0, 0)
+    assert new.tolist() == [min(n, budget) for n in lens]
+    for b, n in enumerate(lens):
+        p, i = pc.where(b)
+        want = definition(before[2][p, :, i].T.cpu(), n, budget, sinks, recent).to(DEV)
+        m = want.shape[1]
+        assert torch.equal(kept[b, :, :m].long(), want) and bool((kept[b, :, m:] == -1).all()), b
+        to = torch.arange(m, device=DEV)
+        for pool, old in zip((pc.k, pc.v, pc.weight), before):
+            bit = bits if pool.dim() == 4 else torch.int32
+            for h in range(heads):
+                got = pool.view(bit)[dst[b].long()[to // page], h, to % page]
+                src = old.view(bit)[pc.table[b].long()[want[h] // page], h, want[h] % page]
+                assert torch.equal(got, src), (b, h)
+
+
+@pytest.mark.parametrize("heads,n,budget,sinks", [(1, 5000, 512, 4), (1, 20000, 16384, 0), (4, 2048, 64, 64),
+                                                  (8, 9001, 4096, 1), (30, 6000, 777, 100), (40, 33333, 1, 1)])
+def test_windows_without_a_middle(qg, heads, n, budget, sinks):
+    """sinks + recent == budget on clusters of two, four and eight blocks: no
+    search precedes the blocks' exchange of counts."""
+    for _ in range(3):
+        run(qg, [n, 0, n // 2], heads, budget, sinks, budget - sinks)

@@ -218,6 +218,8 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
                 break;
             }
         }
+    } else if (ranks > 1) {
+        cluster.sync();                            // every block has started: its shared memory may be written (a search has met them)
     }
     // Emit in slot order, four neighbouring slots a lane: every warp counts its
     // stretch (kept for sure, and equal to the threshold), the counts before it
