@@ -1,5 +1,6 @@
-"""Eviction where several blocks share a head: windows without a middle to
-choose from."""
+"""Eviction where several blocks share a head and where a block's work outgrows
+its registers and its shared memory: windows without a middle to choose from,
+more than 1024 slots a warp, more keys than a block holds."""
 import math
 
 import pytest
@@ -75,3 +76,35 @@ def test_windows_without_a_middle(qg, heads, n, budget, sinks):
     search precedes the blocks' exchange of counts."""
     for _ in range(3):
         run(qg, [n, 0, n // 2], heads, budget, sinks, budget - sinks)
+
+
+@pytest.mark.parametrize("kind", ["ties", "distinct", "special"])
+@pytest.mark.parametrize("n,budget,sinks,recent,page", [(50011, 20000, 4, 100, 16), (50011, 3, 1, 1, 7),
+                                                        (70003, 65000, 0, 0, 64), (52000, 52000 - 1, 10, 3, 20)])
+def test_more_slots_than_a_block_holds(qg, kind, n, budget, sinks, recent, page):
+    """More heads than half the SMs: one block a head, over 1024 slots a warp
+    and keys past the 49152 that shared memory holds."""
+    run(qg, [n], 80, budget, sinks, recent, page=page, kind=kind)
+
+
+def test_protected_ends_fill_the_budget_of_long_heads(qg):
+    run(qg, [60001], 80, 50000, 20000, 30000)
+
+
+def test_capacity_far_above_the_lengths(qg):
+    """max_len is a capacity: blocks, threads and shared memory follow it."""
+    for max_len in (1040, 5000 * 16, 200000 * 16):
+        pc_lens = [1040, 300]
+        kept = -(-600 // 16)
+        pc = Paged(qg, pc_lens, 2, 16, "bf16", weight=True, extra=2 * kept + 1, fill=0.0, seed=3,
+                   width=max(65, -(-max_len // 16))).fill()
+        pc.weight.copy_(torch.rand(pc.weight.shape, generator=pc.gen).to(DEV))
+        dst = ints([[pc.free.pop() for _ in range(kept)] for _ in range(2)])
+        out = torch.empty(2, 2, 600, dtype=torch.int32, device=DEV)
+        new = torch.empty(2, dtype=torch.int32, device=DEV)
+        qg.check(qg.qg_kv_evict(pc.cache, pc.table, pc.width, dst, kept, pc.lens, 2, max_len, 600, 4, 40, out, new))
+        torch.cuda.synchronize()
+        assert qg.qg_device_status() == (0, 0) and new.tolist() == [600, 300]
+        p, i = pc.where(0)
+        assert torch.equal(out[0].long().cpu(), definition(pc.weight[p, :, i].T.cpu(), 1040, 600, 4, 40))
+        assert out[1, :, :300].tolist() == [list(range(300))] * 2 and bool((out[1, :, 300:] == -1).all())
