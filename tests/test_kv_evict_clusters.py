@@ -108,3 +108,17 @@ def test_capacity_far_above_the_lengths(qg):
         p, i = pc.where(0)
         assert torch.equal(out[0].long().cpu(), definition(pc.weight[p, :, i].T.cpu(), 1040, 600, 4, 40))
         assert out[1, :, :300].tolist() == [list(range(300))] * 2 and bool((out[1, :, 300:] == -1).all())
+
+
+@pytest.mark.parametrize("budget", [2 ** 31 - 1, 2 ** 31 - 4000])
+def test_budgets_up_to_the_largest_integer(qg, budget):
+    """A budget that bounds nothing: all slots are kept, the rest of `kept` is -1."""
+    pc = Paged(qg, [100], 1, 16, "bf16", weight=True, extra=8, fill=0.0, seed=5).fill()
+    dst = ints([[pc.free.pop() for _ in range(7)]])
+    kept = torch.full((budget + 8192,), 77, dtype=torch.int32, device=DEV)
+    new = torch.empty(1, dtype=torch.int32, device=DEV)
+    qg.check(qg.qg_kv_evict(pc.cache, pc.table, pc.width, dst, 7, pc.lens, 1, 100, budget, 4, 2000, kept, new))
+    torch.cuda.synchronize()
+    assert qg.qg_device_status() == (0, 0) and new.tolist() == [100]
+    assert kept[:100].tolist() == list(range(100)) and bool((kept[100:budget] == -1).all())
+    assert bool((kept[budget:] == 77).all())

@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_
     int *kept = a.kept + (size_t)bh * a.budget;
     const int first = rank * kSelThreads + tid, step = ranks * kSelThreads;
     if (h == 0 && first == 0) a.new_lens[b] = N;
-    for (int i = N + first; i < a.budget; i += step) kept[i] = -1;
+    for (unsigned i = N + first; i < (unsigned)a.budget; i += step) kept[i] = -1;   // unsigned: the budget may be up to 2^31 - 1
     if (L <= a.budget) {                           // the same for every block of the cluster
         for (int i = first; i < N; i += step) kept[i] = i;
         return;
