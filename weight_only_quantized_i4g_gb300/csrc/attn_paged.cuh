@@ -42,12 +42,17 @@
 // every ~350 cycles and need 24 MMAs per 8 rows, a twelfth of its rate.
 // Precision: products of 16-bit operands are exact and summed in f32.  P is
 // not rounded to one 16-bit value but split into a sum of two (three for f32
-// or f16 output of a bf16 cache), so it keeps 16 to 24 bits; f16 parts are
-// scaled by 2^6 (as are the sums they are divided by) against its subnormals.
+// or f16 output of a bf16 cache), so it keeps 16 to 24 bits.  bf16 parts have
+// f32's range.  f16 parts do not: P (and l) are scaled by 2^11 and the second
+// part by 2^12 more, which its product's sum or V takes back, so that weights
+// keep 16 bits down to 2^-32 of the row's largest and add nothing to O below
+// 2^-48.  (With both parts scaled by 2^6 alone O was 1e-4 off where a slot with a
+// zero v outweighs the others by 2^26, and most of it was lost at 2^32.)
 // Where `fresh`, O itself is summed outside the MMAs, which round towards zero.
 // Softmax.  Each row's exponents are taken against a reference that follows
-// the running maximum only when a score passes it by more than 2^8: a step
-// then needs one vote instead of a maximum over lanes, and p stays <= 2^14.
+// the running maximum only when a score passes it by more than 2^8 (f16 parts:
+// 2^4, so p stays <= 2^15): a step then needs one vote instead of a maximum
+// over lanes.
 // e4m3 codes are exact in f16; q over them is scaled per row by a power of two
 // into f16's range, which is exact for bf16 values within 2^29 of the largest.
 #pragma once
@@ -99,6 +104,12 @@ struct AttnCfg {
     // 216 us for 232 (32 rows at 128 dimensions; 413 for 445 with 64 rows; with
     // e4m3 199 for 265).  With 8 rows there is no difference in time.
     static constexpr bool fresh = FINE || TYPE == kF16 || (NT == 1 && GW == 1);
+    // where the second f16 part of P gets its scale of 2^12 back: in its
+    // product's sum, or in V (exact for e4m3 codes), which several row tiles
+    // share (64 e4m3 sequences of 6000 to 16384, 7 rows: 234 us with the sum, 241
+    // with V, 232 with an unscaled part)
+    static constexpr bool LOW_SUM = TYPE == kF16 || (TYPE == kE4m3 && fresh && NT == 1), LOW_V = TYPE == kE4m3 && !LOW_SUM;
+    static_assert(fresh || !LOW_SUM, "the second part's product is scaled by itself");
     static constexpr int ESZ = TYPE == kE4m3 ? 1 : 2;
     static constexpr int warp_rows = 8 * NT, rows = GW * warp_rows;   // of a warp, of a segment
     static constexpr int KE = 16 / ESZ;               // elements of a K chunk
@@ -215,6 +226,12 @@ __device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint3
             "{%10,%10,%10,%10};"
             : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// An f16 pair by 2^-12.
+__device__ __forceinline__ uint32_t f16x2_down12(uint32_t v) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x0C000C00u));
+    return r;
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
@@ -492,7 +509,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, FINE>::threads, 1
     const uint32_t q_mem = smem_addr(smem) + G * C::ring + W * C::slab + warp * C::q_bytes + lane * 16;
     float rs[NT][2];                                  // score factor of the thread's rows (e4m3: per row)
     const float factor = a.scale * 1.44269504088896340736f;
-    constexpr float shift = TYPE == kBf16 ? 0.f : 6.f;
+    constexpr float shift = TYPE == kBf16 ? 0.f : 11.f, lag = TYPE == kBf16 ? 8.f : 4.f;
     bool fresh = true;                                // at the start of a piece
     bool began_here = false;
     int stage = 0;
@@ -660,7 +677,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, FINE>::threads, 1
                 s[nt][e] += s1[nt][e];
                 x[nt][e] = fmaf(s[nt][e], TYPE == kE4m3 ? rs[nt][e & 1] : factor, -m[nt][e & 1]);
                 if (__builtin_expect(partial, 0)) x[nt][e] = masked(x[nt][e], nt, e);
-                over |= x[nt][e] > shift + 8.f;
+                over |= x[nt][e] > shift + lag;
             }
         if (__builtin_expect(__any_sync(~0u, over), 0)) {
             // raise the references to the maxima; l and O follow
@@ -726,7 +743,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, FINE>::threads, 1
                     const uint32_t h = pack_f16(u, v);
                     const float2 f = unpack_f16(h);
                     ph[nt][half] = transpose8x8(h);
-                    pl[nt][half] = transpose8x8(pack_f16(u - f.x, v - f.y));
+                    pl[nt][half] = transpose8x8(pack_f16((u - f.x) * 4096.f, (v - f.y) * 4096.f));
                 }
             }
         }
@@ -757,6 +774,13 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, FINE>::threads, 1
         auto v_pairs = [&](uint32_t lo, uint32_t hi, int e, uint32_t *x0, uint32_t *x1) {
             if constexpr (TYPE != kE4m3) *x0 = __byte_perm(lo, hi, 0x5410), *x1 = __byte_perm(lo, hi, 0x7632);
             else e4m3x4_to_f16x2(__byte_perm(lo, hi, e & 2 ? 0x7362 : 0x5140), x0, x1);
+        };
+        // sum += V^T by the second part of P^T; LOW_SUM: the sum holds nothing else yet
+        auto add_low = [&](float (&sum)[4], const uint32_t (&v)[4], int nt) {
+            mma16816<TYPE>(sum, v[0], v[1], v[2], v[3], pl[nt][0], pl[nt][1]);
+            if constexpr (C::LOW_SUM)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[e] *= 1.f / 4096.f;
         };
         constexpr int per_word = 4 / C::ESZ;
         bool careful = false;
@@ -796,6 +820,11 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, FINE>::threads, 1
                     v_pairs(x[0][e1 / per_word], x[1][e1 / per_word], e1, &f[0][1], &f[1][1]);
                     v_pairs(x[2][e0 / per_word], x[3][e0 / per_word], e0, &f[0][2], &f[1][2]);
                     v_pairs(x[2][e1 / per_word], x[3][e1 / per_word], e1, &f[0][3], &f[1][3]);
+                    uint32_t low[2][4];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) low[y][z] = C::LOW_V ? f16x2_down12(f[y][z]) : f[y][z];
 #pragma unroll
                     for (int y = 0; y < 2; ++y)
 #pragma unroll
@@ -805,7 +834,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, FINE>::threads, 1
                             float part[4] = {0.f, 0.f, 0.f, 0.f};
                             float(&sum)[4] = C::fresh ? part : acc;
                             if constexpr (C::THIRD) mma16816<TYPE>(sum, v[0], v[1], v[2], v[3], pt[nt][0], pt[nt][1]);
-                            mma16816<TYPE>(sum, v[0], v[1], v[2], v[3], pl[nt][0], pl[nt][1]);
+                            add_low(sum, low[y], nt);
                             mma16816<TYPE>(sum, v[0], v[1], v[2], v[3], ph[nt][0], ph[nt][1]);
                             if (C::fresh)
 #pragma unroll
@@ -838,7 +867,11 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, FINE>::threads, 1
                                 const uint32_t a0 = f[y][0] & m0, a1 = f[y][1] & m0, a2 = f[y][2] & m1, a3 = f[y][3] & m1;
                                 float acc[4] = {0.f, 0.f, 0.f, 0.f};
                                 if constexpr (C::THIRD) mma16816<TYPE>(acc, a0, a1, a2, a3, pt[nt][0], pt[nt][1]);
-                                mma16816<TYPE>(acc, a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+                                uint32_t low[4] = {a0, a1, a2, a3};
+#pragma unroll
+                                for (int z = 0; z < 4; ++z)
+                                    if (C::LOW_V) low[z] = f16x2_down12(low[z]);
+                                add_low(acc, low, nt);
                                 mma16816<TYPE>(acc, a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
