@@ -147,9 +147,9 @@ __global__ void __launch_bounds__(kFinishThreads)
             }
         }
         __syncthreads();
+        float lse = -INFINITY;                        // of row tid, in log2 units
         if (tid < rows) {
             const RowRef r = row_ref(a, w, b, kh, tile * rows + tid);
-            float lse = -INFINITY;                    // in log2 units
             if (r.real) {
                 if (span.y == 1) {
                     lse = a.lse[r.head] * 1.44269504088896340736f;
@@ -167,13 +167,21 @@ __global__ void __launch_bounds__(kFinishThreads)
             }
             s_lse[tid] = lse;
         }
-        __syncthreads();
+        const bool odd = __syncthreads_or(lse != lse);
 #pragma unroll
         for (int x = 0; x < kFinishSlots; ++x) {
             if (ref[x].page < 0) continue;
             auto add = [&](float y, int r) {
                 if (s_lse[r] != -INFINITY) sum[x] += ex2(y - s_lse[r]);
             };
+            if (__builtin_expect(odd, 0)) {
+                // a row is NaN, and so would be its share of a slot that it does not see
+                const int t = t0 + x * kFinishThreads;
+#pragma unroll 1
+                for (int r = 0; r < rows && tile * rows + r < R; ++r)
+                    if (t < len - a.S + 1 + quotient(tile * rows + r, w.group_div)) add(z[x * next + r], r);
+                continue;
+            }
             add(z0[x].x, 0), add(z0[x].y, 1), add(z0[x].z, 2), add(z0[x].w, 3);
             if (w.score_rows > 4) add(z1[x].x, 4), add(z1[x].y, 5), add(z1[x].z, 6), add(z1[x].w, 7);
 #pragma unroll 2
