@@ -85,15 +85,14 @@ int check_max_len(const char *fn, int max_len, int stride, int page) {
     return kOk;
 }
 
-// Rows of all sequences, and steps (up to 16 slots of a page) of all sequences
-// and heads, must be counted in 31 bits.
+// Rows of all sequences, and cost units of one sequence, must be counted in 31
+// bits (a launch takes as many sequences as have their units counted so).
 int check_attn_sizes(const char *fn, const KvView &c, int n_seq, int max_len, int S, int n_q_heads) {
     if (S < 1 || S > 8) QG_REFUSE(kEInval, "%s: S = %d new tokens, must be in 1..8", fn, S);
     if (n_seq < 0) QG_REFUSE(kEInval, "%s: n_seq = %d, must be >= 0", fn, n_seq);
     const int rc = check_heads(fn, n_q_heads, c.n_heads);
     if (rc) return rc;
-    const double steps = ((double)max_len / c.page + 1) * ((c.page + 15) / 16) + 2;   // and a segment's own cost
-    if ((double)n_seq * S * n_q_heads > (double)INT_MAX / 2 || (double)n_seq * n_q_heads * S * steps > (double)INT_MAX / 2)
+    if ((double)n_seq * S * n_q_heads > (double)INT_MAX / 2 || attn_units(c, max_len, S, n_q_heads) > kAttnMaxUnits)
         QG_REFUSE(kEInval, "%s: sizes overflow", fn);
     return kOk;
 }

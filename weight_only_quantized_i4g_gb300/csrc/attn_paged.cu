@@ -203,8 +203,9 @@ AttnPlan plan_of(int type, int rows, int dim) {
            : type == kF16 ? attn_plan<kF16>(rows, dim) : attn_plan<kE4m3>(rows, dim);
 }
 
-// Sequences per launch: their lengths sit in shared memory, and the scores
-// kept for the weights stay within 1 GiB where one sequence's do.
+// Sequences per launch: their lengths sit in shared memory, their cost units
+// are counted in 31 bits, and the scores kept for the weights stay within 1 GiB
+// where one sequence's do.
 struct Layout {
     AttnPlan pl;
     int rows, row_tiles, seqs, score_slots, score_rows;
@@ -220,7 +221,8 @@ Layout layout(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int
     y.score_slots = max_len;
     // whole 16 bytes a slot: 32 query heads over 8 (9 sequences as above) 37.1 us, 39.9 with all 8 rows
     y.score_rows = y.row_tiles == 1 ? (R + 3) & ~3 : y.rows;
-    y.seqs = n_seq < kAttnMaxSeq ? n_seq : kAttnMaxSeq;
+    const int count = (int)fmin(kAttnMaxSeq, kAttnMaxUnits / attn_units(c, max_len, S, n_q_heads));
+    y.seqs = n_seq < count ? n_seq : count;
     // One block, or a cluster of two, four or eight, per segment, where all
     // run at once: the fewest blocks of at most kEnoughBytes of K and V each,
     // else the most of at most kWholeBytes (an SM streams that in less than the
@@ -292,6 +294,12 @@ int cache_map(CUtensorMap *map, const KvView &c, const char *base, int box_bytes
 }
 
 }  // namespace
+
+double attn_units(const KvView &c, int max_len, int S, int n_q_heads) {
+    const int R = S * (n_q_heads / c.n_heads), rows = plan_of(c.type, R, c.dim).rows, full = max_len / c.page;
+    const double steps = (double)full * (c.page / 16 + (c.page % 16 != 0)) + (max_len - full * c.page + 15) / 16;
+    return (double)c.n_heads * ((R + rows - 1) / rows) * (steps + kSegmentCost);
+}
 
 size_t ws_attn_paged(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int accumulate) {
     return layout(c, n_seq, max_len, S, n_q_heads, accumulate).bytes;
