@@ -550,7 +550,8 @@ int qg_rope_append(const qg_kv_cache *cache, const int *table, int table_stride,
  *          of a page that sequences share must not be accumulated to by two
  *          of them in one call)
  *   ws     qattn_workspace_bytes() bytes, 256-byte aligned; contents on entry
- *          do not matter
+ *          do not matter.  The bytes for the largest n_seq, max_len and S serve
+ *          all smaller ones too, with accumulate those without
  * A masked slot never touches its row, whatever it holds (NaN, infinity).
  * A visible slot whose page is not in the pool makes its rows NaN and raises
  * QG_EPAGE; a length outside [0, max_len] is held to it and raises QG_EPAGE.

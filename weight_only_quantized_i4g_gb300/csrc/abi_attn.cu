@@ -163,7 +163,7 @@ size_t qattn_workspace_bytes(const qg_kv_cache *cache, int n_seq, int max_len, i
     if (check_cache(fn, cache, &c) || max_len < 0 || check_attn_sizes(fn, c, n_seq, max_len, S, n_q_heads) ||
         n_seq == 0)
         return 0;
-    return ws_attn_paged(c, n_seq, max_len, S, n_q_heads, accumulate != 0);
+    return ws_attn_paged_most(c, n_seq, max_len, S, n_q_heads, accumulate != 0);
 }
 
 int qattn_paged(const qg_kv_cache *cache, const int *table, int table_stride, const int *lens, int n_seq,

@@ -24,6 +24,7 @@ extern template AttnPlan attn_plan<kE4m3>(int, int);
 namespace {
 
 constexpr long long kEnoughBytes = 128 << 10, kWholeBytes = 384 << 10;
+constexpr size_t kScoreBytes = (size_t)1 << 30;
 // Slots a thread adds weights for: its chain of dependent reads, not bytes,
 // bounds the second kernel (9 sequences of 500 to 8192 slots, 8 heads, 40 query
 // heads: 42.4 us a call with one, 39.8 with two, 41.0 with four; 40 sequences
@@ -244,8 +245,8 @@ Layout layout(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int
     const size_t ctas = y.ctas;
     const size_t tile_f = (size_t)y.rows * y.pl.dp * 4;
     const size_t seq_scores = (size_t)c.n_heads * y.row_tiles * y.score_slots * y.score_rows * 4;
-    if (accumulate && seq_scores * y.seqs > ((size_t)1 << 30)) {
-        const size_t fit = ((size_t)1 << 30) / seq_scores;
+    if (accumulate && seq_scores * y.seqs > kScoreBytes) {
+        const size_t fit = kScoreBytes / seq_scores;
         y.seqs = fit < 1 ? 1 : (int)fit;
     }
     size_t at = 0;
@@ -303,6 +304,27 @@ double attn_units(const KvView &c, int max_len, int S, int n_q_heads) {
 
 size_t ws_attn_paged(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int accumulate) {
     return layout(c, n_seq, max_len, S, n_q_heads, accumulate).bytes;
+}
+
+// Fewer sequences or a smaller max_len may take a plan that needs more: every
+// part at its most over all of them, and over fewer new tokens.  No plan has
+// more blocks than SMs.
+size_t ws_attn_paged_most(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int accumulate) {
+    const size_t ctas = num_sms(), seqs = n_seq < kAttnMaxSeq ? n_seq : kAttnMaxSeq;
+    size_t most = 0;
+    for (int s = 1; s <= S; ++s) {
+        const Layout y = layout(c, n_seq, max_len, s, n_q_heads, accumulate);
+        const size_t row = (size_t)y.pl.dp * 4, segments = (size_t)c.n_heads * y.row_tiles;
+        size_t n = up256(2 * ctas * y.rows * row) + up256(2 * ctas * y.rows * sizeof(float2)) +
+                   up256(ctas * y.pl.piece_rows * row) + up256(ctas * sizeof(int2));
+        if (accumulate) {
+            const size_t one = segments * y.score_slots * y.score_rows * 4;
+            const size_t all = one > kScoreBytes ? one : one * seqs < kScoreBytes ? one * seqs : kScoreBytes;
+            n += up256(seqs * segments * sizeof(int2)) + up256(seqs * s * n_q_heads * 4) + up256(all);
+        }
+        if (n > most) most = n;
+    }
+    return most;
 }
 
 int run_attn_paged(const AttnArgs &args, void *ws, cudaStream_t st) {

@@ -208,7 +208,9 @@ int run_rope_append(const RopeArgs &a, int qkv_type, cudaStream_t st);
 // Cost units (steps and segments' own) of a sequence of max_len slots; a launch counts up to kAttnMaxUnits.
 constexpr double kAttnMaxUnits = 1 << 30;
 double attn_units(const KvView &c, int max_len, int S, int n_q_heads);
+// Workspace of one call, and of every call of at most these sizes.
 size_t ws_attn_paged(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int accumulate);
+size_t ws_attn_paged_most(const KvView &c, int n_seq, int max_len, int S, int n_q_heads, int accumulate);
 int run_attn_paged(const AttnArgs &a, void *ws, cudaStream_t st);
 int run_kv_evict(const EvictArgs &a, cudaStream_t st);
 
