@@ -44,3 +44,30 @@ def test_batches_split_by_their_capacity(qg, kv):  # noqa: F811
     wide[:, :pc.width] = pc.table
     pc.table, pc.width = wide, 1 << 24
     check_attention(pc, queries(pc, 4, 2, 16, kv), 2, 16, 0.125, max_len=1 << 30)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [(1 << 31) - 1, (1 << 31) - 14])
+def test_one_page_of_the_largest_size(qg, page):  # noqa: F811
+    """A cache without pages to speak of: k and v share one pool of 2^31 slots."""
+    torch = pytest.importorskip("torch")
+    if torch.cuda.mem_get_info()[0] < 45 << 30:
+        pytest.skip("needs 45 GB")
+    dim, n = 8, 1000
+    pool = torch.empty(1, 1, page, dim, dtype=torch.bfloat16, device="cuda")
+    pool[:, :, :n + 16] = torch.randn(n + 16, dim, device="cuda").bfloat16()
+    c = qg.kv_cache(pool, pool)
+    q = torch.randn(1, 2 * dim, device="cuda").bfloat16()
+    o = torch.empty(1, 2, dim, device="cuda")
+    table, lens = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([[0]], [n]))
+    for max_len in (n, 1 << 30):
+        size = qg.qattn_workspace_bytes(c, 1, max_len, 1, 2)
+        ws = torch.empty(max(size, 1), dtype=torch.uint8, device="cuda")
+        o.fill_(float("nan"))
+        qg.check(qg.qattn_paged(c, table, 1, lens, 1, max_len, o, qg.QG_F32, None, q, qg.QG_BF16, 2 * dim, 1, 2, 0.3,
+                                0, ws, size))
+        torch.cuda.synchronize()
+        assert qg.qg_device_status() == (0, 0)
+        x = pool[0, 0, :n].double()
+        want = torch.softmax(q.view(2, dim).double() @ x.T * 0.3, -1) @ x
+        assert float((o[0].double() - want).abs().max()) < 1e-4

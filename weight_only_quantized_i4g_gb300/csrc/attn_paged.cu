@@ -197,6 +197,8 @@ __global__ void __launch_bounds__(kFinishThreads)
         if (ref[x].page >= 0) a.c.weight[slot_weight(a.c, ref[x], kh)] = had[x] + sum[x];
 }
 
+int page_steps(int page) { return page / 16 + (page % 16 != 0); }   // page + 15 may pass 2^31 - 1
+
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 AttnPlan plan_of(int type, int rows, int dim) {
@@ -298,7 +300,7 @@ int cache_map(CUtensorMap *map, const KvView &c, const char *base, int box_bytes
 
 double attn_units(const KvView &c, int max_len, int S, int n_q_heads) {
     const int R = S * (n_q_heads / c.n_heads), rows = plan_of(c.type, R, c.dim).rows, full = max_len / c.page;
-    const double steps = (double)full * (c.page / 16 + (c.page % 16 != 0)) + (max_len - full * c.page + 15) / 16;
+    const double steps = (double)full * page_steps(c.page) + (max_len - full * c.page + 15) / 16;
     return (double)c.n_heads * ((R + rows - 1) / rows) * (steps + kSegmentCost);
 }
 
@@ -345,7 +347,7 @@ int run_attn_paged(const AttnArgs &args, void *ws, cudaStream_t st) {
     w.tiles_div = fast_div(w.tiles);
     w.row_tiles_div = fast_div(w.row_tiles);
     w.group_div = fast_div(args.group);
-    w.page_steps = (args.c.page + 15) / 16;
+    w.page_steps = page_steps(args.c.page);
     w.page_steps_div = fast_div(w.page_steps);
     w.box_rows = args.c.page < 16 ? args.c.page : 16;
     CUtensorMap maps[2];
