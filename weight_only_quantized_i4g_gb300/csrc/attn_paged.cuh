@@ -562,9 +562,10 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, FINE>::threads, 1
                     }
                     top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-                    // largest |q| of the row into [2^14, 2^15)
+                    // largest |q| of the row into [2^14, 2^15): by 2^-113 for the largest
+                    // numbers, by 2^126 at most (2^-126 is the last normal inverse)
                     int ex = 141 - (int)(__float_as_uint(top) >> 23);
-                    ex = top == 0.f ? 0 : ex > 100 ? 100 : ex < -100 ? -100 : ex;
+                    ex = top == 0.f ? 0 : ex > 126 ? 126 : ex;
                     const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
 #pragma unroll
                     for (int i = 0; i < NI; ++i)
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, FINE>::threads, 1
                             const float2 f = a.q_type == kF16 ? unpack_f16(qn[i][u]) : unpack_bf16(qn[i][u]);
                             qn[i][u] = pack_f16(f.x * up, f.y * up);
                         }
-                    const float down = factor * a.c.k_scale[kh] * __uint_as_float((uint32_t)(127 - ex) << 23);
+                    const float down = factor * __uint_as_float((uint32_t)(127 - ex) << 23) * a.c.k_scale[kh];
                     rs[nt][0] = __shfl_sync(~0u, down, 8 * c);
                     rs[nt][1] = __shfl_sync(~0u, down, 8 * c + 4);
                 }
