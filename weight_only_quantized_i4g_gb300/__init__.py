@@ -322,18 +322,20 @@ def kv_cache(k, v, k_scale=None, v_scale=None, weight=None, order="head"):
     types = {"bfloat16": QG_BF16, "float16": QG_F16, "float8_e4m3fn": QG_E4M3}
     if name not in types:
         raise ValueError(f"a cache of {name} is not supported")
-    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride() or k.stride(3) != 1:
+    # the stride of an axis of one element says nothing
+    strides = [[x if n > 1 or i == 3 else t.shape[-1] for i, (x, n) in enumerate(zip(t.stride(), t.shape))] for t in (k, v)]
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or strides[0] != strides[1] or strides[0][3] != 1:
         raise ValueError("k and v are [n_pages, ., ., head_dim] of one shape, type and strides, the last stride 1")
     pages, a, b, dim = k.shape
     heads, page = (a, b) if order == "head" else (b, a)
-    hs, ts = (k.stride(1), k.stride(2)) if order == "head" else (k.stride(2), k.stride(1))
+    ps, hs, ts = strides[0][:3] if order == "head" else (strides[0][0], strides[0][2], strides[0][1])
     if weight is not None and (tuple(weight.shape) != (pages, heads, page) or not weight.is_contiguous()
                                or not str(weight.dtype).endswith("float32")):
         raise ValueError("weight is contiguous float32 [n_pages, n_heads, page_size]")
     for s in (k_scale, v_scale):
         if s is not None and (s.numel() != heads or not s.is_contiguous() or not str(s.dtype).endswith("float32")):
             raise ValueError("k_scale and v_scale are contiguous float32 [n_heads]")
-    c = KVCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(weight), k.stride(0), hs, ts, types[name],
+    c = KVCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(weight), ps, hs, ts, types[name],
                 pages, page, heads, dim)
     c.tensors = (k, v, k_scale, v_scale, weight)
     return c
