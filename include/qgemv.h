@@ -522,7 +522,8 @@ typedef struct {
  *          not written.
  * Angles are formed and reduced in 64 bits, the rotation in 32; one rounding
  * (nearest even) to the type stored.  QG_E4M3 stores x / scale, held to the
- * largest finite code; NaN stays NaN.  T = 0 launches nothing.  Alignment:
+ * largest finite code; NaN stays NaN.  T = 0 launches nothing (an empty batch:
+ * n_seq may be 0 too).  Alignment:
  * elements; qkv rows and q on four-element boundaries and rotary_dim % 8 == 0
  * take the fastest path. */
 enum { QG_ROPE_HALF = 0, QG_ROPE_INTERLEAVED = 1 };

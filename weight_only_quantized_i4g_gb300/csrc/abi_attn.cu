@@ -125,7 +125,7 @@ int qg_rope_append(const qg_kv_cache *cache, const int *table, int table_stride,
         for (int j = 0; j < rotary_dim / 2; ++j)
             if (axis[j] >= n_axes)
                 QG_REFUSE(kEInval, "%s: axis[%d] = %d, must be below n_axes = %d", fn, j, (int)axis[j], n_axes);
-    if (n_seq < 1) QG_REFUSE(kEInval, "%s: n_seq = %d, must be >= 1", fn, n_seq);
+    if (n_seq < 0 || (n_seq == 0 && T > 0)) QG_REFUSE(kEInval, "%s: n_seq = %d, must be >= 1 (0 without tokens)", fn, n_seq);
     if (T == 0) return kOk;
     if ((rc = check_table(fn, "table", table, table_stride))) return rc;
     if (!seq || !slot || !q || !qkv) QG_REFUSE(kEInval, "%s: seq, slot, q and qkv must be non-NULL", fn);
