@@ -100,7 +100,10 @@ __global__ void __launch_bounds__(kFinishThreads)
         }
         if (!ref.real || set >= sets) return;
         const float vs = a.c.type == kE4m3 ? a.c.v_scale[kh] : 1.f;
-        if (d < a.c.dim) store_out4(a, ref.head * a.c.dim + d, sum, row_factor(l, vs));
+        if (d < a.c.dim) {
+            if (a.c.type != kE4m3) sum = with_infinities(a, ref, b, kh, d, sum, l);
+            store_out4(a, ref.head * a.c.dim + d, sum, row_factor(l, vs));
+        }
         if (d == 0 && a.lse) a.lse[ref.head] = row_lse(m, l);
         return;
     }

@@ -269,6 +269,34 @@ __device__ __forceinline__ RowRef row_ref(const AttnArgs &a, const AttnWork &w, 
     return x;
 }
 
+// Elements d .. d + 3 of the sum of a row with weight l, over a cache of 16 bits.
+// An infinity in V times a part of P that is zero or negative is NaN where its
+// product with P is infinite.  So where elements are NaN and the weights are not,
+// the infinities that the row sees stand for them: the sign that they agree on.
+__device__ __forceinline__ float4 with_infinities(const AttnArgs &a, const RowRef &row, int b, int kh, int d, float4 sum,
+                                                  float l) {
+    int open = (sum.x != sum.x) | (sum.y != sum.y) << 1 | (sum.z != sum.z) << 2 | (sum.w != sum.w) << 3;
+    if (__builtin_expect(open == 0 || !(l > 0.f), 1)) return sum;
+    const int end = seq_len(a.lens, b, a.max_len, nullptr) - a.S + 1 + row.s, ex = a.c.type == kBf16 ? 0x7F80 : 0x7C00;
+    int up = 0, down = 0;                             // a bit an element: +inf, -inf seen (a NaN: both)
+#pragma unroll 1
+    for (int t = 0; t < end && (open & ~(up & down)); ++t) {
+        const SlotRef r = find_slot(a.c, a.table + (size_t)b * a.table_stride, t);
+        if (r.page < 0) continue;
+        const uint2 w = *reinterpret_cast<const uint2 *>(a.c.v + slot_bytes(a.c, r, kh) + 2 * d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int v = (e < 2 ? w.x : w.y) >> (16 * (e & 1)) & 0xFFFF;
+            if ((v & 0x7FFF) < ex) continue;
+            if (v != (ex | 0x8000)) up |= 1 << e;
+            if (v != ex) down |= 1 << e;
+        }
+    }
+    open &= up ^ down;                                // the infinities agree
+    auto pick = [&](float x, int e) { return open >> e & 1 ? up >> e & 1 ? INFINITY : -INFINITY : x; };
+    return make_float4(pick(sum.x, 0), pick(sum.y, 1), pick(sum.z, 2), pick(sum.w, 3));
+}
+
 // Steps of a sequence of len slots: 16 slots of a page each, fewer at the ends
 // of pages and of the sequence.
 __host__ __device__ __forceinline__ int seq_steps(const KvView &c, const AttnWork &w, int len) {
@@ -930,7 +958,11 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, FINE>::threads, 1
                         const RowRef ref = row_ref(a, w, b, kh, tile * rows + my_rows + 8 * nt + r);
                         const float2 ml = s_ml[row0 + 8 * nt + r];
                         if (!ref.real) continue;
-                        if (d < D) store_out4(a, ref.head * D + d, slab[slab_place<C>(r, d / 4)], row_factor(ml.y, vs));
+                        if (d < D) {
+                            float4 v = slab[slab_place<C>(r, d / 4)];
+                            if constexpr (TYPE != kE4m3) v = with_infinities(a, ref, b, kh, d, v, ml.y);
+                            store_out4(a, ref.head * D + d, v, row_factor(ml.y, vs));
+                        }
                         if (d == 0 && a.lse) a.lse[ref.head] = row_lse(ml.x, ml.y);
                     }
                 } else if (!last) {
@@ -992,6 +1024,8 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, FINE>::threads, 1
                 sum.x += v.x * f, sum.y += v.y * f, sum.z += v.z * f, sum.w += v.w * f;
             }
             if (whole) {
+                if constexpr (TYPE != kE4m3)
+                    if (d < D) sum = with_infinities(a, ref, b, kh, d, sum, ll);
                 if (d < D) store_out4(a, ref.head * D + d, sum, row_factor(ll, vs));
                 if (d == 0 && a.lse) a.lse[ref.head] = row_lse(mm, ll);
             } else {
@@ -1042,6 +1076,8 @@ __global__ void __launch_bounds__(AttnCfg<TYPE, DP_, NT_, GW_, FINE>::threads, 1
                 ll += ml[x].y * f;
                 sum.x += v[x].x * f, sum.y += v[x].y * f, sum.z += v[x].z * f, sum.w += v[x].w * f;
             }
+            if constexpr (TYPE != kE4m3)
+                if (d < D) sum = with_infinities(a, ref, b, kh, d, sum, ll);
             if (d < D) store_out4(a, ref.head * D + d, sum, row_factor(ll, vs));
             if (d == 0 && a.lse) a.lse[ref.head] = row_lse(mm, ll);
         }
