@@ -101,13 +101,7 @@ __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
 __device__ __forceinline__ uint32_t pack_16(int type, float lo, float hi) {
     return type == kF16 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
 }
-// Two e4m3 codes (low 16 bits of w) as an exact f16 pair.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
-    uint32_t r;
-    asm("{.reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t;}" : "=r"(r) : "r"(w));
-    return r;
-}
-// Four codes as two pairs.
+// Four e4m3 codes as two exact f16 pairs.
 __device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t w, uint32_t *lo, uint32_t *hi) {
     asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b;}"
         : "=r"(*lo), "=r"(*hi)
