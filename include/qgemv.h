@@ -543,7 +543,11 @@ int qg_rope_append(const qg_kv_cache *cache, const int *table, int table_stride,
  *          head_dim; q head h reads cache head h / (n_q_heads / n_heads).
  *          The cache's type, QG_BF16 or QG_F16 over a QG_E4M3 cache.
  *   lens   DEVICE int32 [n_seq], each in [0, max_len]; max_len at most
- *          table_stride * page_size (it bounds the workspace)
+ *          table_stride * page_size.  Any capacity is right, the longest length
+ *          is fastest: max_len chooses how the work is split (short sequences
+ *          under a large one take a second kernel) and bounds the workspace
+ *          (with accumulate the scores of max_len slots, 1 GiB or one
+ *          sequence's, and launches for as many sequences as that holds)
  *   o      DEVICE [n_seq * S][n_q_heads][head_dim], QG_F32, QG_BF16 or QG_F16
  *   lse    DEVICE f32 [n_seq * S][n_q_heads], or NULL
  *   accumulate  non-zero: weight[slot] += sum over the S * n_q_heads/n_heads
@@ -553,12 +557,17 @@ int qg_rope_append(const qg_kv_cache *cache, const int *table, int table_stride,
  *   ws     qattn_workspace_bytes() bytes, 256-byte aligned; contents on entry
  *          do not matter.  The bytes for the largest n_seq, max_len and S serve
  *          all smaller ones too, with accumulate those without
- * A masked slot never touches its row, whatever it holds (NaN, infinity).
+ * A masked slot never touches its row, whatever it holds (NaN, infinity); an
+ * infinity that a row sees in v makes that element infinite, or NaN where it
+ * meets a NaN or the other sign.  Over QG_F16 and QG_E4M3 caches a slot whose
+ * weight is below 2^-32 of the row's largest loses bits in o (not in lse), below
+ * 2^-48 it adds nothing.
  * A visible slot whose page is not in the pool makes its rows NaN and raises
  * QG_EPAGE; a length outside [0, max_len] is held to it and raises QG_EPAGE.
- * Sums and softmax statistics are f32, in an order that depends on the
- * lengths alone, so repeated calls give identical results.  n_seq = 0
- * launches nothing. */
+ * Sums and softmax statistics are f32, in an order that follows from the
+ * lengths of all sequences and the call's sizes: the same call on the same
+ * data gives the same bits, while another max_len, batch or accumulate may add
+ * in another order.  n_seq = 0 launches nothing. */
 size_t qattn_workspace_bytes(const qg_kv_cache *cache, int n_seq, int max_len, int S, int n_q_heads, int accumulate);
 
 int qattn_paged(const qg_kv_cache *cache, const int *table, int table_stride, const int *lens, int n_seq,

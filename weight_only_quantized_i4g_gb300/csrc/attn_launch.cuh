@@ -15,13 +15,14 @@ struct AttnPlan {
 // The smallest padded head size (the padding is not read from memory); then as
 // many tiles of 8 rows a warp as its registers take (two, or four at 64
 // dimensions, one at 256: four at 128 spill), and groups of two or four warps
-// for more rows (64 dimensions: 32 rows of 16 f16 sequences 25.6 us with two
-// warps of two tiles, 27.4 with one of four; 64 rows of 48 bf16 sequences 241 us
-// with two of four, 239 with four of two, of e4m3 252 and 271).  More than a
-// group's rows are further segments.  48 ragged bf16 sequences, 128 dimensions,
-// 8 cache heads, 12, 32 and 64 rows: 138, 215 and 413 us (before Q moved to
-// shared memory 264 and 507 with groups, 272 and 543 with segments of 16 rows,
-// 321 and 632 with four tiles a warp).
+// for more rows (64 dimensions: 32 rows of 16 f16 sequences to 4099 slots, four
+// new tokens, 26.9 us with two warps of two tiles, 33.9 with one of four, though
+// 48 to 8190 take 147 and 136; 64 rows of 48 bf16 sequences 256 us with two of
+// four, 251 with four of two, of e4m3 264 and 295).  More than a group's rows are
+// further segments.  48 ragged bf16 sequences, 128 dimensions, 8 cache heads, 12,
+// 32 and 64 rows: 139, 222 and 420 us (before Q moved to shared memory 264 and 507
+// with groups, 272 and 543 with segments of 16 rows, 321 and 632 with four tiles a
+// warp).
 template <int TYPE, bool FINE, class Fn>
 auto attn_dispatch(int rows, int dim, Fn fn) {
     if (dim <= 64)

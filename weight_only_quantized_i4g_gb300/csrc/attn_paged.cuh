@@ -101,15 +101,15 @@ struct AttnCfg {
     // to O, which rounds to nearest.  Only where a warp has 16 rows and more and
     // the output is bf16 the sum stays in the accumulators: 600,000 slots of one
     // warp would make that half a unit of bf16, and 48 ragged sequences take
-    // 216 us for 232 (32 rows at 128 dimensions; 413 for 445 with 64 rows; with
-    // e4m3 199 for 265).  With 8 rows there is no difference in time.
+    // 222 us for 242 (32 rows at 128 dimensions; 420 for 460 with 64 rows; with
+    // e4m3 214 for 291).  With 8 rows there is no difference in time.
     static constexpr bool fresh = FINE || TYPE == kF16 || (NT == 1 && GW == 1);
     // where the second f16 part of P gets its scale of 2^12 back: in its
-    // product's sum, or in V (exact for e4m3 codes), which several row tiles
-    // share (64 e4m3 sequences of 6000 to 16384, 7 rows: 234 us with the sum, 241
-    // with V, 232 with an unscaled part)
-    static constexpr bool LOW_SUM = TYPE == kF16 || (TYPE == kE4m3 && fresh && NT == 1), LOW_V = TYPE == kE4m3 && !LOW_SUM;
-    static_assert(fresh || !LOW_SUM, "the second part's product is scaled by itself");
+    // product's sum where that starts empty, else in V (exact for e4m3 codes).
+    // 64 e4m3 sequences of 6000 to 16384, 7 rows: 233 us with the sum, 241 with V,
+    // 232 with an unscaled part.
+    static constexpr bool LOW_SUM = fresh && TYPE != kBf16, LOW_V = !fresh && TYPE == kE4m3;
+    static_assert(LOW_SUM || TYPE != kF16, "V of a f16 cache cannot be scaled exactly");
     static constexpr int ESZ = TYPE == kE4m3 ? 1 : 2;
     static constexpr int warp_rows = 8 * NT, rows = GW * warp_rows;   // of a warp, of a segment
     static constexpr int KE = 16 / ESZ;               // elements of a K chunk
@@ -124,10 +124,10 @@ struct AttnCfg {
     static constexpr int stage = 2 * NB * box;        // 16 slots of K, then of V
     // as many warps as the registers of O, Q and S allow (16, 12 or 8 an SM);
     // groups keep Q in shared memory where that makes it more: 12 for 8 (48
-    // ragged f16 sequences, 32 rows at 128 dimensions: 251 -> 232 us; e4m3 236 ->
-    // 199), 16 for 12 (64 dimensions: 158 -> 143; with four drafted tokens,
-    // lengths to 4099, 26.2 -> 24.6).  Not where FINE needs more registers, which
-    // then spill (e4m3 236 -> 271, bf16 with its third part of P 261 -> 273)
+    // ragged bf16 sequences, 32 rows at 128 dimensions: 236 -> 222 us; f16 264 ->
+    // 258, e4m3 238 -> 214), 16 for 12 (64 dimensions, f16: 158 -> 147; with four
+    // drafted tokens, lengths to 4099, 29.6 -> 26.9).  Not where FINE needs more
+    // registers (e4m3 243 -> 251, bf16 with its third part of P 287 -> 283)
     static constexpr int regs0 = (ESZ == 1 ? 85 : 70) + 4 * MT * NT + 8 * NT, regs_q = NT * NI * (ESZ == 1 ? 8 : 4);
     static constexpr bool QS = GW > 1 && DP <= 128 && NT == 2 && !FINE && warps_for(regs0) > warps_for(regs0 + regs_q);
     static constexpr int W0 = warps_for(regs0 + (QS ? 0 : regs_q));

@@ -59,7 +59,7 @@ __device__ __forceinline__ void store1(char *base, int type, int d, float x, flo
 // VEC: rows, sizes and pointers allow four elements per access; a thread then
 // takes units of 8 elements of a head (two such groups), otherwise of a pair.
 // Eight blocks an SM: a block is a chain of waits, and only other blocks fill
-// them (6001 tokens, 56 heads: 40.6 us, 95% of the measured copy rate; 43.6 with
+// them (6001 tokens, 56 heads: 40.7 us, 93% of the measured copy rate; 43.6 with
 // six blocks, 50 with four, where a thread kept its pairs' cosines in registers).
 template <int IN, bool VEC>
 __global__ void __launch_bounds__(kRopeThreads, 8) rope_append_kernel(const __grid_constant__ RopeArgs a,
