@@ -48,7 +48,8 @@ class AttentionBlock:
     def __init__(self, w_qkv, w_o, batch, q_heads, kv_heads, dim, budget, page=16, sinks=4, recent=64, theta=1e4):
         dev = w_qkv.device
         self.batch, self.q_heads, self.kv_heads, self.dim = batch, q_heads, kv_heads, dim
-        self.budget, self.page, self.sinks, self.recent = budget, page, sinks, min(recent, budget // 2)
+        self.budget, self.page, self.recent = budget, page, min(recent, budget // 2)
+        self.sinks = min(sinks, budget - self.recent)
         self.qkv, self.out = PackedLinear(w_qkv), PackedLinear(w_o)
         self.limit = budget + page                               # slots at which the caches are cut
         self.width = -(-self.limit // page)                      # pages of a sequence
