@@ -74,7 +74,9 @@ typedef enum {
     QG_ECUDA = -6,       /* CUDA runtime error (no device, launch failure)   */
     QG_ETIMEOUT = -7,    /* a kernel gave up waiting (see qg_device_status)  */
     QG_EEXPERT = -8,     /* qgemv_moe: a slot's expert id was out of range   */
-                         /* or its weights misaligned (qg_device_status)     */
+                         /* or its weights misaligned; qgemm_e4m3_moe: the   */
+                         /* experts' offsets leave the rows                  */
+                         /* (qg_device_status)                               */
     QG_EBOUNDS = -9,     /* bounds-checking build only: a kernel formed an   */
                          /* index outside its arrays and skipped the access  */
                          /* (qg_device_status; never raised by libqgemv.so)  */
@@ -591,6 +593,110 @@ int qattn_paged(const qg_kv_cache *cache, const int *table, int table_stride, co
 int qg_kv_evict(const qg_kv_cache *cache, const int *table, int table_stride, const int *dst_table, int dst_stride,
                 const int *lens, int n_seq, int max_len, int budget, int sinks, int recent, int *kept,
                 int *new_lens, qg_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Expert layer: a prompt's or a batch's tokens to their experts, through   */
+/* 8-bit products, and back, without a number returning to the host         */
+/* (qgemv_moe and qgemm_moe are the weight-only products beside it; hipfire */
+/* docs "MQ4 V2", section 9 and colibri PR #528 name the expert paths).     */
+/*                                                                          */
+/* A router gives n_tokens x k slots: slot s = t * k + j is token t's j-th  */
+/* expert ids[s].  A slot whose id is outside [0, n_experts) has no expert  */
+/* here (it lives on another device, or the token is padding): it takes no  */
+/* row.  Rows are numbered expert by expert, in slot order inside one.      */
+/* place[s] is slot s's row, -1 for none; any place outside [0, n_rows)     */
+/* counts as none.  place = NULL: slot s is row s (as qgemv_moe leaves its  */
+/* outputs); n_rows is then at least n_tokens * k.  n_tokens * k < 2^31.    */
+/* Ids, places, weights and offsets live in device memory and are read      */
+/* after the previous kernel on the stream has finished, so a captured      */
+/* graph replays with new ones.  Outputs must not overlap inputs.           */
+/* Types are QG_F32, QG_BF16 or QG_F16 where nothing else is said; sums are */
+/* f32, rounded once (nearest even) to the type stored; the same call on    */
+/* the same data gives the same bits.  Alignment: elements; rows of whole   */
+/* 16-byte lines at 16-byte addresses take the fastest path.                */
+/* ------------------------------------------------------------------------ */
+
+/* Slots sorted by expert (stable):
+ *   offsets  DEVICE int32 [n_experts + 1]: rows offsets[e] .. offsets[e+1] - 1
+ *            are expert e's
+ *   order    DEVICE int32 [n_tokens * k], or NULL: order[row] = slot; entries
+ *            from offsets[n_experts] on are not written
+ *   place    DEVICE int32 [n_tokens * k]: the slot's row, or -1
+ *   n_experts  1 .. 8192
+ *   ws       qg_moe_sort_workspace_bytes() bytes, 256-byte aligned; contents
+ *            on entry do not matter
+ * n_tokens = 0 writes the offsets (all 0) alone. */
+size_t qg_moe_sort_workspace_bytes(int n_tokens, int k, int n_experts);
+
+int qg_moe_sort(int *offsets, int *order, int *place, const int *ids, int n_tokens, int k, int n_experts, void *ws,
+                size_t ws_bytes, qg_stream_t stream);
+
+/* Token rows to their experts: rows[place[s]] = x[s / k].
+ *   x         DEVICE n_tokens rows of x_stride (>= I) elements
+ *   rows      DEVICE [n_rows][I] in x's type, or QG_E4M3 codes with
+ *   row_scales  DEVICE f32 [n_rows][ceil(I/128)]: the scale of each 128
+ *             elements is 2^e, e the least integer >= -126 for which the
+ *             block's largest finite |x| is at most 448 * 2^e, and
+ *             code = e4m3(x / 2^e), rounded once (nearest even); an infinity
+ *             or NaN becomes the NaN code.  NULL for the wide types.
+ * Rows that no slot has keep their contents.  With place = NULL and k = 1 this
+ * is the quantiser of a whole matrix.  The gradient of the copy is
+ * qg_moe_combine without weights.  n_tokens = 0 or n_rows = 0 launches
+ * nothing. */
+int qg_moe_dispatch(void *rows, int rows_type, float *row_scales, const void *x, int x_type, size_t x_stride,
+                    const int *place, int n_tokens, int k, int I, int n_rows, qg_stream_t stream);
+
+/* Experts' rows back to their tokens: out[t] = sum_j weights[t*k+j] *
+ * y[place[t*k+j]], j ascending; a token without rows gets 0.
+ *   y        DEVICE [n_rows][O];  out  DEVICE [n_tokens][O]
+ *   weights  DEVICE f32 [n_tokens * k], or NULL: ones
+ * n_tokens = 0 launches nothing. */
+int qg_moe_combine(void *out, int out_type, const void *y, int y_type, const float *weights, const int *place,
+                   int n_tokens, int k, int O, int n_rows, qg_stream_t stream);
+
+/* Gradient of qg_moe_combine:
+ *   dy[place[s]] = weights[s] * dout[s / k],  dweights[s] = <dout[s / k], y[place[s]]>
+ *   dout      DEVICE [n_tokens][O];  y, dy  DEVICE [n_rows][O] of y_type
+ *   dweights  DEVICE f32 [n_tokens * k]; 0 for a slot without a row
+ * dy or dweights may be NULL (not wanted; without dweights y may be NULL too).
+ * Rows of dy that no slot has keep their contents.  n_tokens = 0 launches
+ * nothing. */
+int qg_moe_combine_grad(void *dy, float *dweights, const void *dout, int dout_type, const void *y, int y_type,
+                        const float *weights, const int *place, int n_tokens, int k, int O, int n_rows,
+                        qg_stream_t stream);
+
+/* Products of e4m3 activations with e4m3 weights:
+ *   Y[m,o] = sum_b x_scales[m,b] * s[o/128,b] * sum_{i in block b} X[m,i] * w[o,i]
+ * over blocks b of 128 elements along I.
+ *   fmt       QG_FMT_FP8B128 (w_scales f32) or QG_FMT_FP8UE8M0 (bytes)
+ *   X         DEVICE codes [M][I] with x_scales DEVICE f32 [M][ceil(I/128)],
+ *             any values (qg_moe_dispatch makes powers of two)
+ *   w         DEVICE codes [O][I] with w_scales [ceil(O/128)][ceil(I/128)], as
+ *             qgemv_fp8b128 and qgemv_fp8ue8m0 take them; in qgemm_e4m3_moe
+ *             n_experts such matrices one after another, and their scales
+ *   offsets   DEVICE int32 [n_experts + 1] (qg_moe_sort): rows offsets[e] ..
+ *             offsets[e+1] - 1 use expert e.  M is the rows that X and Y hold,
+ *             at least offsets[n_experts]; rows behind that, and rows before
+ *             offsets[0], are not written.  A table that decreases or leaves
+ *             [0, M] is held to the rows that are there, and the device error
+ *             word says QG_EEXPERT.  n_experts 1 .. 8192.
+ *   Y         DEVICE [M][O], y_type QG_F32, QG_BF16 or QG_F16
+ *   ws        qgemm_e4m3_workspace_bytes() bytes (n_experts = 1 for
+ *             qgemm_e4m3), 256-byte aligned; contents on entry do not matter
+ * The products of a block are exact and summed in f32, the blocks' sums times
+ * the product of the two scales (one f32; a subnormal or infinite one is as
+ * good as f32 holds it) are summed in f32: within 1e-3 * sum |x w| of the
+ * definition.  A NaN code makes its row, or column of the expert's rows, NaN.
+ * M = 0 launches nothing; M at most 4194240.  I a multiple of 16 and X, w at
+ * 16-byte addresses take the tensor-core kernel, anything else a general one. */
+size_t qgemm_e4m3_workspace_bytes(int M, int I, int O, int n_experts);
+
+int qgemm_e4m3(int fmt, void *Y, int y_type, const uint8_t *X, const float *x_scales, const uint8_t *w,
+               const void *w_scales, int M, int I, int O, void *ws, size_t ws_bytes, qg_stream_t stream);
+
+int qgemm_e4m3_moe(int fmt, void *Y, int y_type, const uint8_t *X, const float *x_scales, const uint8_t *w,
+                   const void *w_scales, const int *offsets, int n_experts, int M, int I, int O, void *ws,
+                   size_t ws_bytes, qg_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Weight preparation on the device (not on the decode path)                */

@@ -66,6 +66,14 @@ _SIGNATURES = {
     "qattn_workspace_bytes": ([_P, _I, _I, _I, _I, _I], _Z),
     "qattn_paged": ([_P, _P, _I, _P, _I, _I, _P, _I, _P, _P, _I, _Z, _I, _I, ctypes.c_float, _I, _P, _Z, _P], _I),
     "qg_kv_evict": ([_P, _P, _I, _P, _I, _P, _I, _I, _I, _I, _I, _P, _P, _P], _I),
+    "qg_moe_sort_workspace_bytes": ([_I, _I, _I], _Z),
+    "qg_moe_sort": ([_P, _P, _P, _P, _I, _I, _I, _P, _Z, _P], _I),
+    "qg_moe_dispatch": ([_P, _I, _P, _P, _I, _Z, _P, _I, _I, _I, _I, _P], _I),
+    "qg_moe_combine": ([_P, _I, _P, _I, _P, _P, _I, _I, _I, _I, _P], _I),
+    "qg_moe_combine_grad": ([_P, _P, _P, _I, _P, _I, _P, _P, _I, _I, _I, _I, _P], _I),
+    "qgemm_e4m3_workspace_bytes": ([_I, _I, _I, _I], _Z),
+    "qgemm_e4m3": ([_I, _P, _I, _P, _P, _P, _P, _I, _I, _I, _P, _Z, _P], _I),
+    "qgemm_e4m3_moe": ([_I, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _Z, _P], _I),
     "qg_encode_mq4v1": ([_P, _P, _I, _I, _P], _I),
     "qg_encode_mq4c": ([_P, _P, _I, _I, _P], _I),
     "qg_quantize_i4g": ([_P, _P, _P, _I, _I, _I, _P], _I),
@@ -372,3 +380,44 @@ def qg_kv_evict(cache, table, table_stride, dst_table, dst_stride, lens, n_seq, 
                 new_lens, stream=None) -> int:
     return _lib.qg_kv_evict(_cache(cache), _ptr(table), table_stride, _ptr(dst_table), dst_stride, _ptr(lens), n_seq,
                             max_len, budget, sinks, recent, _ptr(kept), _ptr(new_lens), _stream(stream))
+
+
+def qg_moe_sort_workspace_bytes(n_tokens, k, n_experts) -> int:
+    return _lib.qg_moe_sort_workspace_bytes(n_tokens, k, n_experts)
+
+
+def qg_moe_sort(offsets, order, place, ids, n_tokens, k, n_experts, ws=None, ws_bytes=0, stream=None) -> int:
+    return _lib.qg_moe_sort(_ptr(offsets), _ptr(order), _ptr(place), _ptr(ids), n_tokens, k, n_experts, _ptr(ws),
+                            ws_bytes, _stream(stream))
+
+
+def qg_moe_dispatch(rows, rows_type, row_scales, x, x_type, x_stride, place, n_tokens, k, I, n_rows,
+                    stream=None) -> int:
+    return _lib.qg_moe_dispatch(_ptr(rows), rows_type, _ptr(row_scales), _ptr(x), x_type, x_stride, _ptr(place),
+                                n_tokens, k, I, n_rows, _stream(stream))
+
+
+def qg_moe_combine(out, out_type, y, y_type, weights, place, n_tokens, k, O, n_rows, stream=None) -> int:
+    return _lib.qg_moe_combine(_ptr(out), out_type, _ptr(y), y_type, _ptr(weights), _ptr(place), n_tokens, k, O,
+                               n_rows, _stream(stream))
+
+
+def qg_moe_combine_grad(dy, dweights, dout, dout_type, y, y_type, weights, place, n_tokens, k, O, n_rows,
+                        stream=None) -> int:
+    return _lib.qg_moe_combine_grad(_ptr(dy), _ptr(dweights), _ptr(dout), dout_type, _ptr(y), y_type, _ptr(weights),
+                                    _ptr(place), n_tokens, k, O, n_rows, _stream(stream))
+
+
+def qgemm_e4m3_workspace_bytes(M, I, O, n_experts=1) -> int:
+    return _lib.qgemm_e4m3_workspace_bytes(M, I, O, n_experts)
+
+
+def qgemm_e4m3(fmt, Y, y_type, X, x_scales, w, w_scales, M, I, O, ws=None, ws_bytes=0, stream=None) -> int:
+    return _lib.qgemm_e4m3(fmt, _ptr(Y), y_type, _ptr(X), _ptr(x_scales), _ptr(w), _ptr(w_scales), M, I, O, _ptr(ws),
+                           ws_bytes, _stream(stream))
+
+
+def qgemm_e4m3_moe(fmt, Y, y_type, X, x_scales, w, w_scales, offsets, n_experts, M, I, O, ws=None, ws_bytes=0,
+                   stream=None) -> int:
+    return _lib.qgemm_e4m3_moe(fmt, _ptr(Y), y_type, _ptr(X), _ptr(x_scales), _ptr(w), _ptr(w_scales), _ptr(offsets),
+                               n_experts, M, I, O, _ptr(ws), ws_bytes, _stream(stream))

@@ -1,0 +1,108 @@
+// gemm_e4m3.cu -- products of e4m3 activations with e4m3 weights (qgemm_e4m3,
+// qgemm_e4m3_moe):
+//
+//   Y[m, o] = sum_b xs[m, b] ws[o/128, b] sum_{i in block b} X[m, i] W[o, i]
+//
+// with a scale for each token and 128 elements and one for each 128 x 128
+// weights; rows [offsets[e], offsets[e+1]) use expert e's weights.
+//
+// General kernel, for every shape and alignment: 64 x 64 outputs a block, K
+// in steps of 32, codes widened to f32 in shared memory, f32 sums of a
+// 128-block scaled when it ends.  A block of rows that several experts share
+// goes over each of them.
+#include "moe.cuh"
+
+namespace qg {
+namespace {
+
+constexpr int kGT = 64, kGK = 32;
+
+__device__ __forceinline__ float e4m3_to_f32(uint8_t c) {
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)c));
+    return f16_bits_to_f32((uint16_t)h2);
+}
+
+template <class SC>
+__device__ __forceinline__ void store_y(void *Y, int type, size_t at, float v, SC) {
+    if (type == kF32) static_cast<float *>(Y)[at] = v;
+    else if (type == kBf16) static_cast<uint16_t *>(Y)[at] = Elem<kBf16>::put(v);
+    else static_cast<uint16_t *>(Y)[at] = Elem<kF16>::put(v);
+}
+
+template <class SC>
+__global__ void __launch_bounds__(256) gemm_e4m3_general_kernel(const E4m3Args a) {
+    __shared__ float Ws[kGK][kGT + 1];   // [k][o]
+    __shared__ float Xs[kGK][kGT + 1];   // [k][m]
+    griddep_wait();
+    griddep_launch_dependents();
+    const int o0 = blockIdx.x * kGT, m0 = blockIdx.y * kGT;
+    const int nb = (a.I + 127) / 128, nbo = (a.O + 127) / 128;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;   // 16 x 16 threads, 4 x 4 each
+    for (int g = 0; g < a.experts; ++g) {
+        int from = 0, to = a.M;
+        if (a.offsets) group_range(a.offsets, g, a.M, &from, &to, threadIdx.x == 0 ? a.err : nullptr);
+        if (to <= m0 || from >= m0 + kGT || to <= from) continue;      // the same for the whole block
+        const uint8_t *w = a.w + (size_t)g * a.O * a.I;
+        const typename SC::T *ws = static_cast<const typename SC::T *>(a.w_scale) + (size_t)g * nbo * nb;
+        float sum[4][4] = {}, acc[4][4] = {};
+        for (int k0 = 0; k0 < a.I; k0 += kGK) {
+            for (int e = threadIdx.x; e < kGK * kGT; e += blockDim.x) {
+                const int kk = e % kGK, r = e / kGK, i = k0 + kk, o = o0 + r, m = m0 + r;
+                Ws[kk][r] = o < a.O && i < a.I ? e4m3_to_f32(w[(size_t)o * a.I + i]) : 0.f;
+                Xs[kk][r] = m >= from && m < to && i < a.I ? e4m3_to_f32(a.X[(size_t)m * a.I + i]) : 0.f;
+            }
+            __syncthreads();
+#pragma unroll 8
+            for (int kk = 0; kk < kGK; ++kk) {
+                float x[4], v[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    x[t] = Xs[kk][ty * 4 + t];
+                    v[t] = Ws[kk][tx * 4 + t];
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[r][c] = fmaf(x[r], v[c], acc[r][c]);
+            }
+            __syncthreads();
+            if ((k0 + kGK) % 128 && k0 + kGK < a.I) continue;
+            const int b = k0 / 128;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int m = m0 + ty * 4 + r;
+                const float xs = m >= from && m < to ? a.x_scale[(size_t)m * nb + b] : 0.f;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int o = o0 + tx * 4 + c;
+                    if (o < a.O) sum[r][c] = fmaf(acc[r][c], xs * SC::get(ws, (size_t)(o / 128) * nb + b), sum[r][c]);
+                    acc[r][c] = 0.f;
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int m = m0 + ty * 4 + r;
+            if (m < from || m >= to) continue;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int o = o0 + tx * 4 + c;
+                if (o < a.O) store_y(a.Y, a.y_type, (size_t)m * a.O + o, sum[r][c], SC());
+            }
+        }
+    }
+}
+
+}  // namespace
+
+size_t ws_gemm_e4m3(int, int, int, int) { return 0; }
+
+int run_gemm_e4m3(const E4m3Args &a, void *, cudaStream_t st) {
+    const char *what = a.offsets ? "qgemm_e4m3_moe" : "qgemm_e4m3";
+    const dim3 grid((a.O + kGT - 1) / kGT, (a.M + kGT - 1) / kGT);
+    return a.w_power ? launch_pdl(what, gemm_e4m3_general_kernel<ScaleE8M0>, grid, 256, 0, st, a)
+                     : launch_pdl(what, gemm_e4m3_general_kernel<ScaleF32>, grid, 256, 0, st, a);
+}
+
+}  // namespace qg

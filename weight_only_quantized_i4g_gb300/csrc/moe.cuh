@@ -1,0 +1,106 @@
+// moe.cuh -- internal interface of the expert layer's operators (declared in
+// include/qgemv.h): slots sorted by expert, rows dispatched and combined, the
+// combination's gradient, e4m3 x e4m3 products.  Arguments reaching these
+// functions have been validated by abi_moe.cu.
+#pragma once
+
+#include "kv_cache.cuh"   // element types, packing, programmatic launches
+
+namespace qg {
+
+constexpr int kErrExpert = -8;
+constexpr int kMaxSortExperts = 8192;
+
+struct SortArgs {
+    int *offsets, *order, *place;   // order may be NULL
+    const int *ids;
+    int slots, experts;
+};
+size_t ws_moe_sort(int slots, int experts);
+int run_moe_sort(const SortArgs &a, void *ws, cudaStream_t st);
+
+struct DispatchArgs {
+    void *rows;
+    float *scales;                  // e4m3 rows only
+    const void *x;
+    size_t x_stride;                // elements
+    const int *place;               // NULL: slot s is row s
+    int tokens, k, width, n_rows;
+};
+int run_moe_dispatch(const DispatchArgs &a, int x_type, bool codes, cudaStream_t st);
+
+struct CombineArgs {
+    void *out;
+    const void *y;
+    const float *weights;           // NULL: ones
+    const int *place;               // NULL: slot s is row s
+    int tokens, k, width, n_rows;
+};
+int run_moe_combine(const CombineArgs &a, int out_type, int y_type, cudaStream_t st);
+
+struct CombineGradArgs {
+    void *dy;                       // NULL: not wanted
+    float *dweights;                // NULL: not wanted
+    const void *dout, *y;
+    const float *weights;
+    const int *place;
+    int tokens, k, width, n_rows;
+};
+int run_moe_combine_grad(const CombineGradArgs &a, int dout_type, int y_type, cudaStream_t st);
+
+// Y rows of expert e: offsets[e] to offsets[e+1] (device), or all M rows of
+// one matrix where offsets is NULL.
+struct E4m3Args {
+    void *Y;
+    int y_type;
+    const uint8_t *X;
+    const float *x_scale;           // [M, ceil(I/128)]
+    const uint8_t *w;               // [experts, O, I]
+    const void *w_scale;            // [experts, ceil(O/128), ceil(I/128)], f32 or UE8M0
+    bool w_power;                   // UE8M0
+    const int *offsets;
+    int experts, M, I, O;
+    int *err;
+};
+size_t ws_gemm_e4m3(int M, int I, int O, int experts);
+int run_gemm_e4m3(const E4m3Args &a, void *ws, cudaStream_t st);
+
+// Rows [*from, *to) of group g; a table that decreases or passes M is held
+// to the rows that are there, and the thread that asks with err != NULL
+// raises the error word.
+__device__ __forceinline__ void group_range(const int *offsets, int g, int M, int *from, int *to, int *err) {
+    int a = offsets[g], b = offsets[g + 1];
+    if (a < 0 || b < a || b > M) {
+        raise_device_error(err, kErrExpert);
+        a = min(max(a, 0), M);
+        b = min(max(b, a), M);
+    }
+    *from = a;
+    *to = b;
+}
+
+// Row of slot s (NULL table: s), -1 for none.
+__device__ __forceinline__ int row_of(const int *place, long long s, int n_rows) {
+    const long long p = place ? place[s] : s;
+    return p >= 0 && p < n_rows ? (int)p : -1;
+}
+
+// Elements of the three wide types as f32.
+template <int T> struct Elem;
+template <> struct Elem<kF32> {
+    typedef float Word;
+    static __device__ __forceinline__ float get(float v) { return v; }
+    static __device__ __forceinline__ float put(float v) { return v; }
+};
+template <> struct Elem<kBf16> {
+    typedef uint16_t Word;
+    static __device__ __forceinline__ float get(uint16_t v) { return bf16_bits_to_f32(v); }
+    static __device__ __forceinline__ uint16_t put(float v) { return (uint16_t)pack_bf16(v, 0.f); }
+};
+template <> struct Elem<kF16> {
+    typedef uint16_t Word;
+    static __device__ __forceinline__ float get(uint16_t v) { return f16_bits_to_f32(v); }
+    static __device__ __forceinline__ uint16_t put(float v) { return (uint16_t)pack_f16(v, 0.f); }
+};
+
+}  // namespace qg
