@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(256) gemm_e4m3_general_kernel(const E4m3Args a
 size_t ws_gemm_e4m3(int, int, int, int) { return 0; }
 
 int run_gemm_e4m3(const E4m3Args &a, void *, cudaStream_t st) {
+    if (gemm_e4m3_tc_takes(a)) return run_gemm_e4m3_tc(a, st);
     const char *what = a.offsets ? "qgemm_e4m3_moe" : "qgemm_e4m3";
     const dim3 grid((a.O + kGT - 1) / kGT, (a.M + kGT - 1) / kGT);
     return a.w_power ? launch_pdl(what, gemm_e4m3_general_kernel<ScaleE8M0>, grid, 256, 0, st, a)
