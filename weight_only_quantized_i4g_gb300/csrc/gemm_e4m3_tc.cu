@@ -27,25 +27,32 @@ namespace e8 {
 
 using namespace tc;
 
-constexpr int kChunk = 4;              // K steps of one slot of scales
-constexpr int kSlots = 2;
-constexpr int kWarpScale = 2, kWarpPromote = 4;
-constexpr int kBoxRows = 32;           // tokens of one TMA box of X
+constexpr int kWarpMma2 = 2;           // a second issuing warp: they take the stages in turn
 constexpr int kMaxExperts = 1024;      // the tables of tiles and rows in shared memory
 constexpr uint32_t kWBytes = 128 * 128;
+constexpr int kRedStride = 132;        // words between the columns of a reduction: the fragments' rows and columns meet no bank twice
+constexpr int kOutStride = 80;         // bytes between the tokens of a 32-output strip on its way out, for the same reason
 
 template <int BT_>
 struct Cfg8 {
     static constexpr int BT = BT_;
-    static constexpr int kGroups = BT >= 256 ? 2 : 1;              // promoting warps of a lane quarter
+    static constexpr int kBlocks = BT <= 64 ? 2 : 1;               // K blocks of a stage
+    static constexpr int kGroups = BT >= 128 ? 2 : 1;              // promoting warps of a lane quarter
     static constexpr int kWarps = 4 * kGroups;
+    static constexpr bool kWide = BT >= 256;                       // registers move to the promoting warps
+    static constexpr int kScaleWarps = kWide ? 4 : 1;
+    static constexpr int kWarpScale = kWide ? 4 : 3, kWarpPromote = kWide ? 8 : 4;
     static constexpr int kThreads = 32 * (kWarpPromote + kWarps);
-    static constexpr int kBufs = BT >= 256 ? 2 : 4;                // tensor-memory buffers
-    static constexpr uint32_t kTmemCols = kBufs * BT < 32 ? 32 : kBufs * BT;
+    static constexpr int kChunk = 4, kSlots = 2;                   // K blocks of one slot of scales
+    static constexpr int kBufs = BT >= 256 ? 2 : 4;                // tensor-memory buffers, one a stage
+    static constexpr int kBufCols = kBlocks * BT;
+    static constexpr uint32_t kTmemCols = kBufs * kBufCols;
+    static constexpr int kBoxRows = BT < 64 ? BT : 64;             // tokens of one TMA box of X
     static constexpr uint32_t kXBytes = BT * 128;
-    static constexpr uint32_t kStageBytes = kWBytes + kXBytes;
-    static constexpr int kRedCols = BT >= 64 ? 32 : BT;            // columns of one round of the reduction
-    static constexpr uint32_t kRedBytes = kRedCols * 128 * 4;
+    static constexpr uint32_t kBlockBytes = kWBytes + kXBytes;
+    static constexpr uint32_t kStageBytes = kBlocks * kBlockBytes;
+    static constexpr int kRedCols = 32;                            // columns of one round of the reduction
+    static constexpr uint32_t kRedBytes = kRedCols * kRedStride * 4;
     static constexpr uint32_t kScaleBytes = kSlots * kChunk * BT * 4;
     static constexpr uint32_t kTableBytes = (3 * kMaxExperts + 2) * 4;   // first tiles [E + 1], first and last rows [E][2]
     static constexpr uint32_t kBarBytes = 512;
@@ -56,10 +63,12 @@ struct Cfg8 {
     static constexpr uint32_t kBarOff = kRedOff + kRedBytes;
     static constexpr uint32_t kTableOff = kBarOff + kBarBytes;
     static constexpr uint32_t kSmemBytes = 1024 + kTableOff + kTableBytes;
-    static constexpr int kPieces = BT / 16 / kGroups;              // sixteens of columns a promoting warp holds
+    static constexpr int kCols = BT < 64 ? BT : 64;                // columns a promoting warp loads at once
+    static constexpr int kPieces = BT / kCols / kGroups;           // such pieces it holds
     static_assert(BT % 32 == 0 && BT <= 256, "whole boxes, one MMA");
-    static_assert(kStages >= 3 && kNumBars * 8 + 16 <= (int)kBarBytes && kTmemCols <= 512, "");
+    static_assert(kStages >= 3 && kNumBars * 8 + 16 <= (int)kBarBytes && kTmemCols <= 512 && kTmemCols >= 32, "");
     static_assert((kTmemCols & (kTmemCols - 1)) == 0, "allocations are powers of two");
+    static_assert(kWarps * 16 * kOutStride <= (int)kRedBytes, "a strip of 16 tokens a warp on its way out");
 };
 
 struct Args8 {
@@ -86,21 +95,53 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint6
         : "memory");
 }
 
-// 16 columns of this warp's 32 lanes, to be read after tmem_landed on the same registers.
-__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16]) {
+// 8 R columns of 16 tensor-memory lanes, to be read after tmem_landed on the
+// same registers: of columns 8 i + 2 (lane % 4) + {0, 1}, registers 4 i and
+// 4 i + 1 hold tensor-memory lane lane / 4 and the next two lane / 4 + 8.
+template <int R>
+struct Frag {
+    uint32_t r[4 * R];
+};
+__device__ __forceinline__ void tmem_load(uint32_t taddr, Frag<4> &f) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "=r"(f.r[0]), "=r"(f.r[1]), "=r"(f.r[2]), "=r"(f.r[3]), "=r"(f.r[4]), "=r"(f.r[5]), "=r"(f.r[6]),
+          "=r"(f.r[7]), "=r"(f.r[8]), "=r"(f.r[9]), "=r"(f.r[10]), "=r"(f.r[11]), "=r"(f.r[12]), "=r"(f.r[13]),
+          "=r"(f.r[14]), "=r"(f.r[15])
         : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_landed(uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_load(uint32_t taddr, Frag<8> &f) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(f.r[0]), "=r"(f.r[1]), "=r"(f.r[2]), "=r"(f.r[3]), "=r"(f.r[4]), "=r"(f.r[5]), "=r"(f.r[6]),
+          "=r"(f.r[7]), "=r"(f.r[8]), "=r"(f.r[9]), "=r"(f.r[10]), "=r"(f.r[11]), "=r"(f.r[12]), "=r"(f.r[13]),
+          "=r"(f.r[14]), "=r"(f.r[15]), "=r"(f.r[16]), "=r"(f.r[17]), "=r"(f.r[18]), "=r"(f.r[19]),
+          "=r"(f.r[20]), "=r"(f.r[21]), "=r"(f.r[22]), "=r"(f.r[23]), "=r"(f.r[24]), "=r"(f.r[25]),
+          "=r"(f.r[26]), "=r"(f.r[27]), "=r"(f.r[28]), "=r"(f.r[29]), "=r"(f.r[30]), "=r"(f.r[31])
+        : "r"(taddr));
+}
+// Waits for the loads; the registers pass through, so that nothing reads them before.
+__device__ __forceinline__ void tmem_landed(Frag<4> &f) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 : "+r"(f.r[0]), "+r"(f.r[1]), "+r"(f.r[2]), "+r"(f.r[3]), "+r"(f.r[4]), "+r"(f.r[5]), "+r"(f.r[6]),
+                   "+r"(f.r[7]), "+r"(f.r[8]), "+r"(f.r[9]), "+r"(f.r[10]), "+r"(f.r[11]), "+r"(f.r[12]),
+                   "+r"(f.r[13]), "+r"(f.r[14]), "+r"(f.r[15])
                  :
                  : "memory");
+}
+__device__ __forceinline__ void tmem_landed(Frag<8> &f) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(f.r[0]), "+r"(f.r[1]), "+r"(f.r[2]), "+r"(f.r[3]), "+r"(f.r[4]), "+r"(f.r[5]), "+r"(f.r[6]),
+                   "+r"(f.r[7]), "+r"(f.r[8]), "+r"(f.r[9]), "+r"(f.r[10]), "+r"(f.r[11]), "+r"(f.r[12]),
+                   "+r"(f.r[13]), "+r"(f.r[14]), "+r"(f.r[15]), "+r"(f.r[16]), "+r"(f.r[17]), "+r"(f.r[18]),
+                   "+r"(f.r[19]), "+r"(f.r[20]), "+r"(f.r[21]), "+r"(f.r[22]), "+r"(f.r[23]), "+r"(f.r[24]),
+                   "+r"(f.r[25]), "+r"(f.r[26]), "+r"(f.r[27])
+                 :
+                 : "memory");
+    asm volatile("" : "+r"(f.r[28]), "+r"(f.r[29]), "+r"(f.r[30]), "+r"(f.r[31])::"memory");
 }
 // a += (lo, hi) * f, two f32 at a time
 __device__ __forceinline__ void fma2(uint64_t &a, uint32_t lo, uint32_t hi, uint64_t f) {
@@ -109,6 +150,14 @@ __device__ __forceinline__ void fma2(uint64_t &a, uint32_t lo, uint32_t hi, uint
 __device__ __forceinline__ float2 pair_of(uint64_t v) {
     return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
 }
+// Four 8 x 8 matrices of 16-bit fragments, transposed: row lane % 8 of matrix lane / 8 goes to this lane's address.
+__device__ __forceinline__ void stmatrix4_trans(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+}
+template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // Cluster helpers: the address of a local shared variable in another block, arrivals there, loads from there.
 __device__ __forceinline__ uint32_t map_rank(uint32_t local, int rank) {
@@ -185,7 +234,7 @@ gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     float *s_red = reinterpret_cast<float *>(smem + C::kRedOff);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kBarOff);
     uint64_t *full = bars, *empty = full + C::kStages, *acc_full = empty + C::kStages, *acc_empty = acc_full + C::kBufs,
-             *sc_full = acc_empty + C::kBufs, *sc_empty = sc_full + kSlots, *red_full = sc_empty + kSlots,
+             *sc_full = acc_empty + C::kBufs, *sc_empty = sc_full + C::kSlots, *red_full = sc_empty + C::kSlots,
              *red_empty = red_full + 1;
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(bars + C::kNumBars);
     volatile uint32_t *abort = tmem_slot + 1;
@@ -205,8 +254,8 @@ gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], C::kWarps);
         }
-        for (int b = 0; b < kSlots; ++b) {
-            mbar_init(&sc_full[b], 1);
+        for (int b = 0; b < C::kSlots; ++b) {
+            mbar_init(&sc_full[b], C::kScaleWarps);
             mbar_init(&sc_empty[b], C::kWarps);
         }
         mbar_init(red_full, ranks * C::kWarps);
@@ -295,51 +344,69 @@ gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     const int tiles = s_tile[a.experts] * a.NB, first = blockIdx.x / ranks, step = gridDim.x / ranks;
     const int k0 = (int)((long long)a.KB * rank / ranks), k1 = (int)((long long)a.KB * (rank + 1) / ranks);
 
+    // BT = 256: 512 threads start with 128 registers each, 65536 in all, of
+    // which the promoting warps take 8 x 32 x 216 and the others 8 x 32 x 40.
     if (warp == kWarpTma) {
+        if constexpr (C::kWide) regs_down<40>();
         if (lane == 0) {
             uint32_t it = 0;
             for (int t = first; t < tiles; t += step) {
                 const Tile L = find_tile<BT>(a, s_tile, s_row, t);
-                const int boxes = (L.rows + kBoxRows - 1) / kBoxRows, wrow = L.e * a.O + L.ot * 128;
-                for (int k = k0; k < k1; ++k, ++it) {
+                const int boxes = (L.rows + C::kBoxRows - 1) / C::kBoxRows, wrow = L.e * a.O + L.ot * 128;
+                for (int k = k0; k < k1; k += C::kBlocks, ++it) {
                     const uint32_t s = it % C::kStages, r = it / C::kStages;
+                    const int n = min(C::kBlocks, k1 - k);
                     if (r > 0 && !mbar_wait_or_abort(&empty[s], (r & 1) ^ 1, abort))
                         raise_device_error(a.err, kErrTimeout);
-                    const uint32_t st = sbase + s * C::kStageBytes;
-                    mbar_arrive_expect_tx(&full[s], kWBytes + boxes * (kBoxRows * 128));
-                    tma_load_2d(st, &tmW, k * 128, wrow, &full[s]);
-                    for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(st + kWBytes + b * (kBoxRows * 128), &tmX, k * 128, L.m0 + b * kBoxRows, &full[s]);
+                    mbar_arrive_expect_tx(&full[s], n * (kWBytes + boxes * (C::kBoxRows * 128)));
+                    for (int j = 0; j < n; ++j) {
+                        const uint32_t st = sbase + s * C::kStageBytes + j * C::kBlockBytes;
+                        tma_load_2d(st, &tmW, (k + j) * 128, wrow, &full[s]);
+                        for (int b = 0; b < boxes; ++b)
+                            tma_load_2d(st + kWBytes + b * (C::kBoxRows * 128), &tmX, (k + j) * 128, L.m0 + b * C::kBoxRows, &full[s]);
+                    }
                 }
             }
             // Every copy issued must have landed before the block exits.
             for (uint32_t j = it > (uint32_t)C::kStages ? it - C::kStages : 0; j < it; ++j)
                 if (!mbar_wait(&full[j % C::kStages], (j / C::kStages) & 1)) raise_device_error(a.err, kErrTimeout);
         }
-    } else if (warp == kWarpMma) {
+    } else if (warp == kWarpMma || warp == kWarpMma2) {
+        if constexpr (C::kWide) regs_down<40>();
+        // No stage's sums depend on another's, so two threads issue them in
+        // turn: each one's waits and commits pass while the other's MMAs run.
         if (lane == 0) {
             uint32_t it = 0;
+            const uint32_t mine = warp == kWarpMma ? 0u : 1u;
             for (int t = first; t < tiles; t += step) {
                 const Tile L = find_tile<BT>(a, s_tile, s_row, t);
                 const uint32_t idesc = idesc_e4m3((L.rows + 15) & ~15);
-                for (int k = k0; k < k1; ++k, ++it) {
+                for (int k = k0; k < k1; k += C::kBlocks, ++it) {
+                    if ((it & 1u) != mine) continue;
                     const uint32_t s = it % C::kStages, r = it / C::kStages, b = it % C::kBufs, rb = it / C::kBufs;
+                    const int n = min(C::kBlocks, k1 - k);
                     if (rb > 0 && !mbar_wait_or_abort(&acc_empty[b], (rb & 1) ^ 1, abort))
                         raise_device_error(a.err, kErrTimeout);
                     if (!mbar_wait_or_abort(&full[s], r & 1, abort)) raise_device_error(a.err, kErrTimeout);
                     tc_fence_after();
-                    const uint32_t st = sbase + s * C::kStageBytes;
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_e4m3(tmem + b * BT, sw128_desc(st + kk * 32), sw128_desc(st + kWBytes + kk * 32), idesc,
-                                 kk > 0 ? 1u : 0u);
+                    for (int j = 0; j < C::kBlocks; ++j) {
+                        if (j >= n) break;
+                        const uint32_t st = sbase + s * C::kStageBytes + j * C::kBlockBytes;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_e4m3(tmem + b * C::kBufCols + j * BT, sw128_desc(st + kk * 32),
+                                     sw128_desc(st + kWBytes + kk * 32), idesc, kk > 0 ? 1u : 0u);
+                    }
                     mma_commit(&acc_full[b]);
                     mma_commit(&empty[s]);
                 }
             }
         }
-    } else if (warp == kWarpScale) {
-        constexpr int kTok = BT / 32;
+    } else if (warp >= C::kWarpScale && warp < C::kWarpScale + C::kScaleWarps) {
+        if constexpr (C::kWide) regs_down<40>();
+        constexpr int kTok = BT / 32 / C::kScaleWarps, kChunk = C::kChunk, kSlots = C::kSlots;
+        const int m_first = (warp - C::kWarpScale) * 32 * kTok + lane;
         uint32_t ch = 0;
         for (int t = first; t < tiles; t += step) {
             const Tile L = find_tile<BT>(a, s_tile, s_row, t);
@@ -352,28 +419,30 @@ gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                     const float w = k + c < k1 ? SC::get(ws, k + c) : 0.f;
 #pragma unroll
                     for (int i = 0; i < kTok; ++i) {
-                        const int m = lane + 32 * i;
+                        const int m = m_first + 32 * i;
                         v[i][c] = m < L.rows && k + c < k1 ? a.xs[(size_t)(L.m0 + m) * a.KB + k + c] * w : 0.f;
                     }
                 }
                 if (r > 0) {
-                    bool ok = true;
-                    if (lane == 0) ok = mbar_wait_or_abort(&sc_empty[s], (r & 1) ^ 1, abort);
-                    if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0) && lane == 0) raise_device_error(a.err, kErrTimeout);
+                    if (!mbar_wait_or_abort(&sc_empty[s], (r & 1) ^ 1, abort) && lane == 0)
+                        raise_device_error(a.err, kErrTimeout);
+                    __syncwarp();
                 }
-                float *dst = s_scale + s * kChunk * BT;
+                float *dst = s_scale + s * kChunk * BT + m_first;
 #pragma unroll
                 for (int c = 0; c < kChunk; ++c)
 #pragma unroll
-                    for (int i = 0; i < kTok; ++i) dst[c * BT + lane + 32 * i] = v[i][c];
+                    for (int i = 0; i < kTok; ++i) dst[c * BT + 32 * i] = v[i][c];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sc_full[s]);
             }
         }
-    } else if (warp >= kWarpPromote) {
-        const int pw = warp - kWarpPromote, q = warp & 3, grp = pw >> 2, pt = threadIdx.x - 32 * kWarpPromote;
+    } else if (warp >= C::kWarpPromote) {
+        if constexpr (C::kWide) regs_up<216>();
+        const int pw = warp - C::kWarpPromote, q = warp & 3, grp = pw >> 2, pt = threadIdx.x - 32 * C::kWarpPromote;
         const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16);
-        const int row = q * 32 + lane;
+        const int row = q * 32 + (lane >> 2), cl = 2 * (lane & 3);   // of the fragments: rows row + 8 i, columns 8 j + cl, + 1
+        constexpr int kF = C::kCols / 8, kChunk = C::kChunk, kSlots = C::kSlots;
         uint32_t it = 0, ch = 0, round = 0;
         auto wait_warp = [&](uint64_t *bar, uint32_t parity) {
             if (!mbar_wait_or_abort(bar, parity, abort) && lane == 0) raise_device_error(a.err, kErrTimeout);
@@ -381,65 +450,124 @@ gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         };
         for (int t = first; t < tiles; t += step) {
             const Tile L = find_tile<BT>(a, s_tile, s_row, t);
-            const int pieces = (L.rows + 15) >> 4;             // sixteens of the tile; mine: grp, grp + kGroups, ...
-            uint64_t acc[C::kPieces][8];
+            // piece p: columns (p * kGroups + grp) * kCols; sums [upper half of the rows][fragment][row + 8]
+            uint64_t acc[C::kPieces][2][kF][2];
 #pragma unroll
             for (int p = 0; p < C::kPieces; ++p)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) acc[p][j] = 0;
-            for (int k = k0; k < k1; ++k, ++it) {
-                const int c = (k - k0) % kChunk;
-                if (c == 0) wait_warp(&sc_full[ch % kSlots], (ch / kSlots) & 1);
+                for (int j = 0; j < kF; ++j) acc[p][0][j][0] = acc[p][0][j][1] = acc[p][1][j][0] = acc[p][1][j][1] = 0;
+            for (int k = k0; k < k1; k += C::kBlocks, ++it) {
                 const uint32_t b = it % C::kBufs;
-                wait_warp(&acc_full[b], (it / C::kBufs) & 1);
-                tc_fence_after();
-                const float *f = s_scale + ((ch % kSlots) * kChunk + c) * BT;
-                uint32_t r[2][16];
-                const uint32_t tb = tq + b * BT;
-                if (grp < pieces) tmem_ld16_async(tb + grp * 16, r[0]);
 #pragma unroll
-                for (int p = 0; p < C::kPieces; ++p) {
-                    const int at = p * C::kGroups + grp;
-                    if (at >= pieces) break;
-                    tmem_landed(r[p & 1]);
-                    if (p + 1 < C::kPieces && at + C::kGroups < pieces) tmem_ld16_async(tb + (at + C::kGroups) * 16, r[(p + 1) & 1]);
+                for (int x = 0; x < C::kBlocks; ++x) {
+                    if (x > 0 && k + x >= k1) break;
+                    const int c = (k + x - k0) % kChunk;
+                    if (c == 0) wait_warp(&sc_full[ch % kSlots], (ch / kSlots) & 1);
+                    if (x == 0) {
+                        wait_warp(&acc_full[b], (it / C::kBufs) & 1);
+                        tc_fence_after();
+                    }
+                    const float *f = s_scale + ((ch % kSlots) * kChunk + c) * BT + cl;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const ulonglong2 g = *reinterpret_cast<const ulonglong2 *>(f + at * 16 + 4 * j);
-                        fma2(acc[p][2 * j], r[p & 1][4 * j], r[p & 1][4 * j + 1], g.x);
-                        fma2(acc[p][2 * j + 1], r[p & 1][4 * j + 2], r[p & 1][4 * j + 3], g.y);
+                    for (int p = 0; p < C::kPieces; ++p) {
+                        const int col = (p * C::kGroups + grp) * C::kCols;
+                        if (col < L.rows) {
+                            Frag<kF> lo, hi;
+                            const uint32_t ta = tq + b * C::kBufCols + x * BT + col;
+                            tmem_load(ta, lo);
+                            tmem_load(ta + (16u << 16), hi);
+                            uint64_t g[kF];
+#pragma unroll
+                            for (int j = 0; j < kF; ++j) g[j] = *reinterpret_cast<const uint64_t *>(f + col + 8 * j);
+                            tmem_landed(lo);
+                            tmem_landed(hi);
+#pragma unroll
+                            for (int j = 0; j < kF; ++j) {
+                                fma2(acc[p][0][j][0], lo.r[4 * j], lo.r[4 * j + 1], g[j]);
+                                fma2(acc[p][0][j][1], lo.r[4 * j + 2], lo.r[4 * j + 3], g[j]);
+                                fma2(acc[p][1][j][0], hi.r[4 * j], hi.r[4 * j + 1], g[j]);
+                                fma2(acc[p][1][j][1], hi.r[4 * j + 2], hi.r[4 * j + 3], g[j]);
+                            }
+                        }
+                    }
+                    if (c == kChunk - 1 || k + x + 1 == k1) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sc_empty[ch % kSlots]);
+                        ++ch;
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&acc_empty[b]);
-                if (c == kChunk - 1 || k + 1 == k1) {
-                    if (lane == 0) mbar_arrive(&sc_empty[ch % kSlots]);
-                    ++ch;
-                }
             }
             const int o0 = L.ot * 128;
             if (ranks == 1) {
-                const int o = o0 + row;
-                if (o < a.O) {
+                if (a.y_type == kF32) {
+                    // a warp's store: eight outputs, one sector, of four tokens
+                    float *y = static_cast<float *>(a.Y) + (size_t)L.m0 * a.O + o0 + row;
 #pragma unroll
-                    for (int p = 0; p < C::kPieces; ++p) {
-                        const int at = (p * C::kGroups + grp) * 16;
-                        const size_t y = (size_t)(L.m0 + at) * a.O + o;
+                    for (int p = 0; p < C::kPieces; ++p)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float2 v = pair_of(acc[p][j]);
-                            if (at + 2 * j < L.rows) store_y(a, y + (size_t)(2 * j) * a.O, v.x);
-                            if (at + 2 * j + 1 < L.rows) store_y(a, y + (size_t)(2 * j + 1) * a.O, v.y);
-                        }
-                    }
+                        for (int j = 0; j < kF; ++j)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int m = (p * C::kGroups + grp) * C::kCols + 8 * j + cl;
+                                const float2 v = pair_of(acc[p][i >> 1][j][i & 1]);
+                                if (o0 + row + 8 * i < a.O) {
+                                    if (m < L.rows) y[(size_t)m * a.O + 8 * i] = v.x;
+                                    if (m + 1 < L.rows) y[(size_t)(m + 1) * a.O + 8 * i] = v.y;
+                                }
+                            }
+                    continue;
                 }
+                // 16-bit types: sixteen tokens of this warp's 32 outputs at a
+                // time, transposed through shared memory to 64 bytes a token.
+                const uint32_t strip = smem_addr(s_red) + pw * 16 * kOutStride;
+                const int ow = o0 + q * 32, part = lane & 3;
+                const bool whole = ow + 32 <= a.O && a.O % 8 == 0 && reinterpret_cast<uintptr_t>(a.Y) % 16 == 0;
+#pragma unroll
+                for (int p = 0; p < C::kPieces; ++p)
+#pragma unroll
+                    for (int j = 0; j < kF; j += 2) {
+                        const int m = (p * C::kGroups + grp) * C::kCols + 8 * j;
+                        if (m >= L.rows) continue;
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 v = pair_of(acc[p][i >> 1][j + x][i & 1]);
+                                w[i] = pack_16(a.y_type, v.x, v.y);
+                            }
+                            // matrix i (outputs 8 i ..): row lane % 8 is token 8 x + lane % 8
+                            stmatrix4_trans(strip + (8 * x + (lane & 7)) * kOutStride + (lane >> 3) * 16, w[0], w[1], w[2], w[3]);
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const int tok = 8 * x + (lane >> 2);
+                            const uint4 v = *reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(s_red) + pw * 16 * kOutStride +
+                                                                             tok * kOutStride + part * 16);
+                            if (m + tok < L.rows) {
+                                uint16_t *y = static_cast<uint16_t *>(a.Y) + (size_t)(L.m0 + m + tok) * a.O + ow + part * 8;
+                                if (whole) {
+                                    *reinterpret_cast<uint4 *>(y) = v;
+                                } else {
+                                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i)
+                                        if (ow + part * 8 + i < a.O) y[i] = (uint16_t)(u[i >> 1] >> (16 * (i & 1)));
+                                }
+                            }
+                        }
+                        __syncwarp();
+                    }
                 continue;
             }
             // Rounds of kRedCols columns: every block's sums into its shared
             // memory, then each rank adds its share of the columns over all
             // blocks, in rank order, and stores it.
-            constexpr int kPer = C::kRedCols / 16 / C::kGroups;   // pieces a warp brings to a round
+            constexpr int kRounds = C::kCols / C::kRedCols;       // of a piece
 #pragma unroll
             for (int rd = 0; rd < BT / C::kRedCols; ++rd) {
                 if (rd * C::kRedCols >= L.rows) break;
@@ -447,15 +575,17 @@ gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                     if (!wait_cluster(red_empty, (round - 1) & 1, abort) && lane == 0) raise_device_error(a.err, kErrTimeout);
                     __syncwarp();
                 }
+                // the round's columns are one group's
+                const int piece = rd / kRounds, p = piece / C::kGroups, j0 = rd % kRounds * (C::kRedCols / 8);
+                if (piece % C::kGroups == grp) {
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const int p = rd * kPer + i, col = (i * C::kGroups + grp) * 16;
+                    for (int j = 0; j < C::kRedCols / 8; ++j)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 v = pair_of(acc[p][j]);
-                        s_red[(col + 2 * j) * 128 + row] = v.x;
-                        s_red[(col + 2 * j + 1) * 128 + row] = v.y;
-                    }
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 v = pair_of(acc[p][i >> 1][j0 + j][i & 1]);
+                            s_red[(8 * j + cl) * kRedStride + row + 8 * i] = v.x;
+                            s_red[(8 * j + cl + 1) * kRedStride + row + 8 * i] = v.y;
+                        }
                 }
                 __syncwarp();
                 if (lane < (int)ranks) arrive_remote(map_rank(smem_addr(red_full), lane));
@@ -465,7 +595,7 @@ gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                 for (int col = (int)rank + (pt >> 7) * (int)ranks; col < C::kRedCols; col += C::kGroups * (int)ranks) {
                     const int m = rd * C::kRedCols + col;
                     if (m >= L.rows) break;
-                    const uint32_t local = smem_addr(s_red + col * 128 + (pt & 127));
+                    const uint32_t local = smem_addr(s_red + col * kRedStride + (pt & 127));
                     float sum = 0.f;
                     for (int r = 0; r < (int)ranks; ++r) sum += load_remote(map_rank(local, r));
                     if (o < a.O) store_y(a, (size_t)(L.m0 + m) * a.O + o, sum);
@@ -475,6 +605,8 @@ gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                 ++round;
             }
         }
+    } else if constexpr (C::kWide) {
+        regs_down<40>();                   // the spare warp of the first four
     }
 
     tc_fence_before();
@@ -510,7 +642,7 @@ int clusters_at_once(int bt, int cluster) {
         set_max_dynamic_smem(k, (int)smem);
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(cluster);
-        cfg.blockDim = dim3(i == 3 ? Cfg8<256>::kThreads : Cfg8<32>::kThreads);
+        cfg.blockDim = dim3(i == 3 ? Cfg8<256>::kThreads : i == 2 ? Cfg8<128>::kThreads : Cfg8<64>::kThreads);
         cfg.dynamicSmemBytes = smem;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -592,10 +724,10 @@ bool gemm_e4m3_tc_takes(const E4m3Args &a) {
 int run_gemm_e4m3_tc(const E4m3Args &g, cudaStream_t st) {
     const char *what = g.offsets ? "qgemm_e4m3_moe" : "qgemm_e4m3";
     if (!tc::encode_fn()) QG_REFUSE(kECuda, "%s: cuTensorMapEncodeTiled is not available from the driver", what);
-    CUtensorMap w, x;
-    if (!e8::encode_map(&w, g.w, (long long)g.experts * g.O, g.I, 128) || !e8::encode_map(&x, g.X, g.M, g.I, e8::kBoxRows))
-        QG_REFUSE(kECuda, "%s: tensor map refused", what);
     const e8::Plan8 p = e8::plan(g.M, g.I, g.O, g.experts);
+    CUtensorMap w, x;
+    if (!e8::encode_map(&w, g.w, (long long)g.experts * g.O, g.I, 128) || !e8::encode_map(&x, g.X, g.M, g.I, p.bt < 64 ? p.bt : 64))
+        QG_REFUSE(kECuda, "%s: tensor map refused", what);
     const e8::Args8 a{g.Y, g.y_type, g.x_scale, g.w_scale, g.offsets, g.experts, g.M, g.O,
                       (g.I + 127) / 128, (g.O + 127) / 128, g.err};
     return g.w_power ? e8::launch_bt<ScaleE8M0>(what, p, w, x, a, st) : e8::launch_bt<ScaleF32>(what, p, w, x, a, st);
