@@ -6,11 +6,12 @@
 // with a scale for each token and 128 elements and one for each 128 x 128
 // weights; rows [offsets[e], offsets[e+1]) use expert e's weights.
 //
-// General kernel, for every shape and alignment: 64 x 64 outputs a block, K
-// in steps of 32, codes widened to f32 in shared memory, f32 sums of a
-// 128-block scaled when it ends.  A block of rows that several experts share
-// goes over each of them.
-#include "moe.cuh"
+// Rows of whole 16-byte lines run on the tensor cores (gemm_e4m3_tc.cuh);
+// this file has the choice between their kernels, and the general kernel, for
+// every shape and alignment: 64 x 64 outputs a block, K in steps of 32, codes
+// widened to f32 in shared memory, f32 sums of a 128-block scaled when it
+// ends.  A block of rows that several experts share goes over each of them.
+#include "gemm_e4m3_tc.cuh"
 
 namespace qg {
 namespace {
@@ -23,8 +24,7 @@ __device__ __forceinline__ float e4m3_to_f32(uint8_t c) {
     return f16_bits_to_f32((uint16_t)h2);
 }
 
-template <class SC>
-__device__ __forceinline__ void store_y(void *Y, int type, size_t at, float v, SC) {
+__device__ __forceinline__ void store_y(void *Y, int type, size_t at, float v) {
     if (type == kF32) static_cast<float *>(Y)[at] = v;
     else if (type == kBf16) static_cast<uint16_t *>(Y)[at] = Elem<kBf16>::put(v);
     else static_cast<uint16_t *>(Y)[at] = Elem<kF16>::put(v);
@@ -88,10 +88,27 @@ __global__ void __launch_bounds__(256) gemm_e4m3_general_kernel(const E4m3Args a
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int o = o0 + tx * 4 + c;
-                if (o < a.O) store_y(a.Y, a.y_type, (size_t)m * a.O + o, sum[r][c], SC());
+                if (o < a.O) store_y(a.Y, a.y_type, (size_t)m * a.O + o, sum[r][c]);
             }
         }
     }
+}
+
+int run_tc(const char *what, const E4m3Args &g, cudaStream_t st) {
+    if (!tc::encode_fn()) QG_REFUSE(kECuda, "%s: cuTensorMapEncodeTiled is not available from the driver", what);
+    const e8::Args8 a{g.Y, g.y_type, g.x_scale, g.w_scale, g.offsets, g.experts, g.M, g.O,
+                      (g.I + 127) / 128, (g.O + 127) / 128, 0, g.err};
+    const e8::FewPlan few = e8::plan_few(g.M, g.I, g.O, g.experts);
+    const e8::ManyPlan many = e8::plan_many(g.M, g.I, g.O, g.experts);
+    return many.cost < few.cost ? e8::launch_many(what, many, g, a, st) : e8::launch_few(what, few, g, a, st);
+}
+
+// TMA's rules for the rows, the tables in shared memory, and 32-bit rows and tiles.
+bool tc_takes(const E4m3Args &a) {
+    const long long wrows = (long long)a.experts * a.O;
+    const long long tiles = ((long long)a.M / 32 + a.experts) * ((a.O + 127) / 128);
+    return a.I % 16 == 0 && (uintptr_t)a.X % 16 == 0 && (uintptr_t)a.w % 16 == 0 && a.experts <= e8::kMaxExperts &&
+           wrows < (1ll << 31) - 256 && tiles < (1ll << 31) - 65536;
 }
 
 }  // namespace
@@ -99,8 +116,8 @@ __global__ void __launch_bounds__(256) gemm_e4m3_general_kernel(const E4m3Args a
 size_t ws_gemm_e4m3(int, int, int, int) { return 0; }
 
 int run_gemm_e4m3(const E4m3Args &a, void *, cudaStream_t st) {
-    if (gemm_e4m3_tc_takes(a)) return run_gemm_e4m3_tc(a, st);
     const char *what = a.offsets ? "qgemm_e4m3_moe" : "qgemm_e4m3";
+    if (tc_takes(a)) return run_tc(what, a, st);
     const dim3 grid((a.O + kGT - 1) / kGT, (a.M + kGT - 1) / kGT);
     return a.w_power ? launch_pdl(what, gemm_e4m3_general_kernel<ScaleE8M0>, grid, 256, 0, st, a)
                      : launch_pdl(what, gemm_e4m3_general_kernel<ScaleF32>, grid, 256, 0, st, a);

@@ -1,34 +1,26 @@
-// gemm_e4m3_tc.cu -- products of e4m3 activations with e4m3 weights on the
-// 5th-generation tensor cores (tcgen05 kind::f8f6f4, accumulators in tensor
-// memory), for rows of whole 16-byte lines.
-//
-//   Y[m, o] = sum_b xs[m, b] ws[o/128, b] sum_{i in block b} X[m, i] W[o, i]
+// gemm_e4m3_few.cu -- products of e4m3 activations with e4m3 weights, few
+// tokens an expert: the weights' bytes bound it.
 //
 // A tile is 128 outputs (rows of W, MMA M) by up to BT tokens of one expert
-// (MMA N, as many as the tile has, in sixteens).  One K step is one block of
-// 128 elements: four MMAs of K = 32 leave the block's sums in one of several
-// buffers of tensor memory, and the promoting warps add them, times the two
-// scales, to f32 sums in registers.  The outputs of a tile share one weight
-// scale, and the product of both scales comes from shared memory, a token
-// each.  One persistent thread block per SM:
-//   warp 0      TMA producer: per K step the 128 x 128 codes of W and the
-//               tile's tokens x 128 of X, both 128-byte swizzled
-//   warp 1      allocates tensor memory, issues the MMAs from one thread
-//   warp 2      the scales' products, kChunk steps at a time
-//   warps 4..   promote: tensor-memory lanes 32 (w % 4) .. + 31, columns in
-//               sixteens shared by the one or two warps of a lane quarter
+// (MMA N, as many as the tile has, in sixteens), so a token costs an MMA of
+// sixteen and not of 128.  The outputs of a tile share one weight scale, and
+// the product of both scales comes from shared memory, a token each.  One
+// persistent thread block per SM:
+//   warp 0      TMA producer: per K block the 128 x 128 codes of W and BT x
+//               128 of X, both 128-byte swizzled
+//   warps 1, 2  issue the MMAs, a thread each, stages in turn
+//   warp 3      the scales' products, kChunk K blocks at a time
+//   warps 4..   promote: tensor-memory lanes 32 (w % 4) .. + 31, columns
+//               shared by the one or two warps of a lane quarter
 // Calls of few tiles split K over the blocks of a cluster, which add their
 // sums over distributed shared memory, in rank order.
-#include "gemm_tc.cuh"
-#include "moe.cuh"
+#include "gemm_e4m3_tc.cuh"
 
 namespace qg {
 namespace e8 {
 
-using namespace tc;
-
-constexpr int kWarpMma2 = 2;           // a second issuing warp: they take the stages in turn
-constexpr int kMaxExperts = 1024;      // the tables of tiles and rows in shared memory
+constexpr int kChunk = 4, kSlots = 2;  // K blocks of one slot of scales
+constexpr int kWarpScale = 3, kWarpPromote = 4;
 constexpr uint32_t kWBytes = 128 * 128;
 constexpr int kRedStride = 132;        // words between the columns of a reduction: the fragments' rows and columns meet no bank twice
 constexpr int kOutStride = 80;         // bytes between the tokens of a 32-output strip on its way out, for the same reason
@@ -39,22 +31,16 @@ struct Cfg8 {
     static constexpr int kBlocks = BT <= 64 ? 2 : 1;               // K blocks of a stage
     static constexpr int kGroups = BT >= 128 ? 2 : 1;              // promoting warps of a lane quarter
     static constexpr int kWarps = 4 * kGroups;
-    static constexpr bool kWide = BT >= 256;                       // registers move to the promoting warps
-    static constexpr int kScaleWarps = kWide ? 4 : 1;
-    static constexpr int kWarpScale = kWide ? 4 : 3, kWarpPromote = kWide ? 8 : 4;
     static constexpr int kThreads = 32 * (kWarpPromote + kWarps);
-    static constexpr int kChunk = 4, kSlots = 2;                   // K blocks of one slot of scales
-    static constexpr int kBufs = BT >= 256 ? 2 : 4;                // tensor-memory buffers, one a stage
+    static constexpr int kBufs = 4;                                // tensor-memory buffers, one a stage
     static constexpr int kBufCols = kBlocks * BT;
     static constexpr uint32_t kTmemCols = kBufs * kBufCols;
-    static constexpr int kBoxRows = BT < 64 ? BT : 64;             // tokens of one TMA box of X
     static constexpr uint32_t kXBytes = BT * 128;
     static constexpr uint32_t kBlockBytes = kWBytes + kXBytes;
     static constexpr uint32_t kStageBytes = kBlocks * kBlockBytes;
     static constexpr int kRedCols = 32;                            // columns of one round of the reduction
     static constexpr uint32_t kRedBytes = kRedCols * kRedStride * 4;
     static constexpr uint32_t kScaleBytes = kSlots * kChunk * BT * 4;
-    static constexpr uint32_t kTableBytes = (3 * kMaxExperts + 2) * 4;   // first tiles [E + 1], first and last rows [E][2]
     static constexpr uint32_t kBarBytes = 512;
     static constexpr int kStages = (int)((kSmemBudget - 1024 - 256 - kRedBytes - kScaleBytes - kTableBytes - kBarBytes) / kStageBytes);
     static constexpr int kNumBars = 2 * kStages + 2 * kBufs + 2 * kSlots + 2;
@@ -65,35 +51,16 @@ struct Cfg8 {
     static constexpr uint32_t kSmemBytes = 1024 + kTableOff + kTableBytes;
     static constexpr int kCols = BT < 64 ? BT : 64;                // columns a promoting warp loads at once
     static constexpr int kPieces = BT / kCols / kGroups;           // such pieces it holds
-    static_assert(BT % 32 == 0 && BT <= 256, "whole boxes, one MMA");
+    static_assert(BT % 32 == 0 && BT <= 128, "one box of X, one MMA");
     static_assert(kStages >= 3 && kNumBars * 8 + 16 <= (int)kBarBytes && kTmemCols <= 512 && kTmemCols >= 32, "");
     static_assert((kTmemCols & (kTmemCols - 1)) == 0, "allocations are powers of two");
+    // A wait tells one phase of a barrier from the next, not from the one
+    // after that, so a stage must always be the same issuer's: with an odd
+    // number of stages one thread could pass on a phase that the other had
+    // not seen begin.
+    static_assert(kStages % 2 == 0 && kBufs % 2 == 0, "a stage and a buffer belong to the same issuer every time");
     static_assert(kWarps * 16 * kOutStride <= (int)kRedBytes, "a strip of 16 tokens a warp on its way out");
 };
-
-struct Args8 {
-    void *Y;
-    int y_type;
-    const float *xs;
-    const void *ws;
-    const int *offsets;               // NULL: one expert, rows [0, M)
-    int experts, M, O, KB, NB;        // K blocks, output tiles
-    int *err;
-};
-
-// Instruction descriptor of kind::f8f6f4: f32 accumulator, e4m3 A and B (format code 0), K-major, M = 128, N = n.
-__device__ __forceinline__ uint32_t idesc_e4m3(int n) {
-    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kMmaM >> 4) << 24);
-}
-__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                         uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
 
 // 8 R columns of 16 tensor-memory lanes, to be read after tmem_landed on the
 // same registers: of columns 8 i + 2 (lane % 4) + {0, 1}, registers 4 i and
@@ -143,88 +110,15 @@ __device__ __forceinline__ void tmem_landed(Frag<8> &f) {
                  : "memory");
     asm volatile("" : "+r"(f.r[28]), "+r"(f.r[29]), "+r"(f.r[30]), "+r"(f.r[31])::"memory");
 }
-// a += (lo, hi) * f, two f32 at a time
-__device__ __forceinline__ void fma2(uint64_t &a, uint32_t lo, uint32_t hi, uint64_t f) {
-    asm("{.reg .b64 t; mov.b64 t, {%1, %2}; fma.rn.f32x2 %0, t, %3, %0;}" : "+l"(a) : "r"(lo), "r"(hi), "l"(f));
-}
-__device__ __forceinline__ float2 pair_of(uint64_t v) {
-    return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
-}
 // Four 8 x 8 matrices of 16-bit fragments, transposed: row lane % 8 of matrix lane / 8 goes to this lane's address.
 __device__ __forceinline__ void stmatrix4_trans(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(a), "r"(b),
                  "r"(c), "r"(d)
                  : "memory");
 }
-template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
-// Cluster helpers: the address of a local shared variable in another block, arrivals there, loads from there.
-__device__ __forceinline__ uint32_t map_rank(uint32_t local, int rank) {
-    uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ void arrive_remote(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ float load_remote(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile uint32_t *abort) {
-    const uint32_t a = smem_addr(bar);
-    for (uint32_t it = 0; it < kSpinLimit; ++it) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(a), "r"(parity)
-            : "memory");
-        if (done) return true;
-        if ((it & 255u) == 255u && *abort) return false;
-    }
-    *abort = 1u;
-    return false;
-}
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-
-__device__ __forceinline__ void store_y(const Args8 &a, size_t at, float v) {
-    if (a.y_type == kF32) static_cast<float *>(a.Y)[at] = v;
-    else if (a.y_type == kBf16) static_cast<uint16_t *>(a.Y)[at] = Elem<kBf16>::put(v);
-    else static_cast<uint16_t *>(a.Y)[at] = Elem<kF16>::put(v);
-}
-
-struct Tile {
-    int e, m0, rows, ot;              // expert, first row, its rows in the tile, output tile
-};
-// Tiles are numbered expert by expert, output tile by output tile, tokens
-// fastest: blocks of one wave share weights.
-template <int BT>
-__device__ __forceinline__ Tile find_tile(const Args8 &a, const int *s_tile, const int *s_row, int t) {
-    int lo = 0, hi = a.experts;       // the last e with s_tile[e] * NB <= t
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_tile[mid] * a.NB <= t) lo = mid;
-        else hi = mid;
-    }
-    const int nt = s_tile[lo + 1] - s_tile[lo], local = t - s_tile[lo] * a.NB;
-    Tile r;
-    r.e = lo;
-    r.ot = local / nt;
-    r.m0 = s_row[2 * lo] + (local - r.ot * nt) * BT;
-    r.rows = min(s_row[2 * lo + 1] - r.m0, BT);
-    return r;
-}
-
 template <int BT, class SC>
 __global__ void __launch_bounds__(Cfg8<BT>::kThreads, 1)
-gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Args8 a) {
+gemm_e4m3_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Args8 a) {
     using C = Cfg8<BT>;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw_base = smem_addr(smem_raw);
@@ -234,7 +128,7 @@ gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     float *s_red = reinterpret_cast<float *>(smem + C::kRedOff);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kBarOff);
     uint64_t *full = bars, *empty = full + C::kStages, *acc_full = empty + C::kStages, *acc_empty = acc_full + C::kBufs,
-             *sc_full = acc_empty + C::kBufs, *sc_empty = sc_full + C::kSlots, *red_full = sc_empty + C::kSlots,
+             *sc_full = acc_empty + C::kBufs, *sc_empty = sc_full + kSlots, *red_full = sc_empty + kSlots,
              *red_empty = red_full + 1;
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(bars + C::kNumBars);
     volatile uint32_t *abort = tmem_slot + 1;
@@ -254,8 +148,8 @@ gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], C::kWarps);
         }
-        for (int b = 0; b < C::kSlots; ++b) {
-            mbar_init(&sc_full[b], C::kScaleWarps);
+        for (int b = 0; b < kSlots; ++b) {
+            mbar_init(&sc_full[b], 1);
             mbar_init(&sc_empty[b], C::kWarps);
         }
         mbar_init(red_full, ranks * C::kWarps);
@@ -267,103 +161,36 @@ gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     }
     if (warp == kWarpMma) {
         __syncwarp();
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_addr((const void *)tmem_slot)),
-                     "r"(C::kTmemCols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tmem_alloc<false>(tmem_slot, C::kTmemCols);
     }
     griddep_wait();
     griddep_launch_dependents();
-    // Tables of the experts' first tiles and rows.
-    if (a.offsets == nullptr) {
-        if (threadIdx.x == 0) {
-            s_tile[0] = 0;
-            s_tile[1] = (a.M + BT - 1) / BT;
-            s_row[0] = 0;
-            s_row[1] = a.M;
-        }
-    } else {
-        // Row bounds held to [0, M] and to their order (a table that is
-        // neither raises the error word): expert e has rows most[e] to
-        // most[e+1] of the running maximum.
-        int tiles_before = 0, most = min(max(a.offsets[0], 0), a.M);
-        for (int e0 = 0; e0 < a.experts; e0 += C::kThreads) {
-            const int e = e0 + threadIdx.x;
-            int to = 0;
-            if (e < a.experts) {
-                const int lo = a.offsets[e], hi = a.offsets[e + 1];
-                if ((lo < 0 || hi < lo || hi > a.M) && blockIdx.x == 0) raise_device_error(a.err, kErrExpert);
-                to = min(max(hi, 0), a.M);
-            }
-            int top = to;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, top, d);
-                if (lane >= d) top = max(top, y);
-            }
-            if (lane == 31) s_warp[warp].x = top;
-            __syncthreads();
-            int below = most;
-            for (int w = 0; w < C::kThreads / 32; ++w) {
-                if (w < warp) below = max(below, s_warp[w].x);
-                most = max(most, s_warp[w].x);
-            }
-            int from = __shfl_up_sync(0xffffffffu, top, 1);
-            from = lane == 0 ? below : max(from, below);
-            to = max(top, below);
-            const int n = e < a.experts ? (to - from + BT - 1) / BT : 0;
-            int x = n;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, d);
-                if (lane >= d) x += y;
-            }
-            if (lane == 31) s_warp[warp].y = x;
-            __syncthreads();
-            int before = tiles_before;
-            for (int w = 0; w < C::kThreads / 32; ++w) {
-                before += w < warp ? s_warp[w].y : 0;
-                tiles_before += s_warp[w].y;
-            }
-            if (e < a.experts) {
-                s_tile[e] = before + x - n;
-                s_row[2 * e] = from;
-                s_row[2 * e + 1] = to;
-            }
-            __syncthreads();
-        }
-        if (threadIdx.x == 0) s_tile[a.experts] = tiles_before;
-    }
+    build_tables<BT, C::kThreads>(a, s_tile, s_row, s_warp);
     tc_fence_before();
     __syncthreads();
     if (ranks > 1) cluster_barrier();      // every block's barriers are there before another arrives at them
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    const int tiles = s_tile[a.experts] * a.NB, first = blockIdx.x / ranks, step = gridDim.x / ranks;
+    const int tiles = s_tile[a.experts] * a.NT, first = blockIdx.x / ranks, step = gridDim.x / ranks;
     const int k0 = (int)((long long)a.KB * rank / ranks), k1 = (int)((long long)a.KB * (rank + 1) / ranks);
 
-    // BT = 256: 512 threads start with 128 registers each, 65536 in all, of
-    // which the promoting warps take 8 x 32 x 216 and the others 8 x 32 x 40.
     if (warp == kWarpTma) {
-        if constexpr (C::kWide) regs_down<40>();
         if (lane == 0) {
             uint32_t it = 0;
             for (int t = first; t < tiles; t += step) {
                 const Tile L = find_tile<BT>(a, s_tile, s_row, t);
-                const int boxes = (L.rows + C::kBoxRows - 1) / C::kBoxRows, wrow = L.e * a.O + L.ot * 128;
+                const int wrow = L.e * a.O + L.ot * 128;
                 for (int k = k0; k < k1; k += C::kBlocks, ++it) {
                     const uint32_t s = it % C::kStages, r = it / C::kStages;
                     const int n = min(C::kBlocks, k1 - k);
                     if (r > 0 && !mbar_wait_or_abort(&empty[s], (r & 1) ^ 1, abort))
                         raise_device_error(a.err, kErrTimeout);
-                    mbar_arrive_expect_tx(&full[s], n * (kWBytes + boxes * (C::kBoxRows * 128)));
+                    mbar_arrive_expect_tx(&full[s], n * C::kBlockBytes);
                     for (int j = 0; j < n; ++j) {
                         const uint32_t st = sbase + s * C::kStageBytes + j * C::kBlockBytes;
                         tma_load_2d(st, &tmW, (k + j) * 128, wrow, &full[s]);
-                        for (int b = 0; b < boxes; ++b)
-                            tma_load_2d(st + kWBytes + b * (C::kBoxRows * 128), &tmX, (k + j) * 128, L.m0 + b * C::kBoxRows, &full[s]);
+                        tma_load_2d(st + kWBytes, &tmX, (k + j) * 128, L.m0, &full[s]);
                     }
                 }
             }
@@ -372,7 +199,6 @@ gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                 if (!mbar_wait(&full[j % C::kStages], (j / C::kStages) & 1)) raise_device_error(a.err, kErrTimeout);
         }
     } else if (warp == kWarpMma || warp == kWarpMma2) {
-        if constexpr (C::kWide) regs_down<40>();
         // No stage's sums depend on another's, so two threads issue them in
         // turn: each one's waits and commits pass while the other's MMAs run.
         if (lane == 0) {
@@ -380,7 +206,7 @@ gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
             const uint32_t mine = warp == kWarpMma ? 0u : 1u;
             for (int t = first; t < tiles; t += step) {
                 const Tile L = find_tile<BT>(a, s_tile, s_row, t);
-                const uint32_t idesc = idesc_e4m3((L.rows + 15) & ~15);
+                const uint32_t idesc = idesc_e4m3(kMmaM, (L.rows + 15) & ~15);
                 for (int k = k0; k < k1; k += C::kBlocks, ++it) {
                     if ((it & 1u) != mine) continue;
                     const uint32_t s = it % C::kStages, r = it / C::kStages, b = it % C::kBufs, rb = it / C::kBufs;
@@ -395,7 +221,7 @@ gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                         const uint32_t st = sbase + s * C::kStageBytes + j * C::kBlockBytes;
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma_e4m3(tmem + b * C::kBufCols + j * BT, sw128_desc(st + kk * 32),
+                            mma_e4m3<false>(tmem + b * C::kBufCols + j * BT, sw128_desc(st + kk * 32),
                                      sw128_desc(st + kWBytes + kk * 32), idesc, kk > 0 ? 1u : 0u);
                     }
                     mma_commit(&acc_full[b]);
@@ -403,10 +229,8 @@ gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                 }
             }
         }
-    } else if (warp >= C::kWarpScale && warp < C::kWarpScale + C::kScaleWarps) {
-        if constexpr (C::kWide) regs_down<40>();
-        constexpr int kTok = BT / 32 / C::kScaleWarps, kChunk = C::kChunk, kSlots = C::kSlots;
-        const int m_first = (warp - C::kWarpScale) * 32 * kTok + lane;
+    } else if (warp == kWarpScale) {
+        constexpr int kTok = BT / 32;
         uint32_t ch = 0;
         for (int t = first; t < tiles; t += step) {
             const Tile L = find_tile<BT>(a, s_tile, s_row, t);
@@ -419,7 +243,7 @@ gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                     const float w = k + c < k1 ? SC::get(ws, k + c) : 0.f;
 #pragma unroll
                     for (int i = 0; i < kTok; ++i) {
-                        const int m = m_first + 32 * i;
+                        const int m = lane + 32 * i;
                         v[i][c] = m < L.rows && k + c < k1 ? a.xs[(size_t)(L.m0 + m) * a.KB + k + c] * w : 0.f;
                     }
                 }
@@ -428,7 +252,7 @@ gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                         raise_device_error(a.err, kErrTimeout);
                     __syncwarp();
                 }
-                float *dst = s_scale + s * kChunk * BT + m_first;
+                float *dst = s_scale + s * kChunk * BT + lane;
 #pragma unroll
                 for (int c = 0; c < kChunk; ++c)
 #pragma unroll
@@ -437,12 +261,11 @@ gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                 if (lane == 0) mbar_arrive(&sc_full[s]);
             }
         }
-    } else if (warp >= C::kWarpPromote) {
-        if constexpr (C::kWide) regs_up<216>();
-        const int pw = warp - C::kWarpPromote, q = warp & 3, grp = pw >> 2, pt = threadIdx.x - 32 * C::kWarpPromote;
+    } else if (warp >= kWarpPromote) {
+        const int pw = warp - kWarpPromote, q = warp & 3, grp = pw >> 2, pt = threadIdx.x - 32 * kWarpPromote;
         const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16);
         const int row = q * 32 + (lane >> 2), cl = 2 * (lane & 3);   // of the fragments: rows row + 8 i, columns 8 j + cl, + 1
-        constexpr int kF = C::kCols / 8, kChunk = C::kChunk, kSlots = C::kSlots;
+        constexpr int kF = C::kCols / 8;
         uint32_t it = 0, ch = 0, round = 0;
         auto wait_warp = [&](uint64_t *bar, uint32_t parity) {
             if (!mbar_wait_or_abort(bar, parity, abort) && lane == 0) raise_device_error(a.err, kErrTimeout);
@@ -605,132 +428,79 @@ gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                 ++round;
             }
         }
-    } else if constexpr (C::kWide) {
-        regs_down<40>();                   // the spare warp of the first four
     }
 
     tc_fence_before();
     __syncthreads();
     if (warp == kWarpMma) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols)
-                     : "memory");
+        tmem_free<false>(tmem, C::kTmemCols);
     }
     if (ranks > 1) cluster_barrier();      // no block leaves while another reads its sums
 }
 
 // Host side.
 
-struct Plan8 {
-    int bt, cluster, blocks;
-};
+template <class SC, class F>
+int by_width(int bt, F f) {
+    switch (bt) {
+        case 32: return f(gemm_e4m3_few_kernel<32, SC>, Cfg8<32>());
+        case 64: return f(gemm_e4m3_few_kernel<64, SC>, Cfg8<64>());
+        default: return f(gemm_e4m3_few_kernel<128, SC>, Cfg8<128>());
+    }
+}
 
-template <int BT, class SC>
-const void *kernel_of() { return reinterpret_cast<const void *>(gemm_e4m3_kernel<BT, SC>); }
-
-// Clusters of 2, 4 or 8 blocks that run at once (both scale types take the
-// same registers and shared memory).
+// Both scale types take the same registers and shared memory.
 int clusters_at_once(int bt, int cluster) {
-    static PerContext<int> cache[4][3];
-    const int i = bt == 32 ? 0 : bt == 64 ? 1 : bt == 128 ? 2 : 3, j = cluster == 2 ? 0 : cluster == 4 ? 1 : 2;
+    static PerContext<int> cache[3][3];
+    if (cluster == 1) return num_sms();
     int n = 0;
-    const int rc = cache[i][j].get(&n, [&](int *out) {
-        const void *k = i == 0 ? kernel_of<32, ScaleF32>() : i == 1 ? kernel_of<64, ScaleF32>()
-                      : i == 2 ? kernel_of<128, ScaleF32>() : kernel_of<256, ScaleF32>();
-        const uint32_t smem = i == 0 ? Cfg8<32>::kSmemBytes : i == 1 ? Cfg8<64>::kSmemBytes
-                            : i == 2 ? Cfg8<128>::kSmemBytes : Cfg8<256>::kSmemBytes;
-        set_max_dynamic_smem(k, (int)smem);
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(cluster);
-        cfg.blockDim = dim3(i == 3 ? Cfg8<256>::kThreads : i == 2 ? Cfg8<128>::kThreads : Cfg8<64>::kThreads);
-        cfg.dynamicSmemBytes = smem;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)cluster;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(out, k, &cfg) != cudaSuccess) {
-            cudaGetLastError();
-            return (int)kECuda;
-        }
-        return (int)kOk;
+    const int rc = cache[bt == 32 ? 0 : bt == 64 ? 1 : 2][cluster == 2 ? 0 : cluster == 4 ? 1 : 2].get(&n, [&](int *out) {
+        return by_width<ScaleF32>(bt, [&](auto kernel, auto cfg) {
+            using C = decltype(cfg);
+            return count_clusters(kernel, C::kThreads, C::kSmemBytes, cluster, out);
+        });
     });
     return rc == kOk ? n : 0;
 }
 
-inline Plan8 plan(int M, int I, int O, int experts) {
-    const int P = num_sms(), KB = (I + 127) / 128, NB = (O + 127) / 128;
-    Plan8 p;
+FewPlan plan_few(int M, int I, int O, int experts) {
+    const int KB = (I + 127) / 128, NB = (O + 127) / 128;
     // as wide as the experts' rows would be in even shares, and twice that, as they are not even
     const int filled = std::min(experts, M);
     const long long want = experts == 1 ? M : 2LL * ((M + filled - 1) / filled);
-    p.bt = want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : 256;
-    const double tiles = (double)NB * (experts == 1 ? (M + p.bt - 1) / p.bt : filled + M / p.bt);
-    // cycles of a K step and of one round of the reduction over a cluster
-    const double step = p.bt == 256 ? 600.0 : 500.0, rounds = p.bt >= 64 ? p.bt / 32 : 1;
-    double best = 0;
+    FewPlan best{want <= 32 ? 32 : want <= 64 ? 64 : 128, 1, 0, 0.0};
+    const double tiles = (double)NB * (experts == 1 ? (M + best.bt - 1) / best.bt : filled + M / best.bt);
     for (int c = 1; c <= 8; c *= 2) {
         if (c > 1 && KB < 4 * c) break;
-        const int n = c == 1 ? P : clusters_at_once(p.bt, c);
+        const int n = clusters_at_once(best.bt, c);
         if (n < 1) break;
+        // cycles of a K block and of one round of the reduction over a cluster
+        const double step = best.bt == 128 ? 900.0 : best.bt == 64 ? 700.0 : 600.0, rounds = best.bt / 32;
         const double waves = std::ceil(tiles / n);
         const double cost = waves * (((KB + c - 1) / c) * step + (c > 1 ? 1500.0 * rounds : 0.0) + 1500.0);
-        if (c == 1 || cost < best) {
-            best = cost;
-            p.cluster = c;
-            p.blocks = n * c;
-        }
+        if (c == 1 || cost < best.cost) best = FewPlan{best.bt, c, n * c, cost};
     }
-    return p;
-}
-
-inline bool encode_map(CUtensorMap *m, const void *p, long long rows, int I, int box_rows) {
-    const cuuint64_t dims[2] = {(cuuint64_t)I, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)I};
-    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
-    const cuuint32_t es[2] = {1, 1};
-    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p), dims, strides, box, es,
-                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-template <int BT, class SC>
-int launch(const char *what, const Plan8 &p, const CUtensorMap &w, const CUtensorMap &x, const Args8 &a, cudaStream_t st) {
-    using C = Cfg8<BT>;
-    set_max_dynamic_smem(reinterpret_cast<const void *>(gemm_e4m3_kernel<BT, SC>), (int)C::kSmemBytes);
-    return launch_clusters(what, gemm_e4m3_kernel<BT, SC>, p.blocks, C::kThreads, p.cluster, C::kSmemBytes, st, w, x, a);
+    return best;
 }
 
 template <class SC>
-int launch_bt(const char *what, const Plan8 &p, const CUtensorMap &w, const CUtensorMap &x, const Args8 &a, cudaStream_t st) {
-    switch (p.bt) {
-        case 32: return launch<32, SC>(what, p, w, x, a, st);
-        case 64: return launch<64, SC>(what, p, w, x, a, st);
-        case 128: return launch<128, SC>(what, p, w, x, a, st);
-        default: return launch<256, SC>(what, p, w, x, a, st);
-    }
+int launch_few_as(const char *what, const FewPlan &p, const CUtensorMap &w, const CUtensorMap &x, const Args8 &a,
+                  cudaStream_t st) {
+    return by_width<SC>(p.bt, [&](auto kernel, auto cfg) {
+        using C = decltype(cfg);
+        set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), (int)C::kSmemBytes);
+        return launch_clusters(what, kernel, p.blocks, C::kThreads, p.cluster, C::kSmemBytes, st, w, x, a);
+    });
+}
+
+int launch_few(const char *what, const FewPlan &p, const E4m3Args &g, Args8 a, cudaStream_t st) {
+    CUtensorMap w, x;
+    if (!encode_map(&w, g.w, (long long)g.experts * g.O, g.I, 128) || !encode_map(&x, g.X, g.M, g.I, p.bt))
+        QG_REFUSE(kECuda, "%s: tensor map refused", what);
+    a.NT = a.NB;
+    return g.w_power ? launch_few_as<ScaleE8M0>(what, p, w, x, a, st) : launch_few_as<ScaleF32>(what, p, w, x, a, st);
 }
 
 }  // namespace e8
-
-bool gemm_e4m3_tc_takes(const E4m3Args &a) {
-    const long long wrows = (long long)a.experts * a.O;
-    const long long tiles = ((long long)a.M / 32 + a.experts) * ((a.O + 127) / 128);
-    return a.I % 16 == 0 && (uintptr_t)a.X % 16 == 0 && (uintptr_t)a.w % 16 == 0 && a.experts <= e8::kMaxExperts &&
-           wrows < (1ll << 31) - 256 && tiles < (1ll << 31) - 65536;
-}
-
-int run_gemm_e4m3_tc(const E4m3Args &g, cudaStream_t st) {
-    const char *what = g.offsets ? "qgemm_e4m3_moe" : "qgemm_e4m3";
-    if (!tc::encode_fn()) QG_REFUSE(kECuda, "%s: cuTensorMapEncodeTiled is not available from the driver", what);
-    const e8::Plan8 p = e8::plan(g.M, g.I, g.O, g.experts);
-    CUtensorMap w, x;
-    if (!e8::encode_map(&w, g.w, (long long)g.experts * g.O, g.I, 128) || !e8::encode_map(&x, g.X, g.M, g.I, p.bt < 64 ? p.bt : 64))
-        QG_REFUSE(kECuda, "%s: tensor map refused", what);
-    const e8::Args8 a{g.Y, g.y_type, g.x_scale, g.w_scale, g.offsets, g.experts, g.M, g.O,
-                      (g.I + 127) / 128, (g.O + 127) / 128, g.err};
-    return g.w_power ? e8::launch_bt<ScaleE8M0>(what, p, w, x, a, st) : e8::launch_bt<ScaleF32>(what, p, w, x, a, st);
-}
-
 }  // namespace qg

@@ -1,0 +1,419 @@
+// gemm_e4m3_many.cu -- products of e4m3 activations with e4m3 weights, many
+// tokens an expert: the tensor cores and what feeds and empties them bound it.
+//
+// A tile is 128 tokens a block (MMA M) by 256 outputs (two halves of N = 128,
+// a weight scale each), so a promoting thread holds one token and scales a
+// half's sums by one factor.  (With the tokens along N a factor a column has
+// to be read from shared memory: 64 columns then take a warp 290 cycles
+// instead of 134, and a K block 1800 instead of the MMAs' 512.)  PAIR: two
+// blocks of a cluster share one MMA, 256 tokens by the same 256 outputs; each
+// brings its tokens and half of the weights, 32 KB a K block instead of 48.
+// One persistent thread block per SM:
+//   warps 0, 1   TMA producers, a thread each, K blocks in turn: 128 x 128
+//                codes of X and the block's part of 256 x 128 of W, 128-byte
+//                swizzled
+//   warps 2..5   (of the first block) issue the MMAs, a thread each: every
+//                second K block of one half; its four leave the half's sums
+//                in one of four buffers
+//   warps 6, 7   the scales' products, kChunk K blocks at a time
+//   warps 8..15  promote: tensor-memory lanes 32 (w % 4) .. + 31, 64 columns
+//                of each half
+#include "gemm_e4m3_tc.cuh"
+
+namespace qg {
+namespace e8 {
+namespace {
+
+constexpr int kChunk = 4, kSlots = 2;  // K blocks of one slot of scales
+constexpr int kWarpIssue = 2, kWarpScale = 6, kWarpPromote = 8, kWarps = 8, kThreads = 32 * (kWarpPromote + kWarps);
+constexpr int kBufs = 4;               // tensor-memory buffers of 128 columns
+constexpr int kOutStride = 80;         // bytes between the tokens (64 each) of a strip on its way out: eight lanes' 16 bytes meet no bank twice
+
+template <bool PAIR>
+struct CfgMany {
+    static constexpr int kCtas = PAIR ? 2 : 1;
+    static constexpr int kTokens = 128 * kCtas;                    // of a tile
+    static constexpr int kBoxRows = 128 / kCtas;                   // outputs of one TMA box of W: this block's part of a half
+    static constexpr uint32_t kXBytes = 128 * 128, kBoxBytes = kBoxRows * 128;
+    static constexpr uint32_t kStageBytes = kXBytes + 2 * kBoxBytes;
+    static constexpr uint32_t kScaleBytes = kSlots * kChunk * 256 * 4;
+    static constexpr uint32_t kOutAll = kWarps * 16 * kOutStride;   // strips of 16 tokens
+    static constexpr uint32_t kBarBytes = 256;
+    static constexpr int kStages = (int)((kSmemBudget - 1024 - 256 - kScaleBytes - kOutAll - kTableBytes - kBarBytes) / kStageBytes);
+    static constexpr int kNumBars = 2 * kStages + 2 * kBufs + 2 * kSlots;
+    static constexpr uint32_t kScaleOff = kStages * kStageBytes;
+    static constexpr uint32_t kOutOff = kScaleOff + kScaleBytes;
+    static constexpr uint32_t kBarOff = kOutOff + kOutAll;
+    static constexpr uint32_t kTableOff = kBarOff + kBarBytes;
+    static constexpr uint32_t kSmemBytes = 1024 + kTableOff + kTableBytes;
+    static_assert(kStages >= 3 && kNumBars * 8 + 16 <= (int)kBarBytes, "");
+    // A wait tells one phase of a barrier from the next, not from the one
+    // after that, so a stage must always be the same threads': with an odd
+    // number of stages one thread could pass on a phase that the other had
+    // not seen begin.
+    static_assert(kStages % 2 == 0 && kBufs == 4, "a stage and a buffer belong to the same producer and issuers every time");
+};
+
+// 64 columns of this warp's 32 lanes, to be read after landed() on the same registers.
+struct Sums {
+    uint32_t r[64];
+};
+#define QG_R16(n) "%" #n "0, %" #n "1, %" #n "2, %" #n "3, %" #n "4, %" #n "5, %" #n "6, %" #n "7, %" #n "8, %" #n "9"
+__device__ __forceinline__ void load(uint32_t taddr, Sums &s) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, " QG_R16(1) ", " QG_R16(2) ", " QG_R16(3) ", " QG_R16(4) ", " QG_R16(5)
+        ", %60, %61, %62, %63}, [%64];"
+        : "=r"(s.r[0]), "=r"(s.r[1]), "=r"(s.r[2]), "=r"(s.r[3]), "=r"(s.r[4]), "=r"(s.r[5]), "=r"(s.r[6]),
+          "=r"(s.r[7]), "=r"(s.r[8]), "=r"(s.r[9]), "=r"(s.r[10]), "=r"(s.r[11]), "=r"(s.r[12]), "=r"(s.r[13]),
+          "=r"(s.r[14]), "=r"(s.r[15]), "=r"(s.r[16]), "=r"(s.r[17]), "=r"(s.r[18]), "=r"(s.r[19]), "=r"(s.r[20]),
+          "=r"(s.r[21]), "=r"(s.r[22]), "=r"(s.r[23]), "=r"(s.r[24]), "=r"(s.r[25]), "=r"(s.r[26]), "=r"(s.r[27]),
+          "=r"(s.r[28]), "=r"(s.r[29]), "=r"(s.r[30]), "=r"(s.r[31]), "=r"(s.r[32]), "=r"(s.r[33]), "=r"(s.r[34]),
+          "=r"(s.r[35]), "=r"(s.r[36]), "=r"(s.r[37]), "=r"(s.r[38]), "=r"(s.r[39]), "=r"(s.r[40]), "=r"(s.r[41]),
+          "=r"(s.r[42]), "=r"(s.r[43]), "=r"(s.r[44]), "=r"(s.r[45]), "=r"(s.r[46]), "=r"(s.r[47]), "=r"(s.r[48]),
+          "=r"(s.r[49]), "=r"(s.r[50]), "=r"(s.r[51]), "=r"(s.r[52]), "=r"(s.r[53]), "=r"(s.r[54]), "=r"(s.r[55]),
+          "=r"(s.r[56]), "=r"(s.r[57]), "=r"(s.r[58]), "=r"(s.r[59]), "=r"(s.r[60]), "=r"(s.r[61]), "=r"(s.r[62]),
+          "=r"(s.r[63])
+        : "r"(taddr));
+}
+#undef QG_R16
+// Sixteen registers pass through, so that nothing reads them before.
+__device__ __forceinline__ void pass(uint32_t *r) {
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void landed(Sums &s) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    pass(s.r);
+    pass(s.r + 16);
+    pass(s.r + 32);
+    pass(s.r + 48);
+}
+
+template <bool PAIR, class SC>
+__global__ void __launch_bounds__(kThreads, 1)
+gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Args8 a) {
+    using C = CfgMany<PAIR>;
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t raw_base = smem_addr(smem_raw);
+    unsigned char *smem = smem_raw + ((1024u - (raw_base & 1023u)) & 1023u);
+    const uint32_t sbase = smem_addr(smem);
+    float *s_scale = reinterpret_cast<float *>(smem + C::kScaleOff);      // [slot][K block][half][token]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kBarOff);
+    uint64_t *full = bars, *empty = full + C::kStages, *acc_full = empty + C::kStages, *acc_empty = acc_full + kBufs,
+             *sc_full = acc_empty + kBufs, *sc_empty = sc_full + kSlots;
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(bars + C::kNumBars);
+    volatile uint32_t *abort = tmem_slot + 1;
+    int *s_tile = reinterpret_cast<int *>(smem + C::kTableOff), *s_row = s_tile + kMaxExperts + 2;
+    __shared__ int2 s_warp[kThreads / 32];
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int side = (int)(blockIdx.x % C::kCtas);                        // of the two blocks of an MMA (their rank in the cluster)
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 2);
+        }
+        for (int b = 0; b < kBufs; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], C::kCtas * kWarps);
+        }
+        for (int b = 0; b < kSlots; ++b) {
+            mbar_init(&sc_full[b], kWarpPromote - kWarpScale);
+            mbar_init(&sc_empty[b], kWarps);
+        }
+        *abort = 0u;
+        mbar_fence_init();
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmW)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmX)) : "memory");
+    }
+    if (warp == kWarpIssue) {
+        __syncwarp();
+        tmem_alloc<PAIR>(tmem_slot, kBufs * 128);
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    build_tables<C::kTokens, kThreads>(a, s_tile, s_row, s_warp);
+    tc_fence_before();
+    __syncthreads();
+    if (PAIR) cluster_barrier();           // the other block's barriers are there
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int tiles = s_tile[a.experts] * a.NT, first = blockIdx.x / C::kCtas, step = gridDim.x / C::kCtas;
+
+    // 512 threads start with 128 registers each, 65536 in all, of which the
+    // promoting warps take 8 x 32 x 216 and the others 8 x 32 x 40.
+    if (warp < kWarpPromote) {
+        regs_down<40>();
+        if (warp < kWarpIssue) {
+            if (lane == 0) {
+                uint32_t it = 0;
+                for (int t = first; t < tiles; t += step) {
+                    const Tile L = find_tile<C::kTokens>(a, s_tile, s_row, t);
+                    const int m0 = L.m0 + side * 128;
+                    const int wrow = L.e * a.O + L.ot * 256 + side * C::kBoxRows;
+                    for (int k = 0; k < a.KB; ++k, ++it) {
+                        if ((it & 1u) != (uint32_t)warp) continue;
+                        const uint32_t s = it % C::kStages, r = it / C::kStages;
+                        if (r > 0 && !mbar_wait_or_abort(&empty[s], (r & 1) ^ 1, abort))
+                            raise_device_error(a.err, kErrTimeout);
+                        const uint32_t st = sbase + s * C::kStageBytes;
+                        if (side == 0) mbar_arrive_expect_tx(&full[s], C::kCtas * C::kStageBytes);
+                        const uint32_t bar = PAIR ? map_rank(smem_addr(&full[s]), 0) : smem_addr(&full[s]);
+                        load_tile<PAIR>(st, &tmX, k * 128, m0, bar);
+                        for (int h = 0; h < 2; ++h)
+                            load_tile<PAIR>(st + C::kXBytes + h * C::kBoxBytes, &tmW, k * 128, wrow + h * 128, bar);
+                    }
+                }
+                // Every copy issued must have landed, and every arrival that is
+                // on its way to this block, before the block exits.
+                for (uint32_t j = it > (uint32_t)C::kStages ? it - C::kStages : 0; j < it; ++j) {
+                    const uint32_t s = j % C::kStages, r = j / C::kStages;
+                    if ((j & 1u) != (uint32_t)warp) continue;
+                    if (side == 0 && !mbar_wait(&full[s], r & 1)) raise_device_error(a.err, kErrTimeout);
+                    if (PAIR && !mbar_wait_or_abort(&empty[s], r & 1, abort)) raise_device_error(a.err, kErrTimeout);
+                }
+            }
+        } else if (warp < kWarpScale) {
+            // No half's sums depend on another's, so four threads issue them in
+            // turn: each one's waits and commits pass while the others' MMAs run.
+            if (lane == 0 && side == 0) {
+                uint32_t it = 0;
+                const uint32_t odd = (warp - kWarpIssue) & 1, idesc = idesc_e4m3(kMmaM * C::kCtas, 128);
+                const int h = (warp - kWarpIssue) >> 1;
+                const uint32_t b = 2 * odd + h;          // this thread's buffer
+                for (int t = first; t < tiles; t += step) {
+                    for (int k = 0; k < a.KB; ++k, ++it) {
+                        if ((it & 1u) != odd) continue;
+                        const uint32_t s = it % C::kStages, r = it / C::kStages, st = sbase + s * C::kStageBytes;
+                        const uint32_t rb = it / 2, wa = st + C::kXBytes + h * C::kBoxBytes;
+                        if (rb > 0 && !mbar_wait_or_abort(&acc_empty[b], (rb & 1) ^ 1, abort))
+                            raise_device_error(a.err, kErrTimeout);
+                        if (!mbar_wait_or_abort(&full[s], r & 1, abort)) raise_device_error(a.err, kErrTimeout);
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_e4m3<PAIR>(tmem + b * 128, sw128_desc(st + kk * 32), sw128_desc(wa + kk * 32), idesc,
+                                           kk > 0 ? 1u : 0u);
+                        commit_to<PAIR>(&acc_full[b], 3);
+                        commit_to<PAIR>(&empty[s], 3);
+                    }
+                }
+            }
+        } else {
+            const int tok = (warp - kWarpScale) * 64 + lane, m = side * 128 + tok;   // and tok + 32
+            uint32_t ch = 0;
+            for (int t = first; t < tiles; t += step) {
+                const Tile L = find_tile<C::kTokens>(a, s_tile, s_row, t);
+                const typename SC::T *ws = static_cast<const typename SC::T *>(a.ws) + ((size_t)L.e * a.NB + 2 * L.ot) * a.KB;
+                const float *xs = a.xs + (size_t)(L.m0 + m) * a.KB;
+                const bool two = 2 * L.ot + 1 < a.NB, here = m < L.rows, here2 = m + 32 < L.rows;
+                for (int k = 0; k < a.KB; k += kChunk, ++ch) {
+                    const uint32_t s = ch % kSlots, r = ch / kSlots;
+                    float v[2][kChunk], w[2][kChunk];
+#pragma unroll
+                    for (int c = 0; c < kChunk; ++c) {
+                        const bool in = k + c < a.KB;
+                        v[0][c] = in && here ? xs[k + c] : 0.f;
+                        v[1][c] = in && here2 ? xs[(size_t)32 * a.KB + k + c] : 0.f;
+                        w[0][c] = in ? SC::get(ws, k + c) : 0.f;
+                        w[1][c] = in && two ? SC::get(ws, (size_t)a.KB + k + c) : 0.f;
+                    }
+                    if (r > 0) {
+                        if (!mbar_wait_or_abort(&sc_empty[s], (r & 1) ^ 1, abort) && lane == 0)
+                            raise_device_error(a.err, kErrTimeout);
+                        __syncwarp();
+                    }
+                    float *dst = s_scale + s * kChunk * 256 + tok;
+#pragma unroll
+                    for (int c = 0; c < kChunk; ++c) {
+                        dst[c * 256] = v[0][c] * w[0][c];
+                        dst[c * 256 + 32] = v[1][c] * w[0][c];
+                        dst[c * 256 + 128] = v[0][c] * w[1][c];
+                        dst[c * 256 + 160] = v[1][c] * w[1][c];
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sc_full[s]);
+                }
+            }
+        }
+    } else {
+        regs_up<216>();
+        const int pw = warp - kWarpPromote, q = warp & 3, grp = pw >> 2, row = q * 32 + lane;
+        const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16) + grp * 64;
+        uint32_t buf = 0, ch = 0;
+        auto wait_warp = [&](uint64_t *bar, uint32_t parity) {
+            // every lane: with one lane's wait and a vote the warp goes on 170 cycles later
+            if (!mbar_wait_or_abort(bar, parity, abort) && lane == 0) raise_device_error(a.err, kErrTimeout);
+            __syncwarp();
+        };
+        uint64_t acc[2][32];               // token `row`, columns 64 grp .. + 63 of each half, in pairs
+        auto promote = [&](auto half, const float *f) {
+            constexpr int h = decltype(half)::value;
+            const uint32_t b = buf % kBufs;
+            wait_warp(&acc_full[b], (buf / kBufs) & 1);
+            tc_fence_after();
+            Sums s;
+            load(tq + b * 128, s);
+            const float fv = f[h * 128];
+            landed(s);
+            // the sums are in registers: the next MMAs may have the buffer
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (PAIR) signal_remote(map_rank(smem_addr(&acc_empty[b]), 0));
+                else mbar_arrive(&acc_empty[b]);
+            }
+            const uint64_t f2 = f32_pair(fv, fv);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) fma2(acc[h][j], s.r[2 * j], s.r[2 * j + 1], f2);
+            ++buf;
+        };
+        auto tile_sums = [&]() {
+            for (int k = 0; k < a.KB; ++k) {
+                const int c = k % kChunk;
+                if (c == 0) wait_warp(&sc_full[ch % kSlots], (ch / kSlots) & 1);
+                const float *f = s_scale + ((ch % kSlots) * kChunk + c) * 256 + row;
+                promote(std::integral_constant<int, 0>(), f);
+                promote(std::integral_constant<int, 1>(), f);
+                if (c == kChunk - 1 || k + 1 == a.KB) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sc_empty[ch % kSlots]);
+                    ++ch;
+                }
+            }
+        };
+        unsigned char *strip = smem + C::kOutOff + pw * 16 * kOutStride;
+        const int esz = a.y_type == kF32 ? 4 : 2, per16 = 16 / esz;
+        const bool lines = a.O % per16 == 0 && reinterpret_cast<uintptr_t>(a.Y) % 16 == 0;
+        // 64 bytes a token through shared memory, so that four lanes store a token's.
+        auto store_strip = [&](const uint32_t (&w)[16], const Tile &L, int o) {
+            const int part = lane & 3, at = o + part * per16;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (lane >> 4 == x) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint4 *>(strip + (lane & 15) * kOutStride + 16 * i) =
+                            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int tok = 8 * i + (lane >> 2), m = side * 128 + q * 32 + 16 * x + tok;
+                    const uint4 v = *reinterpret_cast<const uint4 *>(strip + tok * kOutStride + 16 * part);
+                    if (m >= L.rows || at >= a.O) continue;
+                    unsigned char *y = static_cast<unsigned char *>(a.Y) + ((size_t)(L.m0 + m) * a.O + at) * esz;
+                    if (lines) {
+                        *reinterpret_cast<uint4 *>(y) = v;
+                        continue;
+                    }
+                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                    if (esz == 4) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (at + e < a.O) reinterpret_cast<uint32_t *>(y)[e] = u[e];
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (at + e < a.O) reinterpret_cast<uint16_t *>(y)[e] = (uint16_t)(u[e >> 1] >> (16 * (e & 1)));
+                    }
+                }
+                __syncwarp();
+            }
+        };
+        for (int t = first; t < tiles; t += step) {
+            const Tile L = find_tile<C::kTokens>(a, s_tile, s_row, t);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[0][j] = acc[1][j] = 0;
+            tile_sums();
+            if (side * 128 + q * 32 >= L.rows) continue;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int o = L.ot * 256 + h * 128 + grp * 64;
+                if (o >= a.O) continue;
+                uint32_t w[16];
+                if (a.y_type == kF32) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            w[2 * j] = (uint32_t)acc[h][8 * x + j];
+                            w[2 * j + 1] = (uint32_t)(acc[h][8 * x + j] >> 32);
+                        }
+                        store_strip(w, L, o + 16 * x);
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float2 v = pair_of(acc[h][16 * x + j]);
+                            w[j] = pack_16(a.y_type, v.x, v.y);
+                        }
+                        store_strip(w, L, o + 32 * x);
+                    }
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpIssue) {
+        tc_fence_after();
+        tmem_free<PAIR>(tmem, kBufs * 128);
+    }
+    if (PAIR) cluster_barrier();           // no block leaves while the other may still reach it
+}
+
+int pairs_at_once() {
+    static PerContext<int> cache;
+    int n = 0;
+    const int rc = cache.get(&n, [&](int *out) {
+        return count_clusters(gemm_e4m3_many_kernel<true, ScaleF32>, kThreads, CfgMany<true>::kSmemBytes, 2, out);
+    });
+    return rc == kOk ? n : 0;
+}
+
+template <bool PAIR, class SC>
+int launch_as(const char *what, int blocks, const CUtensorMap &w, const CUtensorMap &x, const Args8 &a, cudaStream_t st) {
+    using C = CfgMany<PAIR>;
+    set_max_dynamic_smem(reinterpret_cast<const void *>(gemm_e4m3_many_kernel<PAIR, SC>), (int)C::kSmemBytes);
+    return launch_clusters(what, gemm_e4m3_many_kernel<PAIR, SC>, blocks, kThreads, C::kCtas, C::kSmemBytes, st, w, x, a);
+}
+
+}  // namespace
+
+ManyPlan plan_many(int M, int I, int O, int experts) {
+    const int KB = (I + 127) / 128, NT = (O + 255) / 256, filled = std::min(experts, M);
+    ManyPlan best{false, num_sms(), 0.0};
+    for (int pair = 0; pair <= 1; ++pair) {
+        const int tokens = 128 * (pair + 1), n = pair ? pairs_at_once() : num_sms();
+        if (n < 1) break;
+        // an expert's last tile is half empty
+        const double tiles = (double)NT * (experts == 1 ? (M + tokens - 1) / tokens : (double)M / tokens + 0.5 * filled);
+        const double cost = std::max(1.0, experts == 1 ? std::ceil(tiles / n) : tiles / n + 0.5) * (KB * (pair ? 700.0 : 900.0) + 3000.0);
+        if (!pair || cost < best.cost) best = ManyPlan{pair != 0, n * (pair + 1), cost};
+    }
+    return best;
+}
+
+int launch_many(const char *what, const ManyPlan &p, const E4m3Args &g, Args8 a, cudaStream_t st) {
+    CUtensorMap w, x;
+    if (!encode_map(&w, g.w, (long long)g.experts * g.O, g.I, p.pair ? CfgMany<true>::kBoxRows : CfgMany<false>::kBoxRows) ||
+        !encode_map(&x, g.X, g.M, g.I, 128))
+        QG_REFUSE(kECuda, "%s: tensor map refused", what);
+    a.NT = (a.NB + 1) / 2;
+    if (p.pair)
+        return g.w_power ? launch_as<true, ScaleE8M0>(what, p.blocks, w, x, a, st)
+                         : launch_as<true, ScaleF32>(what, p.blocks, w, x, a, st);
+    return g.w_power ? launch_as<false, ScaleE8M0>(what, p.blocks, w, x, a, st)
+                     : launch_as<false, ScaleF32>(what, p.blocks, w, x, a, st);
+}
+
+}  // namespace e8
+}  // namespace qg

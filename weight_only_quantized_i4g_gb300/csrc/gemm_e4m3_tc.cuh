@@ -1,0 +1,303 @@
+// gemm_e4m3_tc.cuh -- what the tensor-core kernels of the e4m3 x e4m3 products
+// share (tcgen05 kind::f8f6f4, f32 accumulators in tensor memory):
+//
+//   Y[m, o] = sum_b xs[m, b] ws[o/128, b] sum_{i in block b} X[m, i] W[o, i]
+//
+// A K step is one block of 128 elements: four MMAs of K = 32 leave the
+// block's sums in a buffer of tensor memory, and "promoting" warps add them,
+// times the two scales, to f32 sums in registers.  gemm_e4m3_few.cu has the
+// tokens along the MMA's N (as few as sixteen: decode), gemm_e4m3_many.cu
+// along its M (prompts).
+#pragma once
+
+#include "gemm_tc.cuh"
+#include "moe.cuh"
+
+namespace qg {
+namespace e8 {
+
+using namespace tc;
+
+constexpr int kWarpMma2 = 2;           // a second issuing warp: they take the stages in turn
+constexpr int kMaxExperts = 1024;      // the tables of tiles and rows in shared memory
+constexpr uint32_t kTableBytes = (3 * kMaxExperts + 2) * 4;   // first tiles [E + 1], first and last rows [E][2]
+
+struct Args8 {
+    void *Y;
+    int y_type;
+    const float *xs;
+    const void *ws;
+    const int *offsets;               // NULL: one expert, rows [0, M)
+    int experts, M, O, KB, NB, NT;    // K blocks, 128-output blocks, output tiles
+    int *err;
+};
+
+// Instruction descriptor of kind::f8f6f4: f32 accumulator, e4m3 A and B (format code 0), K-major, M = m, N = n.
+__device__ __forceinline__ uint32_t idesc_e4m3(int m, int n) {
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+// PAIR: one MMA of two blocks; their A rows make M = 256, and each holds half of B's rows.
+template <bool PAIR>
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+// Arrive on `bar` (PAIR: on both blocks' barriers of that place) once every MMA this thread has issued is done.
+template <bool PAIR>
+__device__ __forceinline__ void commit_to(uint64_t *bar, uint16_t both) {
+    if constexpr (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_addr(bar)),
+            "h"(both)
+            : "memory");
+    else
+        mma_commit(bar);
+}
+// PAIR: the copy counts on the first block's barrier (`bar`: its cluster address).
+template <bool PAIR>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+            "[%1, {%2, %3}], [%4];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+            "[%4];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+            : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void tmem_alloc(volatile uint32_t *slot, uint32_t cols) {
+    if constexpr (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr((const void *)slot)),
+                     "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr((const void *)slot)),
+                     "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+}
+template <bool PAIR>
+__device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
+    if constexpr (PAIR)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
+}
+
+// a += (lo, hi) * f, two f32 at a time
+__device__ __forceinline__ void fma2(uint64_t &a, uint32_t lo, uint32_t hi, uint64_t f) {
+    asm("{.reg .b64 t; mov.b64 t, {%1, %2}; fma.rn.f32x2 %0, t, %3, %0;}" : "+l"(a) : "r"(lo), "r"(hi), "l"(f));
+}
+__device__ __forceinline__ float2 pair_of(uint64_t v) {
+    return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Cluster helpers: the address of a local shared variable in another block, arrivals there, loads from there.
+__device__ __forceinline__ uint32_t map_rank(uint32_t local, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// An arrival that publishes no memory (tensor memory has its own fences).  The
+// release and acquire of the whole cluster, which it spares, took a K step
+// of a block pair from 1600 to 2700 cycles.
+__device__ __forceinline__ void signal_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ float load_remote(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile uint32_t *abort) {
+    const uint32_t a = smem_addr(bar);
+    for (uint32_t it = 0; it < kSpinLimit; ++it) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(a), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if ((it & 255u) == 255u && *abort) return false;
+    }
+    *abort = 1u;
+    return false;
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+__device__ __forceinline__ void store_y(const Args8 &a, size_t at, float v) {
+    if (a.y_type == kF32) static_cast<float *>(a.Y)[at] = v;
+    else if (a.y_type == kBf16) static_cast<uint16_t *>(a.Y)[at] = Elem<kBf16>::put(v);
+    else static_cast<uint16_t *>(a.Y)[at] = Elem<kF16>::put(v);
+}
+
+// Tables of the experts' first tiles (of BT tokens) and rows; ends with the
+// writes of every thread, before a barrier.
+template <int BT, int kThreads>
+__device__ __forceinline__ void build_tables(const Args8 &a, int *s_tile, int *s_row, int2 *s_warp) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (a.offsets == nullptr) {
+        if (threadIdx.x == 0) {
+            s_tile[0] = 0;
+            s_tile[1] = (a.M + BT - 1) / BT;
+            s_row[0] = 0;
+            s_row[1] = a.M;
+        }
+    } else {
+        // Row bounds held to [0, M] and to their order (a table that is
+        // neither raises the error word): expert e has rows most[e] to
+        // most[e+1] of the running maximum.
+        int tiles_before = 0, most = min(max(a.offsets[0], 0), a.M);
+        for (int e0 = 0; e0 < a.experts; e0 += kThreads) {
+            const int e = e0 + threadIdx.x;
+            int to = 0;
+            if (e < a.experts) {
+                const int lo = a.offsets[e], hi = a.offsets[e + 1];
+                if ((lo < 0 || hi < lo || hi > a.M) && blockIdx.x == 0) raise_device_error(a.err, kErrExpert);
+                to = min(max(hi, 0), a.M);
+            }
+            int top = to;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, top, d);
+                if (lane >= d) top = max(top, y);
+            }
+            if (lane == 31) s_warp[warp].x = top;
+            __syncthreads();
+            int below = most;
+            for (int w = 0; w < kThreads / 32; ++w) {
+                if (w < warp) below = max(below, s_warp[w].x);
+                most = max(most, s_warp[w].x);
+            }
+            int from = __shfl_up_sync(0xffffffffu, top, 1);
+            from = lane == 0 ? below : max(from, below);
+            to = max(top, below);
+            const int n = e < a.experts ? (to - from + BT - 1) / BT : 0;
+            int x = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, d);
+                if (lane >= d) x += y;
+            }
+            if (lane == 31) s_warp[warp].y = x;
+            __syncthreads();
+            int before = tiles_before;
+            for (int w = 0; w < kThreads / 32; ++w) {
+                before += w < warp ? s_warp[w].y : 0;
+                tiles_before += s_warp[w].y;
+            }
+            if (e < a.experts) {
+                s_tile[e] = before + x - n;
+                s_row[2 * e] = from;
+                s_row[2 * e + 1] = to;
+            }
+            __syncthreads();
+        }
+        if (threadIdx.x == 0) s_tile[a.experts] = tiles_before;
+    }
+}
+
+struct Tile {
+    int e, m0, rows, ot;              // expert, first row, its rows in the tile, output tile
+};
+// Tiles are numbered expert by expert, output tile by output tile, tokens
+// fastest: blocks of one wave share weights.
+template <int BT>
+__device__ __forceinline__ Tile find_tile(const Args8 &a, const int *s_tile, const int *s_row, int t) {
+    int lo = 0, hi = a.experts;       // the last e with s_tile[e] * NT <= t
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_tile[mid] * a.NT <= t) lo = mid;
+        else hi = mid;
+    }
+    const int nt = s_tile[lo + 1] - s_tile[lo], local = t - s_tile[lo] * a.NT;
+    Tile r;
+    r.e = lo;
+    r.ot = local / nt;
+    r.m0 = s_row[2 * lo] + (local - r.ot * nt) * BT;
+    r.rows = min(s_row[2 * lo + 1] - r.m0, BT);
+    return r;
+}
+
+// Host side: a map of [rows][I] codes in 128-byte swizzled boxes of box_rows x 128.
+inline bool encode_map(CUtensorMap *m, const void *p, long long rows, int I, int box_rows) {
+    const cuuint64_t dims[2] = {(cuuint64_t)I, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)I};
+    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    const cuuint32_t es[2] = {1, 1};
+    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p), dims, strides, box, es,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Clusters of `cluster` blocks of this kernel that run at once.
+template <class K>
+inline int count_clusters(K kernel, int threads, uint32_t smem, int cluster, int *out) {
+    set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), (int)smem);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cluster);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(out, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return kECuda;
+    }
+    return kOk;
+}
+
+// The two kernels.  `cost` receives an estimate of the call's cycles.
+struct FewPlan {
+    int bt, cluster, blocks;
+    double cost;
+};
+struct ManyPlan {
+    bool pair;
+    int blocks;
+    double cost;
+};
+FewPlan plan_few(int M, int I, int O, int experts);
+ManyPlan plan_many(int M, int I, int O, int experts);
+int launch_few(const char *what, const FewPlan &p, const E4m3Args &g, Args8 a, cudaStream_t st);
+int launch_many(const char *what, const ManyPlan &p, const E4m3Args &g, Args8 a, cudaStream_t st);
+
+}  // namespace e8
+}  // namespace qg

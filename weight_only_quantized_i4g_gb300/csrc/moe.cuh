@@ -64,10 +64,6 @@ struct E4m3Args {
 };
 size_t ws_gemm_e4m3(int M, int I, int O, int experts);
 int run_gemm_e4m3(const E4m3Args &a, void *ws, cudaStream_t st);
-// The tensor-core kernel, and whether a call's sizes and addresses suit it.
-bool gemm_e4m3_tc_takes(const E4m3Args &a);
-int run_gemm_e4m3_tc(const E4m3Args &a, cudaStream_t st);
-
 // Rows [*from, *to) of group g; a table that decreases or passes M is held
 // to the rows that are there, and the thread that asks with err != NULL
 // raises the error word.
