@@ -215,14 +215,12 @@ gemm_e4m3_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
                         raise_device_error(a.err, kErrTimeout);
                     if (!mbar_wait_or_abort(&full[s], r & 1, abort)) raise_device_error(a.err, kErrTimeout);
                     tc_fence_after();
+                    const uint32_t w_lo = desc_lo(sbase) + s * (C::kStageBytes >> 4);
 #pragma unroll
                     for (int j = 0; j < C::kBlocks; ++j) {
                         if (j >= n) break;
-                        const uint32_t st = sbase + s * C::kStageBytes + j * C::kBlockBytes;
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_e4m3<false>(tmem + b * C::kBufCols + j * BT, sw128_desc(st + kk * 32),
-                                     sw128_desc(st + kWBytes + kk * 32), idesc, kk > 0 ? 1u : 0u);
+                        mma_block<false>(tmem + b * C::kBufCols + j * BT, w_lo + j * (C::kBlockBytes >> 4),
+                                         w_lo + (j * C::kBlockBytes + kWBytes) / 16, idesc);
                     }
                     mma_commit(&acc_full[b]);
                     mma_commit(&empty[s]);
@@ -470,13 +468,15 @@ FewPlan plan_few(int M, int I, int O, int experts) {
     const int filled = std::min(experts, M);
     const long long want = experts == 1 ? M : 2LL * ((M + filled - 1) / filled);
     FewPlan best{want <= 32 ? 32 : want <= 64 ? 64 : 128, 1, 0, 0.0};
-    const double tiles = (double)NB * (experts == 1 ? (M + best.bt - 1) / best.bt : filled + M / best.bt);
+    const double tiles = NB * token_tiles(M, experts, best.bt);
     for (int c = 1; c <= 8; c *= 2) {
         if (c > 1 && KB < 4 * c) break;
         const int n = clusters_at_once(best.bt, c);
         if (n < 1) break;
-        // cycles of a K block and of one round of the reduction over a cluster
-        const double step = best.bt == 128 ? 900.0 : best.bt == 64 ? 700.0 : 600.0, rounds = best.bt / 32;
+        // cycles of a K block, as measured (32 tokens: what 16 KB of weights
+        // take an SM at the card's bandwidth), and of one round of the
+        // reduction over a cluster
+        const double step = best.bt == 128 ? 1370.0 : best.bt == 64 ? 800.0 : 700.0, rounds = best.bt / 32;
         const double waves = std::ceil(tiles / n);
         const double cost = waves * (((KB + c - 1) / c) * step + (c > 1 ? 1500.0 * rounds : 0.0) + 1500.0);
         if (c == 1 || cost < best.cost) best = FewPlan{best.bt, c, n * c, cost};

@@ -9,23 +9,24 @@
 // blocks of a cluster share one MMA, 256 tokens by the same 256 outputs; each
 // brings its tokens and half of the weights, 32 KB a K block instead of 48.
 // One persistent thread block per SM:
-//   warps 0, 1   TMA producers, a thread each, K blocks in turn: 128 x 128
-//                codes of X and the block's part of 256 x 128 of W, 128-byte
-//                swizzled
-//   warps 2..5   (of the first block) issue the MMAs, a thread each: every
-//                second K block of one half; its four leave the half's sums
-//                in one of four buffers
-//   warps 6, 7   the scales' products, kChunk K blocks at a time
-//   warps 8..15  promote: tensor-memory lanes 32 (w % 4) .. + 31, 64 columns
-//                of each half
+//   warps 0, 1   TMA producers, K blocks in turn: 128 x 128 codes of X and the
+//                block's part of 256 x 128 of W, 128-byte swizzled
+//   warps 2..5   (of the first block) issue the MMAs, each every second K block
+//                of one half; its four leave the half's sums in one of four
+//                buffers (one producer and two issuers took 81 us where these
+//                take 50, without the promotion)
+//   warps 8..15  promote: tensor-memory lanes 32 (w % 4) .. + 31, one half
+//                each, so that a scheduler's two warps are at different points
+//                of their K blocks; a thread loads its token's scale and its
+//                half's four K blocks ahead
 #include "gemm_e4m3_tc.cuh"
 
 namespace qg {
 namespace e8 {
 namespace {
 
-constexpr int kChunk = 4, kSlots = 2;  // K blocks of one slot of scales
-constexpr int kWarpIssue = 2, kWarpScale = 6, kWarpPromote = 8, kWarps = 8, kThreads = 32 * (kWarpPromote + kWarps);
+constexpr int kAhead = 4;              // K blocks of scales in a thread's registers
+constexpr int kWarpIssue = 2, kWarpSpare = 6, kWarpPromote = 8, kWarps = 8, kThreads = 32 * (kWarpPromote + kWarps);
 constexpr int kBufs = 4;               // tensor-memory buffers of 128 columns
 constexpr int kOutStride = 80;         // bytes between the tokens (64 each) of a strip on its way out: eight lanes' 16 bytes meet no bank twice
 
@@ -36,47 +37,39 @@ struct CfgMany {
     static constexpr int kBoxRows = 128 / kCtas;                   // outputs of one TMA box of W: this block's part of a half
     static constexpr uint32_t kXBytes = 128 * 128, kBoxBytes = kBoxRows * 128;
     static constexpr uint32_t kStageBytes = kXBytes + 2 * kBoxBytes;
-    static constexpr uint32_t kScaleBytes = kSlots * kChunk * 256 * 4;
     static constexpr uint32_t kOutAll = kWarps * 16 * kOutStride;   // strips of 16 tokens
     static constexpr uint32_t kBarBytes = 256;
-    static constexpr int kStages = (int)((kSmemBudget - 1024 - 256 - kScaleBytes - kOutAll - kTableBytes - kBarBytes) / kStageBytes);
-    static constexpr int kNumBars = 2 * kStages + 2 * kBufs + 2 * kSlots;
-    static constexpr uint32_t kScaleOff = kStages * kStageBytes;
-    static constexpr uint32_t kOutOff = kScaleOff + kScaleBytes;
+    static constexpr int kStages = ~1 & (int)((kSmemBudget - 1024 - 256 - kOutAll - kTableBytes - kBarBytes) / kStageBytes);
+    static constexpr int kNumBars = 2 * kStages + 2 * kBufs;
+    static constexpr uint32_t kOutOff = kStages * kStageBytes;
     static constexpr uint32_t kBarOff = kOutOff + kOutAll;
     static constexpr uint32_t kTableOff = kBarOff + kBarBytes;
     static constexpr uint32_t kSmemBytes = 1024 + kTableOff + kTableBytes;
     static_assert(kStages >= 3 && kNumBars * 8 + 16 <= (int)kBarBytes, "");
     // A wait tells one phase of a barrier from the next, not from the one
-    // after that, so a stage must always be the same threads': with an odd
-    // number of stages one thread could pass on a phase that the other had
-    // not seen begin.
+    // after that, so a stage must always be the same warps': with an odd
+    // number of stages one could pass on a phase that the other had not seen
+    // begin.
     static_assert(kStages % 2 == 0 && kBufs == 4, "a stage and a buffer belong to the same producer and issuers every time");
 };
 
-// 64 columns of this warp's 32 lanes, to be read after landed() on the same registers.
+// 32 columns of this warp's 32 lanes, to be read after landed() on the same registers.
 struct Sums {
-    uint32_t r[64];
+    uint32_t r[32];
 };
-#define QG_R16(n) "%" #n "0, %" #n "1, %" #n "2, %" #n "3, %" #n "4, %" #n "5, %" #n "6, %" #n "7, %" #n "8, %" #n "9"
 __device__ __forceinline__ void load(uint32_t taddr, Sums &s) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, " QG_R16(1) ", " QG_R16(2) ", " QG_R16(3) ", " QG_R16(4) ", " QG_R16(5)
-        ", %60, %61, %62, %63}, [%64];"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19,"
+        "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
         : "=r"(s.r[0]), "=r"(s.r[1]), "=r"(s.r[2]), "=r"(s.r[3]), "=r"(s.r[4]), "=r"(s.r[5]), "=r"(s.r[6]),
-          "=r"(s.r[7]), "=r"(s.r[8]), "=r"(s.r[9]), "=r"(s.r[10]), "=r"(s.r[11]), "=r"(s.r[12]), "=r"(s.r[13]),
-          "=r"(s.r[14]), "=r"(s.r[15]), "=r"(s.r[16]), "=r"(s.r[17]), "=r"(s.r[18]), "=r"(s.r[19]), "=r"(s.r[20]),
-          "=r"(s.r[21]), "=r"(s.r[22]), "=r"(s.r[23]), "=r"(s.r[24]), "=r"(s.r[25]), "=r"(s.r[26]), "=r"(s.r[27]),
-          "=r"(s.r[28]), "=r"(s.r[29]), "=r"(s.r[30]), "=r"(s.r[31]), "=r"(s.r[32]), "=r"(s.r[33]), "=r"(s.r[34]),
-          "=r"(s.r[35]), "=r"(s.r[36]), "=r"(s.r[37]), "=r"(s.r[38]), "=r"(s.r[39]), "=r"(s.r[40]), "=r"(s.r[41]),
-          "=r"(s.r[42]), "=r"(s.r[43]), "=r"(s.r[44]), "=r"(s.r[45]), "=r"(s.r[46]), "=r"(s.r[47]), "=r"(s.r[48]),
-          "=r"(s.r[49]), "=r"(s.r[50]), "=r"(s.r[51]), "=r"(s.r[52]), "=r"(s.r[53]), "=r"(s.r[54]), "=r"(s.r[55]),
-          "=r"(s.r[56]), "=r"(s.r[57]), "=r"(s.r[58]), "=r"(s.r[59]), "=r"(s.r[60]), "=r"(s.r[61]), "=r"(s.r[62]),
-          "=r"(s.r[63])
+          "=r"(s.r[7]), "=r"(s.r[8]), "=r"(s.r[9]), "=r"(s.r[10]), "=r"(s.r[11]), "=r"(s.r[12]),
+          "=r"(s.r[13]), "=r"(s.r[14]), "=r"(s.r[15]), "=r"(s.r[16]), "=r"(s.r[17]), "=r"(s.r[18]),
+          "=r"(s.r[19]), "=r"(s.r[20]), "=r"(s.r[21]), "=r"(s.r[22]), "=r"(s.r[23]), "=r"(s.r[24]),
+          "=r"(s.r[25]), "=r"(s.r[26]), "=r"(s.r[27]), "=r"(s.r[28]), "=r"(s.r[29]), "=r"(s.r[30]),
+          "=r"(s.r[31])
         : "r"(taddr));
 }
-#undef QG_R16
 // Sixteen registers pass through, so that nothing reads them before.
 __device__ __forceinline__ void pass(uint32_t *r) {
     asm volatile(""
@@ -89,8 +82,6 @@ __device__ __forceinline__ void landed(Sums &s) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
     pass(s.r);
     pass(s.r + 16);
-    pass(s.r + 32);
-    pass(s.r + 48);
 }
 
 template <bool PAIR, class SC>
@@ -101,10 +92,8 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     const uint32_t raw_base = smem_addr(smem_raw);
     unsigned char *smem = smem_raw + ((1024u - (raw_base & 1023u)) & 1023u);
     const uint32_t sbase = smem_addr(smem);
-    float *s_scale = reinterpret_cast<float *>(smem + C::kScaleOff);      // [slot][K block][half][token]
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kBarOff);
-    uint64_t *full = bars, *empty = full + C::kStages, *acc_full = empty + C::kStages, *acc_empty = acc_full + kBufs,
-             *sc_full = acc_empty + kBufs, *sc_empty = sc_full + kSlots;
+    uint64_t *full = bars, *empty = full + C::kStages, *acc_full = empty + C::kStages, *acc_empty = acc_full + kBufs;
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(bars + C::kNumBars);
     volatile uint32_t *abort = tmem_slot + 1;
     int *s_tile = reinterpret_cast<int *>(smem + C::kTableOff), *s_row = s_tile + kMaxExperts + 2;
@@ -119,11 +108,7 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
         }
         for (int b = 0; b < kBufs; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], C::kCtas * kWarps);
-        }
-        for (int b = 0; b < kSlots; ++b) {
-            mbar_init(&sc_full[b], kWarpPromote - kWarpScale);
-            mbar_init(&sc_empty[b], kWarps);
+            mbar_init(&acc_empty[b], C::kCtas * kWarps / 2);
         }
         *abort = 0u;
         mbar_fence_init();
@@ -146,20 +131,24 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
 
     // 512 threads start with 128 registers each, 65536 in all, of which the
     // promoting warps take 8 x 32 x 216 and the others 8 x 32 x 40.
+    // Every lane waits: with one lane's wait and a vote the warp goes on 170 cycles later.
+    auto wait_warp = [&](uint64_t *bar, uint32_t parity) {
+        if (!mbar_wait_or_abort(bar, parity, abort) && lane == 0) raise_device_error(a.err, kErrTimeout);
+        __syncwarp();
+    };
     if (warp < kWarpPromote) {
-        regs_down<40>();
+        regs_down<56>();
         if (warp < kWarpIssue) {
-            if (lane == 0) {
-                uint32_t it = 0;
-                for (int t = first; t < tiles; t += step) {
-                    const Tile L = find_tile<C::kTokens>(a, s_tile, s_row, t);
-                    const int m0 = L.m0 + side * 128;
-                    const int wrow = L.e * a.O + L.ot * 256 + side * C::kBoxRows;
-                    for (int k = 0; k < a.KB; ++k, ++it) {
-                        if ((it & 1u) != (uint32_t)warp) continue;
-                        const uint32_t s = it % C::kStages, r = it / C::kStages;
-                        if (r > 0 && !mbar_wait_or_abort(&empty[s], (r & 1) ^ 1, abort))
-                            raise_device_error(a.err, kErrTimeout);
+            uint32_t it = 0;
+            for (int t = first; t < tiles; t += step) {
+                const Tile L = find_tile<C::kTokens>(a, s_tile, s_row, t);
+                const int m0 = L.m0 + side * 128;
+                const int wrow = L.e * a.O + L.ot * 256 + side * C::kBoxRows;
+                for (int k = 0; k < a.KB; ++k, ++it) {
+                    if ((it & 1u) != (uint32_t)warp) continue;
+                    const uint32_t s = it % C::kStages, r = it / C::kStages;
+                    if (r > 0) wait_warp(&empty[s], (r & 1) ^ 1);
+                    if (lane == 0) {
                         const uint32_t st = sbase + s * C::kStageBytes;
                         if (side == 0) mbar_arrive_expect_tx(&full[s], C::kCtas * C::kStageBytes);
                         const uint32_t bar = PAIR ? map_rank(smem_addr(&full[s]), 0) : smem_addr(&full[s]);
@@ -167,130 +156,121 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
                         for (int h = 0; h < 2; ++h)
                             load_tile<PAIR>(st + C::kXBytes + h * C::kBoxBytes, &tmW, k * 128, wrow + h * 128, bar);
                     }
-                }
-                // Every copy issued must have landed, and every arrival that is
-                // on its way to this block, before the block exits.
-                for (uint32_t j = it > (uint32_t)C::kStages ? it - C::kStages : 0; j < it; ++j) {
-                    const uint32_t s = j % C::kStages, r = j / C::kStages;
-                    if ((j & 1u) != (uint32_t)warp) continue;
-                    if (side == 0 && !mbar_wait(&full[s], r & 1)) raise_device_error(a.err, kErrTimeout);
-                    if (PAIR && !mbar_wait_or_abort(&empty[s], r & 1, abort)) raise_device_error(a.err, kErrTimeout);
+                    __syncwarp();
                 }
             }
-        } else if (warp < kWarpScale) {
-            // No half's sums depend on another's, so four threads issue them in
+            // Every copy issued must have landed, and every arrival that is
+            // on its way to this block, before the block exits.
+            for (uint32_t j = it > (uint32_t)C::kStages ? it - C::kStages : 0; j < it; ++j) {
+                const uint32_t s = j % C::kStages, r = j / C::kStages;
+                if ((j & 1u) != (uint32_t)warp) continue;
+                if (side == 0 && !mbar_wait(&full[s], r & 1) && lane == 0) raise_device_error(a.err, kErrTimeout);
+                wait_warp(&empty[s], r & 1);
+            }
+        } else if (warp < kWarpSpare) {
+            // No half's sums depend on another's, so four warps issue them in
             // turn: each one's waits and commits pass while the others' MMAs run.
-            if (lane == 0 && side == 0) {
+            if (side == 0) {
                 uint32_t it = 0;
-                const uint32_t odd = (warp - kWarpIssue) & 1, idesc = idesc_e4m3(kMmaM * C::kCtas, 128);
-                const int h = (warp - kWarpIssue) >> 1;
-                const uint32_t b = 2 * odd + h;          // this thread's buffer
+                const uint32_t odd = (warp - kWarpIssue) & 1, h = (warp - kWarpIssue) >> 1, b = 2 * odd + h, d = tmem + b * 128;
+                const uint32_t idesc = idesc_e4m3(kMmaM * C::kCtas, 128);
+                const uint32_t x_lo = desc_lo(sbase), w_lo = desc_lo(sbase + C::kXBytes + h * C::kBoxBytes);
                 for (int t = first; t < tiles; t += step) {
                     for (int k = 0; k < a.KB; ++k, ++it) {
                         if ((it & 1u) != odd) continue;
-                        const uint32_t s = it % C::kStages, r = it / C::kStages, st = sbase + s * C::kStageBytes;
-                        const uint32_t rb = it / 2, wa = st + C::kXBytes + h * C::kBoxBytes;
-                        if (rb > 0 && !mbar_wait_or_abort(&acc_empty[b], (rb & 1) ^ 1, abort))
-                            raise_device_error(a.err, kErrTimeout);
-                        if (!mbar_wait_or_abort(&full[s], r & 1, abort)) raise_device_error(a.err, kErrTimeout);
+                        const uint32_t s = it % C::kStages, r = it / C::kStages, rb = it / 2;
+                        const uint32_t at = s * (C::kStageBytes >> 4);
+                        wait_warp(&full[s], r & 1);
+                        if (rb > 0) wait_warp(&acc_empty[b], (rb & 1) ^ 1);
                         tc_fence_after();
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_e4m3<PAIR>(tmem + b * 128, sw128_desc(st + kk * 32), sw128_desc(wa + kk * 32), idesc,
-                                           kk > 0 ? 1u : 0u);
-                        commit_to<PAIR>(&acc_full[b], 3);
-                        commit_to<PAIR>(&empty[s], 3);
-                    }
-                }
-            }
-        } else {
-            const int tok = (warp - kWarpScale) * 64 + lane, m = side * 128 + tok;   // and tok + 32
-            uint32_t ch = 0;
-            for (int t = first; t < tiles; t += step) {
-                const Tile L = find_tile<C::kTokens>(a, s_tile, s_row, t);
-                const typename SC::T *ws = static_cast<const typename SC::T *>(a.ws) + ((size_t)L.e * a.NB + 2 * L.ot) * a.KB;
-                const float *xs = a.xs + (size_t)(L.m0 + m) * a.KB;
-                const bool two = 2 * L.ot + 1 < a.NB, here = m < L.rows, here2 = m + 32 < L.rows;
-                for (int k = 0; k < a.KB; k += kChunk, ++ch) {
-                    const uint32_t s = ch % kSlots, r = ch / kSlots;
-                    float v[2][kChunk], w[2][kChunk];
-#pragma unroll
-                    for (int c = 0; c < kChunk; ++c) {
-                        const bool in = k + c < a.KB;
-                        v[0][c] = in && here ? xs[k + c] : 0.f;
-                        v[1][c] = in && here2 ? xs[(size_t)32 * a.KB + k + c] : 0.f;
-                        w[0][c] = in ? SC::get(ws, k + c) : 0.f;
-                        w[1][c] = in && two ? SC::get(ws, (size_t)a.KB + k + c) : 0.f;
-                    }
-                    if (r > 0) {
-                        if (!mbar_wait_or_abort(&sc_empty[s], (r & 1) ^ 1, abort) && lane == 0)
-                            raise_device_error(a.err, kErrTimeout);
+                        if (lane == 0) {
+                            mma_block<PAIR>(d, x_lo + at, w_lo + at, idesc);
+                            commit_to<PAIR>(&acc_full[b], 3);
+                            commit_to<PAIR>(&empty[s], 3);
+                        }
                         __syncwarp();
                     }
-                    float *dst = s_scale + s * kChunk * 256 + tok;
-#pragma unroll
-                    for (int c = 0; c < kChunk; ++c) {
-                        dst[c * 256] = v[0][c] * w[0][c];
-                        dst[c * 256 + 32] = v[1][c] * w[0][c];
-                        dst[c * 256 + 128] = v[0][c] * w[1][c];
-                        dst[c * 256 + 160] = v[1][c] * w[1][c];
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sc_full[s]);
                 }
             }
         }
     } else {
-        regs_up<216>();
-        const int pw = warp - kWarpPromote, q = warp & 3, grp = pw >> 2, row = q * 32 + lane;
-        const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16) + grp * 64;
-        uint32_t buf = 0, ch = 0;
-        auto wait_warp = [&](uint64_t *bar, uint32_t parity) {
-            // every lane: with one lane's wait and a vote the warp goes on 170 cycles later
-            if (!mbar_wait_or_abort(bar, parity, abort) && lane == 0) raise_device_error(a.err, kErrTimeout);
-            __syncwarp();
-        };
-        uint64_t acc[2][32];               // token `row`, columns 64 grp .. + 63 of each half, in pairs
-        auto promote = [&](auto half, const float *f) {
-            constexpr int h = decltype(half)::value;
-            const uint32_t b = buf % kBufs;
-            wait_warp(&acc_full[b], (buf / kBufs) & 1);
-            tc_fence_after();
-            Sums s;
-            load(tq + b * 128, s);
-            const float fv = f[h * 128];
-            landed(s);
-            // the sums are in registers: the next MMAs may have the buffer
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if constexpr (PAIR) signal_remote(map_rank(smem_addr(&acc_empty[b]), 0));
-                else mbar_arrive(&acc_empty[b]);
+        regs_up<200>();
+        const int pw = warp - kWarpPromote, q = warp & 3, half = pw >> 2, m = side * 128 + q * 32 + lane;
+        const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16) + half * 128;
+        uint32_t it = 0;
+        float acc[4][32];                  // token m of the tile, the half's columns 32 x .. + 31
+        float next_x[kAhead], next_w[kAhead];
+        const float *xs;
+        const typename SC::T *ws;
+        bool here, there;                  // whether the tile has this token and this half
+        // Whole fours of scales at 16-byte addresses (4-byte ones of UE8M0) come in one load.
+        const bool fours = a.KB % kAhead == 0 && reinterpret_cast<uintptr_t>(a.xs) % 16 == 0 &&
+                           reinterpret_cast<uintptr_t>(a.ws) % (kAhead * sizeof(typename SC::T)) == 0;
+        auto fetch = [&](int k) {
+            if (fours) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (here && k < a.KB) v = *reinterpret_cast<const float4 *>(xs + k);
+                next_x[0] = v.x, next_x[1] = v.y, next_x[2] = v.z, next_x[3] = v.w;
+                SC::get4(next_w, ws + k, there && k < a.KB);
+                return;
             }
-            const uint64_t f2 = f32_pair(fv, fv);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) fma2(acc[h][j], s.r[2 * j], s.r[2 * j + 1], f2);
-            ++buf;
+            for (int c = 0; c < kAhead; ++c) {
+                next_x[c] = here && k + c < a.KB ? xs[k + c] : 0.f;
+                next_w[c] = there && k + c < a.KB ? SC::get(ws, k + c) : 0.f;
+            }
+        };
+        auto begin = [&](int t) {          // the tile's first scales are on their way
+            const Tile N = find_tile<C::kTokens>(a, s_tile, s_row, t);
+            here = m < N.rows;
+            there = 2 * N.ot + half < a.NB;
+            xs = a.xs + (size_t)(N.m0 + m) * a.KB;
+            ws = static_cast<const typename SC::T *>(a.ws) + ((size_t)N.e * a.NB + 2 * N.ot + half) * a.KB;
+            fetch(0);
+        };
+        // One K block: the half's sums, times both scales, onto acc.  Scalar
+        // FMAs: packed ones need their operands moved into pairs, 79 us
+        // against 70 for 512 tokens of 16384 x 7168.
+        auto promote = [&](float f) {
+            const uint32_t odd = it & 1u, b = 2 * odd + half, tb = tq + odd * 256;
+            wait_warp(&acc_full[b], (it >> 1) & 1);
+            tc_fence_after();
+            Sums v;
+            load(tb, v);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                landed(v);
+                if (x == 3) {
+                    // the sums are in registers: the next MMAs may have the buffer
+                    tc_fence_before();
+                    __syncwarp();
+                    arrive_if<PAIR>(lane == 0, PAIR ? map_rank(smem_addr(&acc_empty[b]), 0) : smem_addr(&acc_empty[b]));
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) acc[x][j] = fmaf(__uint_as_float(v.r[j]), f, acc[x][j]);
+                if (x < 3) load(tb + 32 * (x + 1), v);
+            }
+            ++it;
         };
         auto tile_sums = [&]() {
-            for (int k = 0; k < a.KB; ++k) {
-                const int c = k % kChunk;
-                if (c == 0) wait_warp(&sc_full[ch % kSlots], (ch / kSlots) & 1);
-                const float *f = s_scale + ((ch % kSlots) * kChunk + c) * 256 + row;
-                promote(std::integral_constant<int, 0>(), f);
-                promote(std::integral_constant<int, 1>(), f);
-                if (c == kChunk - 1 || k + 1 == a.KB) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sc_empty[ch % kSlots]);
-                    ++ch;
+            for (int k = 0; k < a.KB; k += kAhead) {
+                float f[kAhead];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) f[i] = next_x[i] * next_w[i];
+                fetch(k + kAhead);
+                const int n = min(kAhead, a.KB - k);
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    if (i >= n) break;
+                    promote(f[i]);
                 }
             }
         };
         unsigned char *strip = smem + C::kOutOff + pw * 16 * kOutStride;
-        const int esz = a.y_type == kF32 ? 4 : 2, per16 = 16 / esz;
-        const bool lines = a.O % per16 == 0 && reinterpret_cast<uintptr_t>(a.Y) % 16 == 0;
         // 64 bytes a token through shared memory, so that four lanes store a token's.
         auto store_strip = [&](const uint32_t (&w)[16], const Tile &L, int o) {
+            const int esz = a.y_type == kF32 ? 4 : 2, per16 = 16 / esz;
+            const bool lines = a.O % per16 == 0 && reinterpret_cast<uintptr_t>(a.Y) % 16 == 0;
             const int part = lane & 3, at = o + part * per16;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -303,10 +283,10 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int tok = 8 * i + (lane >> 2), m = side * 128 + q * 32 + 16 * x + tok;
+                    const int tok = 8 * i + (lane >> 2), mt = side * 128 + q * 32 + 16 * x + tok;
                     const uint4 v = *reinterpret_cast<const uint4 *>(strip + tok * kOutStride + 16 * part);
-                    if (m >= L.rows || at >= a.O) continue;
-                    unsigned char *y = static_cast<unsigned char *>(a.Y) + ((size_t)(L.m0 + m) * a.O + at) * esz;
+                    if (mt >= L.rows || at >= a.O) continue;
+                    unsigned char *y = static_cast<unsigned char *>(a.Y) + ((size_t)(L.m0 + mt) * a.O + at) * esz;
                     if (lines) {
                         *reinterpret_cast<uint4 *>(y) = v;
                         continue;
@@ -325,37 +305,30 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
                 __syncwarp();
             }
         };
+        if (first < tiles) begin(first);
         for (int t = first; t < tiles; t += step) {
-            const Tile L = find_tile<C::kTokens>(a, s_tile, s_row, t);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) acc[0][j] = acc[1][j] = 0;
+            for (int j = 0; j < 32; ++j) acc[0][j] = acc[1][j] = acc[2][j] = acc[3][j] = 0.f;
             tile_sums();
+            if (t + step < tiles) begin(t + step);
+            const Tile L = find_tile<C::kTokens>(a, s_tile, s_row, t);    // looked up again: no register holds it over the sums
             if (side * 128 + q * 32 >= L.rows) continue;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int o = L.ot * 256 + h * 128 + grp * 64;
+            for (int y = 0; y < 4; ++y) {
+                const int o = L.ot * 256 + half * 128 + y * 32;
                 if (o >= a.O) continue;
                 uint32_t w[16];
                 if (a.y_type == kF32) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
+                    for (int x = 0; x < 2; ++x) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            w[2 * j] = (uint32_t)acc[h][8 * x + j];
-                            w[2 * j + 1] = (uint32_t)(acc[h][8 * x + j] >> 32);
-                        }
+                        for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(acc[y][16 * x + j]);
                         store_strip(w, L, o + 16 * x);
                     }
                 } else {
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float2 v = pair_of(acc[h][16 * x + j]);
-                            w[j] = pack_16(a.y_type, v.x, v.y);
-                        }
-                        store_strip(w, L, o + 32 * x);
-                    }
+                    for (int j = 0; j < 16; ++j) w[j] = pack_16(a.y_type, acc[y][2 * j], acc[y][2 * j + 1]);
+                    store_strip(w, L, o);
                 }
             }
         }
@@ -394,9 +367,11 @@ ManyPlan plan_many(int M, int I, int O, int experts) {
     for (int pair = 0; pair <= 1; ++pair) {
         const int tokens = 128 * (pair + 1), n = pair ? pairs_at_once() : num_sms();
         if (n < 1) break;
-        // an expert's last tile is half empty
-        const double tiles = (double)NT * (experts == 1 ? (M + tokens - 1) / tokens : (double)M / tokens + 0.5 * filled);
-        const double cost = std::max(1.0, experts == 1 ? std::ceil(tiles / n) : tiles / n + 0.5) * (KB * (pair ? 700.0 : 900.0) + 3000.0);
+        const double per_output = token_tiles(M, experts, tokens), tiles = NT * per_output;
+        // cycles of a K block, as measured; where an expert's weights serve one
+        // tile alone, what 32 KB of them take an SM at the card's bandwidth
+        const double step = (pair ? 2.0 : 1.0) * per_output < 1.5 * (experts == 1 ? 1 : filled) ? 1400.0 : pair ? 900.0 : 880.0;
+        const double cost = std::max(1.0, std::ceil(tiles / n)) * (KB * step + 3000.0);
         if (!pair || cost < best.cost) best = ManyPlan{pair != 0, n * (pair + 1), cost};
     }
     return best;

@@ -83,6 +83,19 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, 
             "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
             : "memory");
 }
+// The two words of sw128_desc: where an operand starts, in 16 bytes (32 bytes
+// further along K: + 2), and what never changes.  One thread issues the MMAs,
+// and every instruction before them is on the K step's way.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return (saddr & 0x3FFFFu) >> 4 | 1u << 16; }
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+// Four MMAs along K, the first of which starts the sums.
+template <bool PAIR>
+__device__ __forceinline__ void mma_block(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
+#pragma unroll
+    for (uint32_t kk = 0; kk < 4; ++kk)
+        mma_e4m3<PAIR>(d_tmem, (uint64_t)kDescHi << 32 | (a_lo + 2 * kk), (uint64_t)kDescHi << 32 | (b_lo + 2 * kk), idesc,
+                       kk > 0 ? 1u : 0u);
+}
 template <bool PAIR>
 __device__ __forceinline__ void tmem_alloc(volatile uint32_t *slot, uint32_t cols) {
     if constexpr (PAIR) {
@@ -126,11 +139,25 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t local, int rank) {
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// An arrival that publishes no memory (tensor memory has its own fences).  The
-// release and acquire of the whole cluster, which it spares, took a K step
-// of a block pair from 1600 to 2700 cycles.
-__device__ __forceinline__ void signal_remote(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// One lane's arrival without a branch (a branch costs the warp some 100
+// cycles).  REMOTE: at a barrier's cluster address; it publishes no memory, as
+// tensor memory has its own fences: the release and acquire of the whole
+// cluster, which it spares, took a K step of a block pair from 1600 to 2700
+// cycles.
+template <bool REMOTE>
+__device__ __forceinline__ void arrive_if(bool yes, uint32_t bar) {
+    if constexpr (REMOTE)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t"
+            "@p mbarrier.arrive.shared::cluster.b64 _, [%1];\n\t}" ::"r"((int)yes),
+            "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t"
+            "@p mbarrier.arrive.shared::cta.b64 _, [%1];\n\t}" ::"r"((int)yes),
+            "r"(bar)
+            : "memory");
 }
 __device__ __forceinline__ float load_remote(uint32_t addr) {
     float v;
@@ -282,6 +309,14 @@ inline int count_clusters(K kernel, int threads, uint32_t smem, int cluster, int
         return kECuda;
     }
     return kOk;
+}
+
+// About how many tiles of bt tokens the experts' rows make (the host knows
+// their sum alone): an expert's last tile is half empty.
+inline double token_tiles(int M, int experts, int bt) {
+    if (experts == 1) return (M + bt - 1) / bt;
+    const double filled = std::min(experts, M);
+    return std::max(filled, (double)M / bt + 0.5 * filled);
 }
 
 // The two kernels.  `cost` receives an estimate of the call's cycles.
