@@ -19,6 +19,7 @@ size_t size_of(int type) { return type == QG_F32 ? 4 : type == QG_E4M3 ? 1 : 2; 
 int check_slots(const char *fn, int n_tokens, int k, int width, int n_rows) {
     if (n_tokens < 0 || n_rows < 0)
         QG_REFUSE(kEInval, "%s: n_tokens = %d and n_rows = %d must be >= 0", fn, n_tokens, n_rows);
+    if (width > INT_MAX - 65536) QG_REFUSE(kEInval, "%s: a row of %d elements overflows", fn, width);
     if (k < 1 || width < 1) QG_REFUSE(kEInval, "%s: k = %d and the row's width %d must be >= 1", fn, k, width);
     if ((long long)n_tokens * k > INT_MAX)
         QG_REFUSE(kEInval, "%s: n_tokens * k = %lld slots, must be below 2^31", fn, (long long)n_tokens * k);
