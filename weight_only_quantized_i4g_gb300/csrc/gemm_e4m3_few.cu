@@ -161,7 +161,7 @@ gemm_e4m3_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
     }
     if (warp == kWarpMma) {
         __syncwarp();
-        tmem_alloc<false>(tmem_slot, C::kTmemCols);
+        tmem_alloc(tmem_slot, C::kTmemCols);
     }
     griddep_wait();
     griddep_launch_dependents();
@@ -194,9 +194,11 @@ gemm_e4m3_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
                     }
                 }
             }
-            // Every copy issued must have landed before the block exits.
+            // Every copy issued must have landed, and every commit arrived, before the block exits.
             for (uint32_t j = it > (uint32_t)C::kStages ? it - C::kStages : 0; j < it; ++j)
-                if (!mbar_wait(&full[j % C::kStages], (j / C::kStages) & 1)) raise_device_error(a.err, kErrTimeout);
+                if (!mbar_wait(&full[j % C::kStages], (j / C::kStages) & 1) ||
+                    !mbar_wait_or_abort(&empty[j % C::kStages], (j / C::kStages) & 1, abort))
+                    raise_device_error(a.err, kErrTimeout);
         }
     } else if (warp == kWarpMma || warp == kWarpMma2) {
         // No stage's sums depend on another's, so two threads issue them in
@@ -206,7 +208,7 @@ gemm_e4m3_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
             const uint32_t mine = warp == kWarpMma ? 0u : 1u;
             for (int t = first; t < tiles; t += step) {
                 const Tile L = find_tile<BT>(a, s_tile, s_row, t);
-                const uint32_t idesc = idesc_e4m3(kMmaM, (L.rows + 15) & ~15);
+                const uint32_t idesc = idesc_e4m3((L.rows + 15) & ~15);
                 for (int k = k0; k < k1; k += C::kBlocks, ++it) {
                     if ((it & 1u) != mine) continue;
                     const uint32_t s = it % C::kStages, r = it / C::kStages, b = it % C::kBufs, rb = it / C::kBufs;
@@ -219,7 +221,7 @@ gemm_e4m3_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
 #pragma unroll
                     for (int j = 0; j < C::kBlocks; ++j) {
                         if (j >= n) break;
-                        mma_block<false>(tmem + b * C::kBufCols + j * BT, w_lo + j * (C::kBlockBytes >> 4),
+                        mma_block(tmem + b * C::kBufCols + j * BT, w_lo + j * (C::kBlockBytes >> 4),
                                          w_lo + (j * C::kBlockBytes + kWBytes) / 16, idesc);
                     }
                     mma_commit(&acc_full[b]);
@@ -432,7 +434,7 @@ gemm_e4m3_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
     __syncthreads();
     if (warp == kWarpMma) {
         tc_fence_after();
-        tmem_free<false>(tmem, C::kTmemCols);
+        tmem_free(tmem, C::kTmemCols);
     }
     if (ranks > 1) cluster_barrier();      // no block leaves while another reads its sums
 }

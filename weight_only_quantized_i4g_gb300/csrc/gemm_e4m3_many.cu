@@ -1,42 +1,41 @@
 // gemm_e4m3_many.cu -- products of e4m3 activations with e4m3 weights, many
 // tokens an expert: the tensor cores and what feeds and empties them bound it.
 //
-// A tile is 128 tokens a block (MMA M) by 256 outputs (two halves of N = 128,
-// a weight scale each), so a promoting thread holds one token and scales a
-// half's sums by one factor.  (With the tokens along N a factor a column has
-// to be read from shared memory: 64 columns then take a warp 290 cycles
-// instead of 134, and a K block 1800 instead of the MMAs' 512.)  PAIR: two
-// blocks of a cluster share one MMA, 256 tokens by the same 256 outputs; each
-// brings its tokens and half of the weights, 32 KB a K block instead of 48.
+// A tile is 128 tokens (MMA M) by 256 or 192 outputs, two halves of N = 128 or
+// 96, so a promoting thread holds one token and scales 32 columns by one
+// factor.  (With the tokens along N a factor a column has to be read from
+// shared memory: 64 columns then take a warp 290 cycles instead of 134, and a
+// K block 1800 instead of the MMAs' 512.)  Shared memory bounds it: a K block's
+// MMAs read 64 KB and TMA writes 48, which takes 875 cycles at 128 bytes a
+// cycle; it takes 880.  Block pairs that share an MMA (half the weights a
+// block) were built and measured 0 to 10% slower: their signals cross SMs.
 // One persistent thread block per SM:
-//   warps 0, 1   TMA producers, K blocks in turn: 128 x 128 codes of X and the
-//                block's part of 256 x 128 of W, 128-byte swizzled
-//   warps 2..5   (of the first block) issue the MMAs, each every second K block
-//                of one half; its four leave the half's sums in one of four
+//   warps 0, 1   TMA producers, K blocks in turn: 128 x 128 codes of X and both
+//                halves' of W, 128-byte swizzled
+//   warps 2..5   issue the MMAs, each every second K block of one half; its four leave the half's sums in one of four
 //                buffers (one producer and two issuers took 81 us where these
 //                take 50, without the promotion)
 //   warps 8..15  promote: tensor-memory lanes 32 (w % 4) .. + 31, one half
 //                each, so that a scheduler's two warps are at different points
-//                of their K blocks; a thread loads its token's scale and its
-//                half's four K blocks ahead
+//                of their K blocks; a thread loads its token's scales and its
+//                half's (of the one or two 128-blocks it lies in) four K blocks
+//                ahead
 #include "gemm_e4m3_tc.cuh"
 
 namespace qg {
 namespace e8 {
 namespace {
 
+constexpr int kPrefetchAhead = 8;
 constexpr int kAhead = 4;              // K blocks of scales in a thread's registers
-constexpr int kWarpIssue = 2, kWarpSpare = 6, kWarpPromote = 8, kWarps = 8, kThreads = 32 * (kWarpPromote + kWarps);
-constexpr int kBufs = 4;               // tensor-memory buffers of 128 columns
+constexpr int kWarpIssue = 2, kWarpPromote = 4, kWarps = 8, kThreads = 32 * (kWarpPromote + kWarps);
+constexpr int kBufs = 2;               // tensor-memory buffers of 256 columns
 constexpr int kOutStride = 80;         // bytes between the tokens (64 each) of a strip on its way out: eight lanes' 16 bytes meet no bank twice
 
-template <bool PAIR>
+template <int HALF>                    // outputs of half a tile
 struct CfgMany {
-    static constexpr int kCtas = PAIR ? 2 : 1;
-    static constexpr int kTokens = 128 * kCtas;                    // of a tile
-    static constexpr int kBoxRows = 128 / kCtas;                   // outputs of one TMA box of W: this block's part of a half
-    static constexpr uint32_t kXBytes = 128 * 128, kBoxBytes = kBoxRows * 128;
-    static constexpr uint32_t kStageBytes = kXBytes + 2 * kBoxBytes;
+    static constexpr uint32_t kXBytes = 128 * 128, kWBytes = HALF * 128;
+    static constexpr uint32_t kStageBytes = kXBytes + 2 * kWBytes;
     static constexpr uint32_t kOutAll = kWarps * 16 * kOutStride;   // strips of 16 tokens
     static constexpr uint32_t kBarBytes = 256;
     static constexpr int kStages = ~1 & (int)((kSmemBudget - 1024 - 256 - kOutAll - kTableBytes - kBarBytes) / kStageBytes);
@@ -50,7 +49,7 @@ struct CfgMany {
     // after that, so a stage must always be the same warps': with an odd
     // number of stages one could pass on a phase that the other had not seen
     // begin.
-    static_assert(kStages % 2 == 0 && kBufs == 4, "a stage and a buffer belong to the same producer and issuers every time");
+    static_assert(kStages % 2 == 0 && kBufs == 2, "a stage and a buffer belong to the same producer and issuer every time");
 };
 
 // 32 columns of this warp's 32 lanes, to be read after landed() on the same registers.
@@ -84,10 +83,10 @@ __device__ __forceinline__ void landed(Sums &s) {
     pass(s.r + 16);
 }
 
-template <bool PAIR, class SC>
+template <int HALF, class SC>
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Args8 a) {
-    using C = CfgMany<PAIR>;
+    using C = CfgMany<HALF>;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw_base = smem_addr(smem_raw);
     unsigned char *smem = smem_raw + ((1024u - (raw_base & 1023u)) & 1023u);
@@ -100,15 +99,14 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     __shared__ int2 s_warp[kThreads / 32];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int side = (int)(blockIdx.x % C::kCtas);                        // of the two blocks of an MMA (their rank in the cluster)
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 2);
+            mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < kBufs; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], C::kCtas * kWarps / 2);
+            mbar_init(&acc_empty[b], kWarps);
         }
         *abort = 0u;
         mbar_fence_init();
@@ -117,20 +115,19 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     }
     if (warp == kWarpIssue) {
         __syncwarp();
-        tmem_alloc<PAIR>(tmem_slot, kBufs * 128);
+        tmem_alloc(tmem_slot, kBufs * 256);
     }
     griddep_wait();
     griddep_launch_dependents();
-    build_tables<C::kTokens, kThreads>(a, s_tile, s_row, s_warp);
+    build_tables<128, kThreads>(a, s_tile, s_row, s_warp);
     tc_fence_before();
     __syncthreads();
-    if (PAIR) cluster_barrier();           // the other block's barriers are there
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int tiles = s_tile[a.experts] * a.NT, first = blockIdx.x / C::kCtas, step = gridDim.x / C::kCtas;
+    const int tiles = s_tile[a.experts] * a.NT, first = blockIdx.x, step = gridDim.x;
 
-    // 512 threads start with 128 registers each, 65536 in all, of which the
-    // promoting warps take 8 x 32 x 216 and the others 8 x 32 x 40.
+    // 384 threads start with 168 registers each, 64512 in all, of which the
+    // promoting warps take 8 x 32 x 224 and the others 4 x 32 x 56.
     // Every lane waits: with one lane's wait and a vote the warp goes on 170 cycles later.
     auto wait_warp = [&](uint64_t *bar, uint32_t parity) {
         if (!mbar_wait_or_abort(bar, parity, abort) && lane == 0) raise_device_error(a.err, kErrTimeout);
@@ -141,68 +138,67 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
         if (warp < kWarpIssue) {
             uint32_t it = 0;
             for (int t = first; t < tiles; t += step) {
-                const Tile L = find_tile<C::kTokens>(a, s_tile, s_row, t);
-                const int m0 = L.m0 + side * 128;
-                const int wrow = L.e * a.O + L.ot * 256 + side * C::kBoxRows;
+                const Tile L = find_tile<128>(a, s_tile, s_row, t);
+                const int wrow = L.e * a.O + L.ot * 2 * HALF;
                 for (int k = 0; k < a.KB; ++k, ++it) {
                     if ((it & 1u) != (uint32_t)warp) continue;
                     const uint32_t s = it % C::kStages, r = it / C::kStages;
                     if (r > 0) wait_warp(&empty[s], (r & 1) ^ 1);
                     if (lane == 0) {
                         const uint32_t st = sbase + s * C::kStageBytes;
-                        if (side == 0) mbar_arrive_expect_tx(&full[s], C::kCtas * C::kStageBytes);
-                        const uint32_t bar = PAIR ? map_rank(smem_addr(&full[s]), 0) : smem_addr(&full[s]);
-                        load_tile<PAIR>(st, &tmX, k * 128, m0, bar);
+                        mbar_arrive_expect_tx(&full[s], C::kStageBytes);
+                        tma_load_2d(st, &tmX, k * 128, L.m0, &full[s]);
                         for (int h = 0; h < 2; ++h)
-                            load_tile<PAIR>(st + C::kXBytes + h * C::kBoxBytes, &tmW, k * 128, wrow + h * 128, bar);
+                            tma_load_2d(st + C::kXBytes + h * C::kWBytes, &tmW, k * 128, wrow + h * HALF, &full[s]);
+                        if (k + kPrefetchAhead < a.KB && L.m0 == s_row[2 * L.e])
+                            for (int h = 0; h < 2; ++h) prefetch_tile(&tmW, (k + kPrefetchAhead) * 128, wrow + h * HALF);
                     }
                     __syncwarp();
                 }
             }
-            // Every copy issued must have landed, and every arrival that is
-            // on its way to this block, before the block exits.
+            // Every copy issued must have landed, and every commit arrived, before the block exits.
             for (uint32_t j = it > (uint32_t)C::kStages ? it - C::kStages : 0; j < it; ++j) {
-                const uint32_t s = j % C::kStages, r = j / C::kStages;
                 if ((j & 1u) != (uint32_t)warp) continue;
-                if (side == 0 && !mbar_wait(&full[s], r & 1) && lane == 0) raise_device_error(a.err, kErrTimeout);
-                wait_warp(&empty[s], r & 1);
+                wait_warp(&full[j % C::kStages], (j / C::kStages) & 1);
+                wait_warp(&empty[j % C::kStages], (j / C::kStages) & 1);
             }
-        } else if (warp < kWarpSpare) {
-            // No half's sums depend on another's, so four warps issue them in
-            // turn: each one's waits and commits pass while the others' MMAs run.
-            if (side == 0) {
-                uint32_t it = 0;
-                const uint32_t odd = (warp - kWarpIssue) & 1, h = (warp - kWarpIssue) >> 1, b = 2 * odd + h, d = tmem + b * 128;
-                const uint32_t idesc = idesc_e4m3(kMmaM * C::kCtas, 128);
-                const uint32_t x_lo = desc_lo(sbase), w_lo = desc_lo(sbase + C::kXBytes + h * C::kBoxBytes);
-                for (int t = first; t < tiles; t += step) {
-                    for (int k = 0; k < a.KB; ++k, ++it) {
-                        if ((it & 1u) != odd) continue;
-                        const uint32_t s = it % C::kStages, r = it / C::kStages, rb = it / 2;
-                        const uint32_t at = s * (C::kStageBytes >> 4);
-                        wait_warp(&full[s], r & 1);
-                        if (rb > 0) wait_warp(&acc_empty[b], (rb & 1) ^ 1);
-                        tc_fence_after();
-                        if (lane == 0) {
-                            mma_block<PAIR>(d, x_lo + at, w_lo + at, idesc);
-                            commit_to<PAIR>(&acc_full[b], 3);
-                            commit_to<PAIR>(&empty[s], 3);
-                        }
-                        __syncwarp();
+        } else {
+            // No K block's sums depend on another's, so two warps issue them in
+            // turn: each one's waits and commits pass while the other's MMAs run.
+            uint32_t it = 0;
+            const uint32_t odd = warp - kWarpIssue, d = tmem + odd * 256, idesc = idesc_e4m3(2 * HALF);
+            const uint32_t x_lo = desc_lo(sbase), w_lo = desc_lo(sbase + C::kXBytes);
+            for (int t = first; t < tiles; t += step) {
+                for (int k = 0; k < a.KB; ++k, ++it) {
+                    if ((it & 1u) != odd) continue;
+                    const uint32_t s = it % C::kStages, r = it / C::kStages, rb = it / 2;
+                    const uint32_t at = s * (C::kStageBytes >> 4);
+                    wait_warp(&full[s], r & 1);
+                    if (rb > 0) wait_warp(&acc_empty[odd], (rb & 1) ^ 1);
+                    tc_fence_after();
+                    if (lane == 0) {
+                        mma_block(d, x_lo + at, w_lo + at, idesc);
+                        mma_commit(&acc_full[odd]);
+                        mma_commit(&empty[s]);
                     }
+                    __syncwarp();
                 }
             }
         }
     } else {
-        regs_up<200>();
-        const int pw = warp - kWarpPromote, q = warp & 3, half = pw >> 2, m = side * 128 + q * 32 + lane;
-        const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16) + half * 128;
+        regs_up<224>();
+        const int pw = warp - kWarpPromote, q = warp & 3, half = pw >> 2, m = q * 32 + lane;
+        const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16) + half * HALF;
         uint32_t it = 0;
-        float acc[4][32];                  // token m of the tile, the half's columns 32 x .. + 31
-        float next_x[kAhead], next_w[kAhead];
+        float acc[HALF / 32][32];          // token m of the tile, the half's columns 32 x .. + 31
+        // A half of 96 outputs may lie in two blocks of weight scales: its first
+        // `split` columns in one, the others in the next.
+        constexpr int kParts = HALF % 128 ? 2 : 1;
+        float next_x[kAhead], next_w[kParts][kAhead];
         const float *xs;
         const typename SC::T *ws;
-        bool here, there;                  // whether the tile has this token and this half
+        bool here, there[kParts];          // whether the tile has this token, and the blocks are there
+        int split = HALF;
         // Whole fours of scales at 16-byte addresses (4-byte ones of UE8M0) come in one load.
         const bool fours = a.KB % kAhead == 0 && reinterpret_cast<uintptr_t>(a.xs) % 16 == 0 &&
                            reinterpret_cast<uintptr_t>(a.ws) % (kAhead * sizeof(typename SC::T)) == 0;
@@ -211,52 +207,62 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (here && k < a.KB) v = *reinterpret_cast<const float4 *>(xs + k);
                 next_x[0] = v.x, next_x[1] = v.y, next_x[2] = v.z, next_x[3] = v.w;
-                SC::get4(next_w, ws + k, there && k < a.KB);
+#pragma unroll
+                for (int p = 0; p < kParts; ++p) SC::get4(next_w[p], ws + (size_t)p * a.KB + k, there[p] && k < a.KB);
                 return;
             }
 #pragma unroll
             for (int c = 0; c < kAhead; ++c) {
                 next_x[c] = here && k + c < a.KB ? xs[k + c] : 0.f;
-                next_w[c] = there && k + c < a.KB ? SC::get(ws, k + c) : 0.f;
+#pragma unroll
+                for (int p = 0; p < kParts; ++p)
+                    next_w[p][c] = there[p] && k + c < a.KB ? SC::get(ws, (size_t)p * a.KB + k + c) : 0.f;
             }
         };
         auto begin = [&](int t) {          // the tile's first scales are on their way
-            const Tile N = find_tile<C::kTokens>(a, s_tile, s_row, t);
+            const Tile N = find_tile<128>(a, s_tile, s_row, t);
+            const int o = (2 * N.ot + half) * HALF, block = o / 128;
             here = m < N.rows;
-            there = 2 * N.ot + half < a.NB;
+            if (kParts > 1) split = min(HALF, 128 * (block + 1) - o);
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) there[p] = block + p < a.NB;
             xs = a.xs + (size_t)(N.m0 + m) * a.KB;
-            ws = static_cast<const typename SC::T *>(a.ws) + ((size_t)N.e * a.NB + 2 * N.ot + half) * a.KB;
+            ws = static_cast<const typename SC::T *>(a.ws) + ((size_t)N.e * a.NB + block) * a.KB;
             fetch(0);
         };
         // One K block: the half's sums, times both scales, onto acc.  Scalar
         // FMAs: packed ones need their operands moved into pairs, 79 us
         // against 70 for 512 tokens of 16384 x 7168.
-        auto promote = [&](float f) {
-            const uint32_t odd = it & 1u, b = 2 * odd + half, tb = tq + odd * 256;
-            wait_warp(&acc_full[b], (it >> 1) & 1);
+        auto promote = [&](const float (&f)[kParts]) {
+            const uint32_t odd = it & 1u, tb = tq + odd * 256;
+            wait_warp(&acc_full[odd], (it >> 1) & 1);
             tc_fence_after();
-            Sums v;
-            load(tb, v);
+            Sums v[2];
+            load(tb, v[0]);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                landed(v);
-                if (x == 3) {
+            for (int x = 0; x < HALF / 32; ++x) {
+                landed(v[x & 1]);
+                if (x < HALF / 32 - 1) {
+                    load(tb + 32 * (x + 1), v[(x + 1) & 1]);
+                } else {
                     // the sums are in registers: the next MMAs may have the buffer
                     tc_fence_before();
                     __syncwarp();
-                    arrive_if<PAIR>(lane == 0, PAIR ? map_rank(smem_addr(&acc_empty[b]), 0) : smem_addr(&acc_empty[b]));
+                    arrive_if(lane == 0, &acc_empty[odd]);
                 }
+                const float fx = kParts == 1 || 32 * x < split ? f[0] : f[kParts - 1];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) acc[x][j] = fmaf(__uint_as_float(v.r[j]), f, acc[x][j]);
-                if (x < 3) load(tb + 32 * (x + 1), v);
+                for (int j = 0; j < 32; ++j) acc[x][j] = fmaf(__uint_as_float(v[x & 1].r[j]), fx, acc[x][j]);
             }
             ++it;
         };
         auto tile_sums = [&]() {
             for (int k = 0; k < a.KB; k += kAhead) {
-                float f[kAhead];
+                float f[kAhead][kParts];
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i) f[i] = next_x[i] * next_w[i];
+                for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+                    for (int p = 0; p < kParts; ++p) f[i][p] = next_x[i] * next_w[p][i];
                 fetch(k + kAhead);
                 const int n = min(kAhead, a.KB - k);
 #pragma unroll
@@ -283,7 +289,7 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int tok = 8 * i + (lane >> 2), mt = side * 128 + q * 32 + 16 * x + tok;
+                    const int tok = 8 * i + (lane >> 2), mt = q * 32 + 16 * x + tok;
                     const uint4 v = *reinterpret_cast<const uint4 *>(strip + tok * kOutStride + 16 * part);
                     if (mt >= L.rows || at >= a.O) continue;
                     unsigned char *y = static_cast<unsigned char *>(a.Y) + ((size_t)(L.m0 + mt) * a.O + at) * esz;
@@ -308,14 +314,16 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
         if (first < tiles) begin(first);
         for (int t = first; t < tiles; t += step) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) acc[0][j] = acc[1][j] = acc[2][j] = acc[3][j] = 0.f;
+            for (int x = 0; x < HALF / 32; ++x)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) acc[x][j] = 0.f;
             tile_sums();
             if (t + step < tiles) begin(t + step);
-            const Tile L = find_tile<C::kTokens>(a, s_tile, s_row, t);    // looked up again: no register holds it over the sums
-            if (side * 128 + q * 32 >= L.rows) continue;
+            const Tile L = find_tile<128>(a, s_tile, s_row, t);    // looked up again: no register holds it over the sums
+            if (q * 32 >= L.rows) continue;
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const int o = L.ot * 256 + half * 128 + y * 32;
+            for (int y = 0; y < HALF / 32; ++y) {
+                const int o = (2 * L.ot + half) * HALF + y * 32;
                 if (o >= a.O) continue;
                 uint32_t w[16];
                 if (a.y_type == kF32) {
@@ -338,56 +346,44 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     __syncthreads();
     if (warp == kWarpIssue) {
         tc_fence_after();
-        tmem_free<PAIR>(tmem, kBufs * 128);
+        tmem_free(tmem, kBufs * 256);
     }
-    if (PAIR) cluster_barrier();           // no block leaves while the other may still reach it
 }
 
-int pairs_at_once() {
-    static PerContext<int> cache;
-    int n = 0;
-    const int rc = cache.get(&n, [&](int *out) {
-        return count_clusters(gemm_e4m3_many_kernel<true, ScaleF32>, kThreads, CfgMany<true>::kSmemBytes, 2, out);
-    });
-    return rc == kOk ? n : 0;
-}
-
-template <bool PAIR, class SC>
+template <int HALF, class SC>
 int launch_as(const char *what, int blocks, const CUtensorMap &w, const CUtensorMap &x, const Args8 &a, cudaStream_t st) {
-    using C = CfgMany<PAIR>;
-    set_max_dynamic_smem(reinterpret_cast<const void *>(gemm_e4m3_many_kernel<PAIR, SC>), (int)C::kSmemBytes);
-    return launch_clusters(what, gemm_e4m3_many_kernel<PAIR, SC>, blocks, kThreads, C::kCtas, C::kSmemBytes, st, w, x, a);
+    using C = CfgMany<HALF>;
+    set_max_dynamic_smem(reinterpret_cast<const void *>(gemm_e4m3_many_kernel<HALF, SC>), (int)C::kSmemBytes);
+    return launch_pdl(what, gemm_e4m3_many_kernel<HALF, SC>, blocks, kThreads, C::kSmemBytes, st, w, x, a);
 }
 
 }  // namespace
 
 ManyPlan plan_many(int M, int I, int O, int experts) {
-    const int KB = (I + 127) / 128, NT = (O + 255) / 256, filled = std::min(experts, M);
-    ManyPlan best{false, num_sms(), 0.0};
-    for (int pair = 0; pair <= 1; ++pair) {
-        const int tokens = 128 * (pair + 1), n = pair ? pairs_at_once() : num_sms();
-        if (n < 1) break;
-        const double per_output = token_tiles(M, experts, tokens), tiles = NT * per_output;
+    const int KB = (I + 127) / 128, n = num_sms(), filled = std::min(experts, M);
+    const double per_output = token_tiles(M, experts, 128);
+    ManyPlan best{128, n, 0.0};
+    for (int half = 128; half >= 96; half -= 32) {
+        const double tiles = (double)((O + 2 * half - 1) / (2 * half)) * per_output;
         // cycles of a K block, as measured; where an expert's weights serve one
-        // tile alone, what 32 KB of them take an SM at the card's bandwidth
-        const double step = (pair ? 2.0 : 1.0) * per_output < 1.5 * (experts == 1 ? 1 : filled) ? 1400.0 : pair ? 900.0 : 880.0;
-        const double cost = std::max(1.0, std::ceil(tiles / n)) * (KB * step + 3000.0);
-        if (!pair || cost < best.cost) best = ManyPlan{pair != 0, n * (pair + 1), cost};
+        // tile alone, what a tile's take an SM at the card's bandwidth
+        const double step = per_output < 1.5 * (experts == 1 ? 1 : filled) ? 2 * half * 5.5 : half == 128 ? 880.0 : 680.0;
+        const double cost = std::ceil(tiles / n) * (KB * step + 3000.0);
+        if (half == 128 || cost < best.cost) best = ManyPlan{half, n, cost};
     }
     return best;
 }
 
 int launch_many(const char *what, const ManyPlan &p, const E4m3Args &g, Args8 a, cudaStream_t st) {
     CUtensorMap w, x;
-    if (!encode_map(&w, g.w, (long long)g.experts * g.O, g.I, p.pair ? CfgMany<true>::kBoxRows : CfgMany<false>::kBoxRows) ||
-        !encode_map(&x, g.X, g.M, g.I, 128))
+    if (!encode_map(&w, g.w, (long long)g.experts * g.O, g.I, p.half) || !encode_map(&x, g.X, g.M, g.I, 128))
         QG_REFUSE(kECuda, "%s: tensor map refused", what);
-    a.NT = (a.NB + 1) / 2;
-    if (p.pair)
-        return g.w_power ? launch_as<true, ScaleE8M0>(what, p.blocks, w, x, a, st)
-                         : launch_as<true, ScaleF32>(what, p.blocks, w, x, a, st);
-    return g.w_power ? launch_as<false, ScaleE8M0>(what, p.blocks, w, x, a, st)
-                     : launch_as<false, ScaleF32>(what, p.blocks, w, x, a, st);
+    a.NT = (g.O + 2 * p.half - 1) / (2 * p.half);
+    if (p.half == 96)
+        return g.w_power ? launch_as<96, ScaleE8M0>(what, p.blocks, w, x, a, st)
+                         : launch_as<96, ScaleF32>(what, p.blocks, w, x, a, st);
+    return g.w_power ? launch_as<128, ScaleE8M0>(what, p.blocks, w, x, a, st)
+                     : launch_as<128, ScaleF32>(what, p.blocks, w, x, a, st);
 }
 
 }  // namespace e8

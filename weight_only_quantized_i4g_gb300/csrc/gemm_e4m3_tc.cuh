@@ -28,96 +28,51 @@ struct Args8 {
     const float *xs;
     const void *ws;
     const int *offsets;               // NULL: one expert, rows [0, M)
-    int experts, M, O, KB, NB, NT;    // K blocks, 128-output blocks, output tiles
+    int experts, M, O, KB, NB, NT;    // K blocks, 128-output blocks, output tiles (set by the launch)
     int *err;
 };
 
-// Instruction descriptor of kind::f8f6f4: f32 accumulator, e4m3 A and B (format code 0), K-major, M = m, N = n.
-__device__ __forceinline__ uint32_t idesc_e4m3(int m, int n) {
-    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+// Instruction descriptor of kind::f8f6f4: f32 accumulator, e4m3 A and B (format code 0), K-major, M = 128, N = n.
+__device__ __forceinline__ uint32_t idesc_e4m3(int n) {
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kMmaM >> 4) << 24);
 }
-// PAIR: one MMA of two blocks; their A rows make M = 256, and each holds half of B's rows.
-template <bool PAIR>
 __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                          uint32_t accumulate) {
-    if constexpr (PAIR)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-            : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
-// Arrive on `bar` (PAIR: on both blocks' barriers of that place) once every MMA this thread has issued is done.
-template <bool PAIR>
-__device__ __forceinline__ void commit_to(uint64_t *bar, uint16_t both) {
-    if constexpr (PAIR)
-        asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                smem_addr(bar)),
-            "h"(both)
-            : "memory");
-    else
-        mma_commit(bar);
-}
-// PAIR: the copy counts on the first block's barrier (`bar`: its cluster address).
-template <bool PAIR>
-__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
-    if constexpr (PAIR)
-        asm volatile(
-            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-            "[%1, {%2, %3}], [%4];" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-            "[%4];" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-            : "memory");
-}
+
 // The two words of sw128_desc: where an operand starts, in 16 bytes (32 bytes
 // further along K: + 2), and what never changes.  One thread issues the MMAs,
 // and every instruction before them is on the K step's way.
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return (saddr & 0x3FFFFu) >> 4 | 1u << 16; }
 constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
 // Four MMAs along K, the first of which starts the sums.
-template <bool PAIR>
 __device__ __forceinline__ void mma_block(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
 #pragma unroll
     for (uint32_t kk = 0; kk < 4; ++kk)
-        mma_e4m3<PAIR>(d_tmem, (uint64_t)kDescHi << 32 | (a_lo + 2 * kk), (uint64_t)kDescHi << 32 | (b_lo + 2 * kk), idesc,
-                       kk > 0 ? 1u : 0u);
+        mma_e4m3(d_tmem, (uint64_t)kDescHi << 32 | (a_lo + 2 * kk), (uint64_t)kDescHi << 32 | (b_lo + 2 * kk), idesc,
+                 kk > 0 ? 1u : 0u);
 }
-template <bool PAIR>
+// A box of a tensor map on its way from memory to L2.
+__device__ __forceinline__ void prefetch_tile(const CUtensorMap *map, int c0, int c1) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1)
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_alloc(volatile uint32_t *slot, uint32_t cols) {
-    if constexpr (PAIR) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_addr((const void *)slot)),
-                     "r"(cols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-    } else {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_addr((const void *)slot)),
-                     "r"(cols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr((const void *)slot)),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
 }
-template <bool PAIR>
 __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
-    if constexpr (PAIR)
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
-    else
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
 }
 
 // a += (lo, hi) * f, two f32 at a time
@@ -139,25 +94,13 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t local, int rank) {
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// One lane's arrival without a branch (a branch costs the warp some 100
-// cycles).  REMOTE: at a barrier's cluster address; it publishes no memory, as
-// tensor memory has its own fences: the release and acquire of the whole
-// cluster, which it spares, took a K step of a block pair from 1600 to 2700
-// cycles.
-template <bool REMOTE>
-__device__ __forceinline__ void arrive_if(bool yes, uint32_t bar) {
-    if constexpr (REMOTE)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t"
-            "@p mbarrier.arrive.shared::cluster.b64 _, [%1];\n\t}" ::"r"((int)yes),
-            "r"(bar)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t"
-            "@p mbarrier.arrive.shared::cta.b64 _, [%1];\n\t}" ::"r"((int)yes),
-            "r"(bar)
-            : "memory");
+// One lane's arrival without a branch (a branch costs the warp some 100 cycles).
+__device__ __forceinline__ void arrive_if(bool yes, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t"
+        "@p mbarrier.arrive.shared::cta.b64 _, [%1];\n\t}" ::"r"((int)yes),
+        "r"(smem_addr(bar))
+        : "memory");
 }
 __device__ __forceinline__ float load_remote(uint32_t addr) {
     float v;
@@ -325,8 +268,7 @@ struct FewPlan {
     double cost;
 };
 struct ManyPlan {
-    bool pair;
-    int blocks;
+    int half, blocks;                 // outputs of half a tile
     double cost;
 };
 FewPlan plan_few(int M, int I, int O, int experts);
