@@ -53,7 +53,7 @@ def held(y, want, mag, yt):
 
 DENSE = [(1, 16, 1), (1, 128, 128), (1, 7168, 256), (3, 272, 130), (8, 2048, 500), (17, 1040, 129), (33, 128, 1000),
          (64, 4096, 128), (65, 512, 384), (130, 640, 200), (200, 1152, 1), (257, 256, 257), (300, 2064, 640), (700, 384, 513),
-         (1024, 1024, 1024), (16, 16384, 128), (513, 5120, 264)]
+         (1024, 1024, 1024), (16, 16384, 128), (513, 5120, 264), (3001, 1040, 1500), (2500, 128, 2100), (129, 16384, 2050)]
 
 
 @pytest.mark.parametrize("m,i,o", DENSE)
@@ -98,7 +98,8 @@ def test_odd_addresses(qg, ax, aw, ay):
 
 GROUPS = [([1], 128, 128), ([0, 1, 0], 256, 130), ([1] * 8, 7168, 256), ([0, 0, 5], 272, 128), ([3, 0, 17, 64, 0, 1], 512, 200),
           ([64, 64, 64, 64], 256, 128), ([100, 1, 0, 300, 28], 640, 264), ([0] * 30 + [7] + [0] * 33, 384, 150),
-          ([13] * 37, 256, 384), ([700, 2, 65], 384, 513), ([2, 1] * 40, 1152, 128), ([255, 257, 256, 1], 1024, 300)]
+          ([13] * 37, 256, 384), ([700, 2, 65], 384, 513), ([2, 1] * 40, 1152, 128), ([255, 257, 256, 1], 1024, 300),
+          ([900, 0, 129, 1, 1000, 128, 640], 1040, 1380), ([300] * 9 + [0] * 700 + [17] * 300, 128, 400)]
 
 
 @pytest.mark.parametrize("counts,i,o", GROUPS)
@@ -165,6 +166,44 @@ def test_nan_stays_in_its_row_and_column(qg):
     nan[:20, 170] = True
     assert sum(counts) == 60 and torch.equal(torch.isnan(y), nan)
     assert bool((y[60:] == 7).all())
+
+
+@pytest.mark.parametrize("counts,i,o", [([3, 0, 30], 272, 130), ([900, 700, 1], 1040, 1300), ([3, 30], 271, 70)])
+def test_rows_before_the_first_expert_stay(qg, counts, i, o):
+    bounds = [11]
+    for c in counts:
+        bounds.append(bounds[-1] + c)
+    m = bounds[-1] + 2
+    x, w = codes((m, i), 1), codes((len(counts), o, i), 2)
+    xs, ws = scales((m, blocks(i)), 3, False), scales((len(counts), blocks(o), blocks(i)), 4, False)
+    y = guarded((m, o), torch.bfloat16)
+    qg.check(call(qg, y, x, xs, w, ws, ints(bounds)))
+    want, mag = product(x, xs, w, ws, bounds)
+    assert held(y[11:-2], want[11:-2], mag[11:-2], "bf16")
+    assert bool((y[:11] == 7).all()) and bool((y[-2:] == 7).all()) and unharmed(y)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -40, 2.0 ** 40, 0.0])
+def test_scales_far_from_one(qg, scale):
+    """Scales whose product is a normal f32 keep every bit: times a power of two the result is the same bits, scaled."""
+    m, i, o = 70, 640, 140
+    x, w = codes((m, i), 1), codes((1, o, i), 2)
+    xs, ws = scales((m, 5), 3, False), scales((1, 2, 5), 4, False)
+    y, z = guarded((m, o), torch.float32), guarded((m, o), torch.float32)
+    qg.check(call(qg, y, x, xs, w, ws))
+    qg.check(call(qg, z, x, xs * scale, w, ws))
+    assert torch.equal(z, y * scale)
+
+
+@pytest.mark.parametrize("m,o", [(20, 200), (1500, 1300)])
+def test_infinite_and_nan_scales_stay_in_their_tokens(qg, m, o):
+    x, w = codes((m, 384), 1), codes((1, o, 384), 2)
+    xs, ws = scales((m, 3), 3, False), scales((1, blocks(o), 3), 4, False)
+    xs[5, 1], xs[7, 2] = float("inf"), float("nan")
+    y = guarded((m, o), torch.float32)
+    qg.check(call(qg, y, x, xs, w, ws))
+    bad = ~torch.isfinite(y)
+    assert bool(bad[5].all()) and bool(bad[7].all()) and int(bad.any(1).sum()) == 2
 
 
 @pytest.mark.parametrize("table", [[0, 10, 5, 30], [-5, 10, 20, 30], [0, 10, 20, 99], [40, 50, 2 ** 31 - 1, -2 ** 31]])

@@ -62,12 +62,19 @@ struct ScaleF32 {
     static constexpr const char *kGemmTc = "qgemm_fp8b128 (tensor-core kernel)";
     static constexpr const char *kGemmGeneral = "qgemm_fp8b128 (general kernel)";
     __device__ static float get(const float *p, size_t i) { return ld_nc_f32(p + i); }
-    // four from a 16-byte address, or zeros
-    __device__ static void get4(float (&v)[4], const float *p, bool there) {
-        float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (there) u = __ldg(reinterpret_cast<const float4 *>(p));
-        v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
-    }
+    // Four scales as loaded (`fours`: from a 16-byte address), to be read later.
+    struct Four {
+        float v[4];
+        __device__ void load(const float *p, int n, bool fours) {
+            if (fours) {
+                const float4 u = n > 0 ? __ldg(reinterpret_cast<const float4 *>(p)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+            } else {
+                for (int i = 0; i < 4; ++i) v[i] = i < n ? ld_nc_f32(p + i) : 0.f;
+            }
+        }
+        __device__ float get(int i) const { return v[i]; }
+    };
 };
 struct ScaleE8M0 {
     typedef uint8_t T;
@@ -76,12 +83,20 @@ struct ScaleE8M0 {
     static constexpr const char *kGemmTc = "qgemm_fp8ue8m0 (tensor-core kernel)";
     static constexpr const char *kGemmGeneral = "qgemm_fp8ue8m0 (general kernel)";
     __device__ static float get(const uint8_t *p, size_t i) { return e8m0_to_f32(__ldg(p + i)); }
-    // four from a 4-byte address, or zeros
-    __device__ static void get4(float (&v)[4], const uint8_t *p, bool there) {
-        uint32_t u = 0;
-        if (there) u = __ldg(reinterpret_cast<const uint32_t *>(p));
-        for (int i = 0; i < 4; ++i) v[i] = there ? e8m0_to_f32(u >> (8 * i) & 0xFFu) : 0.f;
-    }
+    // Four scales as loaded (`fours`: from a 4-byte address), to be read later.
+    struct Four {
+        uint32_t w;
+        __device__ void load(const uint8_t *p, int n, bool fours) {
+            if (fours) {
+                w = n > 0 ? __ldg(reinterpret_cast<const uint32_t *>(p)) : 0u;
+            } else {
+                w = 0u;
+                for (int i = 0; i < 4; ++i)
+                    if (i < n) w |= (uint32_t)__ldg(p + i) << (8 * i);
+            }
+        }
+        __device__ float get(int i) const { return e8m0_to_f32(w >> (8 * i) & 0xFFu); }
+    };
 };
 __device__ __forceinline__ uint32_t ld_nc_u32(const void *p) {
     uint32_t v;

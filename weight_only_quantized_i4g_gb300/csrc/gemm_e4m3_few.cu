@@ -480,7 +480,7 @@ FewPlan plan_few(int M, int I, int O, int experts) {
         // reduction over a cluster
         const double step = best.bt == 128 ? 1370.0 : best.bt == 64 ? 800.0 : 700.0, rounds = best.bt / 32;
         const double waves = std::ceil(tiles / n);
-        const double cost = waves * (((KB + c - 1) / c) * step + (c > 1 ? 1500.0 * rounds : 0.0) + 1500.0);
+        const double cost = waves * (((KB + c - 1) / c) * step + (c > 1 ? 2500.0 * rounds : 0.0) + 1500.0);
         if (c == 1 || cost < best.cost) best = FewPlan{best.bt, c, n * c, cost};
     }
     return best;

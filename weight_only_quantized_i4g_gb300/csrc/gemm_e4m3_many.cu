@@ -1,25 +1,24 @@
 // gemm_e4m3_many.cu -- products of e4m3 activations with e4m3 weights, many
 // tokens an expert: the tensor cores and what feeds and empties them bound it.
 //
-// A tile is 128 tokens (MMA M) by 256 or 192 outputs, two halves of N = 128 or
-// 96, so a promoting thread holds one token and scales 32 columns by one
-// factor.  (With the tokens along N a factor a column has to be read from
-// shared memory: 64 columns then take a warp 290 cycles instead of 134, and a
-// K block 1800 instead of the MMAs' 512.)  Shared memory bounds it: a K block's
-// MMAs read 64 KB and TMA writes 48, which takes 875 cycles at 128 bytes a
-// cycle; it takes 880.  Block pairs that share an MMA (half the weights a
-// block) were built and measured 0 to 10% slower: their signals cross SMs.
+// A tile is 128 tokens (MMA M) by 256 outputs (N), two halves with a weight
+// scale each, so a promoting thread holds one token and scales a half's sums by
+// one factor.  (With the tokens along N a factor a column has to be read from
+// shared memory: 64 columns then take a warp 290 cycles instead of 134, and a K
+// block 1800 instead of the MMAs' 512.)  A K block takes about 790 cycles: its
+// MMAs read 48 KB of shared memory and TMA writes as much, 750 cycles at 128
+// bytes a cycle (as two MMAs of N = 128 it took 880: the tokens' codes are read
+// twice).  Measured and left out: block pairs that share an MMA (half the
+// weights a block; 0 to 10% slower, their signals cross SMs) and tiles of 192
+// outputs (a K block takes the same time).
 // One persistent thread block per SM:
-//   warps 0, 1   TMA producers, K blocks in turn: 128 x 128 codes of X and both
-//                halves' of W, 128-byte swizzled
-//   warps 2..5   issue the MMAs, each every second K block of one half; its four leave the half's sums in one of four
-//                buffers (one producer and two issuers took 81 us where these
-//                take 50, without the promotion)
-//   warps 8..15  promote: tensor-memory lanes 32 (w % 4) .. + 31, one half
-//                each, so that a scheduler's two warps are at different points
-//                of their K blocks; a thread loads its token's scales and its
-//                half's (of the one or two 128-blocks it lies in) four K blocks
-//                ahead
+//   warps 0, 1   TMA producers, K blocks in turn: 128 x 128 codes of X and
+//                256 x 128 of W, 128-byte swizzled
+//   warps 2, 3   issue the MMAs, K blocks in turn; a block's four leave its sums
+//                in one of two buffers of tensor memory
+//   warps 4..11  promote: tensor-memory lanes 32 (w % 4) .. + 31, one half
+//                each; a thread loads its token's scales and its half's four K
+//                blocks ahead
 #include "gemm_e4m3_tc.cuh"
 
 namespace qg {
@@ -32,25 +31,18 @@ constexpr int kWarpIssue = 2, kWarpPromote = 4, kWarps = 8, kThreads = 32 * (kWa
 constexpr int kBufs = 2;               // tensor-memory buffers of 256 columns
 constexpr int kOutStride = 80;         // bytes between the tokens (64 each) of a strip on its way out: eight lanes' 16 bytes meet no bank twice
 
-template <int HALF>                    // outputs of half a tile
-struct CfgMany {
-    static constexpr uint32_t kXBytes = 128 * 128, kWBytes = HALF * 128;
-    static constexpr uint32_t kStageBytes = kXBytes + 2 * kWBytes;
-    static constexpr uint32_t kOutAll = kWarps * 16 * kOutStride;   // strips of 16 tokens
-    static constexpr uint32_t kBarBytes = 256;
-    static constexpr int kStages = ~1 & (int)((kSmemBudget - 1024 - 256 - kOutAll - kTableBytes - kBarBytes) / kStageBytes);
-    static constexpr int kNumBars = 2 * kStages + 2 * kBufs;
-    static constexpr uint32_t kOutOff = kStages * kStageBytes;
-    static constexpr uint32_t kBarOff = kOutOff + kOutAll;
-    static constexpr uint32_t kTableOff = kBarOff + kBarBytes;
-    static constexpr uint32_t kSmemBytes = 1024 + kTableOff + kTableBytes;
-    static_assert(kStages >= 3 && kNumBars * 8 + 16 <= (int)kBarBytes, "");
-    // A wait tells one phase of a barrier from the next, not from the one
-    // after that, so a stage must always be the same warps': with an odd
-    // number of stages one could pass on a phase that the other had not seen
-    // begin.
-    static_assert(kStages % 2 == 0 && kBufs == 2, "a stage and a buffer belong to the same producer and issuer every time");
-};
+constexpr uint32_t kXBytes = 128 * 128, kWBytes = 256 * 128, kStageBytes = kXBytes + kWBytes;
+constexpr uint32_t kOutAll = kWarps * 16 * kOutStride;             // strips of 16 tokens
+constexpr uint32_t kBarBytes = 256;
+constexpr int kStages = ~1 & (int)((kSmemBudget - 1024 - 256 - kOutAll - kTableBytes - kBarBytes) / kStageBytes);
+constexpr int kNumBars = 2 * kStages + 2 * kBufs;
+constexpr uint32_t kOutOff = kStages * kStageBytes, kBarOff = kOutOff + kOutAll, kTableOff = kBarOff + kBarBytes;
+constexpr uint32_t kSmemBytes = 1024 + kTableOff + kTableBytes;
+static_assert(kStages >= 3 && kNumBars * 8 + 16 <= (int)kBarBytes, "");
+// A wait tells one phase of a barrier from the next, not from the one after
+// that, so a stage must always be the same warps': with an odd number of
+// stages one could pass on a phase that the other had not seen begin.
+static_assert(kStages % 2 == 0 && kBufs == 2, "a stage and a buffer belong to the same producer and issuer every time");
 
 // 32 columns of this warp's 32 lanes, to be read after landed() on the same registers.
 struct Sums {
@@ -83,24 +75,23 @@ __device__ __forceinline__ void landed(Sums &s) {
     pass(s.r + 16);
 }
 
-template <int HALF, class SC>
+template <class SC>
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Args8 a) {
-    using C = CfgMany<HALF>;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw_base = smem_addr(smem_raw);
     unsigned char *smem = smem_raw + ((1024u - (raw_base & 1023u)) & 1023u);
     const uint32_t sbase = smem_addr(smem);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kBarOff);
-    uint64_t *full = bars, *empty = full + C::kStages, *acc_full = empty + C::kStages, *acc_empty = acc_full + kBufs;
-    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(bars + C::kNumBars);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kBarOff);
+    uint64_t *full = bars, *empty = full + kStages, *acc_full = empty + kStages, *acc_empty = acc_full + kBufs;
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(bars + kNumBars);
     volatile uint32_t *abort = tmem_slot + 1;
-    int *s_tile = reinterpret_cast<int *>(smem + C::kTableOff), *s_row = s_tile + kMaxExperts + 2;
+    int *s_tile = reinterpret_cast<int *>(smem + kTableOff), *s_row = s_tile + kMaxExperts + 2;
     __shared__ int2 s_warp[kThreads / 32];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::kStages; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
@@ -136,43 +127,53 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     if (warp < kWarpPromote) {
         regs_down<56>();
         if (warp < kWarpIssue) {
+            // What comes from memory goes to L2 kPrefetchAhead K blocks before
+            // its copy, over the tile's end: weights by the tile that holds an
+            // expert's first tokens, activations by the one of its first outputs.
+            auto prefetch = [&](const Tile &L, int k) {
+                if (L.m0 == s_row[2 * L.e]) prefetch_tile(&tmW, k * 128, L.e * a.O + L.ot * 256);
+                if (L.ot == 0) prefetch_tile(&tmX, k * 128, L.m0);
+            };
             uint32_t it = 0;
+            Tile L, next;
+            if (first < tiles) next = find_tile<128>(a, s_tile, s_row, first);
             for (int t = first; t < tiles; t += step) {
-                const Tile L = find_tile<128>(a, s_tile, s_row, t);
-                const int wrow = L.e * a.O + L.ot * 2 * HALF;
+                L = next;
+                if (t + step < tiles) next = find_tile<128>(a, s_tile, s_row, t + step);
+                const int wrow = L.e * a.O + L.ot * 256;
                 for (int k = 0; k < a.KB; ++k, ++it) {
                     if ((it & 1u) != (uint32_t)warp) continue;
-                    const uint32_t s = it % C::kStages, r = it / C::kStages;
+                    const uint32_t s = it % kStages, r = it / kStages;
                     if (r > 0) wait_warp(&empty[s], (r & 1) ^ 1);
                     if (lane == 0) {
-                        const uint32_t st = sbase + s * C::kStageBytes;
-                        mbar_arrive_expect_tx(&full[s], C::kStageBytes);
+                        const uint32_t st = sbase + s * kStageBytes;
+                        mbar_arrive_expect_tx(&full[s], kStageBytes);
                         tma_load_2d(st, &tmX, k * 128, L.m0, &full[s]);
-                        for (int h = 0; h < 2; ++h)
-                            tma_load_2d(st + C::kXBytes + h * C::kWBytes, &tmW, k * 128, wrow + h * HALF, &full[s]);
-                        if (k + kPrefetchAhead < a.KB && L.m0 == s_row[2 * L.e])
-                            for (int h = 0; h < 2; ++h) prefetch_tile(&tmW, (k + kPrefetchAhead) * 128, wrow + h * HALF);
+                        tma_load_2d(st + kXBytes, &tmW, k * 128, wrow, &full[s]);
+                        const int ahead = k + kPrefetchAhead;
+                        if (ahead < a.KB) prefetch(L, ahead);
+                        else if (t + step < tiles && ahead - a.KB < a.KB) prefetch(next, ahead - a.KB);
                     }
                     __syncwarp();
                 }
             }
             // Every copy issued must have landed, and every commit arrived, before the block exits.
-            for (uint32_t j = it > (uint32_t)C::kStages ? it - C::kStages : 0; j < it; ++j) {
+            for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0; j < it; ++j) {
                 if ((j & 1u) != (uint32_t)warp) continue;
-                wait_warp(&full[j % C::kStages], (j / C::kStages) & 1);
-                wait_warp(&empty[j % C::kStages], (j / C::kStages) & 1);
+                wait_warp(&full[j % kStages], (j / kStages) & 1);
+                wait_warp(&empty[j % kStages], (j / kStages) & 1);
             }
         } else {
             // No K block's sums depend on another's, so two warps issue them in
             // turn: each one's waits and commits pass while the other's MMAs run.
             uint32_t it = 0;
-            const uint32_t odd = warp - kWarpIssue, d = tmem + odd * 256, idesc = idesc_e4m3(2 * HALF);
-            const uint32_t x_lo = desc_lo(sbase), w_lo = desc_lo(sbase + C::kXBytes);
+            const uint32_t odd = warp - kWarpIssue, d = tmem + odd * 256, idesc = idesc_e4m3(256);
+            const uint32_t x_lo = desc_lo(sbase), w_lo = desc_lo(sbase + kXBytes);
             for (int t = first; t < tiles; t += step) {
                 for (int k = 0; k < a.KB; ++k, ++it) {
                     if ((it & 1u) != odd) continue;
-                    const uint32_t s = it % C::kStages, r = it / C::kStages, rb = it / 2;
-                    const uint32_t at = s * (C::kStageBytes >> 4);
+                    const uint32_t s = it % kStages, r = it / kStages, rb = it / 2;
+                    const uint32_t at = s * (kStageBytes >> 4);
                     wait_warp(&full[s], r & 1);
                     if (rb > 0) wait_warp(&acc_empty[odd], (rb & 1) ^ 1);
                     tc_fence_after();
@@ -188,17 +189,14 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     } else {
         regs_up<224>();
         const int pw = warp - kWarpPromote, q = warp & 3, half = pw >> 2, m = q * 32 + lane;
-        const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16) + half * HALF;
+        const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16) + half * 128;
         uint32_t it = 0;
-        float acc[HALF / 32][32];          // token m of the tile, the half's columns 32 x .. + 31
-        // A half of 96 outputs may lie in two blocks of weight scales: its first
-        // `split` columns in one, the others in the next.
-        constexpr int kParts = HALF % 128 ? 2 : 1;
-        float next_x[kAhead], next_w[kParts][kAhead];
+        float acc[4][32];          // token m of the tile, the half's columns 32 x .. + 31
+        float next_x[kAhead];
+        typename SC::Four next_w;
         const float *xs;
         const typename SC::T *ws;
-        bool here, there[kParts];          // whether the tile has this token, and the blocks are there
-        int split = HALF;
+        bool here, there;                  // whether the tile has this token and this half
         // Whole fours of scales at 16-byte addresses (4-byte ones of UE8M0) come in one load.
         const bool fours = a.KB % kAhead == 0 && reinterpret_cast<uintptr_t>(a.xs) % 16 == 0 &&
                            reinterpret_cast<uintptr_t>(a.ws) % (kAhead * sizeof(typename SC::T)) == 0;
@@ -207,25 +205,17 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (here && k < a.KB) v = *reinterpret_cast<const float4 *>(xs + k);
                 next_x[0] = v.x, next_x[1] = v.y, next_x[2] = v.z, next_x[3] = v.w;
+            } else {
 #pragma unroll
-                for (int p = 0; p < kParts; ++p) SC::get4(next_w[p], ws + (size_t)p * a.KB + k, there[p] && k < a.KB);
-                return;
+                for (int c = 0; c < kAhead; ++c) next_x[c] = here && k + c < a.KB ? xs[k + c] : 0.f;
             }
-#pragma unroll
-            for (int c = 0; c < kAhead; ++c) {
-                next_x[c] = here && k + c < a.KB ? xs[k + c] : 0.f;
-#pragma unroll
-                for (int p = 0; p < kParts; ++p)
-                    next_w[p][c] = there[p] && k + c < a.KB ? SC::get(ws, (size_t)p * a.KB + k + c) : 0.f;
-            }
+            next_w.load(ws + k, there ? a.KB - k : 0, fours);
         };
         auto begin = [&](int t) {          // the tile's first scales are on their way
             const Tile N = find_tile<128>(a, s_tile, s_row, t);
-            const int o = (2 * N.ot + half) * HALF, block = o / 128;
+            const int block = 2 * N.ot + half;
             here = m < N.rows;
-            if (kParts > 1) split = min(HALF, 128 * (block + 1) - o);
-#pragma unroll
-            for (int p = 0; p < kParts; ++p) there[p] = block + p < a.NB;
+            there = block < a.NB;
             xs = a.xs + (size_t)(N.m0 + m) * a.KB;
             ws = static_cast<const typename SC::T *>(a.ws) + ((size_t)N.e * a.NB + block) * a.KB;
             fetch(0);
@@ -233,16 +223,16 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
         // One K block: the half's sums, times both scales, onto acc.  Scalar
         // FMAs: packed ones need their operands moved into pairs, 79 us
         // against 70 for 512 tokens of 16384 x 7168.
-        auto promote = [&](const float (&f)[kParts]) {
+        auto promote = [&](float f) {
             const uint32_t odd = it & 1u, tb = tq + odd * 256;
             wait_warp(&acc_full[odd], (it >> 1) & 1);
             tc_fence_after();
             Sums v[2];
             load(tb, v[0]);
 #pragma unroll
-            for (int x = 0; x < HALF / 32; ++x) {
+            for (int x = 0; x < 4; ++x) {
                 landed(v[x & 1]);
-                if (x < HALF / 32 - 1) {
+                if (x < 3) {
                     load(tb + 32 * (x + 1), v[(x + 1) & 1]);
                 } else {
                     // the sums are in registers: the next MMAs may have the buffer
@@ -250,19 +240,16 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
                     __syncwarp();
                     arrive_if(lane == 0, &acc_empty[odd]);
                 }
-                const float fx = kParts == 1 || 32 * x < split ? f[0] : f[kParts - 1];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) acc[x][j] = fmaf(__uint_as_float(v[x & 1].r[j]), fx, acc[x][j]);
+                for (int j = 0; j < 32; ++j) acc[x][j] = fmaf(__uint_as_float(v[x & 1].r[j]), f, acc[x][j]);
             }
             ++it;
         };
         auto tile_sums = [&]() {
             for (int k = 0; k < a.KB; k += kAhead) {
-                float f[kAhead][kParts];
+                float f[kAhead];
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i)
-#pragma unroll
-                    for (int p = 0; p < kParts; ++p) f[i][p] = next_x[i] * next_w[p][i];
+                for (int i = 0; i < kAhead; ++i) f[i] = next_x[i] * next_w.get(i);
                 fetch(k + kAhead);
                 const int n = min(kAhead, a.KB - k);
 #pragma unroll
@@ -272,12 +259,13 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
                 }
             }
         };
-        unsigned char *strip = smem + C::kOutOff + pw * 16 * kOutStride;
-        // 64 bytes a token through shared memory, so that four lanes store a token's.
-        auto store_strip = [&](const uint32_t (&w)[16], const Tile &L, int o) {
-            const int esz = a.y_type == kF32 ? 4 : 2, per16 = 16 / esz;
-            const bool lines = a.O % per16 == 0 && reinterpret_cast<uintptr_t>(a.Y) % 16 == 0;
-            const int part = lane & 3, at = o + part * per16;
+        // 64 bytes a token, of sixteen tokens at a time, go through shared memory,
+        // so that four lanes store a token's.
+        unsigned char *strip = smem + kOutOff + pw * 16 * kOutStride;
+        const int esz = a.y_type == kF32 ? 4 : 2, per16 = 16 / esz, part = lane & 3;
+        const bool lines = a.O % per16 == 0 && reinterpret_cast<uintptr_t>(a.Y) % 16 == 0;
+        // w: this lane's token's 64 bytes; y, at: where this lane's 16 bytes of the strip's first token go
+        auto store_strip = [&](const uint32_t (&w)[16], unsigned char *y, int at, int rows) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 if (lane >> 4 == x) {
@@ -288,11 +276,10 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
                 }
                 __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int tok = 8 * i + (lane >> 2), mt = q * 32 + 16 * x + tok;
+                for (int i = 0; i < 2; ++i, y += (size_t)8 * a.O * esz) {
+                    const int tok = 8 * i + (lane >> 2);
                     const uint4 v = *reinterpret_cast<const uint4 *>(strip + tok * kOutStride + 16 * part);
-                    if (mt >= L.rows || at >= a.O) continue;
-                    unsigned char *y = static_cast<unsigned char *>(a.Y) + ((size_t)(L.m0 + mt) * a.O + at) * esz;
+                    if (16 * x + tok >= rows || at >= a.O) continue;
                     if (lines) {
                         *reinterpret_cast<uint4 *>(y) = v;
                         continue;
@@ -314,29 +301,31 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
         if (first < tiles) begin(first);
         for (int t = first; t < tiles; t += step) {
 #pragma unroll
-            for (int x = 0; x < HALF / 32; ++x)
+            for (int x = 0; x < 4; ++x)
 #pragma unroll
                 for (int j = 0; j < 32; ++j) acc[x][j] = 0.f;
             tile_sums();
             if (t + step < tiles) begin(t + step);
             const Tile L = find_tile<128>(a, s_tile, s_row, t);    // looked up again: no register holds it over the sums
-            if (q * 32 >= L.rows) continue;
+            const int m0 = L.m0 + q * 32, rows = L.rows - q * 32, o0 = L.ot * 256 + half * 128;
+            if (rows <= 0) continue;
+            unsigned char *y = static_cast<unsigned char *>(a.Y) +
+                               ((size_t)(m0 + (lane >> 2)) * a.O + o0 + part * per16) * esz;
 #pragma unroll
-            for (int y = 0; y < HALF / 32; ++y) {
-                const int o = (2 * L.ot + half) * HALF + y * 32;
-                if (o >= a.O) continue;
+            for (int z = 0; z < 4; ++z) {
+                if (o0 + 32 * z >= a.O) break;
                 uint32_t w[16];
                 if (a.y_type == kF32) {
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(acc[y][16 * x + j]);
-                        store_strip(w, L, o + 16 * x);
+                        for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(acc[z][16 * x + j]);
+                        store_strip(w, y + (32 * z + 16 * x) * 4, o0 + 32 * z + 16 * x + part * per16, rows);
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) w[j] = pack_16(a.y_type, acc[y][2 * j], acc[y][2 * j + 1]);
-                    store_strip(w, L, o);
+                    for (int j = 0; j < 16; ++j) w[j] = pack_16(a.y_type, acc[z][2 * j], acc[z][2 * j + 1]);
+                    store_strip(w, y + 32 * z * 2, o0 + 32 * z + part * per16, rows);
                 }
             }
         }
@@ -350,40 +339,29 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     }
 }
 
-template <int HALF, class SC>
+template <class SC>
 int launch_as(const char *what, int blocks, const CUtensorMap &w, const CUtensorMap &x, const Args8 &a, cudaStream_t st) {
-    using C = CfgMany<HALF>;
-    set_max_dynamic_smem(reinterpret_cast<const void *>(gemm_e4m3_many_kernel<HALF, SC>), (int)C::kSmemBytes);
-    return launch_pdl(what, gemm_e4m3_many_kernel<HALF, SC>, blocks, kThreads, C::kSmemBytes, st, w, x, a);
+    set_max_dynamic_smem(reinterpret_cast<const void *>(gemm_e4m3_many_kernel<SC>), (int)kSmemBytes);
+    return launch_pdl(what, gemm_e4m3_many_kernel<SC>, blocks, kThreads, kSmemBytes, st, w, x, a);
 }
 
 }  // namespace
 
 ManyPlan plan_many(int M, int I, int O, int experts) {
-    const int KB = (I + 127) / 128, n = num_sms(), filled = std::min(experts, M);
-    const double per_output = token_tiles(M, experts, 128);
-    ManyPlan best{128, n, 0.0};
-    for (int half = 128; half >= 96; half -= 32) {
-        const double tiles = (double)((O + 2 * half - 1) / (2 * half)) * per_output;
-        // cycles of a K block, as measured; where an expert's weights serve one
-        // tile alone, what a tile's take an SM at the card's bandwidth
-        const double step = per_output < 1.5 * (experts == 1 ? 1 : filled) ? 2 * half * 5.5 : half == 128 ? 880.0 : 680.0;
-        const double cost = std::ceil(tiles / n) * (KB * step + 3000.0);
-        if (half == 128 || cost < best.cost) best = ManyPlan{half, n, cost};
-    }
-    return best;
+    const int KB = (I + 127) / 128, n = num_sms(), filled = experts == 1 ? 1 : std::min(experts, M);
+    const double per_output = token_tiles(M, experts, 128), tiles = (double)((O + 255) / 256) * per_output;
+    // cycles of a K block, as measured; where an expert's weights serve one
+    // tile alone, what 32 KB of them take an SM at the card's bandwidth
+    const double step = per_output < 1.5 * filled ? 1400.0 : 800.0;
+    return ManyPlan{n, std::ceil(tiles / n) * (KB * step + 5000.0)};
 }
 
 int launch_many(const char *what, const ManyPlan &p, const E4m3Args &g, Args8 a, cudaStream_t st) {
     CUtensorMap w, x;
-    if (!encode_map(&w, g.w, (long long)g.experts * g.O, g.I, p.half) || !encode_map(&x, g.X, g.M, g.I, 128))
+    if (!encode_map(&w, g.w, (long long)g.experts * g.O, g.I, 256) || !encode_map(&x, g.X, g.M, g.I, 128))
         QG_REFUSE(kECuda, "%s: tensor map refused", what);
-    a.NT = (g.O + 2 * p.half - 1) / (2 * p.half);
-    if (p.half == 96)
-        return g.w_power ? launch_as<96, ScaleE8M0>(what, p.blocks, w, x, a, st)
-                         : launch_as<96, ScaleF32>(what, p.blocks, w, x, a, st);
-    return g.w_power ? launch_as<128, ScaleE8M0>(what, p.blocks, w, x, a, st)
-                     : launch_as<128, ScaleF32>(what, p.blocks, w, x, a, st);
+    a.NT = (g.O + 255) / 256;
+    return g.w_power ? launch_as<ScaleE8M0>(what, p.blocks, w, x, a, st) : launch_as<ScaleF32>(what, p.blocks, w, x, a, st);
 }
 
 }  // namespace e8

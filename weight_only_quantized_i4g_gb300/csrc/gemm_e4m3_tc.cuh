@@ -268,7 +268,7 @@ struct FewPlan {
     double cost;
 };
 struct ManyPlan {
-    int half, blocks;                 // outputs of half a tile
+    int blocks;
     double cost;
 };
 FewPlan plan_few(int M, int I, int O, int experts);
