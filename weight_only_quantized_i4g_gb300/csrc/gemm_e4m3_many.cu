@@ -32,7 +32,7 @@ constexpr int kBufs = 2;               // tensor-memory buffers of 256 columns
 constexpr int kOutStride = 80;         // bytes between the tokens (64 each) of a strip on its way out: eight lanes' 16 bytes meet no bank twice
 
 constexpr uint32_t kXBytes = 128 * 128, kWBytes = 256 * 128, kStageBytes = kXBytes + kWBytes;
-constexpr uint32_t kOutAll = kWarps * 16 * kOutStride;             // strips of 16 tokens
+constexpr uint32_t kOutAll = kWarps * 32 * kOutStride;             // strips of 64 bytes of a warp's tokens
 constexpr uint32_t kBarBytes = 256;
 constexpr int kStages = ~1 & (int)((kSmemBudget - 1024 - 256 - kOutAll - kTableBytes - kBarBytes) / kStageBytes);
 constexpr int kNumBars = 2 * kStages + 2 * kBufs;
@@ -118,14 +118,14 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     const int tiles = s_tile[a.experts] * a.NT, first = blockIdx.x, step = gridDim.x;
 
     // 384 threads start with 168 registers each, 64512 in all, of which the
-    // promoting warps take 8 x 32 x 224 and the others 4 x 32 x 56.
+    // promoting warps take 8 x 32 x 232 and the others 4 x 32 x 40.
     // Every lane waits: with one lane's wait and a vote the warp goes on 170 cycles later.
     auto wait_warp = [&](uint64_t *bar, uint32_t parity) {
         if (!mbar_wait_or_abort(bar, parity, abort) && lane == 0) raise_device_error(a.err, kErrTimeout);
         __syncwarp();
     };
     if (warp < kWarpPromote) {
-        regs_down<56>();
+        regs_down<40>();
         if (warp < kWarpIssue) {
             // What comes from memory goes to L2 kPrefetchAhead K blocks before
             // its copy, over the tile's end: weights by the tile that holds an
@@ -136,10 +136,10 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
             };
             uint32_t it = 0;
             Tile L, next;
-            if (first < tiles) next = find_tile<128>(a, s_tile, s_row, first);
+            if (first < tiles) next = find_tile_warp<128>(a, s_tile, s_row, first);
             for (int t = first; t < tiles; t += step) {
                 L = next;
-                if (t + step < tiles) next = find_tile<128>(a, s_tile, s_row, t + step);
+                if (t + step < tiles) next = find_tile_warp<128>(a, s_tile, s_row, t + step);
                 const int wrow = L.e * a.O + L.ot * 256;
                 for (int k = 0; k < a.KB; ++k, ++it) {
                     if ((it & 1u) != (uint32_t)warp) continue;
@@ -187,7 +187,7 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
             }
         }
     } else {
-        regs_up<224>();
+        regs_up<232>();
         const int pw = warp - kWarpPromote, q = warp & 3, half = pw >> 2, m = q * 32 + lane;
         const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16) + half * 128;
         uint32_t it = 0;
@@ -212,7 +212,7 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
             next_w.load(ws + k, there ? a.KB - k : 0, fours);
         };
         auto begin = [&](int t) {          // the tile's first scales are on their way
-            const Tile N = find_tile<128>(a, s_tile, s_row, t);
+            const Tile N = find_tile_warp<128>(a, s_tile, s_row, t);
             const int block = 2 * N.ot + half;
             here = m < N.rows;
             there = block < a.NB;
@@ -259,44 +259,38 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
                 }
             }
         };
-        // 64 bytes a token, of sixteen tokens at a time, go through shared memory,
-        // so that four lanes store a token's.
-        unsigned char *strip = smem + kOutOff + pw * 16 * kOutStride;
+        // 64 bytes a token go through shared memory, so that four lanes store a token's.
+        unsigned char *strip = smem + kOutOff + pw * 32 * kOutStride;
         const int esz = a.y_type == kF32 ? 4 : 2, per16 = 16 / esz, part = lane & 3;
         const bool lines = a.O % per16 == 0 && reinterpret_cast<uintptr_t>(a.Y) % 16 == 0;
         // w: this lane's token's 64 bytes; y, at: where this lane's 16 bytes of the strip's first token go
         auto store_strip = [&](const uint32_t (&w)[16], unsigned char *y, int at, int rows) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                if (lane >> 4 == x) {
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4 *>(strip + lane * kOutStride + 16 * i) =
+                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<uint4 *>(strip + (lane & 15) * kOutStride + 16 * i) =
-                            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            for (int i = 0; i < 4; ++i, y += (size_t)8 * a.O * esz) {
+                const int tok = 8 * i + (lane >> 2);
+                const uint4 v = *reinterpret_cast<const uint4 *>(strip + tok * kOutStride + 16 * part);
+                if (tok >= rows || at >= a.O) continue;
+                if (lines) {
+                    *reinterpret_cast<uint4 *>(y) = v;
+                    continue;
                 }
-                __syncwarp();
+                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                if (esz == 4) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i, y += (size_t)8 * a.O * esz) {
-                    const int tok = 8 * i + (lane >> 2);
-                    const uint4 v = *reinterpret_cast<const uint4 *>(strip + tok * kOutStride + 16 * part);
-                    if (16 * x + tok >= rows || at >= a.O) continue;
-                    if (lines) {
-                        *reinterpret_cast<uint4 *>(y) = v;
-                        continue;
-                    }
-                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-                    if (esz == 4) {
+                    for (int e = 0; e < 4; ++e)
+                        if (at + e < a.O) reinterpret_cast<uint32_t *>(y)[e] = u[e];
+                } else {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (at + e < a.O) reinterpret_cast<uint32_t *>(y)[e] = u[e];
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (at + e < a.O) reinterpret_cast<uint16_t *>(y)[e] = (uint16_t)(u[e >> 1] >> (16 * (e & 1)));
-                    }
+                    for (int e = 0; e < 8; ++e)
+                        if (at + e < a.O) reinterpret_cast<uint16_t *>(y)[e] = (uint16_t)(u[e >> 1] >> (16 * (e & 1)));
                 }
-                __syncwarp();
             }
+            __syncwarp();
         };
         if (first < tiles) begin(first);
         for (int t = first; t < tiles; t += step) {
@@ -306,7 +300,7 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
                 for (int j = 0; j < 32; ++j) acc[x][j] = 0.f;
             tile_sums();
             if (t + step < tiles) begin(t + step);
-            const Tile L = find_tile<128>(a, s_tile, s_row, t);    // looked up again: no register holds it over the sums
+            const Tile L = find_tile_warp<128>(a, s_tile, s_row, t);    // looked up again: no register holds it over the sums
             const int m0 = L.m0 + q * 32, rows = L.rows - q * 32, o0 = L.ot * 256 + half * 128;
             if (rows <= 0) continue;
             unsigned char *y = static_cast<unsigned char *>(a.Y) +

@@ -206,6 +206,16 @@ struct Tile {
 // Tiles are numbered expert by expert, output tile by output tile, tokens
 // fastest: blocks of one wave share weights.
 template <int BT>
+__device__ __forceinline__ Tile tile_of(const Args8 &a, const int *s_tile, const int *s_row, int t, int e) {
+    const int nt = s_tile[e + 1] - s_tile[e], local = t - s_tile[e] * a.NT;
+    Tile r;
+    r.e = e;
+    r.ot = local / nt;
+    r.m0 = s_row[2 * e] + (local - r.ot * nt) * BT;
+    r.rows = min(s_row[2 * e + 1] - r.m0, BT);
+    return r;
+}
+template <int BT>
 __device__ __forceinline__ Tile find_tile(const Args8 &a, const int *s_tile, const int *s_row, int t) {
     int lo = 0, hi = a.experts;       // the last e with s_tile[e] * NT <= t
     while (hi - lo > 1) {
@@ -213,13 +223,18 @@ __device__ __forceinline__ Tile find_tile(const Args8 &a, const int *s_tile, con
         if (s_tile[mid] * a.NT <= t) lo = mid;
         else hi = mid;
     }
-    const int nt = s_tile[lo + 1] - s_tile[lo], local = t - s_tile[lo] * a.NT;
-    Tile r;
-    r.e = lo;
-    r.ot = local / nt;
-    r.m0 = s_row[2 * lo] + (local - r.ot * nt) * BT;
-    r.rows = min(s_row[2 * lo + 1] - r.m0, BT);
-    return r;
+    return tile_of<BT>(a, s_tile, s_row, t, lo);
+}
+// The same by a whole warp, in two votes.
+template <int BT>
+__device__ __forceinline__ Tile find_tile_warp(const Args8 &a, const int *s_tile, const int *s_row, int t) {
+    static_assert(kMaxExperts <= 32 * 32, "two votes of 32 lanes");
+    const int lane = threadIdx.x & 31, apart = (a.experts + 31) / 32;
+    const int far = lane * apart;
+    unsigned yes = __ballot_sync(0xffffffffu, far < a.experts && s_tile[min(far, a.experts)] * a.NT <= t);
+    const int from = (31 - __clz(yes)) * apart, near = from + lane;      // lane 0 votes yes: s_tile[0] = 0
+    yes = __ballot_sync(0xffffffffu, lane < apart && near < a.experts && s_tile[min(near, a.experts)] * a.NT <= t);
+    return tile_of<BT>(a, s_tile, s_row, t, from + 31 - __clz(yes));
 }
 
 // Host side: a map of [rows][I] codes in 128-byte swizzled boxes of box_rows x 128.
