@@ -625,7 +625,8 @@ int qg_kv_evict(const qg_kv_cache *cache, const int *table, int table_stride, co
  *   place    DEVICE int32 [n_tokens * k]: the slot's row, or -1
  *   n_experts  1 .. 8192
  *   ws       qg_moe_sort_workspace_bytes() bytes, 256-byte aligned; contents
- *            on entry do not matter
+ *            on entry do not matter.  The bytes for the most slots serve fewer
+ *            of the same experts too
  * n_tokens = 0 writes the offsets (all 0) alone. */
 size_t qg_moe_sort_workspace_bytes(int n_tokens, int k, int n_experts);
 

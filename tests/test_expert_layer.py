@@ -93,6 +93,22 @@ def test_captured_and_replayed_on_other_tokens(ex):
         assert torch.equal(out, want), seed
 
 
+def test_fewer_tokens_than_the_layer_holds(ex):
+    layer = make(ex, 3000)
+    for tokens in (3000, 1, 1400, 17):
+        x = randn(3, tokens, 400).bfloat16()
+        _, ids, weights = slots(tokens, 3, 6, 4, 0.1)
+        out, want = torch.empty_like(x), torch.empty_like(x)
+        layer(out, x, ids, weights)
+        make(ex, tokens)(want, x, ids, weights)
+        torch.cuda.synchronize()
+        # Another number of rows may choose another kernel, whose sums go in another order, 2^-20 or so apart.  About
+        # one value in 4000 then rounds to the other bf16 neighbour (2^-8), one in 16 of those to another code (2^-4):
+        # with one such code among a token's 3 x 272, its row moves by 2^-4 / sqrt(272) = 0.4%, with four by 0.8%
+        err = (out.double() - want.double()).norm(dim=1)
+        assert bool((err <= 1e-2 * want.double().norm(dim=1)).all())
+
+
 def test_gradients_of_a_trained_layer(ex):
     """f32 throughout: dispatch, an expert's product each, combine; against autograd in 64 bits."""
     tokens, top, experts, hidden = 41, 3, 5, 52

@@ -175,17 +175,21 @@ gemm_e4m3_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
     const int tiles = s_tile[a.experts] * a.NT, first = blockIdx.x / ranks, step = gridDim.x / ranks;
     const int k0 = (int)((long long)a.KB * rank / ranks), k1 = (int)((long long)a.KB * (rank + 1) / ranks);
 
+    // Every lane waits: with one lane's wait and a vote the warp goes on 170 cycles later.
+    auto wait_warp = [&](uint64_t *bar, uint32_t parity) {
+        if (!mbar_wait_or_abort(bar, parity, abort) && lane == 0) raise_device_error(a.err, kErrTimeout);
+        __syncwarp();
+    };
     if (warp == kWarpTma) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            for (int t = first; t < tiles; t += step) {
-                const Tile L = find_tile<BT>(a, s_tile, s_row, t);
-                const int wrow = L.e * a.O + L.ot * 128;
-                for (int k = k0; k < k1; k += C::kBlocks, ++it) {
-                    const uint32_t s = it % C::kStages, r = it / C::kStages;
-                    const int n = min(C::kBlocks, k1 - k);
-                    if (r > 0 && !mbar_wait_or_abort(&empty[s], (r & 1) ^ 1, abort))
-                        raise_device_error(a.err, kErrTimeout);
+        uint32_t it = 0;
+        for (int t = first; t < tiles; t += step) {
+            const Tile L = find_tile_warp<BT>(a, s_tile, s_row, t);
+            const int wrow = L.e * a.O + L.ot * 128;
+            for (int k = k0; k < k1; k += C::kBlocks, ++it) {
+                const uint32_t s = it % C::kStages, r = it / C::kStages;
+                const int n = min(C::kBlocks, k1 - k);
+                if (r > 0) wait_warp(&empty[s], (r & 1) ^ 1);
+                if (lane == 0) {
                     mbar_arrive_expect_tx(&full[s], n * C::kBlockBytes);
                     for (int j = 0; j < n; ++j) {
                         const uint32_t st = sbase + s * C::kStageBytes + j * C::kBlockBytes;
@@ -193,47 +197,48 @@ gemm_e4m3_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
                         tma_load_2d(st + kWBytes, &tmX, (k + j) * 128, L.m0, &full[s]);
                     }
                 }
+                __syncwarp();
             }
-            // Every copy issued must have landed, and every commit arrived, before the block exits.
-            for (uint32_t j = it > (uint32_t)C::kStages ? it - C::kStages : 0; j < it; ++j)
-                if (!mbar_wait(&full[j % C::kStages], (j / C::kStages) & 1) ||
-                    !mbar_wait_or_abort(&empty[j % C::kStages], (j / C::kStages) & 1, abort))
-                    raise_device_error(a.err, kErrTimeout);
+        }
+        // Every copy issued must have landed, and every commit arrived, before the block exits.
+        for (uint32_t j = it > (uint32_t)C::kStages ? it - C::kStages : 0; j < it; ++j) {
+            wait_warp(&full[j % C::kStages], (j / C::kStages) & 1);
+            wait_warp(&empty[j % C::kStages], (j / C::kStages) & 1);
         }
     } else if (warp == kWarpMma || warp == kWarpMma2) {
-        // No stage's sums depend on another's, so two threads issue them in
+        // No stage's sums depend on another's, so two warps issue them in
         // turn: each one's waits and commits pass while the other's MMAs run.
-        if (lane == 0) {
-            uint32_t it = 0;
-            const uint32_t mine = warp == kWarpMma ? 0u : 1u;
-            for (int t = first; t < tiles; t += step) {
-                const Tile L = find_tile<BT>(a, s_tile, s_row, t);
-                const uint32_t idesc = idesc_e4m3((L.rows + 15) & ~15);
-                for (int k = k0; k < k1; k += C::kBlocks, ++it) {
-                    if ((it & 1u) != mine) continue;
-                    const uint32_t s = it % C::kStages, r = it / C::kStages, b = it % C::kBufs, rb = it / C::kBufs;
-                    const int n = min(C::kBlocks, k1 - k);
-                    if (rb > 0 && !mbar_wait_or_abort(&acc_empty[b], (rb & 1) ^ 1, abort))
-                        raise_device_error(a.err, kErrTimeout);
-                    if (!mbar_wait_or_abort(&full[s], r & 1, abort)) raise_device_error(a.err, kErrTimeout);
-                    tc_fence_after();
-                    const uint32_t w_lo = desc_lo(sbase) + s * (C::kStageBytes >> 4);
+        uint32_t it = 0;
+        const uint32_t mine = warp == kWarpMma ? 0u : 1u, lo = desc_lo(sbase);
+        for (int t = first; t < tiles; t += step) {
+            const Tile L = find_tile_warp<BT>(a, s_tile, s_row, t);
+            const uint32_t idesc = idesc_e4m3((L.rows + 15) & ~15);
+            for (int k = k0; k < k1; k += C::kBlocks, ++it) {
+                if ((it & 1u) != mine) continue;
+                const uint32_t s = it % C::kStages, r = it / C::kStages, b = it % C::kBufs, rb = it / C::kBufs;
+                const int n = min(C::kBlocks, k1 - k);
+                wait_warp(&full[s], r & 1);
+                if (rb > 0) wait_warp(&acc_empty[b], (rb & 1) ^ 1);
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t w_lo = lo + s * (C::kStageBytes >> 4);
 #pragma unroll
                     for (int j = 0; j < C::kBlocks; ++j) {
                         if (j >= n) break;
                         mma_block(tmem + b * C::kBufCols + j * BT, w_lo + j * (C::kBlockBytes >> 4),
-                                         w_lo + (j * C::kBlockBytes + kWBytes) / 16, idesc);
+                                  w_lo + (j * C::kBlockBytes + kWBytes) / 16, idesc);
                     }
                     mma_commit(&acc_full[b]);
                     mma_commit(&empty[s]);
                 }
+                __syncwarp();
             }
         }
     } else if (warp == kWarpScale) {
         constexpr int kTok = BT / 32;
         uint32_t ch = 0;
         for (int t = first; t < tiles; t += step) {
-            const Tile L = find_tile<BT>(a, s_tile, s_row, t);
+            const Tile L = find_tile_warp<BT>(a, s_tile, s_row, t);
             const typename SC::T *ws = static_cast<const typename SC::T *>(a.ws) + ((size_t)L.e * a.NB + L.ot) * a.KB;
             for (int k = k0; k < k1; k += kChunk, ++ch) {
                 const uint32_t s = ch % kSlots, r = ch / kSlots;
@@ -267,12 +272,8 @@ gemm_e4m3_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
         const int row = q * 32 + (lane >> 2), cl = 2 * (lane & 3);   // of the fragments: rows row + 8 i, columns 8 j + cl, + 1
         constexpr int kF = C::kCols / 8;
         uint32_t it = 0, ch = 0, round = 0;
-        auto wait_warp = [&](uint64_t *bar, uint32_t parity) {
-            if (!mbar_wait_or_abort(bar, parity, abort) && lane == 0) raise_device_error(a.err, kErrTimeout);
-            __syncwarp();
-        };
         for (int t = first; t < tiles; t += step) {
-            const Tile L = find_tile<BT>(a, s_tile, s_row, t);
+            const Tile L = find_tile_warp<BT>(a, s_tile, s_row, t);
             // piece p: columns (p * kGroups + grp) * kCols; sums [upper half of the rows][fragment][row + 8]
             uint64_t acc[C::kPieces][2][kF][2];
 #pragma unroll

@@ -215,17 +215,7 @@ __device__ __forceinline__ Tile tile_of(const Args8 &a, const int *s_tile, const
     r.rows = min(s_row[2 * e + 1] - r.m0, BT);
     return r;
 }
-template <int BT>
-__device__ __forceinline__ Tile find_tile(const Args8 &a, const int *s_tile, const int *s_row, int t) {
-    int lo = 0, hi = a.experts;       // the last e with s_tile[e] * NT <= t
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_tile[mid] * a.NT <= t) lo = mid;
-        else hi = mid;
-    }
-    return tile_of<BT>(a, s_tile, s_row, t, lo);
-}
-// The same by a whole warp, in two votes.
+// Tile t, by a whole warp in two votes: the last e with s_tile[e] * NT <= t.
 template <int BT>
 __device__ __forceinline__ Tile find_tile_warp(const Args8 &a, const int *s_tile, const int *s_row, int t) {
     static_assert(kMaxExperts <= 32 * 32, "two votes of 32 lanes");

@@ -147,9 +147,12 @@ constexpr int kMaxCounts = 1 << 16;     // counts of all blocks and experts that
 struct SortPlan {
     int blocks, warps, per_warp;        // a warp's slots, whole 32s
 };
+// Never falls as the slots grow, so that the workspace of a long list serves its shorter ones.
+long long most_blocks(int slots, int experts) {
+    return std::min<long long>({((long long)slots + kStretch - 1) / kStretch, std::max(1, kMaxCounts / experts), 1024});
+}
 SortPlan sort_plan(int slots, int experts) {
-    long long blocks = std::min<long long>(((long long)slots + kStretch - 1) / kStretch, std::max(1, kMaxCounts / experts));
-    blocks = std::min<long long>(blocks, 1024);
+    long long blocks = most_blocks(slots, experts);
     int warps = kPlaceThreads / 32;        // a row of counts each in shared memory, and one more
     while ((warps + 1) * experts * 4 > kSortSmem) warps /= 2;
     long long per_warp = ((long long)slots + blocks * warps - 1) / (blocks * warps);
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(kPlaceThreads) sort_place_kernel(const SortArg
 constexpr int kOneBlock = 4096;
 
 size_t ws_moe_sort(int slots, int experts) {
-    return slots <= kOneBlock ? 0 : (size_t)sort_plan(slots, experts).blocks * experts * sizeof(int);
+    return slots <= kOneBlock ? 0 : (size_t)most_blocks(slots, experts) * experts * sizeof(int);
 }
 
 int run_moe_sort(const SortArgs &a, void *ws, cudaStream_t st) {
