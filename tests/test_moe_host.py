@@ -130,6 +130,6 @@ def test_product_refusals(qg, grouped):  # noqa: F811
 
 @pytest.mark.parametrize("e", [1, 7, 64, 256, 1000, 8192])
 def test_sort_workspace_of_more_slots_serves_fewer(qg, e):  # noqa: F811
-    sizes = [qg.qg_moe_sort_workspace_bytes(n, 1, e) for n in [1, 4096, 4097, 5000, 100000] + list(range(900000, 1200000, 777)) +
+    sizes = [qg.qg_moe_sort_workspace_bytes(n, 1, e) for n in [1, 1024, 1025, 5000, 100000] + list(range(900000, 1200000, 777)) +
              [2 ** 31 - 1]]
     assert sizes == sorted(sizes)

@@ -110,7 +110,7 @@ int qg_moe_sort(int *offsets, int *order, int *place, const int *ids, int n_toke
                   ws == nullptr ? (size_t)0 : ws_bytes);
     if (ws && !aligned(ws, 256)) QG_REFUSE(kEAlign, "%s: workspace must be 256-byte aligned", fn);
     cudaGetLastError();
-    const SortArgs a{offsets, order, place, ids, n_tokens * k, n_experts};
+    const SortArgs a{offsets, order, place, ids, n_tokens * k, n_experts, 0};
     return run_moe_sort(a, ws, reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -15,9 +15,10 @@ struct SortArgs {
     int *offsets, *order, *place;   // order may be NULL
     const int *ids;
     int slots, experts;
+    int bits;                       // of the number `experts` (set by the launch)
 };
 size_t ws_moe_sort(int slots, int experts);
-int run_moe_sort(const SortArgs &a, void *ws, cudaStream_t st);
+int run_moe_sort(SortArgs a, void *ws, cudaStream_t st);
 
 struct DispatchArgs {
     void *rows;

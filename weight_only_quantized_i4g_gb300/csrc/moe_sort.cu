@@ -19,11 +19,10 @@ namespace {
 constexpr int kSortThreads = 1024;
 constexpr int kSortSmem = 200 * 1024;   // counts: a word a warp and expert
 constexpr size_t kPlainSmem = 48 * 1024 - 256;   // what a kernel may have without asking
-constexpr int kNone = 0x7FFFFFFF;
 
-// Experts of the 32 kBatch slots from s on, this lane's 32 apart: all loads in
-// flight at once.  Past L1, which may hold what an earlier call left there.
-constexpr int kBatch = 8;
+// Experts of the 32 kBatch slots from s on (`experts` for none here), this
+// lane's 32 apart: all loads in flight at once.  Past L1, which may hold what an earlier call left there.
+constexpr int kBatch = 4;
 __device__ __forceinline__ void load_experts(const SortArgs &a, long long s, long long s1, int lane, int (&e)[kBatch]) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
@@ -31,7 +30,7 @@ __device__ __forceinline__ void load_experts(const SortArgs &a, long long s, lon
         e[i] = at < s1 ? __ldcg(a.ids + at) : -1;
     }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) e[i] = (unsigned)e[i] < (unsigned)a.experts ? e[i] : kNone;
+    for (int i = 0; i < kBatch; ++i) e[i] = (unsigned)e[i] < (unsigned)a.experts ? e[i] : a.experts;
 }
 
 // Exclusive prefix sums over the threads of a block; *total is their sum.
@@ -56,12 +55,25 @@ __device__ __forceinline__ int block_prefix(int v, int *s_warp, int *total) {
     return before + x - v;
 }
 
+// The lanes with this lane's expert, a vote for each of its bits (the match
+// instruction takes a third longer: 16384 x 8 slots 12.5 us against 9.2).
+__device__ __forceinline__ unsigned lanes_of(int e, int bits) {
+    unsigned same = 0xffffffffu;
+    for (int b = 0; b < bits; ++b) {
+        const unsigned yes = __ballot_sync(0xffffffffu, e >> b & 1);
+        same &= e >> b & 1 ? yes : ~yes;
+    }
+    return same;
+}
+
 // A warp counts the experts of a batch in its own row of counts.
-__device__ __forceinline__ void count_batch(const int (&e)[kBatch], int lane, int *mine) {
+__device__ __forceinline__ void count_batch(const SortArgs &a, const int (&e)[kBatch], long long s, long long s1, int lane,
+                                            int *mine) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-        const unsigned same = __match_any_sync(0xffffffffu, e[i]);
-        if (e[i] != kNone && lane == __ffs(same) - 1) mine[e[i]] += __popc(same);
+        if (s + 32 * i >= s1) break;
+        const unsigned same = lanes_of(e[i], a.bits);
+        if (e[i] != a.experts && lane == __ffs(same) - 1) mine[e[i]] += __popc(same);
         __syncwarp();
     }
 }
@@ -71,11 +83,12 @@ __device__ __forceinline__ void place_batch(const SortArgs &a, const int (&e)[kB
                                             int *mine) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
+        if (s + 32 * i >= s1) break;
         const long long slot = s + 32 * i + lane;
-        const unsigned same = __match_any_sync(0xffffffffu, e[i]);
-        const int at = e[i] != kNone ? mine[e[i]] + __popc(same & ((1u << lane) - 1u)) : -1;
+        const unsigned same = lanes_of(e[i], a.bits);
+        const int at = e[i] != a.experts ? mine[e[i]] + __popc(same & ((1u << lane) - 1u)) : -1;
         __syncwarp();
-        if (e[i] != kNone && lane == __ffs(same) - 1) mine[e[i]] += __popc(same);
+        if (e[i] != a.experts && lane == __ffs(same) - 1) mine[e[i]] += __popc(same);
         __syncwarp();
         if (slot < s1) {
             a.place[slot] = at;
@@ -92,7 +105,7 @@ __device__ __forceinline__ void count_and_place(const SortArgs &a, long long s0,
     int e[kBatch];
     for (long long s = s0; s < s1; s += kStep) {
         load_experts(a, s, s1, lane, e);
-        count_batch(e, lane, mine);
+        count_batch(a, e, s, s1, lane, mine);
     }
     between();
     const bool again = s1 - s0 > kStep;
@@ -140,16 +153,19 @@ __global__ void __launch_bounds__(kSortThreads) sort_one_kernel(const SortArgs a
 // Long lists take two kernels: every block of the first counts one stretch,
 // and every block of the second adds up the counts it needs (all experts' sums,
 // and its own experts' before its stretch) and places its stretch.
-constexpr int kStretch = 4096;          // slots of a block, unless the counts grow long
 constexpr int kPlaceThreads = 512;      // 16 warps
 constexpr int kMaxCounts = 1 << 16;     // counts of all blocks and experts that every block reads
 
 struct SortPlan {
     int blocks, warps, per_warp;        // a warp's slots, whole 32s
 };
-// Never falls as the slots grow, so that the workspace of a long list serves its shorter ones.
+// A block for 1024 slots up to 64 blocks, whose counts every block reads in a
+// few batches (16384 slots: 4.8 us, with 2048 a block 6.7; 131072 slots: 8.5 us
+// with 64 blocks, 13 with 128), then one for 4096.  Never falls as the slots
+// grow, so that the workspace of a long list serves its shorter ones.
 long long most_blocks(int slots, int experts) {
-    return std::min<long long>({((long long)slots + kStretch - 1) / kStretch, std::max(1, kMaxCounts / experts), 1024});
+    const long long by_size = std::min((slots + 1023LL) / 1024, std::max(64LL, slots / 4096LL));
+    return std::min<long long>({by_size, std::max(1, kMaxCounts / experts), 1024});
 }
 SortPlan sort_plan(int slots, int experts) {
     long long blocks = most_blocks(slots, experts);
@@ -174,10 +190,8 @@ __global__ void __launch_bounds__(kPlaceThreads) sort_count_kernel(const SortArg
         int e[kBatch];
         load_experts(a, s, s1, lane, e);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {         // sums of whole numbers: any order gives the same
-            const unsigned same = __match_any_sync(0xffffffffu, e[i]);
-            if (e[i] != kNone && lane == __ffs(same) - 1) atomicAdd(&s_count[e[i]], __popc(same));
-        }
+        for (int i = 0; i < kBatch; ++i)           // sums of whole numbers: any order gives the same
+            if (e[i] != E) atomicAdd(&s_count[e[i]], 1);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < E; i += blockDim.x) counts[(size_t)blockIdx.x * E + i] = s_count[i];
@@ -232,14 +246,15 @@ __global__ void __launch_bounds__(kPlaceThreads) sort_place_kernel(const SortArg
 
 }  // namespace
 
-// One block's 32 warps take up to this many slots as fast as two kernels do.
-constexpr int kOneBlock = 4096;
+// One block's 32 warps take up to this many slots.
+constexpr int kOneBlock = 1024;
 
 size_t ws_moe_sort(int slots, int experts) {
     return slots <= kOneBlock ? 0 : (size_t)most_blocks(slots, experts) * experts * sizeof(int);
 }
 
-int run_moe_sort(const SortArgs &a, void *ws, cudaStream_t st) {
+int run_moe_sort(SortArgs a, void *ws, cudaStream_t st) {
+    for (a.bits = 1; a.experts >> a.bits; ++a.bits) {}
     const char *what = "qg_moe_sort";
     if (a.slots <= kOneBlock) {
         // as many warps as there are 32s of slots, and counts in shared memory
