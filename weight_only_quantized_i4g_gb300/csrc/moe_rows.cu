@@ -52,6 +52,16 @@ __device__ __forceinline__ uint4 load16_if(bool there, const void *p) {
         : "r"((int)there), "l"(p));     // volatile: stays behind the wait for the previous kernel
     return v;
 }
+__device__ __forceinline__ uint16_t load_if(bool there, const uint16_t *p) {
+    uint16_t v = 0;
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t@q ld.global.b16 %0, [%2];\n\t}" : "+h"(v) : "r"((int)there), "l"(p));
+    return v;
+}
+__device__ __forceinline__ float load_if(bool there, const float *p) {
+    float v = 0.f;
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t@q ld.global.f32 %0, [%2];\n\t}" : "+f"(v) : "r"((int)there), "l"(p));
+    return v;
+}
 // Eight elements, as loaded from a 16-byte address and as f32.
 template <int T> struct Raw8 {
     uint4 w[T == kF32 ? 2 : 1];
@@ -163,9 +173,8 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_words_kernel(const __gri
     }
 }
 
-// Codes: a thread takes 16 elements, eight threads a block of 128.  VEC: whole
-// lines, else element by element.
-template <int T, bool VEC>
+// Codes: a thread takes 16 elements, eight threads a block of 128.
+template <int T>
 __global__ void __launch_bounds__(kRowThreads) dispatch_codes_kernel(const __grid_constant__ DispatchArgs a, int chunks) {
     griddep_wait();
     griddep_launch_dependents();
@@ -177,14 +186,8 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_codes_kernel(const __gri
     if (here) {
         rows_of(a, at.t, 0, p);
         const size_t x0 = at.t * a.x_stride + c;
-        if constexpr (VEC) {
-            load8<T>(element<T>(a.x, x0), v[0]);
-            if (c + 8 < a.width) load8<T>(element<T>(a.x, x0 + 8), v[1]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (c + i < a.width) v[i >> 3][i & 7] = Elem<T>::get(static_cast<const typename Elem<T>::Word *>(a.x)[x0 + i]);
-        }
+        load8<T>(element<T>(a.x, x0), v[0]);
+        load8<T>(element<T>(a.x, x0 + 8), v[1]);
     }
     float top = 0.f;
 #pragma unroll
@@ -204,18 +207,43 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_codes_kernel(const __gri
 #pragma unroll
         for (int j = 0; j < kTogether; ++j) {
             if (p[j] < 0) continue;
-            uint8_t *dst = static_cast<uint8_t *>(a.rows) + (size_t)p[j] * a.width + c;
-            if constexpr (VEC) {
-                *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (c + i < a.width) dst[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
-            }
+            *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.rows) + (size_t)p[j] * a.width + c) =
+                make_uint4(w[0], w[1], w[2], w[3]);
             if ((at.u & 7) == 0) a.scales[(size_t)p[j] * nb + at.u / 8] = s;
         }
         if ((j0 += kTogether) >= a.k) break;
         rows_of(a, at.t, j0, p);
+    }
+}
+
+// Codes of other rows: a warp takes a block of 128, a lane's four elements 32 apart.
+template <int T>
+__global__ void __launch_bounds__(kRowThreads) dispatch_codes_words_kernel(const __grid_constant__ DispatchArgs a, int chunks) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const Place2 at = unit_of(chunks);
+    const int nb = (a.width + kBlock - 1) / kBlock, block = at.u >> 5, lane = at.u & 31, c = block * kBlock + lane;
+    if (at.t >= (unsigned)a.tokens || block >= nb) return;         // the same for a warp
+    const typename Elem<T>::Word *x = static_cast<const typename Elem<T>::Word *>(a.x) + at.t * a.x_stride;
+    float v[4], top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = c + 32 * i < a.width ? Elem<T>::get(x[c + 32 * i]) : 0.f;
+        top = larger_finite(top, v[i]);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const int ex = scale_exponent(top);
+    const float s = __uint_as_float((uint32_t)(127 + ex) << 23), up = __uint_as_float((uint32_t)(127 - ex) << 23);
+    const uint32_t w[2] = {codes2(v[0], v[1], up), codes2(v[2], v[3], up)};
+    for (int j = 0; j < a.k; ++j) {
+        const int p = row_of(a.place, (long long)at.t * a.k + j, a.n_rows);
+        if (p < 0) continue;
+        uint8_t *dst = static_cast<uint8_t *>(a.rows) + (size_t)p * a.width + c;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c + 32 * i < a.width) dst[32 * i] = (uint8_t)(w[i >> 1] >> (8 * (i & 1)));
+        if (lane == 0) a.scales[(size_t)p * nb + block] = s;
     }
 }
 
@@ -320,15 +348,22 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const __grid_
                     if (a.dy) store8<TY>(element<TY>(a.dy, (size_t)p[j] * a.width + c), g);
                 }
             } else {
+                WordY y[kTogether][8];
+#pragma unroll
+                for (int j = 0; j < kTogether; ++j)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const bool in = p[j] >= 0 && a.dweights && c + 32 * i < a.width;
+                        y[j][i] = load_if(in, static_cast<const WordY *>(a.y) + (size_t)max(p[j], 0) * a.width + c + 32 * i);
+                    }
 #pragma unroll
                 for (int j = 0; j < kTogether; ++j) {
                     if (p[j] < 0) continue;
-                    const size_t at = (size_t)p[j] * a.width + c;
+                    WordY *dy = static_cast<WordY *>(a.dy) + (size_t)p[j] * a.width + c;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        if (c + 32 * i >= a.width) continue;
-                        if (a.dweights) sum[j] = fmaf(d[i], Elem<TY>::get(static_cast<const WordY *>(a.y)[at + 32 * i]), sum[j]);
-                        if (a.dy) static_cast<WordY *>(a.dy)[at + 32 * i] = Elem<TY>::put(w[j] * d[i]);
+                        sum[j] = fmaf(d[i], Elem<TY>::get(y[j][i]), sum[j]);       // zeros past the row's end
+                        if (a.dy && c + 32 * i < a.width) dy[32 * i] = Elem<TY>::put(w[j] * d[i]);
                     }
                 }
             }
@@ -374,10 +409,10 @@ inline int size_of(int type) { return type == kF32 ? 4 : 2; }
 template <int T>
 int launch_codes(const DispatchArgs &a, cudaStream_t st) {
     const bool vec = a.width % 16 == 0 && a.x_stride * kSize<T> % 16 == 0 && lines16(a.x) && lines16(a.rows);
-    const int units = (a.width + kBlock - 1) / kBlock * 8;     // whole blocks: their eight threads meet
-    const RowGrid g(a.tokens, units, threads_for((long long)a.tokens * units), 8);
-    return vec ? launch_pdl("qg_moe_dispatch", dispatch_codes_kernel<T, true>, g.blocks, g.block(), 0, st, a, g.chunks)
-               : launch_pdl("qg_moe_dispatch", dispatch_codes_kernel<T, false>, g.blocks, g.block(), 0, st, a, g.chunks);
+    const int units = (a.width + kBlock - 1) / kBlock * (vec ? 8 : 32);   // whole blocks: their threads meet
+    const RowGrid g(a.tokens, units, threads_for((long long)a.tokens * units), vec ? 8 : 32);
+    return vec ? launch_pdl("qg_moe_dispatch", dispatch_codes_kernel<T>, g.blocks, g.block(), 0, st, a, g.chunks)
+               : launch_pdl("qg_moe_dispatch", dispatch_codes_words_kernel<T>, g.blocks, g.block(), 0, st, a, g.chunks);
 }
 
 }  // namespace
