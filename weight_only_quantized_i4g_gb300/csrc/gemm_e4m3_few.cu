@@ -177,7 +177,7 @@ gemm_e4m3_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
 
     // Every lane waits: with one lane's wait and a vote the warp goes on 170 cycles later.
     auto wait_warp = [&](uint64_t *bar, uint32_t parity) {
-        if (!mbar_wait_or_abort(bar, parity, abort) && lane == 0) raise_device_error(a.err, kErrTimeout);
+        mbar_wait_or_abort(bar, parity, abort);        // a wait that gives up sets *abort, which the block's end reports
         __syncwarp();
     };
     if (warp == kWarpTma) {
@@ -253,9 +253,7 @@ gemm_e4m3_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
                     }
                 }
                 if (r > 0) {
-                    if (!mbar_wait_or_abort(&sc_empty[s], (r & 1) ^ 1, abort) && lane == 0)
-                        raise_device_error(a.err, kErrTimeout);
-                    __syncwarp();
+                    wait_warp(&sc_empty[s], (r & 1) ^ 1);
                 }
                 float *dst = s_scale + s * kChunk * BT + lane;
 #pragma unroll
@@ -396,7 +394,7 @@ gemm_e4m3_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
             for (int rd = 0; rd < BT / C::kRedCols; ++rd) {
                 if (rd * C::kRedCols >= L.rows) break;
                 if (round > 0) {
-                    if (!wait_cluster(red_empty, (round - 1) & 1, abort) && lane == 0) raise_device_error(a.err, kErrTimeout);
+                    wait_cluster(red_empty, (round - 1) & 1, abort);
                     __syncwarp();
                 }
                 // the round's columns are one group's
@@ -413,7 +411,7 @@ gemm_e4m3_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
                 }
                 __syncwarp();
                 if (lane < (int)ranks) arrive_remote(map_rank(smem_addr(red_full), lane));
-                if (!wait_cluster(red_full, round & 1, abort) && lane == 0) raise_device_error(a.err, kErrTimeout);
+                wait_cluster(red_full, round & 1, abort);
                 __syncwarp();
                 const int o = o0 + (pt & 127);
                 for (int col = (int)rank + (pt >> 7) * (int)ranks; col < C::kRedCols; col += C::kGroups * (int)ranks) {
@@ -433,6 +431,7 @@ gemm_e4m3_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
 
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && *abort) raise_device_error(a.err, kErrTimeout);
     if (warp == kWarpMma) {
         tc_fence_after();
         tmem_free(tmem, C::kTmemCols);

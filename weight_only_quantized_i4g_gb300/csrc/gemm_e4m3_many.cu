@@ -121,7 +121,7 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     // promoting warps take 8 x 32 x 232 and the others 4 x 32 x 40.
     // Every lane waits: with one lane's wait and a vote the warp goes on 170 cycles later.
     auto wait_warp = [&](uint64_t *bar, uint32_t parity) {
-        if (!mbar_wait_or_abort(bar, parity, abort) && lane == 0) raise_device_error(a.err, kErrTimeout);
+        mbar_wait_or_abort(bar, parity, abort);        // a wait that gives up sets *abort, which the block's end reports
         __syncwarp();
     };
     if (warp < kWarpPromote) {
@@ -327,6 +327,7 @@ gemm_e4m3_many_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
 
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && *abort) raise_device_error(a.err, kErrTimeout);
     if (warp == kWarpIssue) {
         tc_fence_after();
         tmem_free(tmem, kBufs * 256);
