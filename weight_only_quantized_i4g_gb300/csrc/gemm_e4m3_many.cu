@@ -1,16 +1,19 @@
 // gemm_e4m3_many.cu -- products of e4m3 activations with e4m3 weights, many
-// tokens an expert: the tensor cores and what feeds and empties them bound it.
+// tokens an expert: the tensor cores and the warps that empty them bound it.
 //
 // A tile is 128 tokens (MMA M) by 256 outputs (N), two halves with a weight
 // scale each, so a promoting thread holds one token and scales a half's sums by
 // one factor.  (With the tokens along N a factor a column has to be read from
 // shared memory: 64 columns then take a warp 290 cycles instead of 134, and a K
-// block 1800 instead of the MMAs' 512.)  A K block takes about 790 cycles: its
-// MMAs read 48 KB of shared memory and TMA writes as much, 750 cycles at 128
-// bytes a cycle (as two MMAs of N = 128 it took 880: the tokens' codes are read
-// twice).  Measured and left out: block pairs that share an MMA (half the
-// weights a block; 0 to 10% slower, their signals cross SMs) and tiles of 192
-// outputs (a K block takes the same time).
+// block 1800 instead of the MMAs' 512.)  4096 x 7168 x 7168: 153 us, 2750
+// TFLOP/s, about 770 cycles a K block.  What bounds it is the promoting warps,
+// two a scheduler with 128 additions a thread and the wait and loads before
+// them: without the additions it took 133 us (157 with them at the time), with
+// one of a K block's four MMAs 146, without the copies 152.  As two MMAs of N =
+// 128 a K block took 880 cycles: the tokens' codes are read twice.  Measured and
+// left out: block pairs that share an MMA (half the weights a block; 0 to 10%
+// slower, their signals cross SMs) and tiles of 192 outputs (a K block takes the
+// same time).
 // One persistent thread block per SM:
 //   warps 0, 1   TMA producers, K blocks in turn: 128 x 128 codes of X and
 //                256 x 128 of W, 128-byte swizzled
