@@ -12,8 +12,9 @@
 // one of a K block's four MMAs 146, without the copies 152.  As two MMAs of N =
 // 128 a K block took 880 cycles: the tokens' codes are read twice.  Measured and
 // left out: block pairs that share an MMA (half the weights a block; 0 to 10%
-// slower, their signals cross SMs) and tiles of 192 outputs (a K block takes the
-// same time).
+// slower, their signals cross SMs), tiles of 192 outputs (a K block takes the
+// same time), and the next K block's first sums loaded before this one's last
+// additions (164 us: the wait for its MMAs then stands before the additions).
 // One persistent thread block per SM:
 //   warps 0, 1   TMA producers, K blocks in turn: 128 x 128 codes of X and
 //                256 x 128 of W, 128-byte swizzled
