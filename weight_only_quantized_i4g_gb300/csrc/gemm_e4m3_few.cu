@@ -346,7 +346,7 @@ gemm_e4m3_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
                 // time, transposed through shared memory to 64 bytes a token.
                 const uint32_t strip = smem_addr(s_red) + pw * 16 * kOutStride;
                 const int ow = o0 + q * 32, part = lane & 3;
-                const bool whole = ow + 32 <= a.O && a.O % 8 == 0 && reinterpret_cast<uintptr_t>(a.Y) % 16 == 0;
+                const bool lines = a.O % 8 == 0 && reinterpret_cast<uintptr_t>(a.Y) % 16 == 0;
 #pragma unroll
                 for (int p = 0; p < C::kPieces; ++p)
 #pragma unroll
@@ -365,22 +365,21 @@ gemm_e4m3_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
                             stmatrix4_trans(strip + (8 * x + (lane & 7)) * kOutStride + (lane >> 3) * 16, w[0], w[1], w[2], w[3]);
                         }
                         __syncwarp();
+                        const char *from = reinterpret_cast<const char *>(s_red) + pw * 16 * kOutStride;
+                        uint16_t *y = static_cast<uint16_t *>(a.Y) + (size_t)(L.m0 + m) * a.O + ow;
+                        if (lines) {
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const int tok = 8 * x + (lane >> 2);
-                            const uint4 v = *reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(s_red) + pw * 16 * kOutStride +
-                                                                             tok * kOutStride + part * 16);
-                            if (m + tok < L.rows) {
-                                uint16_t *y = static_cast<uint16_t *>(a.Y) + (size_t)(L.m0 + m + tok) * a.O + ow + part * 8;
-                                if (whole) {
-                                    *reinterpret_cast<uint4 *>(y) = v;
-                                } else {
-                                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i)
-                                        if (ow + part * 8 + i < a.O) y[i] = (uint16_t)(u[i >> 1] >> (16 * (i & 1)));
-                                }
+                            for (int x = 0; x < 2; ++x) {
+                                const int tok = 8 * x + (lane >> 2);
+                                if (m + tok < L.rows && ow + part * 8 < a.O)
+                                    *reinterpret_cast<uint4 *>(y + (size_t)tok * a.O + part * 8) =
+                                        *reinterpret_cast<const uint4 *>(from + tok * kOutStride + part * 16);
                             }
+                        } else if (ow + lane < a.O) {      // neighbouring lanes, neighbouring outputs
+                            const int n = min(L.rows - m, 16);
+#pragma unroll 4
+                            for (int tok = 0; tok < n; ++tok)
+                                y[(size_t)tok * a.O + lane] = *reinterpret_cast<const uint16_t *>(from + tok * kOutStride + 2 * lane);
                         }
                         __syncwarp();
                     }
