@@ -451,7 +451,7 @@ int run_moe_combine_grad(const CombineGradArgs &a, int dout_type, int y_type, cu
     const bool warp = units <= 64;
     const int threads = units >= 256 ? 256 : (units + 31) / 32 * 32;
     const dim3 block = warp ? dim3(32, 4) : dim3(threads, 1);
-    const unsigned blocks = warp ? (unsigned)((a.tokens + 3) / 4) : (unsigned)a.tokens;
+    const unsigned blocks = warp ? ((unsigned)a.tokens + 3) / 4 : (unsigned)a.tokens;
     return by_types(dout_type, y_type, [&](auto td, auto ty) {
         constexpr int TD = decltype(td)::value, TY = decltype(ty)::value;
         return vec ? launch_pdl(what, combine_grad_kernel<TD, TY, true>, blocks, block, 0, st, a)
