@@ -607,7 +607,8 @@ int qg_kv_evict(const qg_kv_cache *cache, const int *table, int table_stride, co
 /* place[s] is slot s's row, -1 for none; any place outside [0, n_rows)     */
 /* counts as none; no two slots may name one row where rows are written.    */
 /* place = NULL: slot s is row s (as qgemv_moe leaves its                   */
-/* outputs); n_rows is then at least n_tokens * k.  n_tokens * k < 2^31.    */
+/* outputs); n_rows is then at least n_tokens * k.  n_tokens * k < 2^31,    */
+/* and where rows move k < 2^31 - 8.                                        */
 /* Ids, places, weights and offsets live in device memory and are read      */
 /* after the previous kernel on the stream has finished, so a captured      */
 /* graph replays with new ones.  Outputs must not overlap inputs.           */

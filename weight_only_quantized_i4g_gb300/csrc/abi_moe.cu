@@ -29,7 +29,9 @@ int check_slots(const char *fn, int n_tokens, int k, int width, int n_rows) {
     return kOk;
 }
 
-int check_identity(const char *fn, const void *place, int n_tokens, int k, int n_rows) {
+// Of the calls that move rows.
+int check_places(const char *fn, const void *place, int n_tokens, int k, int n_rows) {
+    if (k > INT_MAX - kTogether) QG_REFUSE(kEInval, "%s: k = %d slots a token overflow", fn, k);
     if (!place && (long long)n_tokens * k > n_rows)
         QG_REFUSE(kEInval, "%s: without place a row is a slot: n_rows = %d is below n_tokens * k = %lld", fn, n_rows,
                   (long long)n_tokens * k);
@@ -123,7 +125,7 @@ int qg_moe_dispatch(void *rows, int rows_type, float *row_scales, const void *x,
     const bool codes = rows_type == QG_E4M3;
     if (!codes && rows_type != x_type)
         QG_REFUSE(kEInval, "%s: rows_type %d must be x_type %d or QG_E4M3", fn, rows_type, x_type);
-    if ((rc = check_identity(fn, place, n_tokens, k, n_rows))) return rc;
+    if ((rc = check_places(fn, place, n_tokens, k, n_rows))) return rc;
     if (n_tokens > 1 && x_stride < (size_t)I)
         QG_REFUSE(kEInval, "%s: x_stride = %zu is below I = %d", fn, x_stride, I);
     if (x_stride > (size_t)1 << 40) QG_REFUSE(kEInval, "%s: x_stride = %zu overflows", fn, x_stride);
@@ -145,7 +147,7 @@ int qg_moe_combine(void *out, int out_type, const void *y, int y_type, const flo
     if (rc) return rc;
     if (!is_wide(out_type) || !is_wide(y_type))
         QG_REFUSE(kEInval, "%s: out_type %d and y_type %d must be QG_F32, QG_BF16 or QG_F16", fn, out_type, y_type);
-    if ((rc = check_identity(fn, place, n_tokens, k, n_rows))) return rc;
+    if ((rc = check_places(fn, place, n_tokens, k, n_rows))) return rc;
     if (n_tokens == 0) return kOk;
     if (!out || (n_rows > 0 && !y)) QG_REFUSE(kEInval, "%s: out and y must be non-NULL", fn);
     if (!aligned(out, size_of(out_type)) || !aligned(y, size_of(y_type)) || !aligned(weights, 4) || !aligned(place, 4))
@@ -163,7 +165,7 @@ int qg_moe_combine_grad(void *dy, float *dweights, const void *dout, int dout_ty
     if (rc) return rc;
     if (!is_wide(dout_type) || !is_wide(y_type))
         QG_REFUSE(kEInval, "%s: dout_type %d and y_type %d must be QG_F32, QG_BF16 or QG_F16", fn, dout_type, y_type);
-    if ((rc = check_identity(fn, place, n_tokens, k, n_rows))) return rc;
+    if ((rc = check_places(fn, place, n_tokens, k, n_rows))) return rc;
     if (n_tokens == 0) return kOk;
     if (!dy && !dweights) QG_REFUSE(kEInval, "%s: dy and dweights are both NULL", fn);
     if (!dout || (dweights && n_rows > 0 && !y))

@@ -10,6 +10,7 @@ namespace qg {
 
 constexpr int kErrExpert = -8;
 constexpr int kMaxSortExperts = 8192;
+constexpr int kTogether = 8;        // slots of a token in flight at once; their count goes past k by less
 
 struct SortArgs {
     int *offsets, *order, *place;   // order may be NULL

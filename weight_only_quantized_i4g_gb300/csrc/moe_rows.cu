@@ -17,7 +17,6 @@ namespace {
 
 constexpr int kRowThreads = 256;
 constexpr int kBlock = 128;      // elements of one scale
-constexpr int kTogether = 8;     // slots of a token in flight at once
 
 // Blocks of (ux, ty) threads: ty tokens, ux units of one, `chunks` blocks along a row.
 struct RowGrid {
