@@ -680,9 +680,11 @@ int qg_moe_combine_grad(void *dy, float *dweights, const void *dout, int dout_ty
  *   offsets   DEVICE int32 [n_experts + 1] (qg_moe_sort): rows offsets[e] ..
  *             offsets[e+1] - 1 use expert e.  M is the rows that X and Y hold,
  *             at least offsets[n_experts]; rows behind that, and rows before
- *             offsets[0], are not written.  A table that decreases or leaves
- *             [0, M] is held to the rows that are there, and the device error
- *             word says QG_EEXPERT.  n_experts 1 .. 8192.
+ *             offsets[0], are not written.  In a table that decreases or
+ *             leaves [0, M] expert e's rows go from the largest of offsets[0]
+ *             .. offsets[e] to the largest of offsets[0] .. offsets[e+1], each
+ *             held to [0, M], and the device error word says QG_EEXPERT.
+ *             n_experts 1 .. 8192.
  *   Y         DEVICE [M][O], y_type QG_F32, QG_BF16 or QG_F16
  *   ws        qgemm_e4m3_workspace_bytes() bytes (n_experts = 1 for
  *             qgemm_e4m3), 256-byte aligned; contents on entry do not matter

@@ -39,9 +39,10 @@ __global__ void __launch_bounds__(256) gemm_e4m3_general_kernel(const E4m3Args a
     const int o0 = blockIdx.x * kGT, m0 = blockIdx.y * kGT;
     const int nb = (a.I + 127) / 128, nbo = (a.O + 127) / 128;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;   // 16 x 16 threads, 4 x 4 each
+    int to = a.offsets ? held_row(a.offsets[0], a.M) : a.M;
     for (int g = 0; g < a.experts; ++g) {
-        int from = 0, to = a.M;
-        if (a.offsets) group_range(a.offsets, g, a.M, &from, &to, threadIdx.x == 0 ? a.err : nullptr);
+        int from = 0;
+        if (a.offsets) next_rows(a.offsets, g, a.M, &from, &to, threadIdx.x == 0 ? a.err : nullptr);
         if (to <= m0 || from >= m0 + kGT || to <= from) continue;      // the same for the whole block
         const uint8_t *w = a.w + (size_t)g * a.O * a.I;
         const typename SC::T *ws = static_cast<const typename SC::T *>(a.w_scale) + (size_t)g * nbo * nb;

@@ -147,17 +147,15 @@ __device__ __forceinline__ void build_tables(const Args8 &a, int *s_tile, int *s
             s_row[1] = a.M;
         }
     } else {
-        // Row bounds held to [0, M] and to their order (a table that is
-        // neither raises the error word): expert e has rows most[e] to
-        // most[e+1] of the running maximum.
-        int tiles_before = 0, most = min(max(a.offsets[0], 0), a.M);
+        // The rule of next_rows: expert e has rows most[e] to most[e+1] of the running maximum.
+        int tiles_before = 0, most = held_row(a.offsets[0], a.M);
         for (int e0 = 0; e0 < a.experts; e0 += kThreads) {
             const int e = e0 + threadIdx.x;
             int to = 0;
             if (e < a.experts) {
-                const int lo = a.offsets[e], hi = a.offsets[e + 1];
-                if ((lo < 0 || hi < lo || hi > a.M) && blockIdx.x == 0) raise_device_error(a.err, kErrExpert);
-                to = min(max(hi, 0), a.M);
+                const int hi = a.offsets[e + 1];
+                if (blockIdx.x == 0) check_offsets(a.offsets[e], hi, a.M, a.err);
+                to = held_row(hi, a.M);
             }
             int top = to;
 #pragma unroll

@@ -66,18 +66,19 @@ struct E4m3Args {
 };
 size_t ws_gemm_e4m3(int M, int I, int O, int experts);
 int run_gemm_e4m3(const E4m3Args &a, void *ws, cudaStream_t st);
-// Rows [*from, *to) of group g; a table that decreases or passes M is held
-// to the rows that are there, and the thread that asks with err != NULL
-// raises the error word.
-__device__ __forceinline__ void group_range(const int *offsets, int g, int M, int *from, int *to, int *err) {
-    int a = offsets[g], b = offsets[g + 1];
-    if (a < 0 || b < a || b > M) {
-        raise_device_error(err, kErrExpert);
-        a = min(max(a, 0), M);
-        b = min(max(b, a), M);
-    }
-    *from = a;
-    *to = b;
+// Where the first expert's rows begin and, from there, expert by expert, rows
+// [*from, *most) of expert g: row bounds are held to [0, M] and to their order,
+// so a table that leaves the rows or decreases gives no row twice, and the
+// thread that asks with err != NULL raises the error word.
+__device__ __forceinline__ int held_row(int row, int M) { return min(max(row, 0), M); }
+__device__ __forceinline__ void check_offsets(int from, int to, int M, int *err) {
+    if (from < 0 || to < from || to > M) raise_device_error(err, kErrExpert);
+}
+__device__ __forceinline__ void next_rows(const int *offsets, int g, int M, int *from, int *most, int *err) {
+    const int lo = offsets[g], hi = offsets[g + 1];
+    check_offsets(lo, hi, M, err);
+    *from = *most;
+    *most = max(*most, held_row(hi, M));
 }
 
 // Row of slot s (NULL table: s), -1 for none.
