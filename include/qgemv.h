@@ -693,7 +693,9 @@ int qg_moe_combine_grad(void *dy, float *dweights, const void *dout, int dout_ty
  * good as f32 holds it) are summed in f32: within 1e-3 * sum |x w| of the
  * definition.  A NaN code makes its row, or column of the expert's rows, NaN.
  * M = 0 launches nothing; M at most 4194240.  I a multiple of 16 and X, w at
- * 16-byte addresses take the tensor-core kernel, anything else a general one. */
+ * 16-byte addresses take the tensor-core kernels, one launch for each 1024
+ * experts, anything else a general one (and so do sizes whose rows of weights,
+ * O times up to 1024 experts, or output tiles reach 2^31). */
 size_t qgemm_e4m3_workspace_bytes(int M, int I, int O, int n_experts);
 
 int qgemm_e4m3(int fmt, void *Y, int y_type, const uint8_t *X, const float *x_scales, const uint8_t *w,

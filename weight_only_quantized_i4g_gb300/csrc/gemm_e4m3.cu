@@ -11,6 +11,8 @@
 // every shape and alignment: 64 x 64 outputs a block, K in steps of 32, codes
 // widened to f32 in shared memory, f32 sums of a 128-block scaled when it
 // ends.  A block of rows that several experts share goes over each of them.
+#include <algorithm>
+
 #include "gemm_e4m3_tc.cuh"
 
 namespace qg {
@@ -95,21 +97,32 @@ __global__ void __launch_bounds__(256) gemm_e4m3_general_kernel(const E4m3Args a
     }
 }
 
-int run_tc(const char *what, const E4m3Args &g, cudaStream_t st) {
+// A launch for each kMaxExperts experts, planned with their share of the rows.
+int run_tc(const char *what, const E4m3Args &all, cudaStream_t st) {
     if (!tc::encode_fn()) QG_REFUSE(kECuda, "%s: cuTensorMapEncodeTiled is not available from the driver", what);
-    const e8::Args8 a{g.Y, g.y_type, g.x_scale, g.w_scale, g.offsets, g.experts, g.M, g.O,
-                      (g.I + 127) / 128, (g.O + 127) / 128, 0, g.err};
-    const e8::FewPlan few = e8::plan_few(g.M, g.I, g.O, g.experts);
-    const e8::ManyPlan many = e8::plan_many(g.M, g.I, g.O, g.experts);
-    return many.cost < few.cost ? e8::launch_many(what, many, g, a, st) : e8::launch_few(what, few, g, a, st);
+    const int KB = (all.I + 127) / 128, NB = (all.O + 127) / 128;
+    for (int e0 = 0; e0 < all.experts; e0 += e8::kMaxExperts) {
+        E4m3Args g = all;
+        g.experts = std::min(all.experts - e0, e8::kMaxExperts);
+        g.w = all.w + (size_t)e0 * all.O * all.I;
+        g.w_scale = static_cast<const char *>(all.w_scale) + (size_t)e0 * NB * KB * (all.w_power ? 1 : 4);
+        if (all.offsets) g.offsets = all.offsets + e0;
+        const int rows = (int)(((long long)all.M * g.experts + all.experts - 1) / all.experts);
+        const e8::Args8 a{g.Y, g.y_type, g.x_scale, g.w_scale, g.offsets, e0, g.experts, g.M, g.O, KB, NB, 0, g.err};
+        const e8::FewPlan few = e8::plan_few(rows, g.I, g.O, g.experts);
+        const e8::ManyPlan many = e8::plan_many(rows, g.I, g.O, g.experts);
+        const int rc = many.cost < few.cost ? e8::launch_many(what, many, g, a, st) : e8::launch_few(what, few, g, a, st);
+        if (rc != kOk) return rc;
+    }
+    return kOk;
 }
 
-// TMA's rules for the rows, the tables in shared memory, and 32-bit rows and tiles.
+// TMA's rules for the rows, and 32-bit rows and tiles of a launch.
 bool tc_takes(const E4m3Args &a) {
-    const long long wrows = (long long)a.experts * a.O;
-    const long long tiles = ((long long)a.M / 32 + a.experts) * ((a.O + 127) / 128);
-    return a.I % 16 == 0 && (uintptr_t)a.X % 16 == 0 && (uintptr_t)a.w % 16 == 0 && a.experts <= e8::kMaxExperts &&
-           wrows < (1ll << 31) - 256 && tiles < (1ll << 31) - 65536;
+    const long long experts = std::min(a.experts, e8::kMaxExperts), wrows = experts * a.O;
+    const long long tiles = ((long long)a.M / 32 + experts) * ((a.O + 127) / 128);
+    return a.I % 16 == 0 && (uintptr_t)a.X % 16 == 0 && (uintptr_t)a.w % 16 == 0 && wrows < (1ll << 31) - 256 &&
+           tiles < (1ll << 31) - 65536;
 }
 
 }  // namespace

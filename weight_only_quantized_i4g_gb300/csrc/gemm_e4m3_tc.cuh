@@ -19,7 +19,7 @@ namespace e8 {
 using namespace tc;
 
 constexpr int kWarpMma2 = 2;           // a second issuing warp: they take the stages in turn
-constexpr int kMaxExperts = 1024;      // the tables of tiles and rows in shared memory
+constexpr int kMaxExperts = 1024;      // of one launch: the tables of tiles and rows in shared memory
 constexpr uint32_t kTableBytes = (3 * kMaxExperts + 2) * 4;   // first tiles [E + 1], first and last rows [E][2]
 
 struct Args8 {
@@ -28,6 +28,7 @@ struct Args8 {
     const float *xs;
     const void *ws;
     const int *offsets;               // NULL: one expert, rows [0, M)
+    int before;                       // experts of the launches before this one: offsets[-before] is the table's first
     int experts, M, O, KB, NB, NT;    // K blocks, 128-output blocks, output tiles (set by the launch)
     int *err;
 };
@@ -149,6 +150,14 @@ __device__ __forceinline__ void build_tables(const Args8 &a, int *s_tile, int *s
     } else {
         // The rule of next_rows: expert e has rows most[e] to most[e+1] of the running maximum.
         int tiles_before = 0, most = held_row(a.offsets[0], a.M);
+        if (a.before > 0) {
+            for (int i = threadIdx.x; i < a.before; i += kThreads) most = max(most, held_row(a.offsets[i - a.before], a.M));
+            most = __reduce_max_sync(0xffffffffu, most);
+            if (lane == 0) s_warp[warp].x = most;
+            __syncthreads();
+            for (int w = 0; w < kThreads / 32; ++w) most = max(most, s_warp[w].x);
+            __syncthreads();
+        }
         for (int e0 = 0; e0 < a.experts; e0 += kThreads) {
             const int e = e0 + threadIdx.x;
             int to = 0;
