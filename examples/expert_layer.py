@@ -32,6 +32,13 @@ def blocks(n: int) -> int:
     return -(-n // BLOCK)
 
 
+def expect(name: str, t: torch.Tensor, dtype: torch.dtype, *shape: int) -> None:
+    """The library gets addresses alone: the type, the shape and whole rows one after another are checked here."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}, not {t.dtype} {list(t.shape)} with strides "
+                         f"{list(t.stride())}")
+
+
 def pack(w: torch.Tensor):
     """f32 weights [.., O, I] as e4m3 codes and one f32 scale for each 128 x 128 block (largest value -> 448)."""
     *lead, o, i = w.shape
@@ -70,6 +77,13 @@ class ExpertLayer:
     def __call__(self, out: torch.Tensor, tokens: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor) -> None:
         """tokens bf16 [T, H], ids int32 [T, top] (outside [0, E): no expert here), weights f32 [T, top] -> out bf16."""
         t, k, n = tokens.shape[0], self.top, self.rows
+        if t > self.tokens:
+            raise ValueError(f"{t} tokens, but the layer was made for {self.tokens}")
+        if tokens.dtype != torch.bfloat16 or tokens.shape[1:] != (self.H,) or tokens.stride(1) != 1:
+            raise ValueError(f"tokens must be bfloat16 rows of {self.H} elements side by side")
+        expect("out", out, torch.bfloat16, t, self.H)
+        expect("ids", ids, torch.int32, t, k)
+        expect("weights", weights, torch.float32, t, k)
         ws = (self.ws, self.ws_bytes)
         qg.check(qg.qg_moe_sort(self.offsets, None, self.place, ids, t, k, self.E, *ws))
         qg.check(qg.qg_moe_dispatch(self.x, qg.QG_E4M3, self.x_scale, tokens, qg.QG_BF16, tokens.stride(0), self.place,
