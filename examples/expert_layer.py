@@ -98,10 +98,12 @@ class ExpertLayer:
 
 
 class Dispatch(torch.autograd.Function):
-    """Token rows to their experts' rows, copied; their gradient comes back summed over a token's slots."""
+    """Token rows [T, H] to their experts' rows, copied, by places int32 [T, top]; their gradient comes back summed over
+    a token's slots."""
 
     @staticmethod
     def forward(ctx, x, place, n_rows):
+        expect("place", place, torch.int32, x.shape[0], place.shape[-1])
         x = x.contiguous()
         rows = torch.zeros(n_rows, x.shape[1], dtype=x.dtype, device=x.device)
         t = TYPES[x.dtype]
@@ -120,11 +122,14 @@ class Dispatch(torch.autograd.Function):
 
 
 class Combine(torch.autograd.Function):
-    """Experts' rows back to their tokens with the router's weights; gradients of both."""
+    """Experts' rows [n, H] back to their tokens with the router's weights f32 [T, top] by places int32 [T, top];
+    gradients of rows and weights."""
 
     @staticmethod
     def forward(ctx, y, weights, place):
         y, weights = y.contiguous(), weights.contiguous()
+        expect("place", place, torch.int32, *place.shape[:1], place.shape[-1])
+        expect("weights", weights, torch.float32, *place.shape)
         out = torch.empty(place.shape[0], y.shape[1], dtype=y.dtype, device=y.device)
         t = TYPES[y.dtype]
         qg.check(qg.qg_moe_combine(out, t, y, t, weights, place, place.shape[0], place.shape[1], y.shape[1], y.shape[0]))

@@ -46,3 +46,28 @@ def test_layer_refuses_what_it_cannot_take(ex):
         with pytest.raises(ValueError):
             layer(*args)
     assert len(ex.calls) == 18
+
+
+@pytest.mark.parametrize("place,weights", [
+    (torch.zeros(4, 2, dtype=torch.int64), torch.zeros(4, 2)),           # torch's own index type
+    (torch.zeros(2, 4, dtype=torch.int32).t(), torch.zeros(4, 2)),
+    (torch.zeros(8, dtype=torch.int32), torch.zeros(8)),
+    (torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2, dtype=torch.bfloat16)),
+    (torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 3)),
+    (torch.zeros(4, 2, dtype=torch.int32), torch.zeros(3, 2))])
+def test_wrappers_refuse_other_places_and_weights(ex, place, weights):
+    with pytest.raises(ValueError):
+        ex.Combine.apply(torch.zeros(8, 16), weights, place)
+    if place.dtype != torch.int32 or place.dim() != 2 or not place.is_contiguous():
+        with pytest.raises(ValueError):
+            ex.Dispatch.apply(torch.zeros(4, 16), place, 8)
+    with pytest.raises(ValueError):
+        ex.Dispatch.apply(torch.zeros(3, 16), place, 8)                  # places of other tokens
+    assert ex.calls == []
+
+
+def test_wrappers_take_places_and_weights(ex):
+    place = torch.zeros(4, 2, dtype=torch.int32)
+    assert ex.Combine.apply(torch.zeros(8, 16), torch.zeros(2, 4).t(), place).shape == (4, 16)
+    assert ex.Dispatch.apply(torch.zeros(16, 4).t(), place, 8).shape == (8, 16)
+    assert len(ex.calls) == 2
