@@ -20,6 +20,7 @@ import os
 import sys
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import weight_only_quantized_i4g_gb300 as qg  # noqa: E402
@@ -112,6 +113,7 @@ class Dispatch(torch.autograd.Function):
         return rows
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         place, = ctx.saved_tensors
         grad = grad.contiguous()
@@ -137,6 +139,7 @@ class Combine(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         y, weights, place = ctx.saved_tensors
         grad = grad.contiguous()

@@ -71,3 +71,18 @@ def test_wrappers_take_places_and_weights(ex):
     assert ex.Combine.apply(torch.zeros(8, 16), torch.zeros(2, 4).t(), place).shape == (4, 16)
     assert ex.Dispatch.apply(torch.zeros(16, 4).t(), place, 8).shape == (8, 16)
     assert len(ex.calls) == 2
+
+
+@pytest.mark.parametrize("wrapper", ["dispatch", "combine"])
+def test_second_derivatives_are_refused(ex, wrapper):
+    """Where another path carries the graph, a second derivative through the wrapper would be left out without a word."""
+    place = torch.zeros(4, 2, dtype=torch.int32)
+    if wrapper == "dispatch":
+        x = torch.ones(4, 16, requires_grad=True)
+        y = ex.Dispatch.apply(x, place, 8)
+    else:
+        x = torch.ones(8, 16, requires_grad=True)
+        y = ex.Combine.apply(x, torch.zeros(4, 2), place)
+    first, = torch.autograd.grad(y.square().sum() + x.pow(3).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        first.sum().backward()
