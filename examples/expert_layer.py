@@ -143,7 +143,8 @@ class Combine(torch.autograd.Function):
     def backward(ctx, grad):
         y, weights, place = ctx.saved_tensors
         grad = grad.contiguous()
-        dy, dw = torch.zeros_like(y), torch.empty_like(weights)
+        dy = torch.zeros_like(y) if ctx.needs_input_grad[0] else None
+        dw = torch.empty_like(weights) if ctx.needs_input_grad[1] else None
         qg.check(qg.qg_moe_combine_grad(dy, dw, grad, TYPES[grad.dtype], y, TYPES[y.dtype], weights, place, place.shape[0],
                                         place.shape[1], y.shape[1], y.shape[0]))
         return dy, dw, None

@@ -86,3 +86,13 @@ def test_second_derivatives_are_refused(ex, wrapper):
     first, = torch.autograd.grad(y.square().sum() + x.pow(3).sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         first.sum().backward()
+
+
+@pytest.mark.parametrize("rows,router", [(True, True), (True, False), (False, True)])
+def test_only_the_gradients_wanted_are_asked_for(ex, qg, monkeypatch, rows, router):  # noqa: F811
+    asked = []
+    monkeypatch.setattr(qg, "qg_moe_combine_grad", lambda dy, dw, *a: asked.append((dy is not None, dw is not None)) or 0)
+    y, weights = torch.ones(8, 16, requires_grad=rows), torch.ones(4, 2, requires_grad=router)
+    ex.Combine.apply(y, weights, torch.zeros(4, 2, dtype=torch.int32)).sum().backward()
+    assert asked == [(rows, router)]
+    assert (y.grad is not None, weights.grad is not None) == (rows, router)
