@@ -153,6 +153,20 @@ class Combine(torch.autograd.Function):
 TYPES = {torch.float32: qg.QG_F32, torch.bfloat16: qg.QG_BF16, torch.float16: qg.QG_F16}
 
 
+def capture(layer: ExpertLayer, out, tokens, ids, weights) -> torch.cuda.CUDAGraph:
+    """The layer as a graph on these tensors, after one run on a stream of its own (out holds its result); what the
+    current stream has been given so far, such as the tokens and the layer's buffers, comes first."""
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer(out, tokens, ids, weights)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer(out, tokens, ids, weights)
+    return graph
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--tokens", type=int, default=4096)
@@ -176,13 +190,7 @@ def main():
         ids.copy_(top.indices)
         weights.copy_(torch.softmax(top.values, 1))
     route()
-    side = torch.cuda.Stream()
-    with torch.cuda.stream(side):
-        layer(out, x, ids, weights)
-    torch.cuda.synchronize()
-    graph = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(graph):
-        layer(out, x, ids, weights)
+    graph = capture(layer, out, x, ids, weights)
     begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     for i in range(22):
         if i == 2:

@@ -1,0 +1,35 @@
+"""The expert-layer example's warm-up and capture: they wait for what the
+current stream still has to do, and the program runs."""
+import sys
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_expert_layer import ex, make, randn, slots  # noqa: E402, F401
+
+pytestmark = pytest.mark.gpu
+
+
+def test_warm_up_waits_for_the_current_stream(ex):  # noqa: F811
+    x, (_, ids, weights) = randn(3, 70, 400).bfloat16(), slots(70, 3, 6, 4, 0.1)
+    want, out = torch.empty_like(x), torch.empty_like(x)
+    make(ex)(want, x, ids, weights)
+    layer, late_x, late_ids, late_weights = make(ex), torch.zeros_like(x), torch.zeros_like(ids), torch.zeros_like(weights)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)                            # some 50 ms before the inputs are there
+    for late, t in ((late_x, x), (late_ids, ids), (late_weights, weights)):
+        late.copy_(t)
+    graph = ex.capture(layer, out, late_x, late_ids, late_weights)
+    assert torch.equal(out, want)                             # of the warm-up: a capture runs nothing
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_the_program_runs(ex, monkeypatch, capsys):  # noqa: F811
+    monkeypatch.setattr(sys, "argv", ["expert_layer.py", "--tokens", "130", "--experts", "12", "--top", "4", "--hidden", "256",
+                                      "--width", "144"])
+    ex.main()
+    assert "130 tokens, 12 experts" in capsys.readouterr().out
