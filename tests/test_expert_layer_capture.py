@@ -16,6 +16,7 @@ def test_warm_up_waits_for_the_current_stream(ex):  # noqa: F811
     want, out = torch.empty_like(x), torch.empty_like(x)
     make(ex)(want, x, ids, weights)
     layer, late_x, late_ids, late_weights = make(ex), torch.zeros_like(x), torch.zeros_like(ids), torch.zeros_like(weights)
+    torch.cuda.Stream()                                       # the process's first one takes as long as the wait below
     torch.cuda.synchronize()
     torch.cuda._sleep(100_000_000)                            # some 50 ms before the inputs are there
     for late, t in ((late_x, x), (late_ids, ids), (late_weights, weights)):
