@@ -198,6 +198,8 @@ def main():
         graph.replay()
     end.record()
     torch.cuda.synchronize()
+    rc, status = qg.qg_device_status()
+    qg.check(rc or status)
     ms = begin.elapsed_time(end) / 20
     flops = 6.0 * a.tokens * a.top * a.hidden * a.width
     print(f"{a.tokens} tokens, {a.experts} experts of {a.width}, {a.top} a token: {ms * 1e3:.1f} us, "

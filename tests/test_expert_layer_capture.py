@@ -29,8 +29,23 @@ def test_warm_up_waits_for_the_current_stream(ex):  # noqa: F811
     assert torch.equal(out, want)
 
 
+SMALL = ["expert_layer.py", "--tokens", "130", "--experts", "12", "--top", "4", "--hidden", "256", "--width", "144"]
+
+
+def test_the_program_reports_the_device_status(ex, monkeypatch):  # noqa: F811
+    import weight_only_quantized_i4g_gb300 as qg
+    monkeypatch.setattr(sys, "argv", SMALL)
+    layer = make(ex)
+    layer.offsets.copy_(torch.tensor([0, 9, 5, 12, 12, 12, 12]))                 # decreases
+    n = layer.rows
+    qg.check(qg.qgemm_e4m3_moe(qg.QG_FMT_FP8B128, layer.gu, qg.QG_BF16, layer.x, layer.x_scale, layer.up, layer.up_scale,
+                               layer.offsets, layer.E, n, layer.H, 2 * layer.F))
+    with pytest.raises(qg.QGError):
+        ex.main()
+    assert qg.qg_device_status() == (qg.QG_OK, qg.QG_OK)
+
+
 def test_the_program_runs(ex, monkeypatch, capsys):  # noqa: F811
-    monkeypatch.setattr(sys, "argv", ["expert_layer.py", "--tokens", "130", "--experts", "12", "--top", "4", "--hidden", "256",
-                                      "--width", "144"])
+    monkeypatch.setattr(sys, "argv", SMALL)
     ex.main()
     assert "130 tokens, 12 experts" in capsys.readouterr().out
