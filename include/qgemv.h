@@ -686,8 +686,8 @@ int qg_moe_combine_grad(void *dy, float *dweights, const void *dout, int dout_ty
  *             held to [0, M], and the device error word says QG_EEXPERT.
  *             n_experts 1 .. 8192.
  *   Y         DEVICE [M][O], y_type QG_F32, QG_BF16 or QG_F16
- *   ws        qgemm_e4m3_workspace_bytes() bytes (n_experts = 1 for
- *             qgemm_e4m3), 256-byte aligned; contents on entry do not matter
+ *   ws        reserved: qgemm_e4m3_workspace_bytes() is 0 for every size and
+ *             nothing is read or written there.  NULL, or 256-byte aligned
  * The products of a block are exact and summed in f32, the blocks' sums times
  * the product of the two scales (one f32; a subnormal or infinite one is as
  * good as f32 holds it) are summed in f32: within 1e-3 * sum |x w| of the

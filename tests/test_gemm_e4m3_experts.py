@@ -54,3 +54,18 @@ def test_tables_that_decrease_across_launches(qg, i, where):  # noqa: F811
     table[where] = 90
     table[-1] = 97
     check_table(qg, table, 100, i, 40)
+
+
+@pytest.mark.parametrize("experts,i", [(1, 256), (3, 256), (3, 135)])
+def test_without_a_workspace(qg, experts, i):  # noqa: F811
+    """Its size is 0 for every call: NULL will do."""
+    x, w = codes((30, i), 1, 20.0), codes((experts, 40, i), 2, 20.0)
+    xs, ws = scales((30, blocks(i)), 3, False), scales((experts, 1, blocks(i)), 4, False)
+    bounds = [30 * e // experts for e in range(experts + 1)]
+    y = guarded((30, 40), DTYPES["f32"])
+    if experts == 1:
+        qg.check(qg.qgemm_e4m3(qg.QG_FMT_FP8B128, y, qg.QG_F32, x, xs, w, ws, 30, i, 40, None, 0))
+    else:
+        qg.check(qg.qgemm_e4m3_moe(qg.QG_FMT_FP8B128, y, qg.QG_F32, x, xs, w, ws, ints(bounds), experts, 30, i, 40, None, 0))
+    want, mag = product(x, xs, w, ws, bounds)
+    assert held(y, want, mag, "f32") and unharmed(y)

@@ -39,8 +39,7 @@ int check_places(const char *fn, const void *place, int n_tokens, int k, int n_r
 }
 
 int check_product(const char *fn, int fmt, const void *Y, int y_type, const void *X, const void *x_scales,
-                  const void *w, const void *w_scales, int n_experts, int M, int I, int O, const void *ws,
-                  size_t ws_bytes) {
+                  const void *w, const void *w_scales, int n_experts, int M, int I, int O, const void *ws) {
     if (fmt != QG_FMT_FP8B128 && fmt != QG_FMT_FP8UE8M0)
         QG_REFUSE(kEInval, "%s: format id %d is not QG_FMT_FP8B128 or QG_FMT_FP8UE8M0", fn, fmt);
     if (!is_wide(y_type)) QG_REFUSE(kEInval, "%s: y_type %d is not QG_F32, QG_BF16 or QG_F16", fn, y_type);
@@ -54,18 +53,14 @@ int check_product(const char *fn, int fmt, const void *Y, int y_type, const void
         QG_REFUSE(kEInval, "%s: Y, X, x_scales, w and w_scales must be non-NULL", fn);
     if (!aligned(Y, size_of(y_type)) || !aligned(x_scales, 4) || (fmt == QG_FMT_FP8B128 && !aligned(w_scales, 4)))
         QG_REFUSE(kEAlign, "%s: Y must be aligned to its type, x_scales and f32 w_scales to 4 bytes", fn);
-    const size_t need = ws_gemm_e4m3(M, I, O, n_experts);
-    if (need > 0 && (ws == nullptr || ws_bytes < need))
-        QG_REFUSE(kEWorkspace, "%s: needs a workspace of %zu bytes (qgemm_e4m3_workspace_bytes; got %zu)", fn, need,
-                  ws == nullptr ? (size_t)0 : ws_bytes);
     if (ws && !aligned(ws, 256)) QG_REFUSE(kEAlign, "%s: workspace must be 256-byte aligned", fn);
     return kOk;
 }
 
 int product(const char *fn, int fmt, void *Y, int y_type, const uint8_t *X, const float *x_scales, const uint8_t *w,
-            const void *w_scales, const int *offsets, int n_experts, int M, int I, int O, void *ws, size_t ws_bytes,
+            const void *w_scales, const int *offsets, int n_experts, int M, int I, int O, const void *ws,
             qg_stream_t stream) {
-    const int rc = check_product(fn, fmt, Y, y_type, X, x_scales, w, w_scales, n_experts, M, I, O, ws, ws_bytes);
+    const int rc = check_product(fn, fmt, Y, y_type, X, x_scales, w, w_scales, n_experts, M, I, O, ws);
     if (rc || M == 0) return rc;
     cudaGetLastError();
     E4m3Args a{};
@@ -82,7 +77,7 @@ int product(const char *fn, int fmt, void *Y, int y_type, const uint8_t *X, cons
     a.I = I;
     a.O = O;
     a.err = device_error_word();
-    return run_gemm_e4m3(a, ws, reinterpret_cast<cudaStream_t>(stream));
+    return run_gemm_e4m3(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // namespace
@@ -178,25 +173,20 @@ int qg_moe_combine_grad(void *dy, float *dweights, const void *dout, int dout_ty
     return run_moe_combine_grad(a, dout_type, y_type, reinterpret_cast<cudaStream_t>(stream));
 }
 
-size_t qgemm_e4m3_workspace_bytes(int M, int I, int O, int n_experts) {
-    if (M < 1 || I < 1 || O < 1 || n_experts < 1 || n_experts > kMaxSortExperts || M > 65535 * 64 ||
-        I > INT_MAX - 256 || O > INT_MAX - 256)
-        return 0;
-    return ws_gemm_e4m3(M, I, O, n_experts);
-}
+size_t qgemm_e4m3_workspace_bytes(int, int, int, int) { return 0; }   // a split K is added up over clusters
 
 int qgemm_e4m3(int fmt, void *Y, int y_type, const uint8_t *X, const float *x_scales, const uint8_t *w,
-               const void *w_scales, int M, int I, int O, void *ws, size_t ws_bytes, qg_stream_t stream) {
-    return product("qgemm_e4m3", fmt, Y, y_type, X, x_scales, w, w_scales, nullptr, 1, M, I, O, ws, ws_bytes, stream);
+               const void *w_scales, int M, int I, int O, void *ws, size_t, qg_stream_t stream) {
+    return product("qgemm_e4m3", fmt, Y, y_type, X, x_scales, w, w_scales, nullptr, 1, M, I, O, ws, stream);
 }
 
 int qgemm_e4m3_moe(int fmt, void *Y, int y_type, const uint8_t *X, const float *x_scales, const uint8_t *w,
-                   const void *w_scales, const int *offsets, int n_experts, int M, int I, int O, void *ws,
-                   size_t ws_bytes, qg_stream_t stream) {
+                   const void *w_scales, const int *offsets, int n_experts, int M, int I, int O, void *ws, size_t,
+                   qg_stream_t stream) {
     const char *fn = "qgemm_e4m3_moe";
     if (!offsets) QG_REFUSE(kEInval, "%s: offsets must be non-NULL", fn);
     if (!aligned(offsets, 4)) QG_REFUSE(kEAlign, "%s: offsets must be 4-byte aligned", fn);
-    return product(fn, fmt, Y, y_type, X, x_scales, w, w_scales, offsets, n_experts, M, I, O, ws, ws_bytes, stream);
+    return product(fn, fmt, Y, y_type, X, x_scales, w, w_scales, offsets, n_experts, M, I, O, ws, stream);
 }
 
 }  // extern "C"

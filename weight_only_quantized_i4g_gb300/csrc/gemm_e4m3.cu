@@ -127,9 +127,7 @@ bool tc_takes(const E4m3Args &a) {
 
 }  // namespace
 
-size_t ws_gemm_e4m3(int, int, int, int) { return 0; }
-
-int run_gemm_e4m3(const E4m3Args &a, void *, cudaStream_t st) {
+int run_gemm_e4m3(const E4m3Args &a, cudaStream_t st) {
     const char *what = a.offsets ? "qgemm_e4m3_moe" : "qgemm_e4m3";
     if (tc_takes(a)) return run_tc(what, a, st);
     const dim3 grid((a.O + kGT - 1) / kGT, (a.M + kGT - 1) / kGT);

@@ -64,8 +64,7 @@ struct E4m3Args {
     int experts, M, I, O;
     int *err;
 };
-size_t ws_gemm_e4m3(int M, int I, int O, int experts);
-int run_gemm_e4m3(const E4m3Args &a, void *ws, cudaStream_t st);
+int run_gemm_e4m3(const E4m3Args &a, cudaStream_t st);
 // Where the first expert's rows begin and, from there, expert by expert, rows
 // [*from, *most) of expert g: row bounds are held to [0, M] and to their order,
 // so a table that leaves the rows or decreases gives no row twice, and the
