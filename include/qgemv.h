@@ -679,7 +679,9 @@ int qg_moe_combine_grad(void *dy, float *dweights, const void *dout, int dout_ty
  *             n_experts such matrices one after another, and their scales
  *   offsets   DEVICE int32 [n_experts + 1] (qg_moe_sort): rows offsets[e] ..
  *             offsets[e+1] - 1 use expert e.  M is the rows that X and Y hold,
- *             at least offsets[n_experts]; rows behind that, and rows before
+ *             at least offsets[n_experts] (the choice between kernels goes by
+ *             M and n_experts, so a capacity far above the rows in use may
+ *             cost some time); rows behind that, and rows before
  *             offsets[0], are not written.  In a table that decreases or
  *             leaves [0, M] expert e's rows go from the largest of offsets[0]
  *             .. offsets[e] to the largest of offsets[0] .. offsets[e+1], each

@@ -474,9 +474,10 @@ FewPlan plan_few(int M, int I, int O, int experts) {
         if (c > 1 && KB < 4 * c) break;
         const int n = clusters_at_once(best.bt, c);
         if (n < 1) break;
-        // cycles of a K block, as measured (32 tokens: what 16 KB of weights
-        // take an SM at the card's bandwidth), and of one round of the
-        // reduction over a cluster
+        // cycles of a K block, as measured with full tiles (32 tokens: what
+        // 16 KB of weights take an SM at the card's bandwidth), and of one
+        // round of the reduction over a cluster, which takes longer: with 2500
+        // the estimate for 64 rows of 2048 x 7168 is 6 us and the call takes 17
         const double step = best.bt == 128 ? 1370.0 : best.bt == 64 ? 800.0 : 700.0, rounds = best.bt / 32;
         const double waves = std::ceil(tiles / n);
         const double cost = waves * (((KB + c - 1) / c) * step + (c > 1 ? 2500.0 * rounds : 0.0) + 1500.0);

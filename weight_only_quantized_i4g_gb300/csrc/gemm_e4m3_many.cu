@@ -5,8 +5,8 @@
 // scale each, so a promoting thread holds one token and scales a half's sums by
 // one factor.  (With the tokens along N a factor a column has to be read from
 // shared memory: 64 columns then take a warp 290 cycles instead of 134, and a K
-// block 1800 instead of the MMAs' 512.)  4096 x 7168 x 7168: 153 us, 2750
-// TFLOP/s, about 770 cycles a K block.  What bounds it is the promoting warps,
+// block 1800 instead of the MMAs' 512.)  4096 x 7168 x 7168 with normal codes:
+// 157 us, 2685 TFLOP/s, about 770 cycles a K block.  What bounds it is the promoting warps,
 // two a scheduler with 128 additions a thread and the wait and loads before
 // them: without the additions it took 133 us (157 with them at the time), with
 // one of a K block's four MMAs 146, without the copies 152.  As two MMAs of N =

@@ -7,8 +7,10 @@
 // A stable counting sort: every warp counts the experts of a stretch of
 // slots, the counts before it (of lower experts, and of its own expert in
 // earlier stretches) are added up, and a second pass over the stretch hands
-// out the places in order.  No atomics: of the lanes that hold the same
-// expert one counts for all, so the result never depends on timing.
+// out the places in order: of the lanes that hold the same expert one counts
+// for all.  The first kernel of a long list counts a block's stretch by atomic
+// additions in shared memory, whole numbers whose sums are the same in any
+// order, so the result never depends on timing.
 #include <algorithm>
 
 #include "moe.cuh"
