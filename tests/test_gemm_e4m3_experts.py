@@ -69,3 +69,28 @@ def test_without_a_workspace(qg, experts, i):  # noqa: F811
         qg.check(qg.qgemm_e4m3_moe(qg.QG_FMT_FP8B128, y, qg.QG_F32, x, xs, w, ws, ints(bounds), experts, 30, i, 40, None, 0))
     want, mag = product(x, xs, w, ws, bounds)
     assert held(y, want, mag, "f32") and unharmed(y)
+
+
+def test_captured_and_replayed_with_other_offsets(qg):  # noqa: F811
+    """Two launches in a graph, rows before, across and behind the border between them."""
+    experts, m, i, o = 1500, 200, 256, 136
+    x, w = codes((m, i), 1, 20.0), codes((experts, o, i), 2, 20.0)
+    xs, ws = scales((m, blocks(i)), 3, False), scales((experts, blocks(o), blocks(i)), 4, False)
+    off, y = ints([0] * (experts + 1)), torch.zeros(m, o, device=x.device)
+    qg.check(call(qg, y, x, xs, w, ws, off))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qg.check(qg.qgemm_e4m3_moe(qg.QG_FMT_FP8B128, y, qg.QG_F32, x, xs, w, ws, off, experts, m, i, o))
+    for seed, rows in enumerate(({0: 200}, {1499: 150}, {1023: 90, 1024: 110}, {5: 60, 1200: 70}, {})):
+        counts = [rows.get(e, 0) for e in range(experts)]
+        bounds = [0]
+        for c in counts:
+            bounds.append(bounds[-1] + c)
+        off.copy_(ints(bounds))
+        y.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        n = bounds[-1]
+        want, mag = product(x, xs, w, ws, bounds)
+        assert held(y[:n], want[:n], mag[:n], "f32") and bool((y[n:] == 7).all()), seed
